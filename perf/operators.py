@@ -8,7 +8,9 @@ The cache holds K and V as E2M1 codes (4 bits) with one E4M3 scale for every
 
 A group buffer is shared by layers 2j (sliding window) and 2j + 1 (full), and
 is [num_blocks, kv heads, block / 16, 1152] bytes: tiles of 16 tokens, each
-K codes [16][32], V codes [16][32], K scales [8][4][2], V scales [4][4][4].
+K codes [16][32], V codes [16][32], K scales [8][4][2] (token % 8, block of 16
+channels, token / 8), V scales [4][4][2][2] (block, token % 8 / 2, token / 8,
+token % 2).
 
 Four operators:
   write  rotate and quantise the K and V of given tokens of every layer into
@@ -227,10 +229,10 @@ E2M1 = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
 
 
 def _views(cache):
-    """(K codes [..,16,32], V codes [..,16,32], K scales [..,8,4,2], V scales [..,4,4,4])"""
+    """(K codes [..,16,32], V codes [..,16,32], K scales [..,8,4,2], V scales [..,4,4,2,2])"""
     return (cache[..., :512].unflatten(-1, (16, 32)), cache[..., 512:1024].unflatten(-1, (16, 32)),
             cache[..., 1024:1088].unflatten(-1, (8, 4, 2)),
-            cache[..., 1088:].unflatten(-1, (4, 4, 4)))
+            cache[..., 1088:].unflatten(-1, (4, 4, 2, 2)))
 
 
 def _rope(x, cos, sin):
@@ -275,7 +277,7 @@ def _places(s):
     head = (layer // 2)[:, None], (at // B)[:, None], h, (at % B // TILE)[:, None]
     return (layer, token, head + (tau[:, None],),
             head + ((tau % 8)[:, None], slice(None), (tau // 8)[:, None]),
-            head + (slice(None), (tau % 4)[:, None], (tau // 4)[:, None]))
+            head + (slice(None), (tau % 8 // 2)[:, None], (tau // 8)[:, None], (tau % 2)[:, None]))
 
 
 def _plain_write(s):
@@ -311,7 +313,7 @@ def _plain_attn(s):
         # [R, blocks, H, tiles, ..] -> [R, H, tokens, ..]
         kc, vc, ks, vs = (x[table.long()].transpose(1, 2) for x in _views(s["cache"][i // 2]))
         ks = ks.permute(0, 1, 2, 3, 6, 4, 5)      # token = 8 * hi + lo
-        vs = vs.permute(0, 1, 2, 3, 6, 5, 4)      # token = 4 * hi + lo
+        vs = vs.permute(0, 1, 2, 3, 6, 5, 7, 4)   # token = 8 * hi + 2 * pair + lo
         k = _dequantise(kc.flatten(2, 4), ks.reshape(R, H, -1, 4)) * s["k_scale"][i]
         score = (q[i] @ k.transpose(-1, -2)) / math.sqrt(D)
         t = torch.arange(k.shape[2], device=q.device)
@@ -385,7 +387,7 @@ def _tokens64(s, i, slots, heads):
     at = base + 32 * t + e // 2
     nib = lambda a: (flat[a] >> (4 * (e & 1)).to(torch.uint8)) & 15  # noqa: E731
     k = _value64(nib(at), flat[base + 1024 + 8 * (t % 8) + 2 * (e // 16) + t // 8])
-    v = _value64(nib(at + 512), flat[base + 1088 + 16 * (e // 16) + 4 * (t % 4) + t // 4])
+    v = _value64(nib(at + 512), flat[base + 1088 + 16 * (e // 16) + 4 * (t % 8 // 2) + 2 * (t // 8) + t % 2])
     return k * s["k_scale"][i].double(), v * s["v_scale"][i].double()
 
 
