@@ -9,7 +9,9 @@ The functions carry the C names: ``gk_kv_append``, ``gk_decode_attn_stack``,
 ``gk_decode_step``, ``gk_decode_attn_stack_static``,
 ``gk_attn_workspace_bytes``, ``gk_attn_workspace_min_bytes``,
 ``gk_e4m3_quantize``, ``gk_kv_budget``, ``gk_kv_regions``, ``gk_kv_ingest``,
-``gk_di_blocks``, ``gk_read_device_error``, ``gk_status_str``, ``gk_abi_version``.  Tensors are torch tensors; the stream defaults to torch's
+``gk_di_blocks``, ``gk_read_device_error``, ``gk_status_str``, ``gk_abi_version``; and, over a
+4-bit cache (``include/gk_kv4.h``), ``gk_kv4_write``, ``gk_kv4_read``,
+``gk_kv4_decode_attn_stack``, ``gk_kv4_decode_step``, ``gk_kv4_block_bytes``.  Tensors are torch tensors; the stream defaults to torch's
 current stream on the tensors' device.  The cache is a ``KvCache``: per-group
 K and V buffers or stacked ``K_cache`` / ``V_cache``, exactly one of the two,
 with packed-ness read from the K tensors' rank as the "GPT-OSS-120B giga-kernel
@@ -30,8 +32,10 @@ GK_OK, GK_ERR_INVALID_ARG, GK_ERR_UNSUPPORTED, GK_ERR_WORKSPACE, GK_ERR_CUDA, \
 GK_DEVERR_SLOT, GK_DEVERR_BLOCK, GK_DEVERR_POS, GK_DEVERR_TIMEOUT, GK_DEVERR_PLAN, \
     GK_DEVERR_INGEST = 0x1, 0x2, 0x4, 0x8, 0x10, 0x20
 GK_K_PACKED, GK_K_PLAIN = 0, 1
+GK_KV4_TILE_BYTES, GK_KV4_SKIP = 1152, -1
 
 HEADER = os.path.join(_build.INCLUDE, "gk.h")
+KV4_HEADER = os.path.join(_build.INCLUDE, "gk_kv4.h")
 
 _lock = threading.Lock()
 _lib = None
@@ -138,6 +142,47 @@ class KvCache:
         return ctypes.byref(self.c)
 
 
+class Kv4CacheC(ctypes.Structure):
+    """gk_kv4_cache."""
+    _fields_ = [("bufs", ctypes.c_void_p), ("cache", ctypes.c_void_p)]
+
+
+class Kv4Cache:
+    """The 4-bit cache in one of its two forms, uint8 tensors on the device:
+
+    per-group: a sequence of NL/2 group buffers [num_blocks, kv, block // 16, 1152];
+    stacked:   one tensor with a leading group axis.
+    Holds references to the tensors and the pointer array it hands the library;
+    the calls take it, or the tensors themselves.
+    """
+
+    def __init__(self, bufs):
+        self._stacked = hasattr(bufs, "data_ptr")
+        self._keep = [bufs] if self._stacked else list(bufs)
+        if not self._keep:
+            raise ValueError("no group buffer")
+        c = Kv4CacheC()
+        if self._stacked:
+            c.cache = _ptr(bufs, _torch().uint8, "kv")
+        else:
+            self._arr = (ctypes.c_void_p * len(self._keep))(
+                *[_ptr(t, _torch().uint8, f"kv[{i}]") for i, t in enumerate(self._keep)])
+            c.bufs = ctypes.cast(self._arr, ctypes.c_void_p)
+        self.c = c
+
+    def check(self, sh: Shape) -> None:
+        """Buffer sizes against the shape (the C ABI cannot see them)."""
+        groups = sh.num_layers // 2
+        want = sh.num_blocks * sh.num_kv_heads * (sh.block_size // 16) * GK_KV4_TILE_BYTES
+        if self._stacked:
+            want *= groups
+        elif len(self._keep) < groups:
+            raise ValueError(f"{len(self._keep)} group buffers for {sh.num_layers} layers")
+        for t in self._keep:
+            if t.numel() < want:
+                raise ValueError(f"a cache buffer holds {t.numel()} bytes, the shape needs {want}")
+
+
 def infer_k_layout(k, v) -> int:
     """Packed-ness from the ranks, as the page's bind step infers it
     (``k.dim() == v.dim() + 1``: the packed view's extra trailing axis of 2)."""
@@ -176,9 +221,16 @@ def _kv(kv, shape) -> "ctypes._CArgObject":
     return kv.param()
 
 
-def declared_functions() -> list:
-    """Names of the functions include/gk.h declares."""
-    text = open(HEADER).read()
+def _kv4(kv, shape):
+    if not isinstance(kv, Kv4Cache):
+        kv = Kv4Cache(kv)
+    kv.check(shape)
+    return kv
+
+
+def declared_functions(header: str = HEADER) -> list:
+    """Names of the functions include/gk.h (or another header) declares."""
+    text = open(header).read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
     return sorted(set(re.findall(r"\b(gk_[a-z0-9_]+)\s*\(", text)))
 
@@ -224,6 +276,16 @@ def lib(build_if_needed: bool = True) -> ctypes.CDLL:
             L.gk_kv_ingest.argtypes = [ctypes.POINTER(KvRegion), i32, vp, vp, i64, vp, vp]
             L.gk_di_blocks.restype = ctypes.c_int
             L.gk_di_blocks.argtypes = [i64, i32, i32] + [ctypes.POINTER(ctypes.c_int64)] * 3
+            L.gk_kv4_block_bytes.restype = sz
+            L.gk_kv4_block_bytes.argtypes = [sp]
+            L.gk_kv4_write.restype = ctypes.c_int
+            L.gk_kv4_write.argtypes = [sp, i32, i32, i64, vp, vp, i64, i64] + [vp] * 9
+            L.gk_kv4_read.restype = ctypes.c_int
+            L.gk_kv4_read.argtypes = [sp, i32, i32, i64] + [vp] * 9
+            L.gk_kv4_decode_attn_stack.restype = ctypes.c_int
+            L.gk_kv4_decode_attn_stack.argtypes = [sp] + [vp] * 15 + [sz, vp]
+            L.gk_kv4_decode_step.restype = ctypes.c_int
+            L.gk_kv4_decode_step.argtypes = [sp] + [vp] * 19 + [sz, vp]
             L.gk_selftest_wait_timeout.restype = ctypes.c_int
             L.gk_selftest_wait_timeout.argtypes = [ctypes.c_uint64, vp,
                                                    ctypes.POINTER(ctypes.c_uint32)]
@@ -250,6 +312,11 @@ def _ptr(t, dtype=None, name="tensor", allow_none=False):
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     return t.data_ptr()
+
+
+def _torch():
+    import torch
+    return torch
 
 
 def _ptr_array(ts: Sequence, name: str):
@@ -478,6 +545,150 @@ def gk_di_blocks(num_tokens: int, block_size: int, window: int):
                             ctypes.byref(b), ctypes.byref(c))
     _check(st, "gk_di_blocks")
     return a.value, b.value, c.value
+
+
+# --------------------------------------------------------------- 4-bit cache
+def gk_kv4_block_bytes(shape) -> int:
+    return int(lib().gk_kv4_block_bytes(ctypes.byref(_as_shape(shape))))
+
+
+def new_kv4_cache(shape, device="cuda", stacked: bool = True):
+    """An uninitialised 4-bit cache of the shape: one tensor [NL/2, num_blocks, kv, block // 16,
+    1152], or (stacked=False) a list of NL/2 group buffers.  No byte needs a value."""
+    import torch
+    sh = _as_shape(shape)
+    if gk_kv4_block_bytes(sh) == 0:
+        raise GkError(GK_ERR_UNSUPPORTED, "gk_kv4_block_bytes")
+    size = (sh.num_blocks, sh.num_kv_heads, sh.block_size // 16, GK_KV4_TILE_BYTES)
+    if stacked:
+        return torch.empty((sh.num_layers // 2,) + size, dtype=torch.uint8, device=device)
+    return [torch.empty(size, dtype=torch.uint8, device=device)
+            for _ in range(sh.num_layers // 2)]
+
+
+def _kv4_rows(sh, k, v, names, contiguous):
+    """Checks of a [layers, tokens, kv, 64] bf16 pair; returns (layers, tokens, strides)."""
+    import torch
+    for t, name in zip((k, v), names):
+        if t.dtype != torch.bfloat16:
+            raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor (no CPU path)")
+        if t.dim() != 4 or t.shape[2:] != (sh.num_kv_heads, sh.head_dim):
+            raise ValueError(f"{name} must be [layers, tokens, {sh.num_kv_heads}, {sh.head_dim}]")
+    if k.shape != v.shape:
+        raise ValueError(f"{names[0]} and {names[1]} differ in shape")
+    D = sh.head_dim
+    for t, name in zip((k, v), names):
+        s = t.stride()
+        if contiguous and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if t.numel() and (s[3] != 1 or (sh.num_kv_heads > 1 and s[2] != D)):
+            raise ValueError(f"{name}: the heads of a token must be contiguous")
+    n, T = k.shape[:2]
+    # the stride of an axis of one is never used
+    sk = tuple(k.stride(a) if k.shape[a] > 1 else 0 for a in (0, 1))
+    sv = tuple(v.stride(a) if v.shape[a] > 1 else 0 for a in (0, 1))
+    if sk != sv:
+        raise ValueError(f"{names[0]} and {names[1]} must have the same strides")
+    return n, T, sk
+
+
+def _kv4_tokens(sh, T, slot_full, slot_swa, active, cos=None, sin=None, scales=()):
+    for t, name, n in ((slot_full, "slot_full", T), (slot_swa, "slot_swa", T),
+                       (active, "active", T), (cos, "cos", T * sh.head_dim // 2),
+                       (sin, "sin", T * sh.head_dim // 2)):
+        if t is not None and t.numel() != n:
+            raise ValueError(f"{name} must hold {n} values for {T} tokens")
+    for t in scales:
+        if t.numel() < sh.num_layers:
+            raise ValueError("the scales hold one value for every layer of the stack")
+
+
+def gk_kv4_write(shape, k, v, cos, sin, k_scale, v_scale, slot_full, slot_swa, kv, active=None,
+                 layer0: int = 0, stream=None) -> None:
+    """Rotate, quantise and write the K and V of tokens into the 4-bit cache.
+
+    k, v: bf16 [n_layers, n_tokens, kv, 64] of layers layer0 ..; the heads of a token are
+    contiguous, layers and tokens may have any stride that is a multiple of 8.  cos, sin: fp32
+    [n_tokens, 32], or both None for K that is rotated already.  slot_full, slot_swa: int32
+    [n_tokens], GK_KV4_SKIP to leave a token out.  kv: a Kv4Cache or its tensors."""
+    import torch
+    sh = _as_shape(shape)
+    n, T, (ls, ts) = _kv4_rows(sh, k, v, ("k", "v"), False)
+    _kv4_tokens(sh, T, slot_full, slot_swa, active, cos, sin, (k_scale, v_scale))
+    kv = _kv4(kv, sh)
+    st = lib().gk_kv4_write(
+        ctypes.byref(sh), int(layer0), n, T, k.data_ptr(), v.data_ptr(), ls, ts,
+        _ptr(cos, torch.float32, "cos", allow_none=True),
+        _ptr(sin, torch.float32, "sin", allow_none=True),
+        _ptr(k_scale, torch.float32, "k_scale"), _ptr(v_scale, torch.float32, "v_scale"),
+        _ptr(slot_full, torch.int32, "slot_full"), _ptr(slot_swa, torch.int32, "slot_swa"),
+        _ptr(active, torch.uint8, "active", allow_none=True), ctypes.byref(kv.c),
+        _stream(stream, k))
+    _check(st, "gk_kv4_write")
+
+
+def gk_kv4_read(shape, kv, k_scale, v_scale, slot_full, slot_swa, k_out, v_out, active=None,
+                layer0: int = 0, stream=None) -> None:
+    """The values at the given slots of the 4-bit cache, as bf16 [n_layers, n_tokens, kv, 64]
+    (contiguous) of layers layer0 ..; the rows of skipped tokens are left as they were."""
+    import torch
+    sh = _as_shape(shape)
+    n, T, _ = _kv4_rows(sh, k_out, v_out, ("k_out", "v_out"), True)
+    _kv4_tokens(sh, T, slot_full, slot_swa, active, scales=(k_scale, v_scale))
+    kv = _kv4(kv, sh)
+    st = lib().gk_kv4_read(
+        ctypes.byref(sh), int(layer0), n, T, ctypes.byref(kv.c),
+        _ptr(k_scale, torch.float32, "k_scale"), _ptr(v_scale, torch.float32, "v_scale"),
+        _ptr(slot_full, torch.int32, "slot_full"), _ptr(slot_swa, torch.int32, "slot_swa"),
+        _ptr(active, torch.uint8, "active", allow_none=True), k_out.data_ptr(), v_out.data_ptr(),
+        _stream(stream, k_out))
+    _check(st, "gk_kv4_read")
+
+
+def gk_kv4_decode_attn_stack(shape, q, kv, k_scale, v_scale, cos, sin, bt_full, bt_swa, pos,
+                             pos_w, active, out, out_f32=None, workspace=None, stream=None,
+                             sinks=None) -> None:
+    """gk_decode_attn_stack over a 4-bit cache (a Kv4Cache or its tensors)."""
+    import torch
+    sh = _as_shape(shape)
+    if workspace is None:
+        raise ValueError("workspace is required (size: gk_attn_workspace_bytes(shape))")
+    kv = _kv4(kv, sh)
+    st = lib().gk_kv4_decode_attn_stack(
+        ctypes.byref(sh), _ptr(q, torch.bfloat16, "q"), ctypes.byref(kv.c),
+        _ptr(k_scale, torch.float32, "k_scale"), _ptr(v_scale, torch.float32, "v_scale"),
+        _ptr(cos, torch.float32, "cos"), _ptr(sin, torch.float32, "sin"),
+        _ptr(bt_full, torch.int32, "bt_full"), _ptr(bt_swa, torch.int32, "bt_swa"),
+        _ptr(pos, torch.int32, "pos"), _ptr(pos_w, torch.int32, "pos_w"),
+        _ptr(active, torch.uint8, "active"), _sinks(sinks, sh), _ptr(out, torch.bfloat16, "out"),
+        _ptr(out_f32, torch.float32, "out_f32", allow_none=True),
+        _ptr(workspace, torch.uint8, "workspace"), int(workspace.numel()), _stream(stream, q))
+    _check(st, "gk_kv4_decode_attn_stack")
+
+
+def gk_kv4_decode_step(shape, q, k_new, v_new, cos, sin, k_scale, v_scale, upd_full, upd_swa,
+                       bt_full, bt_swa, pos, pos_w, active, kv, out, out_f32=None,
+                       workspace=None, stream=None, sinks=None) -> None:
+    """gk_kv4_write of every row's new token + gk_kv4_decode_attn_stack in two launches."""
+    import torch
+    sh = _as_shape(shape)
+    if workspace is None:
+        raise ValueError("workspace is required (size: gk_attn_workspace_bytes(shape))")
+    kv = _kv4(kv, sh)
+    st = lib().gk_kv4_decode_step(
+        ctypes.byref(sh), _ptr(q, torch.bfloat16, "q"), _ptr(k_new, torch.bfloat16, "k_new"),
+        _ptr(v_new, torch.bfloat16, "v_new"), _ptr(cos, torch.float32, "cos"),
+        _ptr(sin, torch.float32, "sin"), _ptr(k_scale, torch.float32, "k_scale"),
+        _ptr(v_scale, torch.float32, "v_scale"), _ptr(upd_full, torch.int32, "upd_full"),
+        _ptr(upd_swa, torch.int32, "upd_swa"), _ptr(bt_full, torch.int32, "bt_full"),
+        _ptr(bt_swa, torch.int32, "bt_swa"), _ptr(pos, torch.int32, "pos"),
+        _ptr(pos_w, torch.int32, "pos_w"), _ptr(active, torch.uint8, "active"),
+        _sinks(sinks, sh), ctypes.byref(kv.c), _ptr(out, torch.bfloat16, "out"),
+        _ptr(out_f32, torch.float32, "out_f32", allow_none=True),
+        _ptr(workspace, torch.uint8, "workspace"), int(workspace.numel()), _stream(stream, q))
+    _check(st, "gk_kv4_decode_step")
 
 
 def gk_selftest_wait_timeout(limit_ns: int, stream=None) -> int:

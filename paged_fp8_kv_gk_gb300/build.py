@@ -19,8 +19,8 @@ LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
 ROOT = os.path.dirname(HERE)
 INCLUDE = os.path.join(ROOT, "include")
 
-SOURCES = ["gk_kernels.cu", "gk_api.cu", "gk_noalloc.cu", "gk_ingest.cu"]
-HEADERS = ["gk_device.cuh", "gk_internal.h"]
+SOURCES = ["gk_kernels.cu", "gk_api.cu", "gk_noalloc.cu", "gk_ingest.cu", "gk_kv4.cu"]
+HEADERS = ["gk_device.cuh", "gk_internal.h", "gk_plan.cuh", "gk_attn_common.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2",
               "--expt-relaxed-constexpr", "-Xptxas", "-v"]
@@ -42,7 +42,7 @@ def _stale(lib_path: str = LIB_PATH) -> bool:
         return True
     t = os.path.getmtime(lib_path)
     deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [
-        os.path.join(INCLUDE, h) for h in ("gk.h", "gk_testing.h")]
+        os.path.join(INCLUDE, h) for h in ("gk.h", "gk_kv4.h", "gk_testing.h")]
     return any(os.path.getmtime(d) > t for d in deps)
 
 

@@ -4,6 +4,7 @@
 #include <string.h>
 
 #include "gk_internal.h"
+#include "../../include/gk_kv4.h"
 #include "../../include/gk_testing.h"
 
 namespace gk {
@@ -74,6 +75,24 @@ static gk_status resolve_kv(const gk_shape& s, const gk_kv_cache* kv, uint8_t** 
     }
   }
   *k_packed = kv->k_layout == GK_K_PACKED ? 1 : 0;
+  return GK_OK;
+}
+
+// Bytes of one block of a 4-bit group buffer.
+static int64_t kv4_block_bytes(const gk_shape& s) {
+  return int64_t(s.num_kv_heads) * (s.block_size / 16) * GK_KV4_TILE_BYTES;
+}
+
+// The 4-bit cache descriptor -> group buffer pointers, exactly one form.
+static gk_status resolve_kv4(const gk_shape& s, const gk_kv4_cache* kv, uint8_t** buf) {
+  if (!kv || (kv->bufs != nullptr) == (kv->cache != nullptr)) return GK_ERR_INVALID_ARG;
+  const int groups = s.num_layers / 2;
+  const int64_t bytes = int64_t(s.num_blocks) * kv4_block_bytes(s);  // a multiple of 16
+  for (int j = 0; j < groups; ++j) {
+    buf[j] = kv->bufs ? static_cast<uint8_t*>(kv->bufs[j])
+                      : static_cast<uint8_t*>(kv->cache) + int64_t(j) * bytes;
+    if (!buf[j] || !aligned16(buf[j])) return GK_ERR_INVALID_ARG;
+  }
   return GK_OK;
 }
 
@@ -198,14 +217,16 @@ struct AppendInputs {
 };
 
 // Validation and launch shared by gk_decode_attn_stack and gk_decode_step
-// (app != nullptr: gk_decode_step, whose planner grid also appends).
+// (app != nullptr: gk_decode_step, whose planner grid also appends), and by
+// their counterparts over a 4-bit cache (kv4 instead of kv).
 static gk_status decode_attention(const gk_shape* shape, const void* q, const gk_kv_cache* kv,
                                   const float* k_scale, const float* v_scale,
                                   const float* cos, const float* sin, const int32_t* bt_full,
                                   const int32_t* bt_swa, const int32_t* pos, const int32_t* pos_w,
                                   const uint8_t* active, const float* sinks, void* out,
                                   float* out_f32, void* workspace, size_t ws_bytes, void* stream,
-                                  const AppendInputs* app, int force_split_log = -1) {
+                                  const AppendInputs* app, int force_split_log = -1,
+                                  const gk_kv4_cache* kv4 = nullptr) {
   gk_status st = check_shape(shape);
   if (st != GK_OK) return st;
   if (!q || !k_scale || !v_scale || !cos || !sin || !bt_full || !bt_swa ||
@@ -226,8 +247,8 @@ static gk_status decode_attention(const gk_shape* shape, const void* q, const gk
   memset(&p, 0, sizeof(p));
   {
     uint8_t* kb[kMaxGroups];
-    uint8_t* vb[kMaxGroups];
-    st = resolve_kv(*shape, kv, kb, vb, &p.k_packed);
+    uint8_t* vb[kMaxGroups] = {};
+    st = kv4 ? resolve_kv4(*shape, kv4, kb) : resolve_kv(*shape, kv, kb, vb, &p.k_packed);
     if (st != GK_OK) return st;
     for (int j = 0; j < shape->num_layers / 2; ++j) {
       p.kb[j] = kb[j];
@@ -284,6 +305,34 @@ static gk_status decode_attention(const gk_shape* shape, const void* q, const gk
   pl.max_tokens_full = shape->max_blocks_full * shape->block_size;
   pl.max_tokens_swa = shape->max_blocks_swa * shape->block_size;
   pl.force_split_log = force_split_log;
+  if (kv4) {
+    Kv4WriteParams wp;
+    if (app) {
+      // gk_kv4_decode_step: the new tokens are written in the planner's grid
+      memset(&wp, 0, sizeof(wp));
+      wp.k = static_cast<const uint16_t*>(app->k_new);
+      wp.v = static_cast<const uint16_t*>(app->v_new);
+      wp.token_stride = int64_t(shape->num_kv_heads) * kHeadDim;
+      wp.layer_stride = wp.token_stride * shape->batch;
+      wp.cosb = cos;
+      wp.sinb = sin;
+      wp.k_scale = k_scale;
+      wp.v_scale = v_scale;
+      wp.slot_full = app->upd_full;
+      wp.slot_swa = app->upd_swa;
+      wp.active = active;
+      for (int j = 0; j < shape->num_layers / 2; ++j) wp.buf[j] = const_cast<uint8_t*>(p.kb[j]);
+      wp.n_layers = shape->num_layers;
+      wp.n_tokens = shape->batch;
+      wp.Hkv = shape->num_kv_heads;
+      wp.B = shape->block_size;
+      wp.nb = shape->num_blocks;
+    }
+    return launch_kv4_attention(pl, p, static_cast<cudaStream_t>(stream), app ? &wp : nullptr) ==
+                   cudaSuccess
+               ? GK_OK
+               : GK_ERR_CUDA;
+  }
   AppendParams ap;
   if (app) {
     // gk_decode_step: the append runs in the planner's grid
@@ -338,6 +387,117 @@ gk_status gk_decode_step(const gk_shape* shape, const void* q, const void* k_new
   const AppendInputs app = {k_new, v_new, upd_full, upd_swa};
   return decode_attention(shape, q, kv, k_scale, v_scale, cos, sin, bt_full, bt_swa, pos, pos_w,
                           active, sinks, out, out_f32, workspace, ws_bytes, stream, &app);
+}
+
+gk_status gk_kv4_decode_attn_stack(const gk_shape* shape, const void* q, const gk_kv4_cache* kv,
+                                   const float* k_scale, const float* v_scale, const float* cos,
+                                   const float* sin, const int32_t* bt_full,
+                                   const int32_t* bt_swa, const int32_t* pos,
+                                   const int32_t* pos_w, const uint8_t* active,
+                                   const float* sinks, void* out, float* out_f32, void* workspace,
+                                   size_t ws_bytes, void* stream) {
+  if (!kv) return GK_ERR_INVALID_ARG;
+  return decode_attention(shape, q, nullptr, k_scale, v_scale, cos, sin, bt_full, bt_swa, pos,
+                          pos_w, active, sinks, out, out_f32, workspace, ws_bytes, stream, nullptr,
+                          -1, kv);
+}
+
+gk_status gk_kv4_decode_step(const gk_shape* shape, const void* q, const void* k_new,
+                             const void* v_new, const float* cos, const float* sin,
+                             const float* k_scale, const float* v_scale, const int32_t* upd_full,
+                             const int32_t* upd_swa, const int32_t* bt_full,
+                             const int32_t* bt_swa, const int32_t* pos, const int32_t* pos_w,
+                             const uint8_t* active, const float* sinks, const gk_kv4_cache* kv,
+                             void* out, float* out_f32, void* workspace, size_t ws_bytes,
+                             void* stream) {
+  if (!kv) return GK_ERR_INVALID_ARG;
+  const AppendInputs app = {k_new, v_new, upd_full, upd_swa};
+  return decode_attention(shape, q, nullptr, k_scale, v_scale, cos, sin, bt_full, bt_swa, pos,
+                          pos_w, active, sinks, out, out_f32, workspace, ws_bytes, stream, &app,
+                          -1, kv);
+}
+
+size_t gk_kv4_block_bytes(const gk_shape* shape) {
+  return check_shape(shape) == GK_OK ? size_t(kv4_block_bytes(*shape)) : 0;
+}
+
+// Checks that gk_kv4_write and gk_kv4_read share.
+static gk_status check_kv4_tokens(const gk_shape* shape, int32_t layer0, int32_t n_layers,
+                                  int64_t n_tokens) {
+  const gk_status st = check_shape(shape);
+  if (st != GK_OK) return st;
+  if (layer0 < 0 || n_layers < 0 || layer0 > shape->num_layers - n_layers || n_tokens < 0)
+    return GK_ERR_INVALID_ARG;
+  return n_tokens > (int64_t(1) << 28) / shape->num_kv_heads ? GK_ERR_UNSUPPORTED : GK_OK;
+}
+
+gk_status gk_kv4_write(const gk_shape* shape, int32_t layer0, int32_t n_layers, int64_t n_tokens,
+                       const void* k, const void* v, int64_t layer_stride, int64_t token_stride,
+                       const float* cos, const float* sin, const float* k_scale,
+                       const float* v_scale, const int32_t* slot_full, const int32_t* slot_swa,
+                       const uint8_t* active, const gk_kv4_cache* kv, void* stream) {
+  gk_status st = check_kv4_tokens(shape, layer0, n_layers, n_tokens);
+  if (st != GK_OK) return st;
+  if (n_layers == 0 || n_tokens == 0) return GK_OK;
+  if (!k || !v || !k_scale || !v_scale || !slot_full || !slot_swa || !aligned16(k) ||
+      !aligned16(v) || (layer_stride & 7) || (token_stride & 7) || (cos != nullptr) != (sin != nullptr) ||
+      !aligned16(cos) || !aligned16(sin))
+    return GK_ERR_INVALID_ARG;
+  Kv4WriteParams p;
+  memset(&p, 0, sizeof(p));
+  st = resolve_kv4(*shape, kv, p.buf);
+  if (st != GK_OK) return st;
+  p.k = static_cast<const uint16_t*>(k);
+  p.v = static_cast<const uint16_t*>(v);
+  p.layer_stride = layer_stride;
+  p.token_stride = token_stride;
+  p.cosb = cos;
+  p.sinb = sin;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.slot_full = slot_full;
+  p.slot_swa = slot_swa;
+  p.active = active;
+  p.layer0 = layer0;
+  p.n_layers = n_layers;
+  p.n_tokens = int(n_tokens);
+  p.Hkv = shape->num_kv_heads;
+  p.B = shape->block_size;
+  p.nb = shape->num_blocks;
+  return launch_kv4_write(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GK_OK
+                                                                              : GK_ERR_CUDA;
+}
+
+gk_status gk_kv4_read(const gk_shape* shape, int32_t layer0, int32_t n_layers, int64_t n_tokens,
+                      const gk_kv4_cache* kv, const float* k_scale, const float* v_scale,
+                      const int32_t* slot_full, const int32_t* slot_swa, const uint8_t* active,
+                      void* k_out, void* v_out, void* stream) {
+  gk_status st = check_kv4_tokens(shape, layer0, n_layers, n_tokens);
+  if (st != GK_OK) return st;
+  if (n_layers == 0 || n_tokens == 0) return GK_OK;
+  if (!k_out || !v_out || !k_scale || !v_scale || !slot_full || !slot_swa || !aligned16(k_out) ||
+      !aligned16(v_out))
+    return GK_ERR_INVALID_ARG;
+  Kv4ReadParams p;
+  memset(&p, 0, sizeof(p));
+  uint8_t* buf[kMaxGroups];
+  st = resolve_kv4(*shape, kv, buf);
+  if (st != GK_OK) return st;
+  for (int j = 0; j < shape->num_layers / 2; ++j) p.buf[j] = buf[j];
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.slot_full = slot_full;
+  p.slot_swa = slot_swa;
+  p.active = active;
+  p.k_out = static_cast<uint16_t*>(k_out);
+  p.v_out = static_cast<uint16_t*>(v_out);
+  p.layer0 = layer0;
+  p.n_layers = n_layers;
+  p.n_tokens = int(n_tokens);
+  p.Hkv = shape->num_kv_heads;
+  p.B = shape->block_size;
+  p.nb = shape->num_blocks;
+  return launch_kv4_read(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GK_OK : GK_ERR_CUDA;
 }
 
 gk_status gk_kv_budget(uint64_t total_bytes, uint64_t used_bytes, double gmu, double cap_fraction,
@@ -493,7 +653,9 @@ gk_status gk_read_device_error(void* stream, uint32_t* bits, int clear) {
     return GK_ERR_CUDA;
   uint32_t ingest_bits = 0;
   if (read_ingest_error(&ingest_bits, clear != 0) != cudaSuccess) return GK_ERR_CUDA;
-  *bits |= ingest_bits;
+  uint32_t kv4_bits = 0;
+  if (read_kv4_error(&kv4_bits, clear != 0) != cudaSuccess) return GK_ERR_CUDA;
+  *bits |= ingest_bits | kv4_bits;
   return *bits ? GK_ERR_DEVICE_BOUNDS : GK_OK;
 }
 

@@ -145,12 +145,53 @@ struct IngestParams {
   int n_regions;
 };
 
+struct Kv4WriteParams {
+  const uint16_t* k;
+  const uint16_t* v;
+  int64_t layer_stride, token_stride;  // elements
+  const float* cosb;  // null with sinb: K is rotated already
+  const float* sinb;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* slot_full;
+  const int32_t* slot_swa;
+  const uint8_t* active;  // or null
+  uint8_t* buf[kMaxGroups];
+  int layer0, n_layers, n_tokens, Hkv, B, nb;
+};
+
+struct Kv4ReadParams {
+  const uint8_t* buf[kMaxGroups];
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* slot_full;
+  const int32_t* slot_swa;
+  const uint8_t* active;  // or null
+  uint16_t* k_out;
+  uint16_t* v_out;
+  int layer0, n_layers, n_tokens, Hkv, B, nb;
+};
+
 // Launchers (gk_kernels.cu).  They return the launch status.
 cudaError_t launch_append(const AppendParams& p, cudaStream_t st);
 cudaError_t launch_quantize(const float* x, float scale, uint8_t* codes, int64_t n, cudaStream_t st);
 // app: gk_decode_step's append, done in the planner's grid (or null).
 cudaError_t launch_attention(const PlanParams& plan, const AttnParams& p, cudaStream_t st,
                              const AppendParams* app = nullptr);
+// One attention call's launches: planner (plan_func null: the plan-only
+// kernel; plan_arg: its parameter block), attention grid, and, when partial
+// records exist, the combine grid, chained by programmatic dependent launches.
+struct AttnChain {
+  const void* plan_func;
+  const void* plan_arg;
+  unsigned plan_grid;
+  const void* attn_func;
+  unsigned attn_grid, attn_threads;
+  size_t attn_smem;
+};
+cudaError_t launch_chain(const AttnChain& ch, const AttnParams& p, int sms, cudaStream_t st);
+// Kernel attributes of the plan-only kernel on the current device.
+cudaError_t plan_setup();
 // Resident warps of the persistent attention grid on the current device.
 int attention_resident_warps();
 cudaError_t read_device_error(cudaStream_t st, uint32_t* bits, bool clear);
@@ -159,5 +200,13 @@ cudaError_t launch_wait_timeout(uint64_t limit_ns, cudaStream_t st);
 // the stream has been synchronised).
 cudaError_t launch_ingest(const IngestParams& p, cudaStream_t st);
 cudaError_t read_ingest_error(uint32_t* bits, bool clear);
+// gk_kv4.cu: the 4-bit cache, with its own device error word.  In the attention
+// parameters kb[j] is group buffer j and vb is not used.
+cudaError_t launch_kv4_write(const Kv4WriteParams& p, cudaStream_t st);
+cudaError_t launch_kv4_read(const Kv4ReadParams& p, cudaStream_t st);
+// write: gk_kv4_decode_step's new tokens, written in the planner's grid (or null)
+cudaError_t launch_kv4_attention(const PlanParams& plan, const AttnParams& p, cudaStream_t st,
+                                 const Kv4WriteParams* write);
+cudaError_t read_kv4_error(uint32_t* bits, bool clear);
 
 }  // namespace gk

@@ -22,6 +22,7 @@
 #include <stdlib.h>
 #include <string.h>
 
+#include "gk_attn_common.cuh"
 #include "gk_device.cuh"
 #include "gk_internal.h"
 
@@ -31,19 +32,11 @@ __device__ uint32_t g_dev_error;
 
 __device__ __forceinline__ void set_error(uint32_t bits) { atomicOr(&g_dev_error, bits); }
 
-// 1/s when s is a power of two whose reciprocal is a normal float (then
-// x * (1/s) is exactly the correctly rounded x / s for every x); 0 otherwise.
-__device__ __forceinline__ float exact_reciprocal(float s) {
-  const uint32_t u = __float_as_uint(s);
-  const uint32_t e = (u >> 23) & 0xffu;
-  if ((u & 0x7fffffu) != 0 || e < 2 || e > 252) return 0.f;
-  return __uint_as_float((u & 0x80000000u) | ((254u - e) << 23));
-}
+}  // namespace gk
 
-// x / s with IEEE round-to-nearest; r = exact_reciprocal(s) when nonzero.
-__device__ __forceinline__ float div_scale(float x, float s, float r) {
-  return r != 0.f ? x * r : __fdiv_rn(x, s);
-}
+#include "gk_plan.cuh"  // uses set_error
+
+namespace gk {
 
 // =========================================================================
 // KV append
@@ -142,376 +135,8 @@ __global__ void __launch_bounds__(256) quantize_kernel(const float* __restrict__
 }
 
 // =========================================================================
-// Planner (one CTA)
+// Planner launches (the planner itself: gk_plan.cuh)
 // =========================================================================
-constexpr int kPlanThreads = 256;
-constexpr int kPlanWarps = kPlanThreads / 32;
-constexpr int kUnitsPerWarp = 8;   // minimum work units per resident warp
-constexpr int kMinPiece = 512;     // shortest piece cut from a chunk for the last wave
-constexpr int kShortSplit = 1024;  // chunks this short ...
-constexpr int kShortMerge = 8;     // ... are not chosen if a row would need more of them
-constexpr int kSplitCands = 22;    // candidate split lengths kMinSplit << k
-constexpr int kRemBuckets = 256;   // remainder size classes for the largest-first order
-
-__device__ __forceinline__ int warp_sum(int v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-  return v;
-}
-__device__ __forceinline__ long long warp_sum64(long long v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-  return v;
-}
-
-// Work entries are int4 descriptors: {row b, t_begin, t_end, w} with
-// w = s | ns << 16 | kind << 30 (kind 1 = sliding-window layer).  One entry
-// covers the (layer pair, kv head) planes of one row's chunk: unit u is plane
-// u % planes of entry u / planes.  Full-layer entries come first, largest
-// first; then one sliding-window entry per active row; then zero-fill units
-// (one per inactive row and layer).
-
-// The planner's work, done by one CTA.
-__device__ __forceinline__ void plan_body(const PlanParams& p) {
-  extern __shared__ int32_t plan_sm[];
-  int32_t* Ls = plan_sm;          // clamped context length per row (0 = no work)
-  int32_t* Pw = plan_sm + p.Bt;   // window-frame position per row
-  __shared__ long long s_units[kSplitCands], s_need[kSplitCands];
-  __shared__ long long s_full[kSplitCands], s_remtok[kSplitCands];
-  __shared__ int s_ne[kSplitCands], s_maxnf[kSplitCands];
-  __shared__ int s_conv[3];  // chunks cut per eligible row, rows cutting one more, pieces
-  __shared__ int s_erank[kPlanWarps];
-  __shared__ long long s_red[3][kPlanWarps];
-  __shared__ int s_bucket[kRemBuckets];
-  __shared__ int4 s_scan[kPlanWarps];
-  __shared__ int s_nsr[kPlanWarps];
-  __shared__ int s_S_log;
-  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-  const int chunk = (p.Bt + kPlanThreads - 1) / kPlanThreads;
-  const int b_lo = min(p.Bt, tid * chunk), b_hi = min(p.Bt, b_lo + chunk);
-
-  long long tsum = 0;
-  int lmax = 0, nact = 0;
-  for (int b = b_lo; b < b_hi; ++b) {
-    int L = 0;
-    const int act = p.active[b], pos = p.pos[b];   // one round trip for all three
-    Pw[b] = p.pos_w[b];
-    if (act) {
-      if (pos < 0) {
-        set_error(GK_DEVERR_POS);
-      } else {
-        L = pos + 1;
-        if (L > p.max_tokens_full) {
-          set_error(GK_DEVERR_POS);
-          L = p.max_tokens_full;
-        }
-        ++nact;
-      }
-    }
-    Ls[b] = L;
-    tsum += L;
-    lmax = max(lmax, L);
-  }
-  for (int k = tid; k < kRemBuckets; k += kPlanThreads) s_bucket[k] = 0;
-  tsum = warp_sum64(tsum);
-  nact = warp_sum(nact);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) lmax = max(lmax, __shfl_xor_sync(kFull, lmax, o));
-  if (lane == 0) {
-    s_red[0][wid] = tsum;
-    s_red[1][wid] = lmax;
-    s_red[2][wid] = nact;
-  }
-  __syncthreads();
-  long long T = 0, NAct = 0;
-  int Lmax = 0;
-  for (int w = 0; w < kPlanWarps; ++w) {
-    T += s_red[0][w];
-    Lmax = max(Lmax, int(s_red[1][w]));
-    NAct += s_red[2][w];
-  }
-
-  // unit counts and split-record needs of every candidate split length,
-  // one candidate per warp at a time
-  for (int k = wid; k < kSplitCands; k += kPlanWarps) {
-    const int sh = 9 + k;  // log2 of kMinSplit << k
-    const long long S = 1ll << sh;
-    long long units = 0, need = 0, full = 0, remtok = 0;
-    int ne = 0, maxnf = 0;
-    for (int b = lane; b < p.Bt; b += 32) {
-      const int L = Ls[b];
-      if (L > 0) {
-        const long long c = (L + S - 1) >> sh;
-        const int nf = int(L >> sh);
-        units += c;
-        if (L > S) need += c;
-        full += nf;
-        remtok += L & (S - 1);
-        ne += nf >= 2;
-        maxnf = max(maxnf, nf);
-      }
-    }
-    units = warp_sum64(units);
-    need = warp_sum64(need);
-    full = warp_sum64(full);
-    remtok = warp_sum64(remtok);
-    ne = warp_sum(ne);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) maxnf = max(maxnf, __shfl_xor_sync(kFull, maxnf, o));
-    if (lane == 0) {
-      s_units[k] = units;
-      s_need[k] = need;
-      s_full[k] = full;
-      s_remtok[k] = remtok;
-      s_ne[k] = ne;
-      s_maxnf[k] = maxnf;
-    }
-  }
-  __syncthreads();
-  const int planes = (p.NL >> 1) * p.Hkv;
-  const long long warps = max(1, p.n_warps);
-  if (tid == 0) {
-    // Split length S = kMinSplit << k.  Start near a quarter of one warp's
-    // share of the full-layer work, then halve while there are fewer than
-    // kUnitsPerWarp units per resident warp (uniform long rows need many
-    // chunks; mixed rows balance through largest-first order).  Then cap the
-    // chunks per row and fit the partial records into the workspace.
-    const long long share = (T * planes) / (warps * 4);
-    int k = 0;
-    while (k < kSplitCands - 1 && ((long long)kMinSplit << k) < share) ++k;
-    while (k > 0 && (s_units[k] + NAct) * planes < kUnitsPerWarp * warps) --k;
-    // no short chunks that would give a row more than kShortMerge partials:
-    // the per-unit cost of the extra partials outweighs the balance they buy
-    while (k < kSplitCands - 1 && ((long long)kMinSplit << k) <= kShortSplit &&
-           (Lmax - 1) / ((long long)kMinSplit << k) + 1 > kShortMerge)
-      ++k;
-    if (p.force_split_log >= 0) k = p.force_split_log;  // test hook: a fixed split length
-    while (k < kSplitCands - 1 && ((long long)kMinSplit << k) * kMaxSplitsPerRow < Lmax) ++k;
-    while (k < kSplitCands - 1 && s_need[k] > p.cap) ++k;
-    s_S_log = k;
-    // Last wave.  Equal chunks give full * planes units of one size; when
-    // that is at least one wave but not a whole number of waves over the
-    // warps and the smaller
-    // units (remainders, window units) cannot fill the idle part of the last
-    // wave, cut the last chunks of the rows with two or more of them into
-    // p pieces (largest-first order runs them at the end), keeping whole
-    // waves of full chunks.  Rows stay within kMaxSplitsPerRow chunks and
-    // the partial records within the workspace.
-    int conv_c = 0, conv_x = 0, conv_p = 0;
-    const long long Sk = (long long)kMinSplit << k;
-    const long long cunits = s_full[k] * planes;
-    const long long q = cunits / warps, rem = cunits - q * warps;
-    const long long gap = (warps - rem) * Sk;                    // idle token slots
-    const long long small = (s_remtok[k] + NAct * p.W) * planes;  // work in smaller units
-    if (p.force_split_log < 0 && q >= 1 && rem > 0 && small < gap && s_ne[k] > 0) {
-      // cv chunks in all, spread over the eligible rows in row order (fewer
-      // if a row would pass kMaxSplitsPerRow chunks or the records the
-      // workspace holds)
-      const long long cv = s_full[k] - (q * warps) / planes;
-      for (int pp = int(min(8ll, Sk / kMinPiece)); pp >= 2; pp >>= 1) {
-        const long long per_row = (kMaxSplitsPerRow - 1 - s_maxnf[k]) / (pp - 1);
-        const long long room = (p.cap - s_need[k]) / (pp - 1);
-        const long long cvp = min(cv, min(per_row * s_ne[k], room));
-        if (cvp >= 1) {
-          conv_c = int(cvp / s_ne[k]);
-          conv_x = int(cvp - conv_c * s_ne[k]);
-          conv_p = pp;
-          break;
-        }
-      }
-    }
-    s_conv[0] = conv_c;
-    s_conv[1] = conv_x;
-    s_conv[2] = conv_p;
-  }
-  __syncthreads();
-  const int conv_c = s_conv[0], conv_x = s_conv[1], conv_p = s_conv[2];
-  // rank of this thread's first row among the rows with two or more full
-  // chunks (the first conv_x of them cut one chunk more)
-  int erank = 0;
-  if (conv_p > 0) {
-    int e = 0;
-    for (int b = b_lo; b < b_hi; ++b) e += (Ls[b] >> (9 + s_S_log)) >= 2;
-    int inc = e;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(kFull, inc, o);
-      if (lane >= o) inc += y;
-    }
-    if (lane == 31) s_erank[wid] = inc;
-    __syncthreads();
-    erank = inc - e;
-    for (int w = 0; w < wid; ++w) erank += s_erank[w];
-  }
-  const int S_log = s_S_log;
-  const int S_sh = 9 + S_log;  // S = 2^S_sh
-  const long long S = 1ll << S_sh;
-  static_assert(kMinSplit == 512, "split lengths are 2^(9 + k)");
-  const int bshift = max(0, S_log + 9 - 8);  // remainder -> one of 256 classes
-
-  // per-thread counts -> one packed exclusive scan: (full chunks, split
-  // records, active rows, remainders)
-  // a row's chunks: nf - cut full chunks, then cut * conv_p pieces, then the
-  // remainder; split indices follow the keys
-  const int piece_len = conv_p > 0 ? int(S) / conv_p : 0;
-  const int piece_bucket = conv_p > 0 ? kRemBuckets - 1 - (piece_len >> bshift) : 0;
-  auto cut_of = [&](int nf, int& rank) {
-    if (conv_p == 0 || nf < 2) return 0;
-    const int c = conv_c + (rank < conv_x ? 1 : 0);
-    ++rank;
-    return min(c, nf);
-  };
-  int4 cnt = make_int4(0, 0, 0, 0);
-  int nsr = 0;  // rows with split-KV partials
-  int rk = erank;
-  for (int b = b_lo; b < b_hi; ++b) {
-    const int L = Ls[b];
-    if (L > 0) {
-      const int nf = int(L >> S_sh), r = int(L & (S - 1)), cut = cut_of(nf, rk);
-      const int ns = nf + cut * (conv_p - 1) + (r > 0);
-      cnt.x += nf - cut;
-      cnt.y += ns > 1 ? ns : 0;
-      nsr += ns > 1;
-      cnt.z += 1;
-      if (r > 0) {
-        cnt.w += 1;
-        atomicAdd(&s_bucket[kRemBuckets - 1 - (r >> bshift)], 1);  // largest first
-      }
-      if (cut > 0) {
-        cnt.w += cut * conv_p;
-        atomicAdd(&s_bucket[piece_bucket], cut * conv_p);
-      }
-    }
-  }
-  int4 inc = cnt;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(kFull, inc.x, o), y = __shfl_up_sync(kFull, inc.y, o);
-    const int z = __shfl_up_sync(kFull, inc.z, o), w = __shfl_up_sync(kFull, inc.w, o);
-    if (lane >= o) {
-      inc.x += x;
-      inc.y += y;
-      inc.z += z;
-      inc.w += w;
-    }
-  }
-  int nsr_inc = nsr;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(kFull, nsr_inc, o);
-    if (lane >= o) nsr_inc += y;
-  }
-  if (lane == 31) {
-    s_scan[wid] = inc;
-    s_nsr[wid] = nsr_inc;
-  }
-  __syncthreads();
-  int srp = nsr_inc - nsr, n_split_rows = 0;  // this thread's first slot in the split-row list
-  for (int w = 0; w < kPlanWarps; ++w) {
-    if (w < wid) srp += s_nsr[w];
-    n_split_rows += s_nsr[w];
-  }
-  int4 base = make_int4(0, 0, 0, 0), tot = make_int4(0, 0, 0, 0);
-  for (int w = 0; w < kPlanWarps; ++w) {
-    const int4 v = s_scan[w];
-    if (w < wid) {
-      base.x += v.x;
-      base.y += v.y;
-      base.z += v.z;
-      base.w += v.w;
-    }
-    tot.x += v.x;
-    tot.y += v.y;
-    tot.z += v.z;
-    tot.w += v.w;
-  }
-  if (wid == 0) {  // bucket counts -> exclusive offsets: 8 buckets per lane, one warp scan
-    constexpr int per = kRemBuckets / 32;
-    int v[per], sum = 0;
-#pragma unroll
-    for (int k = 0; k < per; ++k) {
-      v[k] = s_bucket[lane * per + k];
-      sum += v[k];
-    }
-    int incl = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(kFull, incl, o);
-      if (lane >= o) incl += y;
-    }
-    int acc = incl - sum;
-#pragma unroll
-    for (int k = 0; k < per; ++k) {
-      s_bucket[lane * per + k] = acc;
-      acc += v[k];
-    }
-  }
-  __syncthreads();
-  int fp = base.x + inc.x - cnt.x;
-  int sp = base.y + inc.y - cnt.y;
-  int ap = base.z + inc.z - cnt.z;
-  const int A = tot.x, TS = tot.y, NA = tot.z, R = tot.w;
-  const int NEF = A + R;  // full-layer entries
-  int ip = b_lo - ap;     // inactive rows before this thread's rows
-  (void)R;
-
-  rk = erank;
-  for (int b = b_lo; b < b_hi; ++b) {
-    const int L = Ls[b];
-    if (L > 0) {
-      const int nf = int(L >> S_sh), r = int(L & (S - 1)), cut = cut_of(nf, rk);
-      const int ns = nf + cut * (conv_p - 1) + (r > 0);
-      const int nk = nf - cut;  // full chunks kept
-      for (int s = 0; s < nk; ++s)
-        p.edesc[fp++] = make_int4(b, int(s * S), int((s + 1) * S), s | (ns << 16));
-      if (cut > 0) {
-        const int np = cut * conv_p;
-        const int slot = atomicAdd(&s_bucket[piece_bucket], np);
-        for (int i = 0; i < np; ++i) {
-          const int t0 = int(nk * S) + i * piece_len;
-          p.edesc[A + slot + i] = make_int4(b, t0, t0 + piece_len, (nk + i) | (ns << 16));
-        }
-      }
-      if (r > 0) {
-        const int slot = atomicAdd(&s_bucket[kRemBuckets - 1 - (r >> bshift)], 1);
-        p.edesc[A + slot] = make_int4(b, int(nf * S), L, (ns - 1) | (ns << 16));
-      }
-      if (ns > 1) {
-        p.part_base[b] = sp;
-        sp += ns;
-        p.split_rows[srp++] = b | (ns << 16);
-      } else {
-        p.part_base[b] = 0;
-      }
-      // sliding-window layer of this row: keys [max(0, pos_w - W + 1), pos_w]
-      int pw = Pw[b];
-      if (pw < 0 || pw >= p.max_tokens_swa) {
-        set_error(GK_DEVERR_POS);
-        pw = min(max(pw, 0), p.max_tokens_swa - 1);
-      }
-      p.edesc[NEF + ap++] = make_int4(b, max(0, pw - p.W + 1), pw + 1, (1 << 16) | (1 << 30));
-    } else {
-      p.part_base[b] = 0;
-      p.zero_list[ip++] = b;
-    }
-  }
-  if (tid == 0) {
-    if (TS > p.cap) set_error(GK_DEVERR_PLAN);
-    p.hdr[kHdrQueue] = p.n_warps;
-    p.hdr[kHdrNUnits] = (NEF + NA) * planes;
-    p.hdr[kHdrNZero] = (p.Bt - NA) * p.NL;
-    p.hdr[kHdrSplit] = int(S);
-    p.hdr[kHdrNEntries] = NEF + NA;
-    p.hdr[kHdrTotalSplits] = TS;
-    p.hdr[kHdrPieces] = conv_p > 0 ? (conv_c * s_ne[s_S_log] + conv_x) * conv_p : 0;
-    p.hdr[kHdrSplitRows] = n_split_rows;
-  }
-  // This grid may have started while the kernel before it (the KV append)
-  // was still running; it completes only after that kernel has, so the
-  // attention grid that waits on this one also sees the appended KV.
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ PlanParams p) {
   // let the attention grid launch now; it waits for this grid before reading the plan
   asm volatile("griddepcontrol.launch_dependents;");
@@ -544,23 +169,6 @@ __global__ void __launch_bounds__(kPlanThreads)
 constexpr int kWarps = 4;    // independent worker warps per CTA
 constexpr int kStages = 3;   // ring depth per warp (stages of 32 tokens)
 constexpr int kFifo = 6;     // unit descriptors in flight per warp (> kStages + 1)
-constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s per barrier wait
-constexpr uint32_t kOnesF16x2 = 0x3C003C00u;        // (1.0, 1.0) in f16
-constexpr float kLazyLog2 = 8.f;  // probabilities stay <= 2^8 between rescales
-
-struct UnitDesc {
-  int32_t kind;  // 1 = full layer, 2 = sliding-window layer
-  int32_t layer, b, kvh, s, ns;
-  int32_t t_begin, t_end;  // key range [t_begin, t_end) in the table's frame
-  int32_t st_begin, n_st;  // 32-token stages covering the range
-};
-
-// q of the unit's 8 heads (bf16) followed by its row's cos and sin (fp32),
-// fetched with the unit's first stage.
-constexpr uint32_t kQBytes = kGroup * kHeadDim * 2;
-constexpr uint32_t kRopeBytes = (kHeadDim / 2) * 4;
-constexpr uint32_t kUnitHeadBytes = kQBytes + 2 * kRopeBytes;
-
 // The FMA comparison path keeps q' in fp32 (rows padded so the eight heads
 // fall in different banks) and one stage of P for the exchange between its
 // token-per-lane and channel-per-lane phases.
@@ -591,29 +199,6 @@ static_assert(kStageBytes % 16 == 0 && kUnitHeadBytes % 16 == 0 && kStageKBytes 
 
 template <bool kMma>
 constexpr size_t attn_smem() { return sizeof(WarpSmemT<kMma>) * kWarps; }
-
-__device__ __forceinline__ void zero_row(const AttnParams& p, int layer, int b, int lane) {
-  const int64_t base = (int64_t(layer) * p.Bt + b) * p.Hq * kHeadDim;
-  uint4* o = reinterpret_cast<uint4*>(p.out + base);
-  const int n16 = p.Hq * kHeadDim * 2 / 16;
-  for (int c = lane; c < n16; c += 32) o[c] = make_uint4(0, 0, 0, 0);
-  if (p.out_f32) {
-    float4* of = reinterpret_cast<float4*>(p.out_f32 + base);
-    for (int c = lane; c < 2 * n16; c += 32) of[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-  }
-}
-
-// Output scale of a head: v_scale / (l + 2^(sg - m)) with the head's
-// attention-sink logit sg (log2 units; none when `sink` is null), l the sum of
-// 2^(s - m) over its keys and m their reference maximum (log2 units).  When
-// sg > m numerator and denominator are scaled by 2^-(sg - m), so nothing
-// overflows.
-__device__ __forceinline__ float out_scale(float l, float m, const float* sink, float vscale) {
-  if (sink == nullptr) return vscale * __frcp_rn(l);
-  const float d = __ldg(sink) * 1.4426950408889634f - m;
-  const float e = ex2(-fabsf(d));
-  return d > 0.f ? vscale * e * __frcp_rn(fmaf(l, e, 1.f)) : vscale * __frcp_rn(l + e);
-}
 
 // Unit u covers plane u % planes of work entry e = u / planes.
 __device__ __forceinline__ void decode_unit(const AttnParams& p, int u, int4 e, UnitDesc& d) {
@@ -1460,6 +1045,11 @@ static const void* const kAttnKernels[4] = {
     (const void*)attn_kernel<true, true>, (const void*)attn_kernel<true, false>,
     (const void*)attn_kernel<false, true>, (const void*)attn_kernel<false, false>};
 
+cudaError_t plan_setup() {
+  return cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              int(2 * kMaxBatch * sizeof(int32_t)));
+}
+
 static cudaError_t device_setup(DeviceCache** out) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1487,8 +1077,7 @@ static cudaError_t device_setup(DeviceCache** out) {
       if (e != cudaSuccess) return e;
       if (blocks < c.attn_blocks_per_sm) c.attn_blocks_per_sm = blocks;
     }
-    e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             int(2 * kMaxBatch * sizeof(int32_t)));
+    e = plan_setup();
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(plan_append_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              int(2 * kMaxBatch * sizeof(int32_t)));
@@ -1536,6 +1125,28 @@ cudaError_t launch_attention(const PlanParams& plan, const AttnParams& p, cudaSt
   if (e != cudaSuccess) return e;
   PlanParams pp = plan;
   pp.n_warps = c->sms * c->attn_blocks_per_sm * kWarps;
+  PlanAppendParams pa;
+  AttnChain ch = {};
+  if (app) {
+    // gk_decode_step appends in CTAs beside the planner's: one warp
+    // per (layer, row) pair
+    pa.plan = pp;
+    pa.app = *app;
+    ch.plan_func = (const void*)plan_append_kernel;
+    ch.plan_arg = &pa;
+    ch.plan_grid = unsigned(1 + (int64_t(app->NL) * app->Bt * 32 + kPlanThreads - 1) /
+                                    kPlanThreads);
+  } else {
+    ch.plan_arg = &pp;
+  }
+  ch.attn_func = kAttnKernels[(c->fma ? 2 : 0) + (p.k_packed ? 0 : 1)];
+  ch.attn_threads = kWarps * 32;
+  ch.attn_grid = unsigned(c->sms * c->attn_blocks_per_sm);
+  ch.attn_smem = c->fma ? attn_smem<false>() : attn_smem<true>();
+  return launch_chain(ch, p, c->sms, st);
+}
+
+cudaError_t launch_chain(const AttnChain& ch, const AttnParams& p, int sms, cudaStream_t st) {
   // Programmatic dependent launches: the planner may overlap the kernel before
   // it (it reads no KV and waits for that kernel before exiting); the
   // attention CTAs start while the planner runs and wait for it
@@ -1544,42 +1155,32 @@ cudaError_t launch_attention(const PlanParams& plan, const AttnParams& p, cudaSt
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t pcfg = {};
-  pcfg.gridDim = dim3(1);
+  pcfg.gridDim = dim3(ch.plan_func ? ch.plan_grid : 1);
   pcfg.blockDim = dim3(kPlanThreads);
   pcfg.dynamicSmemBytes = size_t(2) * p.Bt * sizeof(int32_t);
   pcfg.stream = st;
   pcfg.attrs = attr;
   pcfg.numAttrs = 1;
-  if (app) {
-    // gk_decode_step appends in CTAs beside the planner's: one warp
-    // per (layer, row) pair
-    PlanAppendParams pa;
-    pa.plan = pp;
-    pa.app = *app;
-    pcfg.gridDim = dim3(unsigned(1 + (int64_t(app->NL) * app->Bt * 32 + kPlanThreads - 1) /
-                                         kPlanThreads));
-    e = cudaLaunchKernelEx(&pcfg, plan_append_kernel, pa);
-  } else {
-    e = cudaLaunchKernelEx(&pcfg, plan_kernel, pp);
-  }
+  void* pargs[] = {const_cast<void*>(ch.plan_arg)};
+  cudaError_t e = cudaLaunchKernelExC(
+      &pcfg, ch.plan_func ? ch.plan_func : (const void*)plan_kernel, pargs);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(c->sms * c->attn_blocks_per_sm));
-  cfg.blockDim = dim3(kWarps * 32);
-  cfg.dynamicSmemBytes = c->fma ? attn_smem<false>() : attn_smem<true>();
+  cfg.gridDim = dim3(ch.attn_grid);
+  cfg.blockDim = dim3(ch.attn_threads);
+  cfg.dynamicSmemBytes = ch.attn_smem;
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const int k = (c->fma ? 2 : 0) + (p.k_packed ? 0 : 1);
   void* args[] = {const_cast<AttnParams*>(&p)};
-  e = cudaLaunchKernelExC(&cfg, kAttnKernels[k], args);
+  e = cudaLaunchKernelExC(&cfg, ch.attn_func, args);
   if (e != cudaSuccess || p.cap == 0) return e;  // no partial records: nothing to combine
   // the deep form when even batch x planes items (every row split) fit in
   // one wave of its warps
   const bool deep = int64_t(p.Bt) * int64_t(p.fd_planes.d) <=
-                    int64_t(c->sms) * kCombineDeepBlocks * (kCombineThreads / 32);
+                    int64_t(sms) * kCombineDeepBlocks * (kCombineThreads / 32);
   cudaLaunchConfig_t ccfg = {};
-  ccfg.gridDim = dim3(unsigned(c->sms * (deep ? kCombineDeepBlocks : kCombineBlocks)));
+  ccfg.gridDim = dim3(unsigned(sms * (deep ? kCombineDeepBlocks : kCombineBlocks)));
   ccfg.blockDim = dim3(kCombineThreads);
   ccfg.stream = st;
   ccfg.attrs = attr;

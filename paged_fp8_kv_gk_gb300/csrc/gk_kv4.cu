@@ -1,0 +1,834 @@
+// gk_kv4.cu -- sm_103a kernels of the 4-bit KV cache (include/gk_kv4.h).
+//
+//   kv4_write_kernel       RoPE(k) in IEEE fp32, / layer scale, E4M3 scale of
+//                          each 16 channels, E2M1 codes, scatter into tiles.
+//   kv4_read_kernel        the inverse: bf16 values of given tokens.
+//   kv4_plan_write_kernel  gk_kv4_decode_step's planner launch: CTA 0 plans,
+//                          the others write the rows' new tokens.
+//   kv4_attn_kernel        persistent decode attention over 4-bit tiles: the
+//                          same units, split-KV partials and combine as the
+//                          FP8 kernel's, another stage loop.
+#include <cuda_runtime.h>
+
+#include "gk_attn_common.cuh"
+#include "gk_device.cuh"
+#include "gk_internal.h"
+#include "../../include/gk_kv4.h"
+
+namespace gk {
+
+__device__ uint32_t g_kv4_error;
+
+__device__ __forceinline__ void set_error(uint32_t bits) { atomicOr(&g_kv4_error, bits); }
+
+}  // namespace gk
+
+#include "gk_plan.cuh"  // uses set_error
+
+namespace gk {
+
+constexpr int kTile = 16;                         // tokens of a tile
+constexpr int kTileBytes = GK_KV4_TILE_BYTES;     // 16 tokens of one kv head
+constexpr int kTokBytes = kHeadDim / 2;           // codes of one token
+constexpr int kTileV = kTile * kTokBytes;         // V codes
+constexpr int kTileKs = 2 * kTileV;               // K block scales
+constexpr int kTileVs = kTileKs + kTile * (kHeadDim / 16);  // V block scales
+static_assert(kTileVs + kTile * (kHeadDim / 16) == kTileBytes, "tile layout");
+
+// ---------------------------------------------------------------- conversions
+// The four E2M1 pairs of a word -> f16x2 each (low nibble in the low half).
+__device__ __forceinline__ void e2m1x8_to_f16x2x4(uint32_t w, uint32_t (&r)[4]) {
+  asm("{\n"
+      " .reg .b8 a, b, c, d;\n"
+      " mov.b32 {a, b, c, d}, %4;\n"
+      " cvt.rn.f16x2.e2m1x2 %0, a;\n"
+      " cvt.rn.f16x2.e2m1x2 %1, b;\n"
+      " cvt.rn.f16x2.e2m1x2 %2, c;\n"
+      " cvt.rn.f16x2.e2m1x2 %3, d;\n"
+      "}\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(w));
+}
+
+// Two E4M3 codes in the low 16 bits of w -> f16x2.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
+  uint32_t r;
+  asm("{\n"
+      " .reg .b16 l, h;\n"
+      " mov.b32 {l, h}, %1;\n"
+      " cvt.rn.f16x2.e4m3x2 %0, l;\n"
+      "}\n"
+      : "=r"(r)
+      : "r"(w));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Two fp32 -> two E2M1 codes (lo -> low nibble): to nearest, ties to even,
+// saturating to +-6.
+__device__ __forceinline__ uint32_t f32x2_to_e2m1x2(float lo, float hi) {
+  uint32_t r;
+  asm("{\n"
+      " .reg .b8 d;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 d, %1, %2;\n"
+      " cvt.u32.u8 %0, d;\n"
+      "}\n"
+      : "=r"(r)
+      : "f"(hi), "f"(lo));
+  return r;
+}
+
+// max that gives NaN when either is NaN
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// =========================================================================
+// Write and read
+// =========================================================================
+// Where a token of one kv head lies.
+struct TokenPlace {
+  int64_t tile;  // byte offset of its tile in the group buffer
+  int t;         // token in the tile
+};
+__device__ __forceinline__ TokenPlace place_of(int slot, int h, int Hkv, int B) {
+  const int pb = slot / B, off = slot - pb * B;
+  return {((int64_t(pb) * Hkv + h) * (B / kTile) + off / kTile) * kTileBytes, off % kTile};
+}
+
+// Quantise 16 values (already divided by the layer scale): E4M3 code of the
+// block scale and 16 E2M1 codes.
+//
+// The codes are those of the exact quotient u / sf.  sf has 4 significant bits
+// and a code border t has 3, so u is a border only if it is t * sf exactly; the
+// quotient is refined by one exact remainder (Markstein's correction), which
+// gives such a quotient exactly and any other within a 2^-45 part of u / sf
+// before its last rounding, hence on its own side of the border (the nearest
+// u to t * sf differs by more than half a step of t).
+__device__ __forceinline__ uint32_t quantise16(float (&u)[16], uint2& codes) {
+  float a = fabsf(u[0]);
+#pragma unroll
+  for (int e = 1; e < 16; ++e) a = max_nan(a, fabsf(u[e]));
+  const uint32_t sfc = f32x2_to_e4m3x2(__fdiv_rn(a, 6.f), 0.f) & 0xffu;
+  const float sf = f16x2_to_f32x2(e4m3x2_to_f16x2(sfc)).x;
+  if (a > 1e30f) {
+    // infinities: any value this large has the saturated code, and stays
+    // finite through the remainder below
+#pragma unroll
+    for (int e = 0; e < 16; ++e) u[e] = fminf(fmaxf(u[e], -1e30f), 1e30f);
+  }
+  const float r = sf > 0.f ? __frcp_rn(sf) : 0.f;
+  uint32_t w[2] = {0u, 0u};
+#pragma unroll
+  for (int e = 0; e < 16; e += 2) {
+    float y[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float y0 = u[e + k] * r;
+      y[k] = fmaf(fmaf(-y0, sf, u[e + k]), r, y0);
+    }
+    w[e / 8] |= f32x2_to_e2m1x2(y[0], y[1]) << (4 * (e % 8));
+  }
+  codes = make_uint2(w[0], w[1]);
+  return sfc;
+}
+
+// 16 channels (16 blk ..) of K (kv = 0) or V (kv = 1) of one token and head:
+// load, rotate, divide, quantise, store.
+__device__ __forceinline__ void write_block(const Kv4WriteParams& p, int layer, int n, int h,
+                                            int blk, int kv) {
+  if (p.active && !p.active[n]) return;
+  const int slot = (layer & 1) ? p.slot_full[n] : p.slot_swa[n];
+  if (slot == GK_KV4_SKIP) return;
+  if (slot < 0 || slot >= p.nb * p.B) {
+    set_error(GK_DEVERR_SLOT);
+    return;
+  }
+  const int64_t row = int64_t(layer - p.layer0) * p.layer_stride + int64_t(n) * p.token_stride +
+                      int64_t(h) * kHeadDim;
+  const uint16_t* src = (kv ? p.v : p.k) + row;
+  float x[16];
+  auto load16 = [](const uint16_t* s, float (&d)[16]) {
+    const uint4 a = ldg_nc_v4(s), b = ldg_nc_v4(s + 8);
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      d[2 * k] = bf16lo_to_f32(w[k]);
+      d[2 * k + 1] = bf16hi_to_f32(w[k]);
+    }
+  };
+  load16(src + 16 * blk, x);
+  if (kv == 0 && p.cosb) {
+    // rotate-half: every operation rounded on its own, as in the FP8 append
+    float y[16];
+    load16(src + 16 * (blk ^ 2), y);
+    const float4* cr = reinterpret_cast<const float4*>(p.cosb + int64_t(n) * (kHeadDim / 2)) +
+                       4 * (blk & 1);
+    const float4* sr = reinterpret_cast<const float4*>(p.sinb + int64_t(n) * (kHeadDim / 2)) +
+                       4 * (blk & 1);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float4 c4 = __ldg(cr + k), s4 = __ldg(sr + k);
+      const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float a = __fmul_rn(x[4 * k + e], c[e]), b = __fmul_rn(y[4 * k + e], s[e]);
+        x[4 * k + e] = blk < 2 ? __fsub_rn(a, b) : __fadd_rn(a, b);
+      }
+    }
+  }
+  const float scale = kv ? p.v_scale[layer] : p.k_scale[layer];
+  const float inv = exact_reciprocal(scale);
+#pragma unroll
+  for (int e = 0; e < 16; ++e) x[e] = div_scale(x[e], scale, inv);
+  uint2 codes;
+  const uint32_t sf = quantise16(x, codes);
+  const TokenPlace at = place_of(slot, h, p.Hkv, p.B);
+  uint8_t* tile = p.buf[layer >> 1] + at.tile;
+  const int t = at.t;
+  *reinterpret_cast<uint2*>(tile + (kv ? kTileV : 0) + t * kTokBytes + blk * 8) = codes;
+  tile[kv ? kTileVs + 16 * blk + 4 * ((t & 7) >> 1) + 2 * (t >> 3) + (t & 1)
+          : kTileKs + 8 * (t & 7) + 2 * blk + (t >> 3)] = uint8_t(sf);
+}
+
+constexpr int kWriteThreads = 256;
+
+// Four threads a (token, head), one for every 16 channels; grid y: layer and
+// K or V.
+__global__ void __launch_bounds__(kWriteThreads)
+    kv4_write_kernel(const __grid_constant__ Kv4WriteParams p) {
+  // the decode-attention planner may launch now (see kv_append_kernel)
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int64_t it = int64_t(blockIdx.x) * kWriteThreads + threadIdx.x;
+  if (it >= int64_t(p.n_tokens) * p.Hkv * 4) return;
+  const int nh = int(it >> 2), n = nh / p.Hkv;
+  write_block(p, p.layer0 + int(blockIdx.y >> 1), n, nh - n * p.Hkv, int(it & 3),
+              int(blockIdx.y & 1));
+}
+
+// Eight threads a (token, head): 8 channels of K and of V each.
+__global__ void __launch_bounds__(kWriteThreads)
+    kv4_read_kernel(const __grid_constant__ Kv4ReadParams p) {
+  const int64_t it = int64_t(blockIdx.x) * kWriteThreads + threadIdx.x;
+  if (it >= int64_t(p.n_tokens) * p.Hkv * 8) return;
+  const int layer = p.layer0 + int(blockIdx.y);
+  const int c = int(it & 7);
+  const int64_t nh = it >> 3;
+  const int n = int(nh / p.Hkv), h = int(nh - int64_t(n) * p.Hkv);
+  if (p.active && !p.active[n]) return;
+  const int slot = (layer & 1) ? p.slot_full[n] : p.slot_swa[n];
+  if (slot == GK_KV4_SKIP) return;
+  if (slot < 0 || slot >= p.nb * p.B) {
+    set_error(GK_DEVERR_SLOT);
+    return;
+  }
+  const TokenPlace at = place_of(slot, h, p.Hkv, p.B);
+  const uint8_t* tile = p.buf[layer >> 1] + at.tile;
+  const int t = at.t, blk = c >> 1;
+  const uint32_t kc = *reinterpret_cast<const uint32_t*>(tile + t * kTokBytes + 4 * c);
+  const uint32_t vc = *reinterpret_cast<const uint32_t*>(tile + kTileV + t * kTokBytes + 4 * c);
+  const uint32_t ks = tile[kTileKs + 8 * (t & 7) + 2 * blk + (t >> 3)];
+  const uint32_t vs = tile[kTileVs + 16 * blk + 4 * ((t & 7) >> 1) + 2 * (t >> 3) + (t & 1)];
+  auto store8 = [](uint16_t* dst, uint32_t codes, uint32_t sfc, float scale) {
+    const uint32_t sf = e4m3x2_to_f16x2(sfc | (sfc << 8));
+    uint32_t f[4], o[4];
+    e2m1x8_to_f16x2x4(codes, f);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      // code * sf has at most 6 significant bits: exact in f16
+      const float2 x = f16x2_to_f32x2(mul_f16x2(f[k], sf));
+      o[k] = f32x2_to_bf16x2(x.x * scale, x.y * scale);
+    }
+    *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+  };
+  const int64_t dst = ((int64_t(layer - p.layer0) * p.n_tokens + n) * p.Hkv + h) * kHeadDim + 8 * c;
+  store8(p.k_out + dst, kc, ks, p.k_scale[layer]);
+  store8(p.v_out + dst, vc, vs, p.v_scale[layer]);
+}
+
+// gk_kv4_decode_step: CTA 0 plans; the CTAs after it write the new tokens.
+// The attention grid waits for this whole grid, so it reads the plan and the
+// written cache; the kernel before this grid must be complete before the
+// cache is written.
+struct Kv4PlanWriteParams {
+  PlanParams plan;
+  Kv4WriteParams write;
+};
+
+__global__ void __launch_bounds__(kPlanThreads)
+    kv4_plan_write_kernel(const __grid_constant__ Kv4PlanWriteParams p) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  if (blockIdx.x == 0) {
+    plan_body(p.plan);
+    return;
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t per = int64_t(p.write.n_tokens) * p.write.Hkv * 4;  // of one layer's K
+  const int64_t total = per * 2 * p.write.n_layers;
+  const int64_t it = (int64_t(blockIdx.x) - 1) * kPlanThreads + threadIdx.x;
+  if (it >= total) return;
+  const int64_t y = it / per, r = it - y * per, nh = r >> 2, n = nh / p.write.Hkv;
+  write_block(p.write, p.write.layer0 + int(y >> 1), int(n), int(nh - n * p.write.Hkv),
+              int(r & 3), int(y & 1));
+}
+
+// =========================================================================
+// Decode attention
+// =========================================================================
+constexpr int kWarps4 = 4;      // independent worker warps per CTA
+constexpr int kStTiles = 2;     // tiles per pipeline stage
+constexpr int kStages4 = 5;     // ring depth per warp
+constexpr int kBlocks4 = 4;     // CTAs per SM
+constexpr int kFifo4 = 8;       // unit descriptors in flight per warp (> kStages4 + 1)
+constexpr int kSt4Tok = kStTiles * kTile;
+constexpr uint32_t kSt4Bytes = kStTiles * kTileBytes;
+
+struct alignas(128) Kv4Warp {
+  uint8_t ring[kStages4][kSt4Bytes];
+  uint8_t qbuf[kUnitHeadBytes];
+  unsigned long long bar[kStages4];
+  int4 e_next;            // work descriptor of the claimed unit (copied asynchronously)
+  UnitDesc fifo[kFifo4];  // st_begin: first tile; n_st: stages
+};
+static_assert(sizeof(Kv4Warp) % 128 == 0 && kSt4Bytes % 16 == 0 && kTileBytes % 16 == 0,
+              "bulk-copy destinations must be 16-byte aligned");
+constexpr size_t kAttn4Smem = sizeof(Kv4Warp) * kWarps4;
+static_assert((kAttn4Smem + 1024) * kBlocks4 <= 228 * 1024, "shared memory of the CTAs of one SM");
+
+__global__ void __launch_bounds__(kWarps4 * 32, kBlocks4)
+    kv4_attn_kernel(const __grid_constant__ AttnParams p) {
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, qd = lane & 3;
+  Kv4Warp& ws = reinterpret_cast<Kv4Warp*>(smem_raw)[warp];
+  const uint32_t ring0 = smem_u32(&ws.ring[0][0]);
+  const uint32_t qbuf0 = smem_u32(&ws.qbuf[0]);
+  const uint32_t bar0 = smem_u32(&ws.bar[0]);
+  if (lane == 0) {
+#pragma unroll
+    for (int s = 0; s < kStages4; ++s) mbar_init(bar0 + 8 * s, 1);
+    mbar_init_fence();
+  }
+  __syncwarp();
+
+  // the planner grid (launched just before) must be complete from here on; the
+  // combine grid may launch now (see attn_kernel in gk_kernels.cu)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (p.cap > 0) asm volatile("griddepcontrol.launch_dependents;");
+  const int nU = p.hdr[kHdrNUnits];
+  const int nAll = nU + p.hdr[kHdrNZero];  // units with a descriptor, then zero-fill units
+
+  // ------------------------------------------------ scheduler pipeline
+  // One claimed unit ahead of the one being streamed; its descriptor travels
+  // by cp.async, its first table chunk is loaded while the current one streams.
+  int u_after = 0, u_next = int(blockIdx.x) * kWarps4 + warp;
+  auto claim_desc = [&](int u) {
+    if (lane == 0 && u < nU) cp_async16(smem_u32(&ws.e_next), p.edesc + fdiv(u, p.fd_planes));
+  };
+  auto read_desc = [&]() -> int4 {
+    if (lane == 0) cp_async_wait_all();
+    __syncwarp();
+    const int4 e = ws.e_next;
+    __syncwarp();
+    return e;
+  };
+  claim_desc(u_next);
+  bool tn_ready = false;
+  int32_t tbl_next = 0;
+  int tbl_next_base = 0;
+  // lane l: entry l of the table chunk starting at block `base`
+  auto load_tbl = [&](bool swa, int b, int base) -> int32_t {
+    const int32_t* row = swa ? p.bt_swa + int64_t(b) * p.MBS : p.bt_full + int64_t(b) * p.MBF;
+    const int idx = base + lane;
+    return idx < (swa ? p.MBS : p.MBF) ? __ldg(row + idx) : 0;
+  };
+  auto desc_tbl = [&](int4 e, int& base) -> int32_t {
+    base = fdiv(e.y & ~(kTile - 1), p.fd_b);
+    return load_tbl(((e.w >> 30) & 1) != 0, e.x, base);
+  };
+
+  // ------------------------------------------------ producer state
+  int prod = 0, cons = 0, p_slot = 0;
+  int f_head = 0, f_tail = 0;
+  bool exhausted = false, failed = false;
+  bool q_free = true;           // the q buffer may take the next unit's q
+  int pt = 0, pe = 0;           // the producer unit's next and end tile
+  const uint8_t* pu_src = nullptr;
+  int tbl_base = 0;
+  int32_t tbl = 0;
+
+  // Next unit (warp-uniform); zero-fill units (inactive rows) are done here.
+  auto next_unit = [&](UnitDesc& d) -> bool {
+    for (;;) {
+      const int u = u_next;
+      if (u >= nAll) return false;
+      const int4 e = u < nU ? read_desc() : make_int4(0, 0, 0, 0);
+      if (u < nU) {
+        if (tn_ready) {
+          tbl = tbl_next;
+          tbl_base = tbl_next_base;
+        } else {
+          tbl = desc_tbl(e, tbl_base);
+        }
+      }
+      if (lane == 0) u_after = atomicAdd(p.queue, 1);
+      u_next = __shfl_sync(kFull, u_after, 0);
+      claim_desc(u_next);
+      tn_ready = false;
+      if (u >= nU) {
+        const int v = u - nU;
+        const int zr = fdiv(v, p.fd_nl);
+        zero_row(p, v - zr * p.NL, p.zero_list[zr], lane);
+        continue;
+      }
+      const int pl = u - fdiv(u, p.fd_planes) * int(p.fd_planes.d);
+      const int j = fdiv(pl, p.fd_hkv);
+      const bool swa = ((e.w >> 30) & 1) != 0;
+      d.kind = swa ? 2 : 1;
+      d.layer = swa ? 2 * j : 2 * j + 1;
+      d.b = e.x;
+      d.kvh = pl - j * p.Hkv;
+      d.s = e.w & 0xffff;
+      d.ns = (e.w >> 16) & 0x3fff;
+      d.t_begin = e.y;
+      d.t_end = e.z;
+      d.st_begin = e.y / kTile;
+      d.n_st = ((e.z + kTile - 1) / kTile - d.st_begin + kStTiles - 1) / kStTiles;
+      return true;
+    }
+  };
+
+  auto issue_next = [&]() -> bool {
+    if (exhausted) return false;
+    const uint32_t bar = bar0 + 8 * p_slot;
+    uint32_t head_bytes = 0;
+    if (pt == pe) {
+      if (!q_free) return false;  // the consumer has not read the buffered q yet
+      UnitDesc d;
+      if (!next_unit(d)) {
+        exhausted = true;
+        return false;
+      }
+      if (lane == 0) ws.fifo[f_tail % kFifo4] = d;
+      __syncwarp();
+      ++f_tail;
+      pt = d.st_begin;
+      pe = (d.t_end + kTile - 1) / kTile;
+      pu_src = p.kb[d.layer >> 1] + int64_t(d.kvh) * (p.B / kTile) * kTileBytes;
+      q_free = false;
+      head_bytes = kUnitHeadBytes;
+      if (lane == 0) {
+        // q of the unit's 8 heads and its row's cos and sin, with the first stage
+        const uint16_t* qsrc =
+            p.q + ((int64_t(d.layer) * p.Bt + d.b) * p.Hq + int64_t(d.kvh) * kGroup) * kHeadDim;
+        bulk_g2s(qbuf0, qsrc, kQBytes, bar);
+        bulk_g2s(qbuf0 + kQBytes, p.cosb + int64_t(d.b) * (kHeadDim / 2), kRopeBytes, bar);
+        bulk_g2s(qbuf0 + kQBytes + kRopeBytes, p.sinb + int64_t(d.b) * (kHeadDim / 2), kRopeBytes,
+                 bar);
+      }
+    } else if (!tn_ready && u_next < nU) {
+      tbl_next = desc_tbl(read_desc(), tbl_next_base);
+      tn_ready = true;
+    }
+    const int nt = min(kStTiles, pe - pt);
+    if (fdiv((pt + nt - 1) * kTile, p.fd_b) >= tbl_base + 32) {
+      const UnitDesc& du = ws.fifo[(f_tail + kFifo4 - 1) % kFifo4];
+      tbl_base = fdiv(pt * kTile, p.fd_b);
+      tbl = load_tbl(du.kind == 2, du.b, tbl_base);
+    }
+    // lane l copies tile l of the stage
+    const int tile = pt + min(lane, nt - 1);
+    const int blk = fdiv(tile * kTile, p.fd_b);
+    int32_t pb = __shfl_sync(kFull, tbl, blk - tbl_base);
+    if (uint32_t(pb) >= uint32_t(p.nb)) {
+      if (lane < nt) set_error(GK_DEVERR_BLOCK);
+      pb = 0;
+    }
+    if (lane == 0) mbar_arrive_expect_tx(bar, uint32_t(nt) * kTileBytes + head_bytes);
+    __syncwarp();
+    if (lane < nt) {
+      const int tpb = p.B / kTile;
+      const uint8_t* src =
+          pu_src + (int64_t(pb) * p.Hkv * tpb + (tile - blk * tpb)) * int64_t(kTileBytes);
+      bulk_g2s(ring0 + p_slot * kSt4Bytes + lane * kTileBytes, src, kTileBytes, bar);
+    }
+    pt += nt;
+    p_slot = p_slot == kStages4 - 1 ? 0 : p_slot + 1;
+    ++prod;
+    return true;
+  };
+
+  // ------------------------------------------------ consumer state
+  struct {
+    int t_begin, t_end, n_st;
+  } cd = {0, 0, 0};
+#define CU (ws.fifo[f_head % kFifo4])
+  int k_in_unit = 0, tok0 = 0;
+  int c_slot = 0;
+  uint32_t c_par = 0u;
+  uint32_t qhi[8], qlo[8];  // q' = qhi + qlo (f16 each): ~22-bit significand
+  // as in attn_kernel: scores are x * 2^e_h, si_h = 2^-e_h; mr_h the running
+  // reference maximum, which may lag the true one by kLazyLog2
+  float si0 = 0.f, si1 = 0.f, mr0 = 0.f, mr1 = 0.f, nb0 = 0.f, nb1 = 0.f, thr0 = 0.f, thr1 = 0.f,
+        vscale = 0.f;
+  float o[4][4];
+  float lacc[4];  // softmax denominators from a ones-row MMA over the f16 P
+  // K rows (g, g + 8) of a tile are its tokens (ktok, ktok + 8); the P that the
+  // transpose gives lane qd are then of tokens ktok(2 qd), ktok(2 qd + 1) and
+  // those + 8.  ktok(r) = r for r < 4, r ^ 1 above: every quarter of K rows and
+  // every V row of the four qd falls in distinct banks.
+  const uint32_t koff = uint32_t(g ^ (g >> 2)) * kTokBytes + 8 * qd;
+  const uint32_t ksoff = kTileKs + 8 * uint32_t(g ^ (g >> 2)) + 2 * qd;
+  const int vt = (2 * qd) ^ (qd >> 1);  // its partner: vt ^ 1
+  const uint32_t voff = kTileV + uint32_t(vt) * kTokBytes + 4 * g;
+  const int vstep = (vt & 1) ? -kTokBytes : kTokBytes;
+  const uint32_t vsoff = kTileVs + 16 * uint32_t(g >> 1) + 4 * qd;
+  const uint32_t vsel = (vt & 1) ? 0x2301u : 0x3210u;  // scales in the order vt, vt ^ 1
+
+  while (prod - cons < kStages4 && issue_next()) {
+  }
+
+  while (cons < prod) {
+    if (!mbar_wait_bounded(bar0 + 8 * c_slot, c_par, kWaitLimitNs)) failed = true;
+    if (__any_sync(kFull, failed)) {
+      failed = true;
+      break;
+    }
+    if (k_in_unit == 0) {
+      cd.t_begin = CU.t_begin;
+      cd.t_end = CU.t_end;
+      cd.n_st = CU.n_st;
+      tok0 = CU.st_begin * kTile;
+      // ---- unit prologue: rotated q for head (kvh*8 + g), channels 16qd..16qd+15
+      const uint32_t qrow = qbuf0 + g * (kHeadDim * 2);
+      const uint4 x0 = lds128(qrow + 32 * qd);
+      const uint4 x1 = lds128(qrow + 32 * qd + 16);
+      const uint4 y0 = lds128(qrow + 32 * (qd ^ 2));
+      const uint4 y1 = lds128(qrow + 32 * (qd ^ 2) + 16);
+      const uint32_t cp = qbuf0 + kQBytes + 64 * (qd & 1);
+      const uint32_t sp = cp + kRopeBytes;
+      const uint32_t xw[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+      const uint32_t yw[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
+      uint32_t cw[16], sw[16];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint4 c4 = lds128(cp + 16 * k);
+        const uint4 s4 = lds128(sp + 16 * k);
+        cw[4 * k] = c4.x; cw[4 * k + 1] = c4.y; cw[4 * k + 2] = c4.z; cw[4 * k + 3] = c4.w;
+        sw[4 * k] = s4.x; sw[4 * k + 1] = s4.y; sw[4 * k + 2] = s4.z; sw[4 * k + 3] = s4.w;
+      }
+      __syncwarp();
+      q_free = true;
+      const float sgn = qd < 2 ? -1.f : 1.f;
+      // logits in log2 units: k_scale / sqrt(D) * log2(e) is folded into q,
+      // together with the power-of-two normalisation below
+      const float ck = p.k_scale[CU.layer] * (0.125f * 1.4426950408889634f);
+      float r[16];
+      float amax = 0.f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        const float c0 = __uint_as_float(cw[2 * w]), c1 = __uint_as_float(cw[2 * w + 1]);
+        const float s0 = __uint_as_float(sw[2 * w]), s1 = __uint_as_float(sw[2 * w + 1]);
+        r[2 * w] = bf16lo_to_f32(xw[w]) * c0 + sgn * bf16lo_to_f32(yw[w]) * s0;
+        r[2 * w + 1] = bf16hi_to_f32(xw[w]) * c1 + sgn * bf16hi_to_f32(yw[w]) * s1;
+        amax = fmaxf(amax, fmaxf(fabsf(r[2 * w]), fabsf(r[2 * w + 1])));
+      }
+      amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2)) * ck;
+      int ex = int((__float_as_uint(amax) >> 23) & 0xffu) - 127;
+      ex = amax > 0.f ? min(max(ex, -100), 100) : 13;
+      const float f = __uint_as_float(uint32_t(127 + 13 - ex) << 23);
+      const float finv = __uint_as_float(uint32_t(127 - 13 + ex) << 23);
+      const float fck = f * ck;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        const float a = r[2 * w] * fck, b = r[2 * w + 1] * fck;
+        qhi[w] = f32x2_to_f16x2(a, b);
+        const float2 h = f16x2_to_f32x2(qhi[w]);
+        qlo[w] = f32x2_to_f16x2(a - h.x, b - h.y);  // residual is exact in fp32
+      }
+      si0 = __shfl_sync(kFull, finv, 8 * qd);  // heads 2qd and 2qd+1
+      si1 = __shfl_sync(kFull, finv, 8 * qd + 4);
+      vscale = p.v_scale[CU.layer];
+      mr0 = mr1 = thr0 = thr1 = -INFINITY;
+      nb0 = nb1 = 0.f;
+      lacc[0] = lacc[1] = lacc[2] = lacc[3] = 0.f;
+#pragma unroll
+      for (int m = 0; m < 4; ++m) o[m][0] = o[m][1] = o[m][2] = o[m][3] = 0.f;
+    }
+
+    const uint32_t st = ring0 + c_slot * kSt4Bytes;
+    const bool edge = tok0 < cd.t_begin || tok0 + kSt4Tok > cd.t_end;
+    // ---- S = q' K^T, one MMA row a token.  code * sf is exact in f16.
+    float sc[kStTiles][4];
+#pragma unroll
+    for (int i = 0; i < kStTiles; ++i) {
+      const uint32_t tile = st + i * kTileBytes;
+      const uint2 ka = lds64(tile + koff), kb = lds64(tile + koff + 8 * kTokBytes);
+      const uint32_t sf = e4m3x2_to_f16x2(lds_u16(tile + ksoff));
+      const uint32_t sa = prmt(sf, sf, 0x1010u), sb = prmt(sf, sf, 0x3232u);
+      sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.f;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t a[4], b[4];
+        e2m1x8_to_f16x2x4(h ? ka.y : ka.x, a);
+        e2m1x8_to_f16x2x4(h ? kb.y : kb.x, b);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int j = 2 * h + k;
+          const uint32_t a0 = mul_f16x2(a[2 * k], sa), a2 = mul_f16x2(a[2 * k + 1], sa);
+          const uint32_t a1 = mul_f16x2(b[2 * k], sb), a3 = mul_f16x2(b[2 * k + 1], sb);
+          mma_f16(sc[i], a0, a1, a2, a3, qlo[2 * j], qlo[2 * j + 1]);
+          mma_f16(sc[i], a0, a1, a2, a3, qhi[2 * j], qhi[2 * j + 1]);
+        }
+      }
+    }
+    // ---- online softmax (log2 domain); lane holds heads 2qd (c0,c2), 2qd+1 (c1,c3)
+    if (edge) {
+#pragma unroll
+      for (int i = 0; i < kStTiles; ++i) {
+        const int t0 = tok0 + kTile * i + (g ^ (g >> 2)), t1 = t0 + 8;
+        if (t0 < cd.t_begin || t0 >= cd.t_end) sc[i][0] = sc[i][1] = -INFINITY;
+        if (t1 < cd.t_begin || t1 >= cd.t_end) sc[i][2] = sc[i][3] = -INFINITY;
+      }
+    }
+    float lm0 = fmaxf(sc[0][0], sc[0][2]), lm1 = fmaxf(sc[0][1], sc[0][3]);
+#pragma unroll
+    for (int i = 1; i < kStTiles; ++i) {
+      lm0 = fmaxf(lm0, fmaxf(sc[i][0], sc[i][2]));
+      lm1 = fmaxf(lm1, fmaxf(sc[i][1], sc[i][3]));
+    }
+    if (__any_sync(kFull, lm0 > thr0 || lm1 > thr1)) {
+      float w0 = lm0, w1 = lm1;
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) {
+        w0 = fmaxf(w0, __shfl_xor_sync(kFull, w0, off));
+        w1 = fmaxf(w1, __shfl_xor_sync(kFull, w1, off));
+      }
+      const float n0 = fmaxf(mr0, w0), n1 = fmaxf(mr1, w1);
+      const float al0 = ex2((mr0 - n0) * si0), al1 = ex2((mr1 - n1) * si1);
+      mr0 = n0;
+      mr1 = n1;
+      nb0 = -n0 * si0;
+      nb1 = -n1 * si1;
+      thr0 = n0 + kLazyLog2 / si0;
+      thr1 = n1 + kLazyLog2 / si1;
+      lacc[0] *= al0;
+      lacc[2] *= al0;
+      lacc[1] *= al1;
+      lacc[3] *= al1;
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        o[m][0] *= al0;
+        o[m][2] *= al0;
+        o[m][1] *= al1;
+        o[m][3] *= al1;
+      }
+    }
+    // ---- O += P V; rows (g, g+8) = channels (8g+2m, 8g+2m+1)
+#pragma unroll
+    for (int i = 0; i < kStTiles; ++i) {
+      const uint32_t tile = st + i * kTileBytes;
+      const float p0 = ex2(fmaf(sc[i][0], si0, nb0)), p1 = ex2(fmaf(sc[i][1], si1, nb1));
+      const float p2 = ex2(fmaf(sc[i][2], si0, nb0)), p3 = ex2(fmaf(sc[i][3], si1, nb1));
+      const uint32_t b0 = movmatrix_trans(f32x2_to_f16x2(p0, p1));
+      const uint32_t b1 = movmatrix_trans(f32x2_to_f16x2(p2, p3));
+      // every row of the ones matrix sums the same rounded P the values see
+      mma_f16(lacc, kOnesF16x2, kOnesF16x2, kOnesF16x2, kOnesF16x2, b0, b1);
+      // channels 8g .. 8g+7 (one nibble each) of the lane's four tokens
+      const uint32_t w0 = lds32(tile + voff), w1 = lds32(tile + voff + vstep);
+      const uint32_t w2 = lds32(tile + voff + 8 * kTokBytes);
+      const uint32_t w3 = lds32(tile + voff + 8 * kTokBytes + vstep);
+      uint32_t sf = prmt(lds32(tile + vsoff), 0u, vsel);
+      uint32_t s01 = e4m3x2_to_f16x2(sf), s23 = e4m3x2_to_f16x2(sf >> 16);
+      if (edge) {
+        // scales of keys outside the range may be anything, NaN included
+        const int t0 = tok0 + kTile * i + vt, t1 = tok0 + kTile * i + (vt ^ 1);
+        auto in = [&](int t) { return t >= cd.t_begin && t < cd.t_end; };
+        s01 &= (in(t0) ? 0xffffu : 0u) | (in(t1) ? 0xffff0000u : 0u);
+        s23 &= (in(t0 + 8) ? 0xffffu : 0u) | (in(t1 + 8) ? 0xffff0000u : 0u);
+      }
+      // even and odd channels of a token pair, two nibbles a byte
+      constexpr uint32_t kLow = 0x0f0f0f0fu;
+      uint32_t e01[4], d01[4], e23[4], d23[4];
+      e2m1x8_to_f16x2x4((w0 & kLow) | ((w1 << 4) & ~kLow), e01);
+      e2m1x8_to_f16x2x4(((w0 >> 4) & kLow) | (w1 & ~kLow), d01);
+      e2m1x8_to_f16x2x4((w2 & kLow) | ((w3 << 4) & ~kLow), e23);
+      e2m1x8_to_f16x2x4(((w2 >> 4) & kLow) | (w3 & ~kLow), d23);
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+        mma_f16(o[m], mul_f16x2(e01[m], s01), mul_f16x2(d01[m], s01), mul_f16x2(e23[m], s23),
+                mul_f16x2(d23[m], s23), b0, b1);
+    }
+    __syncwarp();
+    ++cons;
+    if (++c_slot == kStages4) {
+      c_slot = 0;
+      c_par ^= 1u;
+    }
+    ++k_in_unit;
+    tok0 += kSt4Tok;
+    while (prod - cons < kStages4 && issue_next()) {
+    }
+
+    if (k_in_unit == cd.n_st) {
+      // ---- unit epilogue
+      k_in_unit = 0;
+      const float l0 = lacc[0], l1 = lacc[1];
+      if (CU.ns == 1) {
+        const int64_t out_row =
+            ((int64_t(CU.layer) * p.Bt + CU.b) * p.Hq + CU.kvh * kGroup + 2 * qd) * kHeadDim +
+            8 * g;
+        const float* snk =
+            p.sinks ? p.sinks + int64_t(CU.layer) * p.Hq + CU.kvh * kGroup + 2 * qd : nullptr;
+        const float i0 = out_scale(l0, mr0 * si0, snk, vscale);
+        const float i1 = out_scale(l1, mr1 * si1, snk ? snk + 1 : nullptr, vscale);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          o[m][0] *= i0;
+          o[m][2] *= i0;
+          o[m][1] *= i1;
+          o[m][3] *= i1;
+        }
+        uint4 u0, u1;
+        u0.x = f32x2_to_bf16x2(o[0][0], o[0][2]);
+        u0.y = f32x2_to_bf16x2(o[1][0], o[1][2]);
+        u0.z = f32x2_to_bf16x2(o[2][0], o[2][2]);
+        u0.w = f32x2_to_bf16x2(o[3][0], o[3][2]);
+        u1.x = f32x2_to_bf16x2(o[0][1], o[0][3]);
+        u1.y = f32x2_to_bf16x2(o[1][1], o[1][3]);
+        u1.z = f32x2_to_bf16x2(o[2][1], o[2][3]);
+        u1.w = f32x2_to_bf16x2(o[3][1], o[3][3]);
+        *reinterpret_cast<uint4*>(p.out + out_row) = u0;
+        *reinterpret_cast<uint4*>(p.out + out_row + kHeadDim) = u1;
+        if (p.out_f32) {
+          float4* f0 = reinterpret_cast<float4*>(p.out_f32 + out_row);
+          float4* f1 = reinterpret_cast<float4*>(p.out_f32 + out_row + kHeadDim);
+          f0[0] = make_float4(o[0][0], o[0][2], o[1][0], o[1][2]);
+          f0[1] = make_float4(o[2][0], o[2][2], o[3][0], o[3][2]);
+          f1[0] = make_float4(o[0][1], o[0][3], o[1][1], o[1][3]);
+          f1[1] = make_float4(o[2][1], o[2][3], o[3][1], o[3][3]);
+        }
+      } else {
+        // split partial: (m, l, o) unnormalised, in log2 units, for the combine kernel
+        const int64_t plane = int64_t(CU.layer >> 1) * p.Hkv + CU.kvh;
+        float* rec = p.partials + (plane * p.cap + p.part_base[CU.b] + CU.s) * kPartialFloats;
+        if (g == 0) {
+          rec[2 * qd] = mr0 * si0;  // log2 units
+          rec[2 * qd + 1] = mr1 * si1;
+          rec[kGroup + 2 * qd] = l0;
+          rec[kGroup + 2 * qd + 1] = l1;
+        }
+        float4* ro0 = reinterpret_cast<float4*>(rec + 2 * kGroup + (2 * qd) * kHeadDim + 8 * g);
+        float4* ro1 = reinterpret_cast<float4*>(rec + 2 * kGroup + (2 * qd + 1) * kHeadDim + 8 * g);
+        ro0[0] = make_float4(o[0][0], o[0][2], o[1][0], o[1][2]);
+        ro0[1] = make_float4(o[2][0], o[2][2], o[3][0], o[3][2]);
+        ro1[0] = make_float4(o[0][1], o[0][3], o[1][1], o[1][3]);
+        ro1[1] = make_float4(o[2][1], o[2][3], o[3][1], o[3][3]);
+      }
+      ++f_head;
+    }
+  }
+#undef CU
+  if (failed) {
+    // A barrier wait hit its limit: record it, then wait (bounded) for this
+    // warp's copies still in flight before the CTA may exit.
+    if (lane == 0) set_error(GK_DEVERR_TIMEOUT);
+    for (int c = cons; c < prod; ++c)
+      mbar_wait_bounded(bar0 + 8 * (c % kStages4), uint32_t(c / kStages4) & 1u, kWaitLimitNs);
+  }
+}
+
+// =========================================================================
+// Launchers
+// =========================================================================
+struct Kv4Device {
+  int sms = 0, blocks = 0;
+  bool set = false;
+};
+static Kv4Device g_kv4_dev[64];
+
+static cudaError_t kv4_setup(Kv4Device** out) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  Kv4Device& c = g_kv4_dev[dev];
+  if (!c.set) {
+    e = cudaDeviceGetAttribute(&c.sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(kv4_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             int(kAttn4Smem));
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(kv4_plan_write_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             int(2 * kMaxBatch * sizeof(int32_t)));
+    if (e != cudaSuccess) return e;
+    e = plan_setup();
+    if (e != cudaSuccess) return e;
+    int blocks = 0;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, kv4_attn_kernel, kWarps4 * 32,
+                                                      kAttn4Smem);
+    if (e != cudaSuccess) return e;
+    c.blocks = blocks < 1 ? 1 : blocks;
+    c.set = true;
+  }
+  *out = &c;
+  return cudaSuccess;
+}
+
+cudaError_t launch_kv4_attention(const PlanParams& plan, const AttnParams& p, cudaStream_t st,
+                                 const Kv4WriteParams* write) {
+  Kv4Device* c = nullptr;
+  const cudaError_t e = kv4_setup(&c);
+  if (e != cudaSuccess) return e;
+  Kv4PlanWriteParams pw;
+  pw.plan = plan;
+  pw.plan.n_warps = c->sms * c->blocks * kWarps4;
+  AttnChain ch = {};
+  if (write) {
+    pw.write = *write;
+    const int64_t items = int64_t(write->n_tokens) * write->Hkv * 4 * 2 * write->n_layers;
+    ch.plan_func = (const void*)kv4_plan_write_kernel;
+    ch.plan_arg = &pw;
+    ch.plan_grid = unsigned(1 + (items + kPlanThreads - 1) / kPlanThreads);
+  } else {
+    ch.plan_arg = &pw.plan;
+  }
+  ch.attn_func = (const void*)kv4_attn_kernel;
+  ch.attn_threads = kWarps4 * 32;
+  ch.attn_grid = unsigned(c->sms * c->blocks);
+  ch.attn_smem = kAttn4Smem;
+  return launch_chain(ch, p, c->sms, st);
+}
+
+cudaError_t launch_kv4_write(const Kv4WriteParams& p, cudaStream_t st) {
+  const int64_t items = int64_t(p.n_tokens) * p.Hkv * 4;
+  kv4_write_kernel<<<dim3(unsigned((items + kWriteThreads - 1) / kWriteThreads),
+                          unsigned(2 * p.n_layers)),
+                     kWriteThreads, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_kv4_read(const Kv4ReadParams& p, cudaStream_t st) {
+  const int64_t items = int64_t(p.n_tokens) * p.Hkv * 8;
+  kv4_read_kernel<<<dim3(unsigned((items + kWriteThreads - 1) / kWriteThreads),
+                         unsigned(p.n_layers)),
+                    kWriteThreads, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t read_kv4_error(uint32_t* bits, bool clear) {
+  cudaError_t e = cudaMemcpyFromSymbol(bits, g_kv4_error, sizeof(uint32_t));
+  if (e != cudaSuccess || !clear) return e;
+  const uint32_t zero = 0;
+  return cudaMemcpyToSymbol(g_kv4_error, &zero, sizeof(uint32_t));
+}
+
+}  // namespace gk
