@@ -63,6 +63,28 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
   return r;
 }
 
+// A half of an f16x2 twice.
+__device__ __forceinline__ uint32_t dup_lo(uint32_t a) {
+  uint32_t r;
+  asm("{ .reg .b16 l, h; mov.b32 {l, h}, %1; mov.b32 %0, {l, l}; }" : "=r"(r) : "r"(a));
+  return r;
+}
+__device__ __forceinline__ uint32_t dup_hi(uint32_t a) {
+  uint32_t r;
+  asm("{ .reg .b16 l, h; mov.b32 {l, h}, %1; mov.b32 %0, {h, h}; }" : "=r"(r) : "r"(a));
+  return r;
+}
+
+// D(16x8, f32) = A(16x16, f16, row) * B(16x8, f16, col)
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                              uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};\n"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -282,184 +304,158 @@ __global__ void __launch_bounds__(kPlanThreads)
 // =========================================================================
 // Decode attention
 // =========================================================================
-constexpr int kWarps4 = 4;      // independent worker warps per CTA
-constexpr int kStTiles = 2;     // tiles per pipeline stage
-constexpr int kStages4 = 5;     // ring depth per warp
-constexpr int kBlocks4 = 4;     // CTAs per SM
-constexpr int kFifo4 = 8;       // unit descriptors in flight per warp (> kStages4 + 1)
+// One CTA per SM of kCons independent warps; each takes units (layer, row, kv
+// head, split) from the work counter and streams their tiles through a ring of
+// its own, kStTiles tiles a stage.
+constexpr int kStTiles = 4;     // tiles per pipeline stage
+constexpr int kStages4 = 3;     // ring depth per warp
+constexpr int kCons = 15;       // warps
+constexpr int kFifo4 = 6;       // unit descriptors in flight per warp (> kStages4 + 1)
 constexpr int kSt4Tok = kStTiles * kTile;
 constexpr uint32_t kSt4Bytes = kStTiles * kTileBytes;
+constexpr int kAttn4Threads = kCons * 32;
+constexpr int kTileLanes = 32 / kStTiles;              // lanes that copy one tile
+constexpr int kTileCopies = kTileBytes / 16 / kTileLanes;  // 16-byte copies of a lane
+static_assert(kTileCopies * kTileLanes * 16 == kTileBytes, "a tile is copied by whole lanes");
 
-struct alignas(128) Kv4Warp {
+struct alignas(128) Kv4Ring {
   uint8_t ring[kStages4][kSt4Bytes];
   uint8_t qbuf[kUnitHeadBytes];
-  unsigned long long bar[kStages4];
-  int4 e_next;            // work descriptor of the claimed unit (copied asynchronously)
   UnitDesc fifo[kFifo4];  // st_begin: first tile; n_st: stages
 };
-static_assert(sizeof(Kv4Warp) % 128 == 0 && kSt4Bytes % 16 == 0 && kTileBytes % 16 == 0,
-              "bulk-copy destinations must be 16-byte aligned");
-constexpr size_t kAttn4Smem = sizeof(Kv4Warp) * kWarps4;
-static_assert((kAttn4Smem + 1024) * kBlocks4 <= 228 * 1024, "shared memory of the CTAs of one SM");
+static_assert(sizeof(Kv4Ring) % 128 == 0 && kSt4Bytes % 16 == 0, "16-byte copies");
+constexpr size_t kAttn4Smem = sizeof(Kv4Ring) * kCons;
+static_assert(kAttn4Smem <= 227 * 1024, "shared memory of an SM");
 
-__global__ void __launch_bounds__(kWarps4 * 32, kBlocks4)
+__global__ void __launch_bounds__(kAttn4Threads, 1)
     kv4_attn_kernel(const __grid_constant__ AttnParams p) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, qd = lane & 3;
-  Kv4Warp& ws = reinterpret_cast<Kv4Warp*>(smem_raw)[warp];
+  Kv4Ring& ws = reinterpret_cast<Kv4Ring*>(smem_raw)[warp];
   const uint32_t ring0 = smem_u32(&ws.ring[0][0]);
   const uint32_t qbuf0 = smem_u32(&ws.qbuf[0]);
-  const uint32_t bar0 = smem_u32(&ws.bar[0]);
-  if (lane == 0) {
-#pragma unroll
-    for (int s = 0; s < kStages4; ++s) mbar_init(bar0 + 8 * s, 1);
-    mbar_init_fence();
-  }
-  __syncwarp();
 
   // the planner grid (launched just before) must be complete from here on; the
   // combine grid may launch now (see attn_kernel in gk_kernels.cu)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (p.cap > 0) asm volatile("griddepcontrol.launch_dependents;");
   const int nU = p.hdr[kHdrNUnits];
-  const int nAll = nU + p.hdr[kHdrNZero];  // units with a descriptor, then zero-fill units
+  // zero-fill units (inactive rows)
+  for (int v = int(blockIdx.x) * kCons + warp, n = p.hdr[kHdrNZero]; v < n;
+       v += int(gridDim.x) * kCons) {
+    const int zr = fdiv(v, p.fd_nl);
+    zero_row(p, v - zr * p.NL, p.zero_list[zr], lane);
+  }
 
-  // ------------------------------------------------ scheduler pipeline
-  // One claimed unit ahead of the one being streamed; its descriptor travels
-  // by cp.async, its first table chunk is loaded while the current one streams.
-  int u_after = 0, u_next = int(blockIdx.x) * kWarps4 + warp;
-  auto claim_desc = [&](int u) {
-    if (lane == 0 && u < nU) cp_async16(smem_u32(&ws.e_next), p.edesc + fdiv(u, p.fd_planes));
-  };
-  auto read_desc = [&]() -> int4 {
-    if (lane == 0) cp_async_wait_all();
-    __syncwarp();
-    const int4 e = ws.e_next;
-    __syncwarp();
-    return e;
-  };
-  claim_desc(u_next);
-  bool tn_ready = false;
-  int32_t tbl_next = 0;
-  int tbl_next_base = 0;
+  // ------------------------------------------------ producer state
+  // The next unit is fetched in steps, one with each stage issued, so that no
+  // step waits for the one before it: the claim when a unit starts, its
+  // descriptor with the second stage, its first table chunk with the third.
+  int u_nx = int(blockIdx.x) * kCons + warp, nx_step = 1;
+  int4 e_nx = make_int4(0, 0, 0, 0);
+  int32_t tbl_nx = 0;
+  auto swa_of = [](int4 e) { return ((e.w >> 30) & 1) != 0; };
   // lane l: entry l of the table chunk starting at block `base`
   auto load_tbl = [&](bool swa, int b, int base) -> int32_t {
     const int32_t* row = swa ? p.bt_swa + int64_t(b) * p.MBS : p.bt_full + int64_t(b) * p.MBF;
     const int idx = base + lane;
     return idx < (swa ? p.MBS : p.MBF) ? __ldg(row + idx) : 0;
   };
-  auto desc_tbl = [&](int4 e, int& base) -> int32_t {
-    base = fdiv(e.y & ~(kTile - 1), p.fd_b);
-    return load_tbl(((e.w >> 30) & 1) != 0, e.x, base);
-  };
-
-  // ------------------------------------------------ producer state
-  int prod = 0, cons = 0, p_slot = 0;
-  int f_head = 0, f_tail = 0;
-  bool exhausted = false, failed = false;
-  bool q_free = true;           // the q buffer may take the next unit's q
-  int pt = 0, pe = 0;           // the producer unit's next and end tile
-  const uint8_t* pu_src = nullptr;
-  int tbl_base = 0;
-  int32_t tbl = 0;
-
-  // Next unit (warp-uniform); zero-fill units (inactive rows) are done here.
-  auto next_unit = [&](UnitDesc& d) -> bool {
-    for (;;) {
-      const int u = u_next;
-      if (u >= nAll) return false;
-      const int4 e = u < nU ? read_desc() : make_int4(0, 0, 0, 0);
-      if (u < nU) {
-        if (tn_ready) {
-          tbl = tbl_next;
-          tbl_base = tbl_next_base;
-        } else {
-          tbl = desc_tbl(e, tbl_base);
-        }
-      }
-      if (lane == 0) u_after = atomicAdd(p.queue, 1);
-      u_next = __shfl_sync(kFull, u_after, 0);
-      claim_desc(u_next);
-      tn_ready = false;
-      if (u >= nU) {
-        const int v = u - nU;
-        const int zr = fdiv(v, p.fd_nl);
-        zero_row(p, v - zr * p.NL, p.zero_list[zr], lane);
-        continue;
-      }
-      const int pl = u - fdiv(u, p.fd_planes) * int(p.fd_planes.d);
-      const int j = fdiv(pl, p.fd_hkv);
-      const bool swa = ((e.w >> 30) & 1) != 0;
-      d.kind = swa ? 2 : 1;
-      d.layer = swa ? 2 * j : 2 * j + 1;
-      d.b = e.x;
-      d.kvh = pl - j * p.Hkv;
-      d.s = e.w & 0xffff;
-      d.ns = (e.w >> 16) & 0x3fff;
-      d.t_begin = e.y;
-      d.t_end = e.z;
-      d.st_begin = e.y / kTile;
-      d.n_st = ((e.z + kTile - 1) / kTile - d.st_begin + kStTiles - 1) / kStTiles;
-      return true;
+  auto first_blk = [&](int4 e) { return fdiv(e.y & ~(kTile - 1), p.fd_b); };
+  auto fetch_next = [&]() {
+    if (nx_step == 1) {
+      u_nx = __shfl_sync(kFull, u_nx, 0);  // the claim's answer is lane 0's
+      if (u_nx < nU) e_nx = __ldcg(p.edesc + fdiv(u_nx, p.fd_planes));
+      nx_step = 2;
+    } else if (nx_step == 2) {
+      if (u_nx < nU) tbl_nx = load_tbl(swa_of(e_nx), e_nx.x, first_blk(e_nx));
+      nx_step = 3;
     }
   };
+  int prod = 0, cons = 0, p_slot = 0;
+  int f_head = 0, f_tail = 0;
+  bool exhausted = false;
+  bool q_free = true;   // the q buffer may take the next unit's q
+  int pt = 0, pe = 0;   // the producer unit's next and end tile
+  const uint8_t* src = nullptr;  // its kv head's tiles of block 0, at this lane's bytes
+  int tbl_base = 0;
+  int32_t tbl = 0;
+  const int tpb = p.B / kTile;
+  const uint32_t blk_bytes = uint32_t(p.Hkv * tpb * kTileBytes);
+  const int my_tile = lane / kTileLanes;  // this lane's tile of a stage
+  const uint32_t my_off = uint32_t(lane % kTileLanes) * 16;
 
+  // Copy one stage; lanes 8i .. 8i+7 copy tile i.  A group is committed for
+  // every stage.
   auto issue_next = [&]() -> bool {
     if (exhausted) return false;
-    const uint32_t bar = bar0 + 8 * p_slot;
-    uint32_t head_bytes = 0;
     if (pt == pe) {
       if (!q_free) return false;  // the consumer has not read the buffered q yet
-      UnitDesc d;
-      if (!next_unit(d)) {
+      while (nx_step < 3) fetch_next();
+      const int u = u_nx;
+      if (u >= nU) {
         exhausted = true;
         return false;
       }
-      if (lane == 0) ws.fifo[f_tail % kFifo4] = d;
-      __syncwarp();
-      ++f_tail;
-      pt = d.st_begin;
-      pe = (d.t_end + kTile - 1) / kTile;
-      pu_src = p.kb[d.layer >> 1] + int64_t(d.kvh) * (p.B / kTile) * kTileBytes;
-      q_free = false;
-      head_bytes = kUnitHeadBytes;
+      const int4 e = e_nx;
+      tbl = tbl_nx;
+      tbl_base = first_blk(e);
+      if (lane == 0) u_nx = atomicAdd(p.queue, 1);
+      nx_step = 1;
+      const int pl = u - fdiv(u, p.fd_planes) * int(p.fd_planes.d);
+      const int j = fdiv(pl, p.fd_hkv);
+      const int kvh = pl - j * p.Hkv, layer = swa_of(e) ? 2 * j : 2 * j + 1;
+      pt = e.y / kTile;
+      pe = (e.z + kTile - 1) / kTile;
+      src = p.kb[j] + int64_t(kvh) * tpb * kTileBytes + my_off;
       if (lane == 0) {
-        // q of the unit's 8 heads and its row's cos and sin, with the first stage
-        const uint16_t* qsrc =
-            p.q + ((int64_t(d.layer) * p.Bt + d.b) * p.Hq + int64_t(d.kvh) * kGroup) * kHeadDim;
-        bulk_g2s(qbuf0, qsrc, kQBytes, bar);
-        bulk_g2s(qbuf0 + kQBytes, p.cosb + int64_t(d.b) * (kHeadDim / 2), kRopeBytes, bar);
-        bulk_g2s(qbuf0 + kQBytes + kRopeBytes, p.sinb + int64_t(d.b) * (kHeadDim / 2), kRopeBytes,
-                 bar);
+        UnitDesc& d = ws.fifo[f_tail];
+        d.layer = layer;
+        d.b = e.x;
+        d.kvh = kvh;
+        d.s = e.w & 0xffff;
+        d.ns = (e.w >> 16) & 0x3fff;
+        d.t_begin = e.y;
+        d.t_end = e.z;
+        d.st_begin = pt;
+        d.n_st = (pe - pt + kStTiles - 1) / kStTiles;
       }
-    } else if (!tn_ready && u_next < nU) {
-      tbl_next = desc_tbl(read_desc(), tbl_next_base);
-      tn_ready = true;
+      f_tail = f_tail == kFifo4 - 1 ? 0 : f_tail + 1;
+      q_free = false;
+      // q of the unit's 8 heads and its row's cos and sin, with the first stage
+      const uint16_t* q =
+          p.q + ((int64_t(layer) * p.Bt + e.x) * p.Hq + int64_t(kvh) * kGroup) * kHeadDim;
+      cp_async16(qbuf0 + 16 * lane, q + 8 * lane);
+      cp_async16(qbuf0 + 512 + 16 * lane, q + 256 + 8 * lane);
+      if (lane < 16)
+        cp_async16(qbuf0 + kQBytes + 16 * lane,
+                   (lane < 8 ? p.cosb : p.sinb) + int64_t(e.x) * (kHeadDim / 2) + 4 * (lane & 7));
+    } else {
+      fetch_next();
     }
-    const int nt = min(kStTiles, pe - pt);
-    if (fdiv((pt + nt - 1) * kTile, p.fd_b) >= tbl_base + 32) {
-      const UnitDesc& du = ws.fifo[(f_tail + kFifo4 - 1) % kFifo4];
+    const int tile = pt + my_tile;
+    const int blk = fdiv(min(tile, pe - 1) * kTile, p.fd_b);
+    if (__any_sync(kFull, blk >= tbl_base + 32)) {
+      const UnitDesc& du = ws.fifo[f_tail == 0 ? kFifo4 - 1 : f_tail - 1];
       tbl_base = fdiv(pt * kTile, p.fd_b);
-      tbl = load_tbl(du.kind == 2, du.b, tbl_base);
+      tbl = load_tbl((du.layer & 1) == 0, du.b, tbl_base);
     }
-    // lane l copies tile l of the stage
-    const int tile = pt + min(lane, nt - 1);
-    const int blk = fdiv(tile * kTile, p.fd_b);
     int32_t pb = __shfl_sync(kFull, tbl, blk - tbl_base);
     if (uint32_t(pb) >= uint32_t(p.nb)) {
-      if (lane < nt) set_error(GK_DEVERR_BLOCK);
+      set_error(GK_DEVERR_BLOCK);
       pb = 0;
     }
-    if (lane == 0) mbar_arrive_expect_tx(bar, uint32_t(nt) * kTileBytes + head_bytes);
-    __syncwarp();
-    if (lane < nt) {
-      const int tpb = p.B / kTile;
-      const uint8_t* src =
-          pu_src + (int64_t(pb) * p.Hkv * tpb + (tile - blk * tpb)) * int64_t(kTileBytes);
-      bulk_g2s(ring0 + p_slot * kSt4Bytes + lane * kTileBytes, src, kTileBytes, bar);
+    if (tile < pe) {
+      const uint8_t* s =
+          src + (uint64_t(uint32_t(pb)) * blk_bytes + uint32_t((tile - blk * tpb) * kTileBytes));
+      const uint32_t d = ring0 + p_slot * kSt4Bytes + my_tile * kTileBytes + my_off;
+#pragma unroll
+      for (int i = 0; i < kTileCopies; ++i)
+        cp_async16(d + i * kTileLanes * 16, s + i * kTileLanes * 16);
     }
-    pt += nt;
+    cp_async_commit();
+    pt = min(pt + kStTiles, pe);
     p_slot = p_slot == kStages4 - 1 ? 0 : p_slot + 1;
     ++prod;
     return true;
@@ -467,12 +463,11 @@ __global__ void __launch_bounds__(kWarps4 * 32, kBlocks4)
 
   // ------------------------------------------------ consumer state
   struct {
-    int t_begin, t_end, n_st;
-  } cd = {0, 0, 0};
-#define CU (ws.fifo[f_head % kFifo4])
-  int k_in_unit = 0, tok0 = 0;
+    int t_begin, t_end;
+  } cd = {0, 0};
+#define CU (ws.fifo[f_head])
+  int left = 0, tok0 = 0;  // the unit's stages left, first token of the next one
   int c_slot = 0;
-  uint32_t c_par = 0u;
   uint32_t qhi[8], qlo[8];  // q' = qhi + qlo (f16 each): ~22-bit significand
   // as in attn_kernel: scores are x * 2^e_h, si_h = 2^-e_h; mr_h the running
   // reference maximum, which may lag the true one by kLazyLog2
@@ -491,20 +486,20 @@ __global__ void __launch_bounds__(kWarps4 * 32, kBlocks4)
   const int vstep = (vt & 1) ? -kTokBytes : kTokBytes;
   const uint32_t vsoff = kTileVs + 16 * uint32_t(g >> 1) + 4 * qd;
   const uint32_t vsel = (vt & 1) ? 0x2301u : 0x3210u;  // scales in the order vt, vt ^ 1
-
-  while (prod - cons < kStages4 && issue_next()) {
-  }
-
-  while (cons < prod) {
-    if (!mbar_wait_bounded(bar0 + 8 * c_slot, c_par, kWaitLimitNs)) failed = true;
-    if (__any_sync(kFull, failed)) {
-      failed = true;
-      break;
+  for (;;) {
+    while (prod - cons < kStages4 && issue_next()) {
     }
-    if (k_in_unit == 0) {
+    if (cons == prod) break;
+    // a group a stage: with the ring full all but the newest ones have landed
+    if (prod - cons == kStages4)
+      cp_async_wait<kStages4 - 1>();
+    else
+      cp_async_wait<0>();
+    __syncwarp();
+    if (left == 0) {
       cd.t_begin = CU.t_begin;
       cd.t_end = CU.t_end;
-      cd.n_st = CU.n_st;
+      left = CU.n_st;
       tok0 = CU.st_begin * kTile;
       // ---- unit prologue: rotated q for head (kvh*8 + g), channels 16qd..16qd+15
       const uint32_t qrow = qbuf0 + g * (kHeadDim * 2);
@@ -573,8 +568,7 @@ __global__ void __launch_bounds__(kWarps4 * 32, kBlocks4)
       const uint32_t tile = st + i * kTileBytes;
       const uint2 ka = lds64(tile + koff), kb = lds64(tile + koff + 8 * kTokBytes);
       const uint32_t sf = e4m3x2_to_f16x2(lds_u16(tile + ksoff));
-      const uint32_t sa = prmt(sf, sf, 0x1010u), sb = prmt(sf, sf, 0x3232u);
-      sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.f;
+      const uint32_t sa = dup_lo(sf), sb = dup_hi(sf);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t a[4], b[4];
@@ -585,13 +579,28 @@ __global__ void __launch_bounds__(kWarps4 * 32, kBlocks4)
           const int j = 2 * h + k;
           const uint32_t a0 = mul_f16x2(a[2 * k], sa), a2 = mul_f16x2(a[2 * k + 1], sa);
           const uint32_t a1 = mul_f16x2(b[2 * k], sb), a3 = mul_f16x2(b[2 * k + 1], sb);
-          mma_f16(sc[i], a0, a1, a2, a3, qlo[2 * j], qlo[2 * j + 1]);
+          if (j == 0)
+            mma_f16_first(sc[i], a0, a1, a2, a3, qlo[0], qlo[1]);
+          else
+            mma_f16(sc[i], a0, a1, a2, a3, qlo[2 * j], qlo[2 * j + 1]);
           mma_f16(sc[i], a0, a1, a2, a3, qhi[2 * j], qhi[2 * j + 1]);
         }
       }
     }
     // ---- online softmax (log2 domain); lane holds heads 2qd (c0,c2), 2qd+1 (c1,c3)
     if (edge) {
+      // V scales of keys outside the range may be anything, NaN included: 0.
+      // Lane l has token l % 16 of every tile, and two of the four blocks.
+      for (int i = 0; i < kStTiles; ++i) {
+        const int t = lane & 15, tok = tok0 + kTile * i + t;
+        if (tok < cd.t_begin || tok >= cd.t_end) {
+          uint8_t* vs = ws.ring[c_slot] + i * kTileBytes + kTileVs + 4 * ((t & 7) >> 1) +
+                        2 * (t >> 3) + (t & 1) + 32 * (lane >> 4);
+          vs[0] = 0;
+          vs[16] = 0;
+        }
+      }
+      __syncwarp();
 #pragma unroll
       for (int i = 0; i < kStTiles; ++i) {
         const int t0 = tok0 + kTile * i + (g ^ (g >> 2)), t1 = t0 + 8;
@@ -646,15 +655,8 @@ __global__ void __launch_bounds__(kWarps4 * 32, kBlocks4)
       const uint32_t w0 = lds32(tile + voff), w1 = lds32(tile + voff + vstep);
       const uint32_t w2 = lds32(tile + voff + 8 * kTokBytes);
       const uint32_t w3 = lds32(tile + voff + 8 * kTokBytes + vstep);
-      uint32_t sf = prmt(lds32(tile + vsoff), 0u, vsel);
-      uint32_t s01 = e4m3x2_to_f16x2(sf), s23 = e4m3x2_to_f16x2(sf >> 16);
-      if (edge) {
-        // scales of keys outside the range may be anything, NaN included
-        const int t0 = tok0 + kTile * i + vt, t1 = tok0 + kTile * i + (vt ^ 1);
-        auto in = [&](int t) { return t >= cd.t_begin && t < cd.t_end; };
-        s01 &= (in(t0) ? 0xffffu : 0u) | (in(t1) ? 0xffff0000u : 0u);
-        s23 &= (in(t0 + 8) ? 0xffffu : 0u) | (in(t1 + 8) ? 0xffff0000u : 0u);
-      }
+      uint32_t s01, s23;
+      e4m3x4_to_f16x2x2(prmt(lds32(tile + vsoff), 0u, vsel), s01, s23);
       // even and odd channels of a token pair, two nibbles a byte
       constexpr uint32_t kLow = 0x0f0f0f0fu;
       uint32_t e01[4], d01[4], e23[4], d23[4];
@@ -669,18 +671,10 @@ __global__ void __launch_bounds__(kWarps4 * 32, kBlocks4)
     }
     __syncwarp();
     ++cons;
-    if (++c_slot == kStages4) {
-      c_slot = 0;
-      c_par ^= 1u;
-    }
-    ++k_in_unit;
+    c_slot = c_slot == kStages4 - 1 ? 0 : c_slot + 1;
     tok0 += kSt4Tok;
-    while (prod - cons < kStages4 && issue_next()) {
-    }
-
-    if (k_in_unit == cd.n_st) {
+    if (--left == 0) {
       // ---- unit epilogue
-      k_in_unit = 0;
       const float l0 = lacc[0], l1 = lacc[1];
       if (CU.ns == 1) {
         const int64_t out_row =
@@ -733,24 +727,17 @@ __global__ void __launch_bounds__(kWarps4 * 32, kBlocks4)
         ro1[0] = make_float4(o[0][1], o[0][3], o[1][1], o[1][3]);
         ro1[1] = make_float4(o[2][1], o[2][3], o[3][1], o[3][3]);
       }
-      ++f_head;
+      f_head = f_head == kFifo4 - 1 ? 0 : f_head + 1;
     }
   }
 #undef CU
-  if (failed) {
-    // A barrier wait hit its limit: record it, then wait (bounded) for this
-    // warp's copies still in flight before the CTA may exit.
-    if (lane == 0) set_error(GK_DEVERR_TIMEOUT);
-    for (int c = cons; c < prod; ++c)
-      mbar_wait_bounded(bar0 + 8 * (c % kStages4), uint32_t(c / kStages4) & 1u, kWaitLimitNs);
-  }
 }
 
 // =========================================================================
 // Launchers
 // =========================================================================
 struct Kv4Device {
-  int sms = 0, blocks = 0;
+  int sms = 0;
   bool set = false;
 };
 static Kv4Device g_kv4_dev[64];
@@ -772,11 +759,6 @@ static cudaError_t kv4_setup(Kv4Device** out) {
     if (e != cudaSuccess) return e;
     e = plan_setup();
     if (e != cudaSuccess) return e;
-    int blocks = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, kv4_attn_kernel, kWarps4 * 32,
-                                                      kAttn4Smem);
-    if (e != cudaSuccess) return e;
-    c.blocks = blocks < 1 ? 1 : blocks;
     c.set = true;
   }
   *out = &c;
@@ -790,7 +772,7 @@ cudaError_t launch_kv4_attention(const PlanParams& plan, const AttnParams& p, cu
   if (e != cudaSuccess) return e;
   Kv4PlanWriteParams pw;
   pw.plan = plan;
-  pw.plan.n_warps = c->sms * c->blocks * kWarps4;
+  pw.plan.n_warps = c->sms * kCons;
   AttnChain ch = {};
   if (write) {
     pw.write = *write;
@@ -802,8 +784,8 @@ cudaError_t launch_kv4_attention(const PlanParams& plan, const AttnParams& p, cu
     ch.plan_arg = &pw.plan;
   }
   ch.attn_func = (const void*)kv4_attn_kernel;
-  ch.attn_threads = kWarps4 * 32;
-  ch.attn_grid = unsigned(c->sms * c->blocks);
+  ch.attn_threads = kAttn4Threads;
+  ch.attn_grid = unsigned(c->sms);
   ch.attn_smem = kAttn4Smem;
   return launch_chain(ch, p, c->sms, st);
 }
