@@ -105,6 +105,29 @@ __device__ __forceinline__ uint32_t f32x2_to_e2m1x2(float lo, float hi) {
   return r;
 }
 
+// a * b + c in both components.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n"
+      " .reg .b64 a, b, c;\n"
+      " mov.b64 a, {%2, %3};\n"
+      " mov.b64 b, {%4, %5};\n"
+      " mov.b64 c, {%6, %7};\n"
+      " fma.rn.f32x2 a, a, b, c;\n"
+      " mov.b64 {%0, %1}, a;\n"
+      "}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+
+// The low nibble of every byte from a, the high one from b.
+__device__ __forceinline__ uint32_t low_nibbles(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, 0x0f0f0f0f, 0xd8;" : "=r"(r) : "r"(b), "r"(a));
+  return r;
+}
+
 // max that gives NaN when either is NaN
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
@@ -308,8 +331,8 @@ __global__ void __launch_bounds__(kPlanThreads)
 // head, split) from the work counter and streams their tiles through a ring of
 // its own, kStTiles tiles a stage.
 constexpr int kStTiles = 4;     // tiles per pipeline stage
-constexpr int kStages4 = 3;     // ring depth per warp
-constexpr int kCons = 15;       // warps
+constexpr int kStages4 = 2;     // ring depth per warp
+constexpr int kCons = 16;       // warps
 constexpr int kFifo4 = 6;       // unit descriptors in flight per warp (> kStages4 + 1)
 constexpr int kSt4Tok = kStTiles * kTile;
 constexpr uint32_t kSt4Bytes = kStTiles * kTileBytes;
@@ -356,22 +379,27 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
   int4 e_nx = make_int4(0, 0, 0, 0);
   int32_t tbl_nx = 0;
   auto swa_of = [](int4 e) { return ((e.w >> 30) & 1) != 0; };
-  // lane l: entry l of the table chunk starting at block `base`
-  auto load_tbl = [&](bool swa, int b, int base) -> int32_t {
+  // lane l: entry l of the table chunk starting at block `base`, of a unit
+  // whose last tile is `last`; 0 past it and for an entry outside the pool
+  auto load_tbl = [&](bool swa, int b, int base, int last) -> int32_t {
     const int32_t* row = swa ? p.bt_swa + int64_t(b) * p.MBS : p.bt_full + int64_t(b) * p.MBF;
     const int idx = base + lane;
-    return idx < (swa ? p.MBS : p.MBF) ? __ldg(row + idx) : 0;
+    int32_t pb = idx <= fdiv(last * kTile, p.fd_b) ? __ldg(row + idx) : 0;
+    if (uint32_t(pb) >= uint32_t(p.nb)) {
+      set_error(GK_DEVERR_BLOCK);
+      pb = 0;
+    }
+    return pb;
   };
   auto first_blk = [&](int4 e) { return fdiv(e.y & ~(kTile - 1), p.fd_b); };
   auto fetch_next = [&]() {
     if (nx_step == 1) {
       u_nx = __shfl_sync(kFull, u_nx, 0);  // the claim's answer is lane 0's
       if (u_nx < nU) e_nx = __ldcg(p.edesc + fdiv(u_nx, p.fd_planes));
-      nx_step = 2;
-    } else if (nx_step == 2) {
-      if (u_nx < nU) tbl_nx = load_tbl(swa_of(e_nx), e_nx.x, first_blk(e_nx));
-      nx_step = 3;
+    } else if (u_nx < nU) {
+      tbl_nx = load_tbl(swa_of(e_nx), e_nx.x, first_blk(e_nx), (e_nx.z - 1) / kTile);
     }
+    ++nx_step;
   };
   int prod = 0, cons = 0, p_slot = 0;
   int f_head = 0, f_tail = 0;
@@ -379,7 +407,7 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
   bool q_free = true;   // the q buffer may take the next unit's q
   int pt = 0, pe = 0;   // the producer unit's next and end tile
   const uint8_t* src = nullptr;  // its kv head's tiles of block 0, at this lane's bytes
-  int tbl_base = 0;
+  int tbl_base = 0, tbl_end = 0;  // the chunk's first block, its end in tiles
   int32_t tbl = 0;
   const int tpb = p.B / kTile;
   const uint32_t blk_bytes = uint32_t(p.Hkv * tpb * kTileBytes);
@@ -401,6 +429,7 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
       const int4 e = e_nx;
       tbl = tbl_nx;
       tbl_base = first_blk(e);
+      tbl_end = (tbl_base + 32) * tpb;
       if (lane == 0) u_nx = atomicAdd(p.queue, 1);
       nx_step = 1;
       const int pl = u - fdiv(u, p.fd_planes) * int(p.fd_planes.d);
@@ -431,21 +460,18 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
       if (lane < 16)
         cp_async16(qbuf0 + kQBytes + 16 * lane,
                    (lane < 8 ? p.cosb : p.sinb) + int64_t(e.x) * (kHeadDim / 2) + 4 * (lane & 7));
-    } else {
+    } else if (nx_step < 3) {
       fetch_next();
     }
-    const int tile = pt + my_tile;
-    const int blk = fdiv(min(tile, pe - 1) * kTile, p.fd_b);
-    if (__any_sync(kFull, blk >= tbl_base + 32)) {
+    if (min(pt + kStTiles, pe) > tbl_end) {
       const UnitDesc& du = ws.fifo[f_tail == 0 ? kFifo4 - 1 : f_tail - 1];
       tbl_base = fdiv(pt * kTile, p.fd_b);
-      tbl = load_tbl((du.layer & 1) == 0, du.b, tbl_base);
+      tbl_end = (tbl_base + 32) * tpb;
+      tbl = load_tbl((du.layer & 1) == 0, du.b, tbl_base, pe - 1);
     }
-    int32_t pb = __shfl_sync(kFull, tbl, blk - tbl_base);
-    if (uint32_t(pb) >= uint32_t(p.nb)) {
-      set_error(GK_DEVERR_BLOCK);
-      pb = 0;
-    }
+    const int tile = pt + my_tile;
+    const int blk = fdiv(tile * kTile, p.fd_b);
+    const int32_t pb = __shfl_sync(kFull, tbl, blk - tbl_base);  // past the unit's end: not used
     if (tile < pe) {
       const uint8_t* s =
           src + (uint64_t(uint32_t(pb)) * blk_bytes + uint32_t((tile - blk * tpb) * kTileBytes));
@@ -468,13 +494,13 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
 #define CU (ws.fifo[f_head])
   int left = 0, tok0 = 0;  // the unit's stages left, first token of the next one
   int c_slot = 0;
-  uint32_t qhi[8], qlo[8];  // q' = qhi + qlo (f16 each): ~22-bit significand
+  uint32_t qf[8];  // q' in f16
   // as in attn_kernel: scores are x * 2^e_h, si_h = 2^-e_h; mr_h the running
   // reference maximum, which may lag the true one by kLazyLog2
-  float si0 = 0.f, si1 = 0.f, mr0 = 0.f, mr1 = 0.f, nb0 = 0.f, nb1 = 0.f, thr0 = 0.f, thr1 = 0.f,
-        vscale = 0.f;
+  float2 si = make_float2(0.f, 0.f), nb = si;
+  float mr0 = 0.f, mr1 = 0.f, thr0 = 0.f, thr1 = 0.f, vscale = 0.f;
   float o[4][4];
-  float lacc[4];  // softmax denominators from a ones-row MMA over the f16 P
+  float l0 = 0.f, l1 = 0.f;  // this lane's part of the softmax denominators
   // K rows (g, g + 8) of a tile are its tokens (ktok, ktok + 8); the P that the
   // transpose gives lane qd are then of tokens ktok(2 qd), ktok(2 qd + 1) and
   // those + 8.  ktok(r) = r for r < 4, r ^ 1 above: every quarter of K rows and
@@ -544,17 +570,14 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
       const float fck = f * ck;
 #pragma unroll
       for (int w = 0; w < 8; ++w) {
-        const float a = r[2 * w] * fck, b = r[2 * w + 1] * fck;
-        qhi[w] = f32x2_to_f16x2(a, b);
-        const float2 h = f16x2_to_f32x2(qhi[w]);
-        qlo[w] = f32x2_to_f16x2(a - h.x, b - h.y);  // residual is exact in fp32
+        qf[w] = f32x2_to_f16x2(r[2 * w] * fck, r[2 * w + 1] * fck);
       }
-      si0 = __shfl_sync(kFull, finv, 8 * qd);  // heads 2qd and 2qd+1
-      si1 = __shfl_sync(kFull, finv, 8 * qd + 4);
+      si.x = __shfl_sync(kFull, finv, 8 * qd);  // heads 2qd and 2qd+1
+      si.y = __shfl_sync(kFull, finv, 8 * qd + 4);
       vscale = p.v_scale[CU.layer];
       mr0 = mr1 = thr0 = thr1 = -INFINITY;
-      nb0 = nb1 = 0.f;
-      lacc[0] = lacc[1] = lacc[2] = lacc[3] = 0.f;
+      nb.x = nb.y = 0.f;
+      l0 = l1 = 0.f;
 #pragma unroll
       for (int m = 0; m < 4; ++m) o[m][0] = o[m][1] = o[m][2] = o[m][3] = 0.f;
     }
@@ -580,10 +603,9 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
           const uint32_t a0 = mul_f16x2(a[2 * k], sa), a2 = mul_f16x2(a[2 * k + 1], sa);
           const uint32_t a1 = mul_f16x2(b[2 * k], sb), a3 = mul_f16x2(b[2 * k + 1], sb);
           if (j == 0)
-            mma_f16_first(sc[i], a0, a1, a2, a3, qlo[0], qlo[1]);
+            mma_f16_first(sc[i], a0, a1, a2, a3, qf[0], qf[1]);
           else
-            mma_f16(sc[i], a0, a1, a2, a3, qlo[2 * j], qlo[2 * j + 1]);
-          mma_f16(sc[i], a0, a1, a2, a3, qhi[2 * j], qhi[2 * j + 1]);
+            mma_f16(sc[i], a0, a1, a2, a3, qf[2 * j], qf[2 * j + 1]);
         }
       }
     }
@@ -615,6 +637,7 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
       lm1 = fmaxf(lm1, fmaxf(sc[i][1], sc[i][3]));
     }
     if (__any_sync(kFull, lm0 > thr0 || lm1 > thr1)) {
+      // move the reference to the true running maximum and rescale what was summed
       float w0 = lm0, w1 = lm1;
 #pragma unroll
       for (int off = 4; off < 32; off <<= 1) {
@@ -622,17 +645,15 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
         w1 = fmaxf(w1, __shfl_xor_sync(kFull, w1, off));
       }
       const float n0 = fmaxf(mr0, w0), n1 = fmaxf(mr1, w1);
-      const float al0 = ex2((mr0 - n0) * si0), al1 = ex2((mr1 - n1) * si1);
+      const float al0 = ex2((mr0 - n0) * si.x), al1 = ex2((mr1 - n1) * si.y);
       mr0 = n0;
       mr1 = n1;
-      nb0 = -n0 * si0;
-      nb1 = -n1 * si1;
-      thr0 = n0 + kLazyLog2 / si0;
-      thr1 = n1 + kLazyLog2 / si1;
-      lacc[0] *= al0;
-      lacc[2] *= al0;
-      lacc[1] *= al1;
-      lacc[3] *= al1;
+      nb.x = -n0 * si.x;
+      nb.y = -n1 * si.y;
+      thr0 = n0 + kLazyLog2 / si.x;
+      thr1 = n1 + kLazyLog2 / si.y;
+      l0 *= al0;
+      l1 *= al1;
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
         o[m][0] *= al0;
@@ -645,12 +666,13 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
 #pragma unroll
     for (int i = 0; i < kStTiles; ++i) {
       const uint32_t tile = st + i * kTileBytes;
-      const float p0 = ex2(fmaf(sc[i][0], si0, nb0)), p1 = ex2(fmaf(sc[i][1], si1, nb1));
-      const float p2 = ex2(fmaf(sc[i][2], si0, nb0)), p3 = ex2(fmaf(sc[i][3], si1, nb1));
+      const float2 xa = fma2(make_float2(sc[i][0], sc[i][1]), si, nb);
+      const float2 xb = fma2(make_float2(sc[i][2], sc[i][3]), si, nb);
+      const float p0 = ex2(xa.x), p1 = ex2(xa.y), p2 = ex2(xb.x), p3 = ex2(xb.y);
+      l0 += p0 + p2;
+      l1 += p1 + p3;
       const uint32_t b0 = movmatrix_trans(f32x2_to_f16x2(p0, p1));
       const uint32_t b1 = movmatrix_trans(f32x2_to_f16x2(p2, p3));
-      // every row of the ones matrix sums the same rounded P the values see
-      mma_f16(lacc, kOnesF16x2, kOnesF16x2, kOnesF16x2, kOnesF16x2, b0, b1);
       // channels 8g .. 8g+7 (one nibble each) of the lane's four tokens
       const uint32_t w0 = lds32(tile + voff), w1 = lds32(tile + voff + vstep);
       const uint32_t w2 = lds32(tile + voff + 8 * kTokBytes);
@@ -658,12 +680,11 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
       uint32_t s01, s23;
       e4m3x4_to_f16x2x2(prmt(lds32(tile + vsoff), 0u, vsel), s01, s23);
       // even and odd channels of a token pair, two nibbles a byte
-      constexpr uint32_t kLow = 0x0f0f0f0fu;
       uint32_t e01[4], d01[4], e23[4], d23[4];
-      e2m1x8_to_f16x2x4((w0 & kLow) | ((w1 << 4) & ~kLow), e01);
-      e2m1x8_to_f16x2x4(((w0 >> 4) & kLow) | (w1 & ~kLow), d01);
-      e2m1x8_to_f16x2x4((w2 & kLow) | ((w3 << 4) & ~kLow), e23);
-      e2m1x8_to_f16x2x4(((w2 >> 4) & kLow) | (w3 & ~kLow), d23);
+      e2m1x8_to_f16x2x4(low_nibbles(w0, w1 << 4), e01);
+      e2m1x8_to_f16x2x4(low_nibbles(w0 >> 4, w1), d01);
+      e2m1x8_to_f16x2x4(low_nibbles(w2, w3 << 4), e23);
+      e2m1x8_to_f16x2x4(low_nibbles(w2 >> 4, w3), d23);
 #pragma unroll
       for (int m = 0; m < 4; ++m)
         mma_f16(o[m], mul_f16x2(e01[m], s01), mul_f16x2(d01[m], s01), mul_f16x2(e23[m], s23),
@@ -675,15 +696,19 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
     tok0 += kSt4Tok;
     if (--left == 0) {
       // ---- unit epilogue
-      const float l0 = lacc[0], l1 = lacc[1];
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) {
+        l0 += __shfl_xor_sync(kFull, l0, off);
+        l1 += __shfl_xor_sync(kFull, l1, off);
+      }
       if (CU.ns == 1) {
         const int64_t out_row =
             ((int64_t(CU.layer) * p.Bt + CU.b) * p.Hq + CU.kvh * kGroup + 2 * qd) * kHeadDim +
             8 * g;
         const float* snk =
             p.sinks ? p.sinks + int64_t(CU.layer) * p.Hq + CU.kvh * kGroup + 2 * qd : nullptr;
-        const float i0 = out_scale(l0, mr0 * si0, snk, vscale);
-        const float i1 = out_scale(l1, mr1 * si1, snk ? snk + 1 : nullptr, vscale);
+        const float i0 = out_scale(l0, mr0 * si.x, snk, vscale);
+        const float i1 = out_scale(l1, mr1 * si.y, snk ? snk + 1 : nullptr, vscale);
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
           o[m][0] *= i0;
@@ -715,8 +740,8 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
         const int64_t plane = int64_t(CU.layer >> 1) * p.Hkv + CU.kvh;
         float* rec = p.partials + (plane * p.cap + p.part_base[CU.b] + CU.s) * kPartialFloats;
         if (g == 0) {
-          rec[2 * qd] = mr0 * si0;  // log2 units
-          rec[2 * qd + 1] = mr1 * si1;
+          rec[2 * qd] = mr0 * si.x;  // log2 units
+          rec[2 * qd + 1] = mr1 * si.y;
           rec[kGroup + 2 * qd] = l0;
           rec[kGroup + 2 * qd + 1] = l1;
         }
