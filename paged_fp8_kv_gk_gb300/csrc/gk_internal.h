@@ -158,6 +158,7 @@ struct Kv4WriteParams {
   const uint8_t* active;  // or null
   uint8_t* buf[kMaxGroups];
   int layer0, n_layers, n_tokens, Hkv, B, nb;
+  int seg;  // layers a CTA takes (set by the launcher)
 };
 
 struct Kv4ReadParams {
@@ -170,6 +171,7 @@ struct Kv4ReadParams {
   uint16_t* k_out;
   uint16_t* v_out;
   int layer0, n_layers, n_tokens, Hkv, B, nb;
+  int seg;  // layers a CTA takes (set by the launcher)
 };
 
 // Launchers (gk_kernels.cu).  They return the launch status.
@@ -202,8 +204,8 @@ cudaError_t launch_ingest(const IngestParams& p, cudaStream_t st);
 cudaError_t read_ingest_error(uint32_t* bits, bool clear);
 // gk_kv4.cu: the 4-bit cache, with its own device error word.  In the attention
 // parameters kb[j] is group buffer j and vb is not used.
-cudaError_t launch_kv4_write(const Kv4WriteParams& p, cudaStream_t st);
-cudaError_t launch_kv4_read(const Kv4ReadParams& p, cudaStream_t st);
+cudaError_t launch_kv4_write(Kv4WriteParams& p, cudaStream_t st);
+cudaError_t launch_kv4_read(Kv4ReadParams& p, cudaStream_t st);
 // write: gk_kv4_decode_step's new tokens, written in the planner's grid (or null)
 cudaError_t launch_kv4_attention(const PlanParams& plan, const AttnParams& p, cudaStream_t st,
                                  const Kv4WriteParams* write);

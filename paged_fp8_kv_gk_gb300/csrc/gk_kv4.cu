@@ -138,36 +138,74 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // =========================================================================
 // Write and read
 // =========================================================================
-// Where a token of one kv head lies.
+// Where a token of kv head h lies: byte offset of its tile in a group buffer,
+// and its place in the tile.
 struct TokenPlace {
-  int64_t tile;  // byte offset of its tile in the group buffer
-  int t;         // token in the tile
+  int64_t tile;
+  int t;
 };
 __device__ __forceinline__ TokenPlace place_of(int slot, int h, int Hkv, int B) {
   const int pb = slot / B, off = slot - pb * B;
   return {((int64_t(pb) * Hkv + h) * (B / kTile) + off / kTile) * kTileBytes, off % kTile};
 }
 
-// Quantise 16 values (already divided by the layer scale): E4M3 code of the
-// block scale and 16 E2M1 codes.
+// Whether token n is written or read in the layers whose slots are `slots`.
+template <typename P>
+__device__ __forceinline__ bool token_slot(const P& p, const int32_t* slots, int64_t n, int& slot) {
+  slot = GK_KV4_SKIP;
+  if (n >= p.n_tokens || (p.active && !p.active[n])) return false;
+  slot = slots[n];
+  if (slot >= 0 && slot < p.nb * p.B) return true;
+  if (slot != GK_KV4_SKIP) set_error(GK_DEVERR_SLOT);
+  slot = GK_KV4_SKIP;
+  return false;
+}
+
+// x / s, correctly rounded: r = 1 / s correctly rounded, 2^-40 <= s <= 2^40 and
+// |x| < 2^60.  Two corrections by the exact remainder (Markstein): the first
+// leaves a quotient within one step, which the second rounds correctly.  For
+// |x| < 2^-100 the remainder may underflow; such a quotient is far below half
+// of the smallest block scale and only its sign counts.
+__device__ __forceinline__ float div_by(float x, float s, float r) {
+  const float q0 = x * r;
+  const float q1 = fmaf(fmaf(-q0, s, x), r, q0);
+  return fmaf(fmaf(-q1, s, x), r, q1);
+}
+
+// Quantise x[16] / scale: E4M3 code of the block scale and 16 E2M1 codes.
+// exact: exact_reciprocal(scale); rcp: 1 / scale, or 0 outside div_by's range.
 //
 // The codes are those of the exact quotient u / sf.  sf has 4 significant bits
 // and a code border t has 3, so u is a border only if it is t * sf exactly; the
-// quotient is refined by one exact remainder (Markstein's correction), which
-// gives such a quotient exactly and any other within a 2^-45 part of u / sf
-// before its last rounding, hence on its own side of the border (the nearest
-// u to t * sf differs by more than half a step of t).
-__device__ __forceinline__ uint32_t quantise16(float (&u)[16], uint2& codes) {
-  float a = fabsf(u[0]);
+// quotient is refined by one exact remainder, which gives such a quotient
+// exactly and any other within a 2^-45 part of u / sf before its last rounding,
+// hence on its own side of the border (the nearest u to t * sf differs by more
+// than half a step of t).
+__device__ __forceinline__ uint32_t quantise16(float (&x)[16], float scale, float exact, float rcp,
+                                               uint2& codes) {
+  float a = fabsf(x[0]);
 #pragma unroll
-  for (int e = 1; e < 16; ++e) a = max_nan(a, fabsf(u[e]));
+  for (int e = 1; e < 16; ++e) a = max_nan(a, fabsf(x[e]));
+  if (exact != 0.f) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) x[e] *= exact;
+    a *= fabsf(exact);
+  } else if (rcp != 0.f && a < 0x1p60f) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) x[e] = div_by(x[e], scale, rcp);
+    a = fabsf(div_by(a, scale, rcp));  // rounding is monotonic: the largest quotient
+  } else {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) x[e] = __fdiv_rn(x[e], scale);
+    a = __fdiv_rn(a, fabsf(scale));
+  }
   const uint32_t sfc = f32x2_to_e4m3x2(__fdiv_rn(a, 6.f), 0.f) & 0xffu;
   const float sf = f16x2_to_f32x2(e4m3x2_to_f16x2(sfc)).x;
   if (a > 1e30f) {
     // infinities: any value this large has the saturated code, and stays
     // finite through the remainder below
 #pragma unroll
-    for (int e = 0; e < 16; ++e) u[e] = fminf(fmaxf(u[e], -1e30f), 1e30f);
+    for (int e = 0; e < 16; ++e) x[e] = fminf(fmaxf(x[e], -1e30f), 1e30f);
   }
   const float r = sf > 0.f ? __frcp_rn(sf) : 0.f;
   uint32_t w[2] = {0u, 0u};
@@ -176,8 +214,8 @@ __device__ __forceinline__ uint32_t quantise16(float (&u)[16], uint2& codes) {
     float y[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const float y0 = u[e + k] * r;
-      y[k] = fmaf(fmaf(-y0, sf, u[e + k]), r, y0);
+      const float y0 = x[e + k] * r;
+      y[k] = fmaf(fmaf(-y0, sf, x[e + k]), r, y0);
     }
     w[e / 8] |= f32x2_to_e2m1x2(y[0], y[1]) << (4 * (e % 8));
   }
@@ -185,102 +223,127 @@ __device__ __forceinline__ uint32_t quantise16(float (&u)[16], uint2& codes) {
   return sfc;
 }
 
-// 16 channels (16 blk ..) of K (kv = 0) or V (kv = 1) of one token and head:
-// load, rotate, divide, quantise, store.
-__device__ __forceinline__ void write_block(const Kv4WriteParams& p, int layer, int n, int h,
-                                            int blk, int kv) {
-  if (p.active && !p.active[n]) return;
-  const int slot = (layer & 1) ? p.slot_full[n] : p.slot_swa[n];
-  if (slot == GK_KV4_SKIP) return;
-  if (slot < 0 || slot >= p.nb * p.B) {
-    set_error(GK_DEVERR_SLOT);
-    return;
-  }
-  const int64_t row = int64_t(layer - p.layer0) * p.layer_stride + int64_t(n) * p.token_stride +
-                      int64_t(h) * kHeadDim;
-  const uint16_t* src = (kv ? p.v : p.k) + row;
-  float x[16];
-  auto load16 = [](const uint16_t* s, float (&d)[16]) {
-    const uint4 a = ldg_nc_v4(s), b = ldg_nc_v4(s + 8);
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      d[2 * k] = bf16lo_to_f32(w[k]);
-      d[2 * k + 1] = bf16hi_to_f32(w[k]);
-    }
-  };
-  load16(src + 16 * blk, x);
-  if (kv == 0 && p.cosb) {
-    // rotate-half: every operation rounded on its own, as in the FP8 append
-    float y[16];
-    load16(src + 16 * (blk ^ 2), y);
-    const float4* cr = reinterpret_cast<const float4*>(p.cosb + int64_t(n) * (kHeadDim / 2)) +
-                       4 * (blk & 1);
-    const float4* sr = reinterpret_cast<const float4*>(p.sinb + int64_t(n) * (kHeadDim / 2)) +
-                       4 * (blk & 1);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float4 c4 = __ldg(cr + k), s4 = __ldg(sr + k);
-      const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float a = __fmul_rn(x[4 * k + e], c[e]), b = __fmul_rn(y[4 * k + e], s[e]);
-        x[4 * k + e] = blk < 2 ? __fsub_rn(a, b) : __fadd_rn(a, b);
-      }
-    }
-  }
-  const float scale = kv ? p.v_scale[layer] : p.k_scale[layer];
-  const float inv = exact_reciprocal(scale);
-#pragma unroll
-  for (int e = 0; e < 16; ++e) x[e] = div_scale(x[e], scale, inv);
-  uint2 codes;
-  const uint32_t sf = quantise16(x, codes);
-  const TokenPlace at = place_of(slot, h, p.Hkv, p.B);
-  uint8_t* tile = p.buf[layer >> 1] + at.tile;
-  const int t = at.t;
-  *reinterpret_cast<uint2*>(tile + (kv ? kTileV : 0) + t * kTokBytes + blk * 8) = codes;
-  tile[kv ? kTileVs + 16 * blk + 4 * ((t & 7) >> 1) + 2 * (t >> 3) + (t & 1)
-          : kTileKs + 8 * (t & 7) + 2 * blk + (t >> 3)] = uint8_t(sf);
+struct LayerScale {
+  float scale, exact, rcp;
+};
+__device__ __forceinline__ LayerScale layer_scale(float s) {
+  const float a = fabsf(s);
+  return {s, exact_reciprocal(s), a >= 0x1p-40f && a <= 0x1p40f ? __frcp_rn(s) : 0.f};
 }
 
-constexpr int kWriteThreads = 256;
+constexpr int kWriteTok = 8;  // tokens a warp writes at a time: four lanes each
+constexpr int kReadTok = 4;   // tokens a warp reads at a time: eight lanes each
+constexpr int kTokThreads = 256;
+constexpr int kTokWarps = kTokThreads / 32;
 
-// Four threads a (token, head), one for every 16 channels; grid y: layer and
-// K or V.
-__global__ void __launch_bounds__(kWriteThreads)
+// One warp writes the 8 tokens from 8 tg and kv head h, layers [l0, l1).  Lane
+// (n, blk) has 16 channels of K and of V; its slots, its place in the tiles and
+// its cos and sin serve every layer.
+__device__ __forceinline__ void write_tokens(const Kv4WriteParams& p, int tg, int h, int l0,
+                                             int l1) {
+  const int lane = threadIdx.x & 31, blk = lane & 3;
+  const int64_t n = int64_t(tg) * kWriteTok + (lane >> 2);
+  int slot_f, slot_s;
+  const bool ok_f = token_slot(p, p.slot_full, n, slot_f);
+  const bool ok_s = token_slot(p, p.slot_swa, n, slot_s);
+  const bool any_f = __any_sync(kFull, ok_f), any_s = __any_sync(kFull, ok_s);
+  if (!any_f && !any_s) return;
+  float c[16], sn[16];
+  const bool rotate = p.cosb != nullptr;
+  if (rotate && (ok_f || ok_s)) {
+    const int64_t at = n * (kHeadDim / 2) + 16 * (blk & 1);
+    const float sgn = blk < 2 ? -1.f : 1.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float4 c4 = __ldg(reinterpret_cast<const float4*>(p.cosb + at) + k);
+      const float4 s4 = __ldg(reinterpret_cast<const float4*>(p.sinb + at) + k);
+      c[4 * k] = c4.x, c[4 * k + 1] = c4.y, c[4 * k + 2] = c4.z, c[4 * k + 3] = c4.w;
+      sn[4 * k] = sgn * s4.x, sn[4 * k + 1] = sgn * s4.y;
+      sn[4 * k + 2] = sgn * s4.z, sn[4 * k + 3] = sgn * s4.w;
+    }
+  }
+  const int64_t row = n * p.token_stride + h * kHeadDim + 16 * blk;
+  for (int i = l0; i < l1; ++i) {
+    if (!((i & 1) ? any_f : any_s)) continue;
+    const bool ok = (i & 1) ? ok_f : ok_s;
+    uint4 k0 = make_uint4(0, 0, 0, 0), k1 = k0, v0 = k0, v1 = k0;
+    if (ok) {
+      const uint16_t* ks = p.k + int64_t(i - p.layer0) * p.layer_stride + row;
+      const uint16_t* vs = p.v + int64_t(i - p.layer0) * p.layer_stride + row;
+      k0 = ldg_nc_v4(ks);
+      k1 = ldg_nc_v4(ks + 8);
+      v0 = ldg_nc_v4(vs);
+      v1 = ldg_nc_v4(vs + 8);
+    }
+    const LayerScale sk = layer_scale(__ldg(p.k_scale + i));
+    const LayerScale sv = layer_scale(__ldg(p.v_scale + i));
+    const uint32_t kw[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
+    const uint32_t vw[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+    float x[16];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      x[2 * k] = bf16lo_to_f32(kw[k]);
+      x[2 * k + 1] = bf16hi_to_f32(kw[k]);
+    }
+    if (rotate) {
+      // rotate-half, the pair's other half two lanes away: every operation
+      // rounded on its own, as in the FP8 append (x - y s = x + y (-s))
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t y = __shfl_xor_sync(kFull, kw[k], 2);
+        x[2 * k] = __fadd_rn(__fmul_rn(x[2 * k], c[2 * k]),
+                             __fmul_rn(bf16lo_to_f32(y), sn[2 * k]));
+        x[2 * k + 1] = __fadd_rn(__fmul_rn(x[2 * k + 1], c[2 * k + 1]),
+                                 __fmul_rn(bf16hi_to_f32(y), sn[2 * k + 1]));
+      }
+    }
+    if (!ok) continue;
+    const TokenPlace at = place_of((i & 1) ? slot_f : slot_s, h, p.Hkv, p.B);
+    uint8_t* tile = p.buf[i >> 1] + at.tile;
+    const int t = at.t;
+    uint2 codes;
+    uint32_t sf = quantise16(x, sk.scale, sk.exact, sk.rcp, codes);
+    *reinterpret_cast<uint2*>(tile + t * kTokBytes + blk * 8) = codes;
+    tile[kTileKs + 8 * (t & 7) + 2 * blk + (t >> 3)] = uint8_t(sf);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      x[2 * k] = bf16lo_to_f32(vw[k]);
+      x[2 * k + 1] = bf16hi_to_f32(vw[k]);
+    }
+    sf = quantise16(x, sv.scale, sv.exact, sv.rcp, codes);
+    *reinterpret_cast<uint2*>(tile + kTileV + t * kTokBytes + blk * 8) = codes;
+    tile[kTileVs + 16 * blk + 4 * ((t & 7) >> 1) + 2 * (t >> 3) + (t & 1)] = uint8_t(sf);
+  }
+}
+
+// grid x: (8 tokens, kv head) a warp; grid y: p.seg layers
+__global__ void __launch_bounds__(kTokThreads)
     kv4_write_kernel(const __grid_constant__ Kv4WriteParams p) {
   // the decode-attention planner may launch now (see kv_append_kernel)
   asm volatile("griddepcontrol.launch_dependents;");
-  const int64_t it = int64_t(blockIdx.x) * kWriteThreads + threadIdx.x;
-  if (it >= int64_t(p.n_tokens) * p.Hkv * 4) return;
-  const int nh = int(it >> 2), n = nh / p.Hkv;
-  write_block(p, p.layer0 + int(blockIdx.y >> 1), n, nh - n * p.Hkv, int(it & 3),
-              int(blockIdx.y & 1));
+  const int w = int(blockIdx.x) * kTokWarps + (threadIdx.x >> 5);
+  const int tg = w / p.Hkv;
+  if (int64_t(tg) * kWriteTok >= p.n_tokens) return;
+  const int l0 = p.layer0 + int(blockIdx.y) * p.seg;
+  write_tokens(p, tg, w - tg * p.Hkv, l0, min(l0 + p.seg, p.layer0 + p.n_layers));
 }
 
-// Eight threads a (token, head): 8 channels of K and of V each.
-__global__ void __launch_bounds__(kWriteThreads)
+// grid x: (4 tokens, kv head) a warp, lane (n, c): channels 8c .. 8c+7 of K and
+// of V; grid y: p.seg layers
+__global__ void __launch_bounds__(kTokThreads)
     kv4_read_kernel(const __grid_constant__ Kv4ReadParams p) {
-  const int64_t it = int64_t(blockIdx.x) * kWriteThreads + threadIdx.x;
-  if (it >= int64_t(p.n_tokens) * p.Hkv * 8) return;
-  const int layer = p.layer0 + int(blockIdx.y);
-  const int c = int(it & 7);
-  const int64_t nh = it >> 3;
-  const int n = int(nh / p.Hkv), h = int(nh - int64_t(n) * p.Hkv);
-  if (p.active && !p.active[n]) return;
-  const int slot = (layer & 1) ? p.slot_full[n] : p.slot_swa[n];
-  if (slot == GK_KV4_SKIP) return;
-  if (slot < 0 || slot >= p.nb * p.B) {
-    set_error(GK_DEVERR_SLOT);
-    return;
-  }
-  const TokenPlace at = place_of(slot, h, p.Hkv, p.B);
-  const uint8_t* tile = p.buf[layer >> 1] + at.tile;
-  const int t = at.t, blk = c >> 1;
-  const uint32_t kc = *reinterpret_cast<const uint32_t*>(tile + t * kTokBytes + 4 * c);
-  const uint32_t vc = *reinterpret_cast<const uint32_t*>(tile + kTileV + t * kTokBytes + 4 * c);
-  const uint32_t ks = tile[kTileKs + 8 * (t & 7) + 2 * blk + (t >> 3)];
-  const uint32_t vs = tile[kTileVs + 16 * blk + 4 * ((t & 7) >> 1) + 2 * (t >> 3) + (t & 1)];
+  const int w = int(blockIdx.x) * kTokWarps + (threadIdx.x >> 5);
+  const int tg = w / p.Hkv, h = w - tg * p.Hkv;
+  const int lane = threadIdx.x & 31, c = lane & 7;
+  const int64_t n = int64_t(tg) * kReadTok + (lane >> 3);
+  int slot_f, slot_s;
+  const bool ok_f = token_slot(p, p.slot_full, n, slot_f);
+  const bool ok_s = token_slot(p, p.slot_swa, n, slot_s);
+  if (!ok_f && !ok_s) return;
+  // byte offsets of the lane's codes and scales, of the full and the window layers
+  const int blk = c >> 1;
+  const TokenPlace at_f = place_of(max(slot_f, 0), h, p.Hkv, p.B);
+  const TokenPlace at_s = place_of(max(slot_s, 0), h, p.Hkv, p.B);
   auto store8 = [](uint16_t* dst, uint32_t codes, uint32_t sfc, float scale) {
     const uint32_t sf = e4m3x2_to_f16x2(sfc | (sfc << 8));
     uint32_t f[4], o[4];
@@ -293,15 +356,31 @@ __global__ void __launch_bounds__(kWriteThreads)
     }
     *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
   };
-  const int64_t dst = ((int64_t(layer - p.layer0) * p.n_tokens + n) * p.Hkv + h) * kHeadDim + 8 * c;
-  store8(p.k_out + dst, kc, ks, p.k_scale[layer]);
-  store8(p.v_out + dst, vc, vs, p.v_scale[layer]);
+  const int l0 = p.layer0 + int(blockIdx.y) * p.seg;
+  const int l1 = min(l0 + p.seg, p.layer0 + p.n_layers);
+  const int64_t out_layer = int64_t(p.n_tokens) * p.Hkv * kHeadDim;
+  const int64_t out = (n * p.Hkv + h) * kHeadDim + 8 * c;
+#pragma unroll 2
+  for (int i = l0; i < l1; ++i) {
+    if (!((i & 1) ? ok_f : ok_s)) continue;
+    const uint8_t* tile = p.buf[i >> 1] + ((i & 1) ? at_f.tile : at_s.tile);
+    const int t = (i & 1) ? at_f.t : at_s.t;
+    const uint32_t kc = __ldg(reinterpret_cast<const uint32_t*>(tile + t * kTokBytes + 4 * c));
+    const uint32_t vc =
+        __ldg(reinterpret_cast<const uint32_t*>(tile + kTileV + t * kTokBytes + 4 * c));
+    const uint32_t ks = __ldg(tile + kTileKs + 8 * (t & 7) + 2 * blk + (t >> 3));
+    const uint32_t vs =
+        __ldg(tile + kTileVs + 16 * blk + 4 * ((t & 7) >> 1) + 2 * (t >> 3) + (t & 1));
+    const int64_t dst = (i - p.layer0) * out_layer + out;
+    store8(p.k_out + dst, kc, ks, __ldg(p.k_scale + i));
+    store8(p.v_out + dst, vc, vs, __ldg(p.v_scale + i));
+  }
 }
 
-// gk_kv4_decode_step: CTA 0 plans; the CTAs after it write the new tokens.
-// The attention grid waits for this whole grid, so it reads the plan and the
-// written cache; the kernel before this grid must be complete before the
-// cache is written.
+// gk_kv4_decode_step: CTA 0 plans; the CTAs after it write the new tokens, one
+// warp per (layer, 8 tokens, kv head).  The attention grid waits for this whole
+// grid, so it reads the plan and the written cache; the kernel before this grid
+// must be complete before the cache is written.
 struct Kv4PlanWriteParams {
   PlanParams plan;
   Kv4WriteParams write;
@@ -315,13 +394,11 @@ __global__ void __launch_bounds__(kPlanThreads)
     return;
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int64_t per = int64_t(p.write.n_tokens) * p.write.Hkv * 4;  // of one layer's K
-  const int64_t total = per * 2 * p.write.n_layers;
-  const int64_t it = (int64_t(blockIdx.x) - 1) * kPlanThreads + threadIdx.x;
-  if (it >= total) return;
-  const int64_t y = it / per, r = it - y * per, nh = r >> 2, n = nh / p.write.Hkv;
-  write_block(p.write, p.write.layer0 + int(y >> 1), int(n), int(nh - n * p.write.Hkv),
-              int(r & 3), int(y & 1));
+  const int per = (p.write.n_tokens + kWriteTok - 1) / kWriteTok * p.write.Hkv;  // warps a layer
+  const int64_t w = (int64_t(blockIdx.x) - 1) * (kPlanThreads / 32) + (threadIdx.x >> 5);
+  const int i = int(w / per), r = int(w - int64_t(i) * per), tg = r / p.write.Hkv;
+  if (i >= p.write.n_layers) return;
+  write_tokens(p.write, tg, r - tg * p.write.Hkv, p.write.layer0 + i, p.write.layer0 + i + 1);
 }
 
 // =========================================================================
@@ -340,6 +417,11 @@ constexpr int kAttn4Threads = kCons * 32;
 constexpr int kTileLanes = 32 / kStTiles;              // lanes that copy one tile
 constexpr int kTileCopies = kTileBytes / 16 / kTileLanes;  // 16-byte copies of a lane
 static_assert(kTileCopies * kTileLanes * 16 == kTileBytes, "a tile is copied by whole lanes");
+
+template <int kN>
+struct Tiles {
+  static constexpr int value = kN;
+};
 
 struct alignas(128) Kv4Ring {
   uint8_t ring[kStages4][kSt4Bytes];
@@ -512,6 +594,119 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
   const int vstep = (vt & 1) ? -kTokBytes : kTokBytes;
   const uint32_t vsoff = kTileVs + 16 * uint32_t(g >> 1) + 4 * qd;
   const uint32_t vsel = (vt & 1) ? 0x2301u : 0x3210u;  // scales in the order vt, vt ^ 1
+  // One stage, or the first kT tiles of one.
+  auto process = [&](auto tiles) {
+    constexpr int kT = decltype(tiles)::value;
+    const uint32_t st = ring0 + c_slot * kSt4Bytes;
+    const bool edge = tok0 < cd.t_begin || tok0 + kT * kTile > cd.t_end;
+    // ---- S = q' K^T, one MMA row a token.  code * sf is exact in f16.
+    float sc[kT][4];
+#pragma unroll
+    for (int i = 0; i < kT; ++i) {
+      const uint32_t tile = st + i * kTileBytes;
+      const uint2 ka = lds64(tile + koff), kb = lds64(tile + koff + 8 * kTokBytes);
+      const uint32_t sf = e4m3x2_to_f16x2(lds_u16(tile + ksoff));
+      const uint32_t sa = dup_lo(sf), sb = dup_hi(sf);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t a[4], b[4];
+        e2m1x8_to_f16x2x4(h ? ka.y : ka.x, a);
+        e2m1x8_to_f16x2x4(h ? kb.y : kb.x, b);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int j = 2 * h + k;
+          const uint32_t a0 = mul_f16x2(a[2 * k], sa), a2 = mul_f16x2(a[2 * k + 1], sa);
+          const uint32_t a1 = mul_f16x2(b[2 * k], sb), a3 = mul_f16x2(b[2 * k + 1], sb);
+          if (j == 0)
+            mma_f16_first(sc[i], a0, a1, a2, a3, qf[0], qf[1]);
+          else
+            mma_f16(sc[i], a0, a1, a2, a3, qf[2 * j], qf[2 * j + 1]);
+        }
+      }
+    }
+    // ---- online softmax (log2 domain); lane holds heads 2qd (c0,c2), 2qd+1 (c1,c3)
+    if (edge) {
+      // V scales of keys outside the range may be anything, NaN included: 0.
+      // Lane l has token l % 16 of every tile, and two of the four blocks.
+      for (int i = 0; i < kT; ++i) {
+        const int t = lane & 15, tok = tok0 + kTile * i + t;
+        if (tok < cd.t_begin || tok >= cd.t_end) {
+          uint8_t* vs = ws.ring[c_slot] + i * kTileBytes + kTileVs + 4 * ((t & 7) >> 1) +
+                        2 * (t >> 3) + (t & 1) + 32 * (lane >> 4);
+          vs[0] = 0;
+          vs[16] = 0;
+        }
+      }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < kT; ++i) {
+        const int t0 = tok0 + kTile * i + (g ^ (g >> 2)), t1 = t0 + 8;
+        if (t0 < cd.t_begin || t0 >= cd.t_end) sc[i][0] = sc[i][1] = -INFINITY;
+        if (t1 < cd.t_begin || t1 >= cd.t_end) sc[i][2] = sc[i][3] = -INFINITY;
+      }
+    }
+    float lm0 = fmaxf(sc[0][0], sc[0][2]), lm1 = fmaxf(sc[0][1], sc[0][3]);
+#pragma unroll
+    for (int i = 1; i < kT; ++i) {
+      lm0 = fmaxf(lm0, fmaxf(sc[i][0], sc[i][2]));
+      lm1 = fmaxf(lm1, fmaxf(sc[i][1], sc[i][3]));
+    }
+    if (__any_sync(kFull, lm0 > thr0 || lm1 > thr1)) {
+      // move the reference to the true running maximum and rescale what was summed
+      float w0 = lm0, w1 = lm1;
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) {
+        w0 = fmaxf(w0, __shfl_xor_sync(kFull, w0, off));
+        w1 = fmaxf(w1, __shfl_xor_sync(kFull, w1, off));
+      }
+      const float n0 = fmaxf(mr0, w0), n1 = fmaxf(mr1, w1);
+      const float al0 = ex2((mr0 - n0) * si.x), al1 = ex2((mr1 - n1) * si.y);
+      mr0 = n0;
+      mr1 = n1;
+      nb.x = -n0 * si.x;
+      nb.y = -n1 * si.y;
+      thr0 = n0 + kLazyLog2 / si.x;
+      thr1 = n1 + kLazyLog2 / si.y;
+      l0 *= al0;
+      l1 *= al1;
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        o[m][0] *= al0;
+        o[m][2] *= al0;
+        o[m][1] *= al1;
+        o[m][3] *= al1;
+      }
+    }
+    // ---- O += P V; rows (g, g+8) = channels (8g+2m, 8g+2m+1)
+#pragma unroll
+    for (int i = 0; i < kT; ++i) {
+      const uint32_t tile = st + i * kTileBytes;
+      const float2 xa = fma2(make_float2(sc[i][0], sc[i][1]), si, nb);
+      const float2 xb = fma2(make_float2(sc[i][2], sc[i][3]), si, nb);
+      const float p0 = ex2(xa.x), p1 = ex2(xa.y), p2 = ex2(xb.x), p3 = ex2(xb.y);
+      l0 += p0 + p2;
+      l1 += p1 + p3;
+      const uint32_t b0 = movmatrix_trans(f32x2_to_f16x2(p0, p1));
+      const uint32_t b1 = movmatrix_trans(f32x2_to_f16x2(p2, p3));
+      // channels 8g .. 8g+7 (one nibble each) of the lane's four tokens
+      const uint32_t w0 = lds32(tile + voff), w1 = lds32(tile + voff + vstep);
+      const uint32_t w2 = lds32(tile + voff + 8 * kTokBytes);
+      const uint32_t w3 = lds32(tile + voff + 8 * kTokBytes + vstep);
+      uint32_t s01, s23;
+      e4m3x4_to_f16x2x2(prmt(lds32(tile + vsoff), 0u, vsel), s01, s23);
+      // even and odd channels of a token pair, two nibbles a byte
+      uint32_t e01[4], d01[4], e23[4], d23[4];
+      e2m1x8_to_f16x2x4(low_nibbles(w0, w1 << 4), e01);
+      e2m1x8_to_f16x2x4(low_nibbles(w0 >> 4, w1), d01);
+      e2m1x8_to_f16x2x4(low_nibbles(w2, w3 << 4), e23);
+      e2m1x8_to_f16x2x4(low_nibbles(w2 >> 4, w3), d23);
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+        mma_f16(o[m], mul_f16x2(e01[m], s01), mul_f16x2(d01[m], s01), mul_f16x2(e23[m], s23),
+                mul_f16x2(d23[m], s23), b0, b1);
+    }
+  };
+
   for (;;) {
     while (prod - cons < kStages4 && issue_next()) {
     }
@@ -582,114 +777,11 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
       for (int m = 0; m < 4; ++m) o[m][0] = o[m][1] = o[m][2] = o[m][3] = 0.f;
     }
 
-    const uint32_t st = ring0 + c_slot * kSt4Bytes;
-    const bool edge = tok0 < cd.t_begin || tok0 + kSt4Tok > cd.t_end;
-    // ---- S = q' K^T, one MMA row a token.  code * sf is exact in f16.
-    float sc[kStTiles][4];
-#pragma unroll
-    for (int i = 0; i < kStTiles; ++i) {
-      const uint32_t tile = st + i * kTileBytes;
-      const uint2 ka = lds64(tile + koff), kb = lds64(tile + koff + 8 * kTokBytes);
-      const uint32_t sf = e4m3x2_to_f16x2(lds_u16(tile + ksoff));
-      const uint32_t sa = dup_lo(sf), sb = dup_hi(sf);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t a[4], b[4];
-        e2m1x8_to_f16x2x4(h ? ka.y : ka.x, a);
-        e2m1x8_to_f16x2x4(h ? kb.y : kb.x, b);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int j = 2 * h + k;
-          const uint32_t a0 = mul_f16x2(a[2 * k], sa), a2 = mul_f16x2(a[2 * k + 1], sa);
-          const uint32_t a1 = mul_f16x2(b[2 * k], sb), a3 = mul_f16x2(b[2 * k + 1], sb);
-          if (j == 0)
-            mma_f16_first(sc[i], a0, a1, a2, a3, qf[0], qf[1]);
-          else
-            mma_f16(sc[i], a0, a1, a2, a3, qf[2 * j], qf[2 * j + 1]);
-        }
-      }
-    }
-    // ---- online softmax (log2 domain); lane holds heads 2qd (c0,c2), 2qd+1 (c1,c3)
-    if (edge) {
-      // V scales of keys outside the range may be anything, NaN included: 0.
-      // Lane l has token l % 16 of every tile, and two of the four blocks.
-      for (int i = 0; i < kStTiles; ++i) {
-        const int t = lane & 15, tok = tok0 + kTile * i + t;
-        if (tok < cd.t_begin || tok >= cd.t_end) {
-          uint8_t* vs = ws.ring[c_slot] + i * kTileBytes + kTileVs + 4 * ((t & 7) >> 1) +
-                        2 * (t >> 3) + (t & 1) + 32 * (lane >> 4);
-          vs[0] = 0;
-          vs[16] = 0;
-        }
-      }
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < kStTiles; ++i) {
-        const int t0 = tok0 + kTile * i + (g ^ (g >> 2)), t1 = t0 + 8;
-        if (t0 < cd.t_begin || t0 >= cd.t_end) sc[i][0] = sc[i][1] = -INFINITY;
-        if (t1 < cd.t_begin || t1 >= cd.t_end) sc[i][2] = sc[i][3] = -INFINITY;
-      }
-    }
-    float lm0 = fmaxf(sc[0][0], sc[0][2]), lm1 = fmaxf(sc[0][1], sc[0][3]);
-#pragma unroll
-    for (int i = 1; i < kStTiles; ++i) {
-      lm0 = fmaxf(lm0, fmaxf(sc[i][0], sc[i][2]));
-      lm1 = fmaxf(lm1, fmaxf(sc[i][1], sc[i][3]));
-    }
-    if (__any_sync(kFull, lm0 > thr0 || lm1 > thr1)) {
-      // move the reference to the true running maximum and rescale what was summed
-      float w0 = lm0, w1 = lm1;
-#pragma unroll
-      for (int off = 4; off < 32; off <<= 1) {
-        w0 = fmaxf(w0, __shfl_xor_sync(kFull, w0, off));
-        w1 = fmaxf(w1, __shfl_xor_sync(kFull, w1, off));
-      }
-      const float n0 = fmaxf(mr0, w0), n1 = fmaxf(mr1, w1);
-      const float al0 = ex2((mr0 - n0) * si.x), al1 = ex2((mr1 - n1) * si.y);
-      mr0 = n0;
-      mr1 = n1;
-      nb.x = -n0 * si.x;
-      nb.y = -n1 * si.y;
-      thr0 = n0 + kLazyLog2 / si.x;
-      thr1 = n1 + kLazyLog2 / si.y;
-      l0 *= al0;
-      l1 *= al1;
-#pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        o[m][0] *= al0;
-        o[m][2] *= al0;
-        o[m][1] *= al1;
-        o[m][3] *= al1;
-      }
-    }
-    // ---- O += P V; rows (g, g+8) = channels (8g+2m, 8g+2m+1)
-#pragma unroll
-    for (int i = 0; i < kStTiles; ++i) {
-      const uint32_t tile = st + i * kTileBytes;
-      const float2 xa = fma2(make_float2(sc[i][0], sc[i][1]), si, nb);
-      const float2 xb = fma2(make_float2(sc[i][2], sc[i][3]), si, nb);
-      const float p0 = ex2(xa.x), p1 = ex2(xa.y), p2 = ex2(xb.x), p3 = ex2(xb.y);
-      l0 += p0 + p2;
-      l1 += p1 + p3;
-      const uint32_t b0 = movmatrix_trans(f32x2_to_f16x2(p0, p1));
-      const uint32_t b1 = movmatrix_trans(f32x2_to_f16x2(p2, p3));
-      // channels 8g .. 8g+7 (one nibble each) of the lane's four tokens
-      const uint32_t w0 = lds32(tile + voff), w1 = lds32(tile + voff + vstep);
-      const uint32_t w2 = lds32(tile + voff + 8 * kTokBytes);
-      const uint32_t w3 = lds32(tile + voff + 8 * kTokBytes + vstep);
-      uint32_t s01, s23;
-      e4m3x4_to_f16x2x2(prmt(lds32(tile + vsoff), 0u, vsel), s01, s23);
-      // even and odd channels of a token pair, two nibbles a byte
-      uint32_t e01[4], d01[4], e23[4], d23[4];
-      e2m1x8_to_f16x2x4(low_nibbles(w0, w1 << 4), e01);
-      e2m1x8_to_f16x2x4(low_nibbles(w0 >> 4, w1), d01);
-      e2m1x8_to_f16x2x4(low_nibbles(w2, w3 << 4), e23);
-      e2m1x8_to_f16x2x4(low_nibbles(w2 >> 4, w3), d23);
-#pragma unroll
-      for (int m = 0; m < 4; ++m)
-        mma_f16(o[m], mul_f16x2(e01[m], s01), mul_f16x2(d01[m], s01), mul_f16x2(e23[m], s23),
-                mul_f16x2(d23[m], s23), b0, b1);
-    }
+    // a unit's last stage may hold half of its tiles or fewer
+    if (tok0 + kSt4Tok / 2 >= cd.t_end)
+      process(Tiles<kStTiles / 2>());
+    else
+      process(Tiles<kStTiles>());
     __syncwarp();
     ++cons;
     c_slot = c_slot == kStages4 - 1 ? 0 : c_slot + 1;
@@ -790,6 +882,12 @@ static cudaError_t kv4_setup(Kv4Device** out) {
   return cudaSuccess;
 }
 
+// Warps of the write and read kernels for one layer.
+template <typename P>
+static int64_t token_warps(const P& p, int tokens) {
+  return (int64_t(p.n_tokens) + tokens - 1) / tokens * p.Hkv;
+}
+
 cudaError_t launch_kv4_attention(const PlanParams& plan, const AttnParams& p, cudaStream_t st,
                                  const Kv4WriteParams* write) {
   Kv4Device* c = nullptr;
@@ -801,10 +899,11 @@ cudaError_t launch_kv4_attention(const PlanParams& plan, const AttnParams& p, cu
   AttnChain ch = {};
   if (write) {
     pw.write = *write;
-    const int64_t items = int64_t(write->n_tokens) * write->Hkv * 4 * 2 * write->n_layers;
+    const int64_t warps =
+        int64_t(token_warps(*write, kWriteTok)) * write->n_layers;
     ch.plan_func = (const void*)kv4_plan_write_kernel;
     ch.plan_arg = &pw;
-    ch.plan_grid = unsigned(1 + (items + kPlanThreads - 1) / kPlanThreads);
+    ch.plan_grid = unsigned(1 + (warps * 32 + kPlanThreads - 1) / kPlanThreads);
   } else {
     ch.plan_arg = &pw.plan;
   }
@@ -815,19 +914,34 @@ cudaError_t launch_kv4_attention(const PlanParams& plan, const AttnParams& p, cu
   return launch_chain(ch, p, c->sms, st);
 }
 
-cudaError_t launch_kv4_write(const Kv4WriteParams& p, cudaStream_t st) {
-  const int64_t items = int64_t(p.n_tokens) * p.Hkv * 4;
-  kv4_write_kernel<<<dim3(unsigned((items + kWriteThreads - 1) / kWriteThreads),
-                          unsigned(2 * p.n_layers)),
-                     kWriteThreads, 0, st>>>(p);
+// Grid of the write and read kernels: p.seg layers a CTA, as many as leave
+// kTokWaves CTAs per SM, so that a thread's slots, places and rotation serve
+// several layers of a long prompt while a decode step still spreads over the SMs.
+constexpr int kTokWaves = 16;
+
+template <typename P>
+static dim3 token_grid(P& p, int tokens, int sms) {
+  const int64_t x = (token_warps(p, tokens) + kTokWarps - 1) / kTokWarps;
+  const int64_t seg = x * p.n_layers / (int64_t(sms) * kTokWaves);
+  p.seg = int(seg < 1 ? 1 : seg > p.n_layers ? p.n_layers : seg);
+  return dim3(unsigned(x), unsigned((p.n_layers + p.seg - 1) / p.seg));
+}
+
+cudaError_t launch_kv4_write(Kv4WriteParams& p, cudaStream_t st) {
+  Kv4Device* c = nullptr;
+  const cudaError_t e = kv4_setup(&c);
+  if (e != cudaSuccess) return e;
+  const dim3 grid = token_grid(p, kWriteTok, c->sms);
+  kv4_write_kernel<<<grid, kTokThreads, 0, st>>>(p);
   return cudaGetLastError();
 }
 
-cudaError_t launch_kv4_read(const Kv4ReadParams& p, cudaStream_t st) {
-  const int64_t items = int64_t(p.n_tokens) * p.Hkv * 8;
-  kv4_read_kernel<<<dim3(unsigned((items + kWriteThreads - 1) / kWriteThreads),
-                         unsigned(p.n_layers)),
-                    kWriteThreads, 0, st>>>(p);
+cudaError_t launch_kv4_read(Kv4ReadParams& p, cudaStream_t st) {
+  Kv4Device* c = nullptr;
+  const cudaError_t e = kv4_setup(&c);
+  if (e != cudaSuccess) return e;
+  const dim3 grid = token_grid(p, kReadTok, c->sms);
+  kv4_read_kernel<<<grid, kTokThreads, 0, st>>>(p);
   return cudaGetLastError();
 }
 
