@@ -91,17 +91,20 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// Two fp32 -> two E2M1 codes (lo -> low nibble): to nearest, ties to even,
-// saturating to +-6.
-__device__ __forceinline__ uint32_t f32x2_to_e2m1x2(float lo, float hi) {
+// Eight fp32 -> eight E2M1 codes (the first in the low nibble): to nearest,
+// ties to even, saturating to +-6.
+__device__ __forceinline__ uint32_t f32x8_to_e2m1x8(float2 a, float2 b, float2 c, float2 d) {
   uint32_t r;
   asm("{\n"
-      " .reg .b8 d;\n"
-      " cvt.rn.satfinite.e2m1x2.f32 d, %1, %2;\n"
-      " cvt.u32.u8 %0, d;\n"
+      " .reg .b8 a, b, c, d;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
+      " mov.b32 %0, {a, b, c, d};\n"
       "}\n"
       : "=r"(r)
-      : "f"(hi), "f"(lo));
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y), "f"(d.x), "f"(d.y));
   return r;
 }
 
@@ -118,6 +121,34 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
       "}\n"
       : "=f"(r.x), "=f"(r.y)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n"
+      " .reg .b64 a, b;\n"
+      " mov.b64 a, {%2, %3};\n"
+      " mov.b64 b, {%4, %5};\n"
+      " mul.rn.f32x2 a, a, b;\n"
+      " mov.b64 {%0, %1}, a;\n"
+      "}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n"
+      " .reg .b64 a, b;\n"
+      " mov.b64 a, {%2, %3};\n"
+      " mov.b64 b, {%4, %5};\n"
+      " add.rn.f32x2 a, a, b;\n"
+      " mov.b64 {%0, %1}, a;\n"
+      "}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return r;
 }
 
@@ -161,74 +192,78 @@ __device__ __forceinline__ bool token_slot(const P& p, const int32_t* slots, int
   return false;
 }
 
-// x / s, correctly rounded: r = 1 / s correctly rounded, 2^-40 <= s <= 2^40 and
-// |x| < 2^60.  Two corrections by the exact remainder (Markstein): the first
-// leaves a quotient within one step, which the second rounds correctly.  For
-// |x| < 2^-100 the remainder may underflow; such a quotient is far below half
-// of the smallest block scale and only its sign counts.
-__device__ __forceinline__ float div_by(float x, float s, float r) {
-  const float q0 = x * r;
-  const float q1 = fmaf(fmaf(-q0, s, x), r, q0);
-  return fmaf(fmaf(-q1, s, x), r, q1);
-}
-
-// Quantise x[16] / scale: E4M3 code of the block scale and 16 E2M1 codes.
-// exact: exact_reciprocal(scale); rcp: 1 / scale, or 0 outside div_by's range.
-//
-// The codes are those of the exact quotient u / sf.  sf has 4 significant bits
-// and a code border t has 3, so u is a border only if it is t * sf exactly; the
-// quotient is refined by one exact remainder, which gives such a quotient
-// exactly and any other within a 2^-45 part of u / sf before its last rounding,
-// hence on its own side of the border (the nearest u to t * sf differs by more
-// than half a step of t).
-__device__ __forceinline__ uint32_t quantise16(float (&x)[16], float scale, float exact, float rcp,
-                                               uint2& codes) {
-  float a = fabsf(x[0]);
-#pragma unroll
-  for (int e = 1; e < 16; ++e) a = max_nan(a, fabsf(x[e]));
-  if (exact != 0.f) {
-#pragma unroll
-    for (int e = 0; e < 16; ++e) x[e] *= exact;
-    a *= fabsf(exact);
-  } else if (rcp != 0.f && a < 0x1p60f) {
-#pragma unroll
-    for (int e = 0; e < 16; ++e) x[e] = div_by(x[e], scale, rcp);
-    a = fabsf(div_by(a, scale, rcp));  // rounding is monotonic: the largest quotient
-  } else {
-#pragma unroll
-    for (int e = 0; e < 16; ++e) x[e] = __fdiv_rn(x[e], scale);
-    a = __fdiv_rn(a, fabsf(scale));
-  }
-  const uint32_t sfc = f32x2_to_e4m3x2(__fdiv_rn(a, 6.f), 0.f) & 0xffu;
-  const float sf = f16x2_to_f32x2(e4m3x2_to_f16x2(sfc)).x;
-  if (a > 1e30f) {
-    // infinities: any value this large has the saturated code, and stays
-    // finite through the remainder below
-#pragma unroll
-    for (int e = 0; e < 16; ++e) x[e] = fminf(fmaxf(x[e], -1e30f), 1e30f);
-  }
-  const float r = sf > 0.f ? __frcp_rn(sf) : 0.f;
-  uint32_t w[2] = {0u, 0u};
-#pragma unroll
-  for (int e = 0; e < 16; e += 2) {
-    float y[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const float y0 = x[e + k] * r;
-      y[k] = fmaf(fmaf(-y0, sf, x[e + k]), r, y0);
-    }
-    w[e / 8] |= f32x2_to_e2m1x2(y[0], y[1]) << (4 * (e % 8));
-  }
-  codes = make_uint2(w[0], w[1]);
-  return sfc;
-}
-
+// What divides by a layer scale.
 struct LayerScale {
-  float scale, exact, rcp;
+  float scale;
+  float exact;  // exact_reciprocal(scale)
+  float rcp;    // 1 / scale, correctly rounded; 0 outside 2^-40 .. 2^40
 };
 __device__ __forceinline__ LayerScale layer_scale(float s) {
   const float a = fabsf(s);
   return {s, exact_reciprocal(s), a >= 0x1p-40f && a <= 0x1p40f ? __frcp_rn(s) : 0.f};
+}
+
+// x / s, correctly rounded, for |x| < 2^60 and r = LayerScale::rcp: two
+// corrections by the exact remainder (Markstein), of which the first leaves a
+// quotient within one step and the second rounds it correctly.  For |x| <
+// 2^-100 the remainder may underflow; such a quotient is far below half of the
+// smallest block scale and only its sign counts.
+__device__ __forceinline__ float2 div_by(float2 x, float2 ns, float2 r) {  // ns = -s
+  const float2 q0 = mul2(x, r);
+  const float2 q1 = fma2(fma2(q0, ns, x), r, q0);
+  return fma2(fma2(q1, ns, x), r, q1);
+}
+
+// Quantise the 16 values x / scale: E4M3 code of the block scale, E2M1 codes.
+//
+// The codes are those of the exact quotient u / sf, u = x / scale rounded to
+// fp32.  sf has 4 significant bits and a code border t has 3, so u is a border
+// only if it is t * sf exactly; the quotient is refined by one exact remainder,
+// which gives such a quotient exactly and any other within a 2^-45 part of
+// u / sf before its last rounding, hence on its own side of the border (the
+// nearest u to t * sf differs by more than half a step of t).
+__device__ __forceinline__ uint32_t quantise16(float2 (&x)[8], const LayerScale& ls,
+                                               uint2& codes) {
+  float a = max_nan(fabsf(x[0].x), fabsf(x[0].y));
+#pragma unroll
+  for (int e = 1; e < 8; ++e) a = max_nan(a, max_nan(fabsf(x[e].x), fabsf(x[e].y)));
+  // rounding is monotonic: the largest quotient is that of the largest value
+  if (a < 0x1p60f && ls.rcp != 0.f) {
+    const float2 ns = make_float2(-ls.scale, -ls.scale), r = make_float2(ls.rcp, ls.rcp);
+    if (ls.exact != 0.f) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = mul2(x[e], r);
+      a = fabsf(a * ls.rcp);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = div_by(x[e], ns, r);
+      a = fabsf(div_by(make_float2(a, a), ns, r).x);
+    }
+    const float2 six = make_float2(-6.f, -6.f), sixth = make_float2(1.f / 6.f, 1.f / 6.f);
+    a = a < 0x1p60f ? div_by(make_float2(a, a), six, sixth).x : a;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      // infinities: any value this large has the saturated code, and stays
+      // finite through the remainder below
+      x[e].x = fminf(fmaxf(__fdiv_rn(x[e].x, ls.scale), -1e30f), 1e30f);
+      x[e].y = fminf(fmaxf(__fdiv_rn(x[e].y, ls.scale), -1e30f), 1e30f);
+    }
+    a = __fdiv_rn(__fdiv_rn(a, fabsf(ls.scale)), 6.f);
+  }
+  const uint32_t sfc = f32x2_to_e4m3x2(a, 0.f) & 0xffu;
+  const float sf = f16x2_to_f32x2(e4m3x2_to_f16x2(sfc)).x;
+  const float r1 = sf > 0.f ? __frcp_rn(sf) : 0.f;
+  const float2 r = make_float2(r1, r1), nsf = make_float2(-sf, -sf);
+  float2 y[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float2 y0 = mul2(x[e], r);
+    y[e] = fma2(fma2(y0, nsf, x[e]), r, y0);
+  }
+  codes = make_uint2(f32x8_to_e2m1x8(y[0], y[1], y[2], y[3]),
+                     f32x8_to_e2m1x8(y[4], y[5], y[6], y[7]));
+  return sfc;
 }
 
 constexpr int kWriteTok = 8;  // tokens a warp writes at a time: four lanes each
@@ -248,7 +283,7 @@ __device__ __forceinline__ void write_tokens(const Kv4WriteParams& p, int tg, in
   const bool ok_s = token_slot(p, p.slot_swa, n, slot_s);
   const bool any_f = __any_sync(kFull, ok_f), any_s = __any_sync(kFull, ok_s);
   if (!any_f && !any_s) return;
-  float c[16], sn[16];
+  float2 c[8], sn[8];
   const bool rotate = p.cosb != nullptr;
   if (rotate && (ok_f || ok_s)) {
     const int64_t at = n * (kHeadDim / 2) + 16 * (blk & 1);
@@ -257,67 +292,87 @@ __device__ __forceinline__ void write_tokens(const Kv4WriteParams& p, int tg, in
     for (int k = 0; k < 4; ++k) {
       const float4 c4 = __ldg(reinterpret_cast<const float4*>(p.cosb + at) + k);
       const float4 s4 = __ldg(reinterpret_cast<const float4*>(p.sinb + at) + k);
-      c[4 * k] = c4.x, c[4 * k + 1] = c4.y, c[4 * k + 2] = c4.z, c[4 * k + 3] = c4.w;
-      sn[4 * k] = sgn * s4.x, sn[4 * k + 1] = sgn * s4.y;
-      sn[4 * k + 2] = sgn * s4.z, sn[4 * k + 3] = sgn * s4.w;
+      c[2 * k] = make_float2(c4.x, c4.y);
+      c[2 * k + 1] = make_float2(c4.z, c4.w);
+      sn[2 * k] = make_float2(sgn * s4.x, sgn * s4.y);
+      sn[2 * k + 1] = make_float2(sgn * s4.z, sgn * s4.w);
     }
   }
+  const TokenPlace at_f = place_of(max(slot_f, 0), h, p.Hkv, p.B);
+  const TokenPlace at_s = place_of(max(slot_s, 0), h, p.Hkv, p.B);
   const int64_t row = n * p.token_stride + h * kHeadDim + 16 * blk;
-  for (int i = l0; i < l1; ++i) {
-    if (!((i & 1) ? any_f : any_s)) continue;
-    const bool ok = (i & 1) ? ok_f : ok_s;
-    uint4 k0 = make_uint4(0, 0, 0, 0), k1 = k0, v0 = k0, v1 = k0;
-    if (ok) {
+  LayerScale mk = {}, mv = {};  // lane l: of layer lb + l
+  int lb = l0 - 32;
+  // the first layer from i on that some lane writes
+  auto next_layer = [&](int i) { return ((i & 1) ? any_f : any_s) ? i : i + 1; };
+  struct Rows {
+    uint4 k0, k1, v0, v1;
+  };
+  auto load = [&](int i) -> Rows {
+    Rows r = {};
+    if (i < l1 && ((i & 1) ? ok_f : ok_s)) {
       const uint16_t* ks = p.k + int64_t(i - p.layer0) * p.layer_stride + row;
       const uint16_t* vs = p.v + int64_t(i - p.layer0) * p.layer_stride + row;
-      k0 = ldg_nc_v4(ks);
-      k1 = ldg_nc_v4(ks + 8);
-      v0 = ldg_nc_v4(vs);
-      v1 = ldg_nc_v4(vs + 8);
+      r.k0 = ldg_nc_v4(ks);
+      r.k1 = ldg_nc_v4(ks + 8);
+      r.v0 = ldg_nc_v4(vs);
+      r.v1 = ldg_nc_v4(vs + 8);
     }
-    const LayerScale sk = layer_scale(__ldg(p.k_scale + i));
-    const LayerScale sv = layer_scale(__ldg(p.v_scale + i));
-    const uint32_t kw[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
-    const uint32_t vw[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-    float x[16];
+    return r;
+  };
+  int i = next_layer(l0);
+  Rows ahead = load(i);
+  while (i < l1) {
+    const Rows cur = ahead;
+    const int i_next = next_layer(i + 1);
+    ahead = load(i_next);
+    if (i - lb >= 32) {
+      lb = i;
+      if (lb + lane < l1) {
+        mk = layer_scale(__ldg(p.k_scale + lb + lane));
+        mv = layer_scale(__ldg(p.v_scale + lb + lane));
+      }
+    }
+    auto of_layer = [&](const LayerScale& m) -> LayerScale {
+      return {__shfl_sync(kFull, m.scale, i - lb), __shfl_sync(kFull, m.exact, i - lb),
+              __shfl_sync(kFull, m.rcp, i - lb)};
+    };
+    const LayerScale sk = of_layer(mk), sv = of_layer(mv);
+    const uint32_t kw[8] = {cur.k0.x, cur.k0.y, cur.k0.z, cur.k0.w,
+                            cur.k1.x, cur.k1.y, cur.k1.z, cur.k1.w};
+    const uint32_t vw[8] = {cur.v0.x, cur.v0.y, cur.v0.z, cur.v0.w,
+                            cur.v1.x, cur.v1.y, cur.v1.z, cur.v1.w};
+    float2 x[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      x[2 * k] = bf16lo_to_f32(kw[k]);
-      x[2 * k + 1] = bf16hi_to_f32(kw[k]);
-    }
+    for (int k = 0; k < 8; ++k) x[k] = make_float2(bf16lo_to_f32(kw[k]), bf16hi_to_f32(kw[k]));
     if (rotate) {
       // rotate-half, the pair's other half two lanes away: every operation
       // rounded on its own, as in the FP8 append (x - y s = x + y (-s))
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const uint32_t y = __shfl_xor_sync(kFull, kw[k], 2);
-        x[2 * k] = __fadd_rn(__fmul_rn(x[2 * k], c[2 * k]),
-                             __fmul_rn(bf16lo_to_f32(y), sn[2 * k]));
-        x[2 * k + 1] = __fadd_rn(__fmul_rn(x[2 * k + 1], c[2 * k + 1]),
-                                 __fmul_rn(bf16hi_to_f32(y), sn[2 * k + 1]));
+        const uint32_t w = __shfl_xor_sync(kFull, kw[k], 2);
+        x[k] = add2(mul2(x[k], c[k]), mul2(make_float2(bf16lo_to_f32(w), bf16hi_to_f32(w)), sn[k]));
       }
     }
-    if (!ok) continue;
-    const TokenPlace at = place_of((i & 1) ? slot_f : slot_s, h, p.Hkv, p.B);
-    uint8_t* tile = p.buf[i >> 1] + at.tile;
-    const int t = at.t;
-    uint2 codes;
-    uint32_t sf = quantise16(x, sk.scale, sk.exact, sk.rcp, codes);
-    *reinterpret_cast<uint2*>(tile + t * kTokBytes + blk * 8) = codes;
-    tile[kTileKs + 8 * (t & 7) + 2 * blk + (t >> 3)] = uint8_t(sf);
+    if ((i & 1) ? ok_f : ok_s) {
+      uint8_t* tile = p.buf[i >> 1] + ((i & 1) ? at_f.tile : at_s.tile);
+      const int t = (i & 1) ? at_f.t : at_s.t;
+      uint2 codes;
+      uint32_t sf = quantise16(x, sk, codes);
+      *reinterpret_cast<uint2*>(tile + t * kTokBytes + blk * 8) = codes;
+      tile[kTileKs + 8 * (t & 7) + 2 * blk + (t >> 3)] = uint8_t(sf);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      x[2 * k] = bf16lo_to_f32(vw[k]);
-      x[2 * k + 1] = bf16hi_to_f32(vw[k]);
+      for (int k = 0; k < 8; ++k) x[k] = make_float2(bf16lo_to_f32(vw[k]), bf16hi_to_f32(vw[k]));
+      sf = quantise16(x, sv, codes);
+      *reinterpret_cast<uint2*>(tile + kTileV + t * kTokBytes + blk * 8) = codes;
+      tile[kTileVs + 16 * blk + 4 * ((t & 7) >> 1) + 2 * (t >> 3) + (t & 1)] = uint8_t(sf);
     }
-    sf = quantise16(x, sv.scale, sv.exact, sv.rcp, codes);
-    *reinterpret_cast<uint2*>(tile + kTileV + t * kTokBytes + blk * 8) = codes;
-    tile[kTileVs + 16 * blk + 4 * ((t & 7) >> 1) + 2 * (t >> 3) + (t & 1)] = uint8_t(sf);
+    i = i_next;
   }
 }
 
 // grid x: (8 tokens, kv head) a warp; grid y: p.seg layers
-__global__ void __launch_bounds__(kTokThreads)
+__global__ void __launch_bounds__(kTokThreads, 2)
     kv4_write_kernel(const __grid_constant__ Kv4WriteParams p) {
   // the decode-attention planner may launch now (see kv_append_kernel)
   asm volatile("griddepcontrol.launch_dependents;");
