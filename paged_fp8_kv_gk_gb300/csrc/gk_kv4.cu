@@ -159,11 +159,21 @@ __device__ __forceinline__ uint32_t low_nibbles(uint32_t a, uint32_t b) {
   return r;
 }
 
-// max that gives NaN when either is NaN
-__device__ __forceinline__ float max_nan(float a, float b) {
+// max(|a|, |b|, |c|), NaN when one of them is.
+__device__ __forceinline__ float max3_abs_nan(float a, float b, float c) {
   float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
+}
+
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ float2 bf16x2_to_f32x2(uint32_t w) {
+  return make_float2(bf16lo_to_f32(w), bf16hi_to_f32(w));
 }
 
 // =========================================================================
@@ -224,9 +234,9 @@ __device__ __forceinline__ float2 div_by(float2 x, float2 ns, float2 r) {  // ns
 // nearest u to t * sf differs by more than half a step of t).
 __device__ __forceinline__ uint32_t quantise16(float2 (&x)[8], const LayerScale& ls,
                                                uint2& codes) {
-  float a = max_nan(fabsf(x[0].x), fabsf(x[0].y));
+  float a = 0.f;
 #pragma unroll
-  for (int e = 1; e < 8; ++e) a = max_nan(a, max_nan(fabsf(x[e].x), fabsf(x[e].y)));
+  for (int e = 0; e < 8; ++e) a = max3_abs_nan(a, x[e].x, x[e].y);
   // rounding is monotonic: the largest quotient is that of the largest value
   if (a < 0x1p60f && ls.rcp != 0.f) {
     const float2 ns = make_float2(-ls.scale, -ls.scale), r = make_float2(ls.rcp, ls.rcp);
@@ -253,7 +263,7 @@ __device__ __forceinline__ uint32_t quantise16(float2 (&x)[8], const LayerScale&
   }
   const uint32_t sfc = f32x2_to_e4m3x2(a, 0.f) & 0xffu;
   const float sf = f16x2_to_f32x2(e4m3x2_to_f16x2(sfc)).x;
-  const float r1 = sf > 0.f ? __frcp_rn(sf) : 0.f;
+  const float r1 = sf > 0.f ? rcp_approx(sf) : 0.f;  // within 2^-23: enough for the remainder
   const float2 r = make_float2(r1, r1), nsf = make_float2(-sf, -sf);
   float2 y[8];
 #pragma unroll
@@ -283,21 +293,9 @@ __device__ __forceinline__ void write_tokens(const Kv4WriteParams& p, int tg, in
   const bool ok_s = token_slot(p, p.slot_swa, n, slot_s);
   const bool any_f = __any_sync(kFull, ok_f), any_s = __any_sync(kFull, ok_s);
   if (!any_f && !any_s) return;
-  float2 c[8], sn[8];
   const bool rotate = p.cosb != nullptr;
-  if (rotate && (ok_f || ok_s)) {
-    const int64_t at = n * (kHeadDim / 2) + 16 * (blk & 1);
-    const float sgn = blk < 2 ? -1.f : 1.f;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float4 c4 = __ldg(reinterpret_cast<const float4*>(p.cosb + at) + k);
-      const float4 s4 = __ldg(reinterpret_cast<const float4*>(p.sinb + at) + k);
-      c[2 * k] = make_float2(c4.x, c4.y);
-      c[2 * k + 1] = make_float2(c4.z, c4.w);
-      sn[2 * k] = make_float2(sgn * s4.x, sgn * s4.y);
-      sn[2 * k + 1] = make_float2(sgn * s4.z, sgn * s4.w);
-    }
-  }
+  const int64_t rope_at = min(n, int64_t(p.n_tokens) - 1) * (kHeadDim / 2) + 16 * (blk & 1);
+  const uint32_t flip = blk < 2 ? 0x80008000u : 0u;
   const TokenPlace at_f = place_of(max(slot_f, 0), h, p.Hkv, p.B);
   const TokenPlace at_s = place_of(max(slot_s, 0), h, p.Hkv, p.B);
   const int64_t row = n * p.token_stride + h * kHeadDim + 16 * blk;
@@ -305,27 +303,17 @@ __device__ __forceinline__ void write_tokens(const Kv4WriteParams& p, int tg, in
   int lb = l0 - 32;
   // the first layer from i on that some lane writes
   auto next_layer = [&](int i) { return ((i & 1) ? any_f : any_s) ? i : i + 1; };
-  struct Rows {
-    uint4 k0, k1, v0, v1;
-  };
-  auto load = [&](int i) -> Rows {
-    Rows r = {};
-    if (i < l1 && ((i & 1) ? ok_f : ok_s)) {
-      const uint16_t* ks = p.k + int64_t(i - p.layer0) * p.layer_stride + row;
-      const uint16_t* vs = p.v + int64_t(i - p.layer0) * p.layer_stride + row;
-      r.k0 = ldg_nc_v4(ks);
-      r.k1 = ldg_nc_v4(ks + 8);
-      r.v0 = ldg_nc_v4(vs);
-      r.v1 = ldg_nc_v4(vs + 8);
-    }
-    return r;
-  };
   int i = next_layer(l0);
-  Rows ahead = load(i);
   while (i < l1) {
-    const Rows cur = ahead;
-    const int i_next = next_layer(i + 1);
-    ahead = load(i_next);
+    const bool ok = (i & 1) ? ok_f : ok_s;
+    uint4 k0 = make_uint4(0, 0, 0, 0), k1 = k0, v0 = k0, v1 = k0;
+    if (ok) {
+      const int64_t at = int64_t(i - p.layer0) * p.layer_stride + row;
+      k0 = ldg_nc_v4(p.k + at);
+      k1 = ldg_nc_v4(p.k + at + 8);
+      v0 = ldg_nc_v4(p.v + at);
+      v1 = ldg_nc_v4(p.v + at + 8);
+    }
     if (i - lb >= 32) {
       lb = i;
       if (lb + lane < l1) {
@@ -338,23 +326,29 @@ __device__ __forceinline__ void write_tokens(const Kv4WriteParams& p, int tg, in
               __shfl_sync(kFull, m.rcp, i - lb)};
     };
     const LayerScale sk = of_layer(mk), sv = of_layer(mv);
-    const uint32_t kw[8] = {cur.k0.x, cur.k0.y, cur.k0.z, cur.k0.w,
-                            cur.k1.x, cur.k1.y, cur.k1.z, cur.k1.w};
-    const uint32_t vw[8] = {cur.v0.x, cur.v0.y, cur.v0.z, cur.v0.w,
-                            cur.v1.x, cur.v1.y, cur.v1.z, cur.v1.w};
+    const uint32_t kw[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
+    const uint32_t vw[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
     float2 x[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] = make_float2(bf16lo_to_f32(kw[k]), bf16hi_to_f32(kw[k]));
+    for (int k = 0; k < 8; ++k) x[k] = bf16x2_to_f32x2(kw[k]);
     if (rotate) {
       // rotate-half, the pair's other half two lanes away: every operation
-      // rounded on its own, as in the FP8 append (x - y s = x + y (-s))
+      // rounded on its own, as in the FP8 append (x - y s = x + (-y) s).  cos
+      // and sin come from L1 for every layer: 32 registers for them would cost
+      // a third of the resident warps.
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const uint32_t w = __shfl_xor_sync(kFull, kw[k], 2);
-        x[k] = add2(mul2(x[k], c[k]), mul2(make_float2(bf16lo_to_f32(w), bf16hi_to_f32(w)), sn[k]));
+      for (int q = 0; q < 4; ++q) {
+        const float4 c4 = ldg_nc_f4(p.cosb + rope_at + 4 * q);
+        const float4 s4 = ldg_nc_f4(p.sinb + rope_at + 4 * q);
+        const uint32_t y0 = __shfl_xor_sync(kFull, kw[2 * q], 2) ^ flip;
+        const uint32_t y1 = __shfl_xor_sync(kFull, kw[2 * q + 1], 2) ^ flip;
+        x[2 * q] = add2(mul2(x[2 * q], make_float2(c4.x, c4.y)),
+                        mul2(bf16x2_to_f32x2(y0), make_float2(s4.x, s4.y)));
+        x[2 * q + 1] = add2(mul2(x[2 * q + 1], make_float2(c4.z, c4.w)),
+                            mul2(bf16x2_to_f32x2(y1), make_float2(s4.z, s4.w)));
       }
     }
-    if ((i & 1) ? ok_f : ok_s) {
+    if (ok) {
       uint8_t* tile = p.buf[i >> 1] + ((i & 1) ? at_f.tile : at_s.tile);
       const int t = (i & 1) ? at_f.t : at_s.t;
       uint2 codes;
@@ -362,17 +356,17 @@ __device__ __forceinline__ void write_tokens(const Kv4WriteParams& p, int tg, in
       *reinterpret_cast<uint2*>(tile + t * kTokBytes + blk * 8) = codes;
       tile[kTileKs + 8 * (t & 7) + 2 * blk + (t >> 3)] = uint8_t(sf);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) x[k] = make_float2(bf16lo_to_f32(vw[k]), bf16hi_to_f32(vw[k]));
+      for (int k = 0; k < 8; ++k) x[k] = bf16x2_to_f32x2(vw[k]);
       sf = quantise16(x, sv, codes);
       *reinterpret_cast<uint2*>(tile + kTileV + t * kTokBytes + blk * 8) = codes;
       tile[kTileVs + 16 * blk + 4 * ((t & 7) >> 1) + 2 * (t >> 3) + (t & 1)] = uint8_t(sf);
     }
-    i = i_next;
+    i = next_layer(i + 1);
   }
 }
 
 // grid x: (8 tokens, kv head) a warp; grid y: p.seg layers
-__global__ void __launch_bounds__(kTokThreads, 2)
+__global__ void __launch_bounds__(kTokThreads, 3)
     kv4_write_kernel(const __grid_constant__ Kv4WriteParams p) {
   // the decode-attention planner may launch now (see kv_append_kernel)
   asm volatile("griddepcontrol.launch_dependents;");
