@@ -39,6 +39,7 @@ KV4_HEADER = os.path.join(_build.INCLUDE, "gk_kv4.h")
 
 _lock = threading.Lock()
 _lib = None
+_torch_module = None
 
 
 class GkError(RuntimeError):
@@ -170,8 +171,8 @@ class Kv4Cache:
             c.bufs = ctypes.cast(self._arr, ctypes.c_void_p)
         self.c = c
 
-    def check(self, sh: Shape) -> None:
-        """Buffer sizes against the shape (the C ABI cannot see them)."""
+    def check(self, sh: Shape, dev: Optional[int] = None) -> None:
+        """Buffer sizes against the shape, and their device (the C ABI cannot see them)."""
         groups = sh.num_layers // 2
         want = sh.num_blocks * sh.num_kv_heads * (sh.block_size // 16) * GK_KV4_TILE_BYTES
         if self._stacked:
@@ -181,6 +182,9 @@ class Kv4Cache:
         for t in self._keep:
             if t.numel() < want:
                 raise ValueError(f"a cache buffer holds {t.numel()} bytes, the shape needs {want}")
+            if dev is not None and t.get_device() != dev:
+                raise ValueError(f"a cache buffer is on cuda:{t.get_device()}, the current device "
+                                 f"is cuda:{dev}")
 
 
 def infer_k_layout(k, v) -> int:
@@ -221,11 +225,31 @@ def _kv(kv, shape) -> "ctypes._CArgObject":
     return kv.param()
 
 
-def _kv4(kv, shape):
+def _kv4(kv, shape, dev):
     if not isinstance(kv, Kv4Cache):
         kv = Kv4Cache(kv)
-    kv.check(shape)
+    kv.check(shape, dev)
     return kv
+
+
+def _current_device() -> int:
+    return _torch()._C._cuda_getDevice()
+
+
+def _ptr4(t, dtype, name, dev, n, allow_none=False):
+    """_ptr, of a tensor of at least n values that must lie on device `dev` (the current one: the
+    library launches there)."""
+    if t is None and allow_none:
+        return None
+    if hasattr(t, "get_device"):
+        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and t.numel() >= n:
+            return t.data_ptr()
+        if t.is_cuda and t.get_device() != dev:
+            raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is "
+                             f"cuda:{dev}")
+        if t.numel() < n:
+            raise ValueError(f"{name} holds {t.numel()} values, the call needs {n}")
+    return _ptr(t, dtype, name)
 
 
 def declared_functions(header: str = HEADER) -> list:
@@ -238,6 +262,8 @@ def declared_functions(header: str = HEADER) -> list:
 def lib(build_if_needed: bool = True) -> ctypes.CDLL:
     """Load libgk.so (building it with nvcc first if it is missing or stale)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = _build.build() if build_if_needed else _build.LIB_PATH
@@ -315,8 +341,11 @@ def _ptr(t, dtype=None, name="tensor", allow_none=False):
 
 
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr_array(ts: Sequence, name: str):
@@ -326,9 +355,10 @@ def _ptr_array(ts: Sequence, name: str):
 
 def _stream(stream, like=None):
     if stream is None:
-        import torch
-        dev = like.device if like is not None and hasattr(like, "device") else None
-        return torch.cuda.current_stream(dev).cuda_stream
+        torch = _torch()
+        if like is not None and hasattr(like, "get_device"):
+            return torch._C._cuda_getCurrentRawStream(like.get_device())
+        return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -353,7 +383,10 @@ def _sinks(sinks, shape):
 def _as_shape(shape) -> Shape:
     if isinstance(shape, Shape):
         return shape
-    return Shape.make(**shape)
+    try:
+        return Shape(**shape)
+    except TypeError:      # values that are not plain ints
+        return Shape.make(**shape)
 
 
 # --------------------------------------------------------------- entry points
@@ -566,43 +599,73 @@ def new_kv4_cache(shape, device="cuda", stacked: bool = True):
             for _ in range(sh.num_layers // 2)]
 
 
-def _kv4_rows(sh, k, v, names, contiguous):
+def _kv4_rows(sh, k, v, names, dev, contiguous):
     """Checks of a [layers, tokens, kv, 64] bf16 pair; returns (layers, tokens, strides)."""
-    import torch
+    bf16 = _torch().bfloat16
+    H, D = sh.num_kv_heads, sh.head_dim
+    size = k.shape
+    if k.is_contiguous() and v.is_contiguous() and k.dtype is bf16 and v.dtype is bf16 and \
+            k.get_device() == dev == v.get_device() and size == v.shape and len(size) == 4 and \
+            size[2] == H and size[3] == D:
+        return size[0], size[1], (size[1] * H * D, H * D)
     for t, name in zip((k, v), names):
-        if t.dtype != torch.bfloat16:
-            raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
+        if t.dtype != bf16:
+            raise TypeError(f"{name}: expected {bf16}, got {t.dtype}")
         if not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor (no CPU path)")
-        if t.dim() != 4 or t.shape[2:] != (sh.num_kv_heads, sh.head_dim):
-            raise ValueError(f"{name} must be [layers, tokens, {sh.num_kv_heads}, {sh.head_dim}]")
-    if k.shape != v.shape:
-        raise ValueError(f"{names[0]} and {names[1]} differ in shape")
-    D = sh.head_dim
-    for t, name in zip((k, v), names):
-        s = t.stride()
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is "
+                             f"cuda:{dev}")
+        if t.dim() != 4 or t.shape[2:] != (H, D):
+            raise ValueError(f"{name} must be [layers, tokens, {H}, {D}]")
         if contiguous and not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
-        if t.numel() and (s[3] != 1 or (sh.num_kv_heads > 1 and s[2] != D)):
+        if t.numel() and (t.stride(3) != 1 or (H > 1 and t.stride(2) != D)):
             raise ValueError(f"{name}: the heads of a token must be contiguous")
-    n, T = k.shape[:2]
+    if size != v.shape:
+        raise ValueError(f"{names[0]} and {names[1]} differ in shape")
     # the stride of an axis of one is never used
-    sk = tuple(k.stride(a) if k.shape[a] > 1 else 0 for a in (0, 1))
-    sv = tuple(v.stride(a) if v.shape[a] > 1 else 0 for a in (0, 1))
+    sk = tuple(k.stride(a) if size[a] > 1 else 0 for a in (0, 1))
+    sv = tuple(v.stride(a) if size[a] > 1 else 0 for a in (0, 1))
     if sk != sv:
         raise ValueError(f"{names[0]} and {names[1]} must have the same strides")
-    return n, T, sk
+    return size[0], size[1], sk
 
 
-def _kv4_tokens(sh, T, slot_full, slot_swa, active, cos=None, sin=None, scales=()):
-    for t, name, n in ((slot_full, "slot_full", T), (slot_swa, "slot_swa", T),
-                       (active, "active", T), (cos, "cos", T * sh.head_dim // 2),
-                       (sin, "sin", T * sh.head_dim // 2)):
-        if t is not None and t.numel() != n:
-            raise ValueError(f"{name} must hold {n} values for {T} tokens")
-    for t in scales:
-        if t.numel() < sh.num_layers:
-            raise ValueError("the scales hold one value for every layer of the stack")
+def _kv4_step_args(sh, dev, q, k_scale, v_scale, cos, sin, bt_full, bt_swa, pos, pos_w, active,
+                   sinks, out, out_f32, workspace, new=None):
+    """The pointers that gk_kv4_decode_attn_stack and gk_kv4_decode_step share, in three runs: q;
+    the scales and, for the step (new: k_new, v_new, upd_full, upd_swa), the new tokens around
+    them; the control tensors and outputs."""
+    torch = _torch()
+    f32, i32, bf16 = torch.float32, torch.int32, torch.bfloat16
+    NL, Bt = sh.num_layers, sh.batch
+    rope, rows = Bt * sh.head_dim // 2, NL * Bt * sh.num_q_heads * sh.head_dim
+    if workspace is None:
+        raise ValueError("workspace is required (size: gk_attn_workspace_bytes(shape))")
+    scales = [_ptr4(cos, f32, "cos", dev, rope), _ptr4(sin, f32, "sin", dev, rope)]
+    ks = [_ptr4(k_scale, f32, "k_scale", dev, NL), _ptr4(v_scale, f32, "v_scale", dev, NL)]
+    if new is None:
+        head = [_ptr4(q, bf16, "q", dev, rows)]
+        mid = ks + scales
+    else:
+        k_new, v_new, upd_full, upd_swa = new
+        kv = NL * Bt * sh.num_kv_heads * sh.head_dim
+        head = [_ptr4(q, bf16, "q", dev, rows), _ptr4(k_new, bf16, "k_new", dev, kv),
+                _ptr4(v_new, bf16, "v_new", dev, kv)]
+        mid = scales + ks + [_ptr4(upd_full, i32, "upd_full", dev, Bt),
+                             _ptr4(upd_swa, i32, "upd_swa", dev, Bt)]
+    if sinks is not None and sinks.numel() != NL * sh.num_q_heads:
+        raise ValueError(f"sinks must hold num_layers * num_q_heads = "
+                         f"{NL * sh.num_q_heads} values")
+    mid += [_ptr4(bt_full, i32, "bt_full", dev, Bt * sh.max_blocks_full),
+            _ptr4(bt_swa, i32, "bt_swa", dev, Bt * sh.max_blocks_swa),
+            _ptr4(pos, i32, "pos", dev, Bt), _ptr4(pos_w, i32, "pos_w", dev, Bt),
+            _ptr4(active, torch.uint8, "active", dev, Bt),
+            _ptr4(sinks, f32, "sinks", dev, 1, True)]
+    tail = [_ptr4(out, bf16, "out", dev, rows), _ptr4(out_f32, f32, "out_f32", dev, rows, True),
+            _ptr4(workspace, torch.uint8, "workspace", dev, 1), workspace.numel()]
+    return head, mid, tail
 
 
 def gk_kv4_write(shape, k, v, cos, sin, k_scale, v_scale, slot_full, slot_swa, kv, active=None,
@@ -613,19 +676,19 @@ def gk_kv4_write(shape, k, v, cos, sin, k_scale, v_scale, slot_full, slot_swa, k
     contiguous, layers and tokens may have any stride that is a multiple of 8.  cos, sin: fp32
     [n_tokens, 32], or both None for K that is rotated already.  slot_full, slot_swa: int32
     [n_tokens], GK_KV4_SKIP to leave a token out.  kv: a Kv4Cache or its tensors."""
-    import torch
-    sh = _as_shape(shape)
-    n, T, (ls, ts) = _kv4_rows(sh, k, v, ("k", "v"), False)
-    _kv4_tokens(sh, T, slot_full, slot_swa, active, cos, sin, (k_scale, v_scale))
-    kv = _kv4(kv, sh)
+    torch = _torch()
+    f32, i32 = torch.float32, torch.int32
+    sh, dev = _as_shape(shape), _current_device()
+    n, T, (ls, ts) = _kv4_rows(sh, k, v, ("k", "v"), dev, False)
+    kv = _kv4(kv, sh, dev)
+    rope = T * sh.head_dim // 2
     st = lib().gk_kv4_write(
         ctypes.byref(sh), int(layer0), n, T, k.data_ptr(), v.data_ptr(), ls, ts,
-        _ptr(cos, torch.float32, "cos", allow_none=True),
-        _ptr(sin, torch.float32, "sin", allow_none=True),
-        _ptr(k_scale, torch.float32, "k_scale"), _ptr(v_scale, torch.float32, "v_scale"),
-        _ptr(slot_full, torch.int32, "slot_full"), _ptr(slot_swa, torch.int32, "slot_swa"),
-        _ptr(active, torch.uint8, "active", allow_none=True), ctypes.byref(kv.c),
-        _stream(stream, k))
+        _ptr4(cos, f32, "cos", dev, rope, True), _ptr4(sin, f32, "sin", dev, rope, True),
+        _ptr4(k_scale, f32, "k_scale", dev, sh.num_layers),
+        _ptr4(v_scale, f32, "v_scale", dev, sh.num_layers),
+        _ptr4(slot_full, i32, "slot_full", dev, T), _ptr4(slot_swa, i32, "slot_swa", dev, T),
+        _ptr4(active, torch.uint8, "active", dev, T, True), ctypes.byref(kv.c), _stream(stream, k))
     _check(st, "gk_kv4_write")
 
 
@@ -633,16 +696,17 @@ def gk_kv4_read(shape, kv, k_scale, v_scale, slot_full, slot_swa, k_out, v_out, 
                 layer0: int = 0, stream=None) -> None:
     """The values at the given slots of the 4-bit cache, as bf16 [n_layers, n_tokens, kv, 64]
     (contiguous) of layers layer0 ..; the rows of skipped tokens are left as they were."""
-    import torch
-    sh = _as_shape(shape)
-    n, T, _ = _kv4_rows(sh, k_out, v_out, ("k_out", "v_out"), True)
-    _kv4_tokens(sh, T, slot_full, slot_swa, active, scales=(k_scale, v_scale))
-    kv = _kv4(kv, sh)
+    torch = _torch()
+    f32, i32 = torch.float32, torch.int32
+    sh, dev = _as_shape(shape), _current_device()
+    n, T, _ = _kv4_rows(sh, k_out, v_out, ("k_out", "v_out"), dev, True)
+    kv = _kv4(kv, sh, dev)
     st = lib().gk_kv4_read(
         ctypes.byref(sh), int(layer0), n, T, ctypes.byref(kv.c),
-        _ptr(k_scale, torch.float32, "k_scale"), _ptr(v_scale, torch.float32, "v_scale"),
-        _ptr(slot_full, torch.int32, "slot_full"), _ptr(slot_swa, torch.int32, "slot_swa"),
-        _ptr(active, torch.uint8, "active", allow_none=True), k_out.data_ptr(), v_out.data_ptr(),
+        _ptr4(k_scale, f32, "k_scale", dev, sh.num_layers),
+        _ptr4(v_scale, f32, "v_scale", dev, sh.num_layers),
+        _ptr4(slot_full, i32, "slot_full", dev, T), _ptr4(slot_swa, i32, "slot_swa", dev, T),
+        _ptr4(active, torch.uint8, "active", dev, T, True), k_out.data_ptr(), v_out.data_ptr(),
         _stream(stream, k_out))
     _check(st, "gk_kv4_read")
 
@@ -651,20 +715,12 @@ def gk_kv4_decode_attn_stack(shape, q, kv, k_scale, v_scale, cos, sin, bt_full, 
                              pos_w, active, out, out_f32=None, workspace=None, stream=None,
                              sinks=None) -> None:
     """gk_decode_attn_stack over a 4-bit cache (a Kv4Cache or its tensors)."""
-    import torch
-    sh = _as_shape(shape)
-    if workspace is None:
-        raise ValueError("workspace is required (size: gk_attn_workspace_bytes(shape))")
-    kv = _kv4(kv, sh)
-    st = lib().gk_kv4_decode_attn_stack(
-        ctypes.byref(sh), _ptr(q, torch.bfloat16, "q"), ctypes.byref(kv.c),
-        _ptr(k_scale, torch.float32, "k_scale"), _ptr(v_scale, torch.float32, "v_scale"),
-        _ptr(cos, torch.float32, "cos"), _ptr(sin, torch.float32, "sin"),
-        _ptr(bt_full, torch.int32, "bt_full"), _ptr(bt_swa, torch.int32, "bt_swa"),
-        _ptr(pos, torch.int32, "pos"), _ptr(pos_w, torch.int32, "pos_w"),
-        _ptr(active, torch.uint8, "active"), _sinks(sinks, sh), _ptr(out, torch.bfloat16, "out"),
-        _ptr(out_f32, torch.float32, "out_f32", allow_none=True),
-        _ptr(workspace, torch.uint8, "workspace"), int(workspace.numel()), _stream(stream, q))
+    sh, dev = _as_shape(shape), _current_device()
+    head, mid, tail = _kv4_step_args(sh, dev, q, k_scale, v_scale, cos, sin, bt_full, bt_swa, pos,
+                                     pos_w, active, sinks, out, out_f32, workspace)
+    kv = _kv4(kv, sh, dev)
+    st = lib().gk_kv4_decode_attn_stack(ctypes.byref(sh), *head, ctypes.byref(kv.c), *mid, *tail,
+                                        _stream(stream, q))
     _check(st, "gk_kv4_decode_attn_stack")
 
 
@@ -672,22 +728,13 @@ def gk_kv4_decode_step(shape, q, k_new, v_new, cos, sin, k_scale, v_scale, upd_f
                        bt_full, bt_swa, pos, pos_w, active, kv, out, out_f32=None,
                        workspace=None, stream=None, sinks=None) -> None:
     """gk_kv4_write of every row's new token + gk_kv4_decode_attn_stack in two launches."""
-    import torch
-    sh = _as_shape(shape)
-    if workspace is None:
-        raise ValueError("workspace is required (size: gk_attn_workspace_bytes(shape))")
-    kv = _kv4(kv, sh)
-    st = lib().gk_kv4_decode_step(
-        ctypes.byref(sh), _ptr(q, torch.bfloat16, "q"), _ptr(k_new, torch.bfloat16, "k_new"),
-        _ptr(v_new, torch.bfloat16, "v_new"), _ptr(cos, torch.float32, "cos"),
-        _ptr(sin, torch.float32, "sin"), _ptr(k_scale, torch.float32, "k_scale"),
-        _ptr(v_scale, torch.float32, "v_scale"), _ptr(upd_full, torch.int32, "upd_full"),
-        _ptr(upd_swa, torch.int32, "upd_swa"), _ptr(bt_full, torch.int32, "bt_full"),
-        _ptr(bt_swa, torch.int32, "bt_swa"), _ptr(pos, torch.int32, "pos"),
-        _ptr(pos_w, torch.int32, "pos_w"), _ptr(active, torch.uint8, "active"),
-        _sinks(sinks, sh), ctypes.byref(kv.c), _ptr(out, torch.bfloat16, "out"),
-        _ptr(out_f32, torch.float32, "out_f32", allow_none=True),
-        _ptr(workspace, torch.uint8, "workspace"), int(workspace.numel()), _stream(stream, q))
+    sh, dev = _as_shape(shape), _current_device()
+    head, mid, tail = _kv4_step_args(sh, dev, q, k_scale, v_scale, cos, sin, bt_full, bt_swa, pos,
+                                     pos_w, active, sinks, out, out_f32, workspace,
+                                     (k_new, v_new, upd_full, upd_swa))
+    kv = _kv4(kv, sh, dev)
+    st = lib().gk_kv4_decode_step(ctypes.byref(sh), *head, *mid, ctypes.byref(kv.c), *tail,
+                                  _stream(stream, q))
     _check(st, "gk_kv4_decode_step")
 
 

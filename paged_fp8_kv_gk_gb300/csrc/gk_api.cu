@@ -305,6 +305,7 @@ static gk_status decode_attention(const gk_shape* shape, const void* q, const gk
   pl.max_tokens_full = shape->max_blocks_full * shape->block_size;
   pl.max_tokens_swa = shape->max_blocks_swa * shape->block_size;
   pl.force_split_log = force_split_log;
+  pl.short_merge = kShortMerge;
   if (kv4) {
     Kv4WriteParams wp;
     if (app) {

@@ -19,6 +19,7 @@ constexpr int kStageTok = 32;         // tokens per pipeline stage
 constexpr int kStageKBytes = kStageTok * kHeadDim;   // 2 KB of K codes
 constexpr int kStageBytes = 2 * kStageKBytes;        // K + V
 constexpr int kMinSplit = 512;        // smallest split-KV chunk, tokens (power of two)
+constexpr int kShortMerge = 8;        // short_merge of the FP8 step
 constexpr int kMaxSplitsPerRow = 64;  // cap on chunks per (layer, row, kv head)
 constexpr int kPartialFloats = 2 * kGroup + kGroup * kHeadDim;  // m[8], l[8], o[8][64]
 
@@ -91,6 +92,7 @@ struct PlanParams {
   int64_t cap;
   int NL, Bt, Hkv, W, n_warps;
   int max_tokens_full, max_tokens_swa;  // table row lengths in tokens
+  int short_merge;  // most chunks of a row that short chunks may give it
   // test hook: split length kMinSplit << force_split_log (-1: the planner's
   // choice), still raised if a row would need more than kMaxSplitsPerRow
   // chunks or the records would not fit; no last-wave pieces

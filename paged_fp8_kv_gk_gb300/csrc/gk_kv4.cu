@@ -500,6 +500,9 @@ constexpr int kFifo4 = 6;       // unit descriptors in flight per warp (> kStage
 constexpr int kSt4Tok = kStTiles * kTile;
 constexpr uint32_t kSt4Bytes = kStTiles * kTileBytes;
 constexpr int kAttn4Threads = kCons * 32;
+// A warp takes 1.8 us for a stage whatever the others do, so the length of a
+// chunk is the length of the tail: rows may have 16 chunks of 512 keys.
+constexpr int kShortMerge4 = 16;
 constexpr int kTileLanes = 32 / kStTiles;              // lanes that copy one tile
 constexpr int kTileCopies = kTileBytes / 16 / kTileLanes;  // 16-byte copies of a lane
 static_assert(kTileCopies * kTileLanes * 16 == kTileBytes, "a tile is copied by whole lanes");
@@ -982,6 +985,7 @@ cudaError_t launch_kv4_attention(const PlanParams& plan, const AttnParams& p, cu
   Kv4PlanWriteParams pw;
   pw.plan = plan;
   pw.plan.n_warps = c->sms * kCons;
+  pw.plan.short_merge = kShortMerge4;
   AttnChain ch = {};
   if (write) {
     pw.write = *write;

@@ -17,7 +17,7 @@ constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kUnitsPerWarp = 8;   // minimum work units per resident warp
 constexpr int kMinPiece = 512;     // shortest piece cut from a chunk for the last wave
 constexpr int kShortSplit = 1024;  // chunks this short ...
-constexpr int kShortMerge = 8;     // ... are not chosen if a row would need more of them
+                                   // ... are not chosen if a row would need more than short_merge of them
 constexpr int kSplitCands = 22;    // candidate split lengths kMinSplit << k
 constexpr int kRemBuckets = 256;   // remainder size classes for the largest-first order
 
@@ -148,10 +148,10 @@ __device__ __forceinline__ void plan_body(const PlanParams& p) {
     int k = 0;
     while (k < kSplitCands - 1 && ((long long)kMinSplit << k) < share) ++k;
     while (k > 0 && (s_units[k] + NAct) * planes < kUnitsPerWarp * warps) --k;
-    // no short chunks that would give a row more than kShortMerge partials:
+    // no short chunks that would give a row more than short_merge partials:
     // the per-unit cost of the extra partials outweighs the balance they buy
     while (k < kSplitCands - 1 && ((long long)kMinSplit << k) <= kShortSplit &&
-           (Lmax - 1) / ((long long)kMinSplit << k) + 1 > kShortMerge)
+           (Lmax - 1) / ((long long)kMinSplit << k) + 1 > p.short_merge)
       ++k;
     if (p.force_split_log >= 0) k = p.force_split_log;  // test hook: a fixed split length
     while (k < kSplitCands - 1 && ((long long)kMinSplit << k) * kMaxSplitsPerRow < Lmax) ++k;
