@@ -543,54 +543,64 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
   }
 
   // ------------------------------------------------ producer state
-  // The next unit is fetched in steps, one with each stage issued, so that no
-  // step waits for the one before it: the claim when a unit starts, its
-  // descriptor with the second stage, its first table chunk with the third.
-  int u_nx = int(blockIdx.x) * kCons + warp, nx_step = 1;
-  int4 e_nx = make_int4(0, 0, 0, 0);
-  int32_t tbl_nx = 0;
+  // Where a unit's tiles lie is worked out 32 tiles at a time, one a lane, from
+  // table entries loaded a window earlier; a stage then takes its tiles' places
+  // by a shuffle.
+  const int tpb = p.B / kTile;
+  const uint32_t blk_tiles = uint32_t(p.Hkv * tpb);
   auto swa_of = [](int4 e) { return ((e.w >> 30) & 1) != 0; };
-  // lane l: entry l of the table chunk starting at block `base`, of a unit
-  // whose last tile is `last`; 0 past it and for an entry outside the pool
-  auto load_tbl = [&](bool swa, int b, int base, int last) -> int32_t {
-    const int32_t* row = swa ? p.bt_swa + int64_t(b) * p.MBS : p.bt_full + int64_t(b) * p.MBF;
-    const int idx = base + lane;
-    int32_t pb = idx <= fdiv(last * kTile, p.fd_b) ? __ldg(row + idx) : 0;
+  auto row_of = [&](int4 e) -> const int32_t* {
+    return swa_of(e) ? p.bt_swa + int64_t(e.x) * p.MBS : p.bt_full + int64_t(e.x) * p.MBF;
+  };
+  // the block that holds `tile` of the row; 0 from tile `end` on
+  auto load_entry = [&](const int32_t* row, int tile, int end) -> int32_t {
+    return tile < end ? __ldg(row + fdiv(tile * kTile, p.fd_b)) : 0;
+  };
+  // offset of a tile from its kv head's tiles of block 0, in 128 bytes
+  auto place = [&](int32_t pb, int tile) -> uint32_t {
     if (uint32_t(pb) >= uint32_t(p.nb)) {
       set_error(GK_DEVERR_BLOCK);
       pb = 0;
     }
-    return pb;
+    const int off = tile - fdiv(tile * kTile, p.fd_b) * tpb;
+    return (uint32_t(pb) * blk_tiles + uint32_t(off)) * (kTileBytes / 128);
   };
-  auto first_blk = [&](int4 e) { return fdiv(e.y & ~(kTile - 1), p.fd_b); };
+  // The next unit is fetched in steps, one with each stage issued, so that no
+  // step waits for the one before it: the claim when a unit starts, its
+  // descriptor with the second stage, its first table entries with the third.
+  int u_nx = int(blockIdx.x) * kCons + warp, nx_step = 1;
+  int4 e_nx = make_int4(0, 0, 0, 0);
+  int32_t ent_nx = 0;
   auto fetch_next = [&]() {
     if (nx_step == 1) {
       u_nx = __shfl_sync(kFull, u_nx, 0);  // the claim's answer is lane 0's
       if (u_nx < nU) e_nx = __ldcg(p.edesc + fdiv(u_nx, p.fd_planes));
     } else if (u_nx < nU) {
-      tbl_nx = load_tbl(swa_of(e_nx), e_nx.x, first_blk(e_nx), (e_nx.z - 1) / kTile);
+      ent_nx = load_entry(row_of(e_nx), e_nx.y / kTile + lane, (e_nx.z + kTile - 1) / kTile);
     }
     ++nx_step;
   };
-  int prod = 0, cons = 0, p_slot = 0;
+  int avail = 0;        // stages issued and not consumed yet
   int f_head = 0, f_tail = 0;
   bool exhausted = false;
   bool q_free = true;   // the q buffer may take the next unit's q
   int pt = 0, pe = 0;   // the producer unit's next and end tile
-  const uint8_t* src = nullptr;  // its kv head's tiles of block 0, at this lane's bytes
-  int tbl_base = 0, tbl_end = 0;  // the chunk's first block, its end in tiles
-  int32_t tbl = 0;
-  const int tpb = p.B / kTile;
-  const uint32_t blk_bytes = uint32_t(p.Hkv * tpb * kTileBytes);
+  const uint8_t* src = nullptr;   // its kv head's tiles of block 0, at this lane's bytes
+  const int32_t* row = nullptr;   // its table row
+  uint32_t where = 0;             // lane l: place of tile l of the window
+  int w_idx = 0;                  // tiles of the window issued
+  int32_t ent = 0;                // lane l: block of tile l of the next window
   const int my_tile = lane / kTileLanes;  // this lane's tile of a stage
   const uint32_t my_off = uint32_t(lane % kTileLanes) * 16;
+  const uint32_t ring_flip = 2 * ring0 + kSt4Bytes;  // slot a <-> slot b: flip - a
+  static_assert(kStages4 == 2, "two slots");
+  uint32_t p_slot = ring0;        // slot of the next stage to issue
 
   // Copy one stage; lanes 8i .. 8i+7 copy tile i.  A group is committed for
   // every stage.
   auto issue_next = [&]() -> bool {
-    if (exhausted) return false;
-    if (pt == pe) {
-      if (!q_free) return false;  // the consumer has not read the buffered q yet
+    if (pt >= pe) {
+      if (!q_free || exhausted) return false;  // not free: the buffered q is still to be read
       while (nx_step < 3) fetch_next();
       const int u = u_nx;
       if (u >= nU) {
@@ -598,9 +608,6 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
         return false;
       }
       const int4 e = e_nx;
-      tbl = tbl_nx;
-      tbl_base = first_blk(e);
-      tbl_end = (tbl_base + 32) * tpb;
       if (lane == 0) u_nx = atomicAdd(p.queue, 1);
       nx_step = 1;
       const int pl = u - fdiv(u, p.fd_planes) * int(p.fd_planes.d);
@@ -609,6 +616,10 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
       pt = e.y / kTile;
       pe = (e.z + kTile - 1) / kTile;
       src = p.kb[j] + int64_t(kvh) * tpb * kTileBytes + my_off;
+      row = row_of(e);
+      where = place(ent_nx, pt + lane);
+      ent = load_entry(row, pt + 32 + lane, pe);
+      w_idx = 0;
       if (lane == 0) {
         UnitDesc& d = ws.fifo[f_tail];
         d.layer = layer;
@@ -631,30 +642,27 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
       if (lane < 16)
         cp_async16(qbuf0 + kQBytes + 16 * lane,
                    (lane < 8 ? p.cosb : p.sinb) + int64_t(e.x) * (kHeadDim / 2) + 4 * (lane & 7));
-    } else if (nx_step < 3) {
-      fetch_next();
+    } else {
+      if (nx_step < 3) fetch_next();
+      if (w_idx == 32) {
+        where = place(ent, pt + lane);
+        ent = load_entry(row, pt + 32 + lane, pe);
+        w_idx = 0;
+      }
     }
-    if (min(pt + kStTiles, pe) > tbl_end) {
-      const UnitDesc& du = ws.fifo[f_tail == 0 ? kFifo4 - 1 : f_tail - 1];
-      tbl_base = fdiv(pt * kTile, p.fd_b);
-      tbl_end = (tbl_base + 32) * tpb;
-      tbl = load_tbl((du.layer & 1) == 0, du.b, tbl_base, pe - 1);
-    }
-    const int tile = pt + my_tile;
-    const int blk = fdiv(tile * kTile, p.fd_b);
-    const int32_t pb = __shfl_sync(kFull, tbl, blk - tbl_base);  // past the unit's end: not used
-    if (tile < pe) {
-      const uint8_t* s =
-          src + (uint64_t(uint32_t(pb)) * blk_bytes + uint32_t((tile - blk * tpb) * kTileBytes));
-      const uint32_t d = ring0 + p_slot * kSt4Bytes + my_tile * kTileBytes + my_off;
+    const uint32_t at = __shfl_sync(kFull, where, w_idx + my_tile);
+    if (pt + my_tile < pe) {
+      const uint8_t* s = src + uint64_t(at) * 128u;
+      const uint32_t d = p_slot + my_tile * kTileBytes + my_off;
 #pragma unroll
       for (int i = 0; i < kTileCopies; ++i)
         cp_async16(d + i * kTileLanes * 16, s + i * kTileLanes * 16);
     }
     cp_async_commit();
-    pt = min(pt + kStTiles, pe);
-    p_slot = p_slot == kStages4 - 1 ? 0 : p_slot + 1;
-    ++prod;
+    pt += kStTiles;
+    w_idx += kStTiles;
+    p_slot = ring_flip - p_slot;
+    ++avail;
     return true;
   };
 
@@ -664,7 +672,7 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
   } cd = {0, 0};
 #define CU (ws.fifo[f_head])
   int left = 0, tok0 = 0;  // the unit's stages left, first token of the next one
-  int c_slot = 0;
+  uint32_t c_slot = ring0;  // slot of the next stage to consume
   uint32_t qf[8];  // q' in f16
   // as in attn_kernel: scores are x * 2^e_h, si_h = 2^-e_h; mr_h the running
   // reference maximum, which may lag the true one by kLazyLog2
@@ -686,7 +694,7 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
   // One stage, or the first kT tiles of one.
   auto process = [&](auto tiles) {
     constexpr int kT = decltype(tiles)::value;
-    const uint32_t st = ring0 + c_slot * kSt4Bytes;
+    const uint32_t st = c_slot;
     const bool edge = tok0 < cd.t_begin || tok0 + kT * kTile > cd.t_end;
     // ---- S = q' K^T, one MMA row a token.  code * sf is exact in f16.
     float sc[kT][4];
@@ -720,10 +728,10 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
       for (int i = 0; i < kT; ++i) {
         const int t = lane & 15, tok = tok0 + kTile * i + t;
         if (tok < cd.t_begin || tok >= cd.t_end) {
-          uint8_t* vs = ws.ring[c_slot] + i * kTileBytes + kTileVs + 4 * ((t & 7) >> 1) +
-                        2 * (t >> 3) + (t & 1) + 32 * (lane >> 4);
-          vs[0] = 0;
-          vs[16] = 0;
+          const uint32_t vs = st + i * kTileBytes + kTileVs + 4 * ((t & 7) >> 1) + 2 * (t >> 3) +
+                              (t & 1) + 32 * (lane >> 4);
+          sts8(vs, 0);
+          sts8(vs + 16, 0);
         }
       }
       __syncwarp();
@@ -797,11 +805,11 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
   };
 
   for (;;) {
-    while (prod - cons < kStages4 && issue_next()) {
+    while (avail < kStages4 && issue_next()) {
     }
-    if (cons == prod) break;
-    // a group a stage: with the ring full all but the newest ones have landed
-    if (prod - cons == kStages4)
+    if (avail == 0) break;
+    // a group a stage: with the ring full all but the newest one have landed
+    if (avail == kStages4)
       cp_async_wait<kStages4 - 1>();
     else
       cp_async_wait<0>();
@@ -872,8 +880,8 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
     else
       process(Tiles<kStTiles>());
     __syncwarp();
-    ++cons;
-    c_slot = c_slot == kStages4 - 1 ? 0 : c_slot + 1;
+    --avail;
+    c_slot = ring_flip - c_slot;
     tok0 += kSt4Tok;
     if (--left == 0) {
       // ---- unit epilogue
