@@ -534,6 +534,10 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
   // combine grid may launch now (see attn_kernel in gk_kernels.cu)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (p.cap > 0) asm volatile("griddepcontrol.launch_dependents;");
+  // the first unit's descriptor, if there is such a unit, with the header words
+  // (any entry of the list otherwise)
+  int u_nx = int(blockIdx.x) * kCons + warp, nx_step = 2;
+  int4 e_nx = __ldcg(p.edesc + min(int64_t(fdiv(u_nx, p.fd_planes)), 2 * p.Bt + p.cap - 1));
   const int nU = p.hdr[kHdrNUnits];
   // zero-fill units (inactive rows)
   for (int v = int(blockIdx.x) * kCons + warp, n = p.hdr[kHdrNZero]; v < n;
@@ -568,8 +572,6 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
   // The next unit is fetched in steps, one with each stage issued, so that no
   // step waits for the one before it: the claim when a unit starts, its
   // descriptor with the second stage, its first table entries with the third.
-  int u_nx = int(blockIdx.x) * kCons + warp, nx_step = 1;
-  int4 e_nx = make_int4(0, 0, 0, 0);
   int32_t ent_nx = 0;
   auto fetch_next = [&]() {
     if (nx_step == 1) {
@@ -875,7 +877,7 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
     }
 
     // a unit's last stage may hold half of its tiles or fewer
-    if (tok0 + kSt4Tok / 2 >= cd.t_end)
+    if (__builtin_expect(tok0 + kSt4Tok / 2 >= cd.t_end, 0))
       process(Tiles<kStTiles / 2>());
     else
       process(Tiles<kStTiles>());
