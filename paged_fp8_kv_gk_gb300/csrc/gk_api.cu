@@ -328,6 +328,7 @@ static gk_status decode_attention(const gk_shape* shape, const void* q, const gk
       wp.Hkv = shape->num_kv_heads;
       wp.B = shape->block_size;
       wp.nb = shape->num_blocks;
+      wp.fd_b = p.fd_b;
     }
     return launch_kv4_attention(pl, p, static_cast<cudaStream_t>(stream), app ? &wp : nullptr) ==
                    cudaSuccess
@@ -462,6 +463,7 @@ gk_status gk_kv4_write(const gk_shape* shape, int32_t layer0, int32_t n_layers, 
   p.layer0 = layer0;
   p.n_layers = n_layers;
   p.n_tokens = int(n_tokens);
+  p.fd_b = make_fastdiv(uint32_t(shape->block_size));
   p.Hkv = shape->num_kv_heads;
   p.B = shape->block_size;
   p.nb = shape->num_blocks;
@@ -495,6 +497,7 @@ gk_status gk_kv4_read(const gk_shape* shape, int32_t layer0, int32_t n_layers, i
   p.layer0 = layer0;
   p.n_layers = n_layers;
   p.n_tokens = int(n_tokens);
+  p.fd_b = make_fastdiv(uint32_t(shape->block_size));
   p.Hkv = shape->num_kv_heads;
   p.B = shape->block_size;
   p.nb = shape->num_blocks;

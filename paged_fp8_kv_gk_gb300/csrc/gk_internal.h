@@ -161,6 +161,7 @@ struct Kv4WriteParams {
   uint8_t* buf[kMaxGroups];
   int layer0, n_layers, n_tokens, Hkv, B, nb;
   int seg;  // layers a CTA takes (set by the launcher)
+  FastDiv fd_b;
 };
 
 struct Kv4ReadParams {
@@ -174,6 +175,7 @@ struct Kv4ReadParams {
   uint16_t* v_out;
   int layer0, n_layers, n_tokens, Hkv, B, nb;
   int seg;  // layers a CTA takes (set by the launcher)
+  FastDiv fd_b;
 };
 
 // Launchers (gk_kernels.cu).  They return the launch status.

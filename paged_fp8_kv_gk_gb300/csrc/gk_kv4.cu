@@ -185,9 +185,10 @@ struct TokenPlace {
   int64_t tile;
   int t;
 };
-__device__ __forceinline__ TokenPlace place_of(int slot, int h, int Hkv, int B) {
-  const int pb = slot / B, off = slot - pb * B;
-  return {((int64_t(pb) * Hkv + h) * (B / kTile) + off / kTile) * kTileBytes, off % kTile};
+template <typename P>
+__device__ __forceinline__ TokenPlace place_of(const P& p, int slot, int h) {
+  const int pb = fdiv(slot, p.fd_b), off = slot - pb * p.B;
+  return {((int64_t(pb) * p.Hkv + h) * (p.B / kTile) + off / kTile) * kTileBytes, off % kTile};
 }
 
 // Whether token n is written or read in the layers whose slots are `slots`.
@@ -302,8 +303,8 @@ __device__ __forceinline__ void write_tokens(const Kv4WriteParams& p, int tg, in
   const bool rotate = p.cosb != nullptr;
   const int64_t rope_at = min(n, int64_t(p.n_tokens) - 1) * (kHeadDim / 2) + 16 * (blk & 1);
   const uint32_t flip = blk < 2 ? 0x80008000u : 0u;
-  const TokenPlace at_f = place_of(max(slot_f, 0), h, p.Hkv, p.B);
-  const TokenPlace at_s = place_of(max(slot_s, 0), h, p.Hkv, p.B);
+  const TokenPlace at_f = place_of(p, max(slot_f, 0), h);
+  const TokenPlace at_s = place_of(p, max(slot_s, 0), h);
   const int64_t row = n * p.token_stride + h * kHeadDim + 16 * blk;
   LayerScale mk = {}, mv = {};  // lane l: of layer lb + l
   int lb = l0 - 32;
@@ -424,40 +425,49 @@ __global__ void __launch_bounds__(kTokThreads)
   const bool ok_f = token_slot(p, p.slot_full, n, slot_f);
   const bool ok_s = token_slot(p, p.slot_swa, n, slot_s);
   if (!ok_f && !ok_s) return;
-  // byte offsets of the lane's codes and scales, of the full and the window layers
-  const int blk = c >> 1;
-  const TokenPlace at_f = place_of(max(slot_f, 0), h, p.Hkv, p.B);
-  const TokenPlace at_s = place_of(max(slot_s, 0), h, p.Hkv, p.B);
+  // offsets in a group buffer of the lane's K codes (V codes 512 bytes on) and
+  // of its K and V block scales
+  struct Lane {
+    int64_t codes;
+    int ks, vs;  // from the codes
+  };
+  auto lane_of = [&](int slot) -> Lane {
+    const TokenPlace at = place_of(p, max(slot, 0), h);
+    const int t = at.t, blk = c >> 1, codes = t * kTokBytes + 4 * c;
+    return {at.tile + codes, kTileKs + 8 * (t & 7) + 2 * blk + (t >> 3) - codes,
+            kTileVs + 16 * blk + 4 * ((t & 7) >> 1) + 2 * (t >> 3) + (t & 1) - codes};
+  };
+  const Lane full = lane_of(slot_f), win = lane_of(slot_s);
   auto store8 = [](uint16_t* dst, uint32_t codes, uint32_t sfc, float scale) {
     const uint32_t sf = e4m3x2_to_f16x2(sfc | (sfc << 8));
+    const float2 sc = make_float2(scale, scale);
     uint32_t f[4], o[4];
     e2m1x8_to_f16x2x4(codes, f);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       // code * sf has at most 6 significant bits: exact in f16
-      const float2 x = f16x2_to_f32x2(mul_f16x2(f[k], sf));
-      o[k] = f32x2_to_bf16x2(x.x * scale, x.y * scale);
+      const float2 x = mul2(f16x2_to_f32x2(mul_f16x2(f[k], sf)), sc);
+      o[k] = f32x2_to_bf16x2(x.x, x.y);
     }
     *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
   };
   const int l0 = p.layer0 + int(blockIdx.y) * p.seg;
   const int l1 = min(l0 + p.seg, p.layer0 + p.n_layers);
   const int64_t out_layer = int64_t(p.n_tokens) * p.Hkv * kHeadDim;
-  const int64_t out = (n * p.Hkv + h) * kHeadDim + 8 * c;
-#pragma unroll 2
-  for (int i = l0; i < l1; ++i) {
-    if (!((i & 1) ? ok_f : ok_s)) continue;
-    const uint8_t* tile = p.buf[i >> 1] + ((i & 1) ? at_f.tile : at_s.tile);
-    const int t = (i & 1) ? at_f.t : at_s.t;
-    const uint32_t kc = __ldg(reinterpret_cast<const uint32_t*>(tile + t * kTokBytes + 4 * c));
-    const uint32_t vc =
-        __ldg(reinterpret_cast<const uint32_t*>(tile + kTileV + t * kTokBytes + 4 * c));
-    const uint32_t ks = __ldg(tile + kTileKs + 8 * (t & 7) + 2 * blk + (t >> 3));
-    const uint32_t vs =
-        __ldg(tile + kTileVs + 16 * blk + 4 * ((t & 7) >> 1) + 2 * (t >> 3) + (t & 1));
-    const int64_t dst = (i - p.layer0) * out_layer + out;
-    store8(p.k_out + dst, kc, ks, __ldg(p.k_scale + i));
-    store8(p.v_out + dst, vc, vs, __ldg(p.v_scale + i));
+  int64_t dst = ((l0 & ~1) - p.layer0) * out_layer + (n * p.Hkv + h) * kHeadDim + 8 * c;
+  auto read_layer = [&](int i, const uint8_t* codes, const Lane& at, int64_t to) {
+    const uint32_t kc = __ldg(reinterpret_cast<const uint32_t*>(codes));
+    const uint32_t vc = __ldg(reinterpret_cast<const uint32_t*>(codes + kTileV));
+    const uint32_t ks = __ldg(codes + at.ks), vs = __ldg(codes + at.vs);
+    store8(p.k_out + to, kc, ks, __ldg(p.k_scale + i));
+    store8(p.v_out + to, vc, vs, __ldg(p.v_scale + i));
+  };
+  // a group buffer at a time: its window layer, its full layer
+#pragma unroll 1  // 32 registers: full occupancy outweighs two layers' loads at once
+  for (int i = l0 & ~1; i < l1; i += 2, dst += 2 * out_layer) {
+    const uint8_t* buf = p.buf[i >> 1];
+    if (ok_s && i >= l0) read_layer(i, buf + win.codes, win, dst);
+    if (ok_f && i + 1 < l1) read_layer(i + 1, buf + full.codes, full, dst + out_layer);
   }
 }
 
