@@ -691,7 +691,7 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
   float2 si = make_float2(0.f, 0.f), nb = si;
   float mr0 = 0.f, mr1 = 0.f, thr0 = 0.f, thr1 = 0.f, vscale = 0.f;
   float o[4][4];
-  float l0 = 0.f, l1 = 0.f;  // this lane's part of the softmax denominators
+  float2 l01 = make_float2(0.f, 0.f);  // this lane's part of the softmax denominators
   // K rows (g, g + 8) of a tile are its tokens (ktok, ktok + 8); the P that the
   // transpose gives lane qd are then of tokens ktok(2 qd), ktok(2 qd + 1) and
   // those + 8.  ktok(r) = r for r < 4, r ^ 1 above: every quarter of K rows and
@@ -776,8 +776,8 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
       nb.y = -n1 * si.y;
       thr0 = n0 + kLazyLog2 / si.x;
       thr1 = n1 + kLazyLog2 / si.y;
-      l0 *= al0;
-      l1 *= al1;
+      l01.x *= al0;
+      l01.y *= al1;
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
         o[m][0] *= al0;
@@ -793,8 +793,7 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
       const float2 xa = fma2(make_float2(sc[i][0], sc[i][1]), si, nb);
       const float2 xb = fma2(make_float2(sc[i][2], sc[i][3]), si, nb);
       const float p0 = ex2(xa.x), p1 = ex2(xa.y), p2 = ex2(xb.x), p3 = ex2(xb.y);
-      l0 += p0 + p2;
-      l1 += p1 + p3;
+      l01 = add2(l01, add2(make_float2(p0, p1), make_float2(p2, p3)));
       const uint32_t b0 = movmatrix_trans(f32x2_to_f16x2(p0, p1));
       const uint32_t b1 = movmatrix_trans(f32x2_to_f16x2(p2, p3));
       // channels 8g .. 8g+7 (one nibble each) of the lane's four tokens
@@ -881,22 +880,23 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
       vscale = p.v_scale[CU.layer];
       mr0 = mr1 = thr0 = thr1 = -INFINITY;
       nb.x = nb.y = 0.f;
-      l0 = l1 = 0.f;
+      l01 = make_float2(0.f, 0.f);
 #pragma unroll
       for (int m = 0; m < 4; ++m) o[m][0] = o[m][1] = o[m][2] = o[m][3] = 0.f;
     }
 
     // a unit's last stage may hold half of its tiles or fewer
-    if (__builtin_expect(tok0 + kSt4Tok / 2 >= cd.t_end, 0))
-      process(Tiles<kStTiles / 2>());
-    else
+    if (tok0 + kSt4Tok / 2 < cd.t_end)
       process(Tiles<kStTiles>());
+    else
+      process(Tiles<kStTiles / 2>());
     __syncwarp();
     --avail;
     c_slot = ring_flip - c_slot;
     tok0 += kSt4Tok;
     if (--left == 0) {
       // ---- unit epilogue
+      float l0 = l01.x, l1 = l01.y;
 #pragma unroll
       for (int off = 4; off < 32; off <<= 1) {
         l0 += __shfl_xor_sync(kFull, l0, off);
