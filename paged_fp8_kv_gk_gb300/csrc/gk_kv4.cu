@@ -840,29 +840,28 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
       const uint32_t sp = cp + kRopeBytes;
       const uint32_t xw[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
       const uint32_t yw[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
-      uint32_t cw[16], sw[16];
+      float2 cw[8], sw[8];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const uint4 c4 = lds128(cp + 16 * k);
         const uint4 s4 = lds128(sp + 16 * k);
-        cw[4 * k] = c4.x; cw[4 * k + 1] = c4.y; cw[4 * k + 2] = c4.z; cw[4 * k + 3] = c4.w;
-        sw[4 * k] = s4.x; sw[4 * k + 1] = s4.y; sw[4 * k + 2] = s4.z; sw[4 * k + 3] = s4.w;
+        cw[2 * k] = make_float2(__uint_as_float(c4.x), __uint_as_float(c4.y));
+        cw[2 * k + 1] = make_float2(__uint_as_float(c4.z), __uint_as_float(c4.w));
+        sw[2 * k] = make_float2(__uint_as_float(s4.x), __uint_as_float(s4.y));
+        sw[2 * k + 1] = make_float2(__uint_as_float(s4.z), __uint_as_float(s4.w));
       }
       __syncwarp();
       q_free = true;
-      const float sgn = qd < 2 ? -1.f : 1.f;
+      const uint32_t flip = qd < 2 ? 0x80008000u : 0u;
       // logits in log2 units: k_scale / sqrt(D) * log2(e) is folded into q,
       // together with the power-of-two normalisation below
       const float ck = p.k_scale[CU.layer] * (0.125f * 1.4426950408889634f);
-      float r[16];
+      float2 r[8];
       float amax = 0.f;
 #pragma unroll
       for (int w = 0; w < 8; ++w) {
-        const float c0 = __uint_as_float(cw[2 * w]), c1 = __uint_as_float(cw[2 * w + 1]);
-        const float s0 = __uint_as_float(sw[2 * w]), s1 = __uint_as_float(sw[2 * w + 1]);
-        r[2 * w] = bf16lo_to_f32(xw[w]) * c0 + sgn * bf16lo_to_f32(yw[w]) * s0;
-        r[2 * w + 1] = bf16hi_to_f32(xw[w]) * c1 + sgn * bf16hi_to_f32(yw[w]) * s1;
-        amax = fmaxf(amax, fmaxf(fabsf(r[2 * w]), fabsf(r[2 * w + 1])));
+        r[w] = fma2(bf16x2_to_f32x2(xw[w]), cw[w], mul2(bf16x2_to_f32x2(yw[w] ^ flip), sw[w]));
+        amax = fmaxf(amax, fmaxf(fabsf(r[w].x), fabsf(r[w].y)));
       }
       amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2)) * ck;
@@ -873,7 +872,8 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
       const float fck = f * ck;
 #pragma unroll
       for (int w = 0; w < 8; ++w) {
-        qf[w] = f32x2_to_f16x2(r[2 * w] * fck, r[2 * w + 1] * fck);
+        const float2 q = mul2(r[w], make_float2(fck, fck));
+        qf[w] = f32x2_to_f16x2(q.x, q.y);
       }
       si.x = __shfl_sync(kFull, finv, 8 * qd);  // heads 2qd and 2qd+1
       si.y = __shfl_sync(kFull, finv, 8 * qd + 4);
