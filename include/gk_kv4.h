@@ -66,9 +66,9 @@ size_t gk_kv4_block_bytes(const gk_shape *shape);
  *        (or k itself when cos and sin are both NULL: K that is rotated already)
  *   x = k' / k_scale[i], v / v_scale[i]            (fp32 division, RNE)
  *   for each 16 channels: a = max |x|,  sf = E4M3(a / 6),  code = E2M1(x / sf)
- * with both conversions to nearest, ties to even, saturating (448 and 6), and
- * code 0 with x's sign where sf is 0.  A NaN among the 16 makes sf NaN, and the
- * 16 values read back as NaN.
+ * with both conversions to nearest, ties to even, saturating (448 and 6);
+ * codes carry x's sign, zeros too, and are +-0 where sf is 0.  A NaN among the
+ * 16 makes sf NaN, and the 16 values read back as NaN.
  *   k, v         bf16; element (i, n, h, e) at (i - layer0) * layer_stride +
  *                n * token_stride + h * 64 + e.  The strides are in elements,
  *                multiples of 8; k and v 16-byte aligned.  Both take the same
@@ -79,9 +79,9 @@ size_t gk_kv4_block_bytes(const gk_shape *shape);
  *                layers of that kind; any other slot outside the buffer is
  *                skipped and sets GK_DEVERR_SLOT
  *   active       uint8 [n_tokens] or NULL; 0 skips the token in every layer
- * Slots must be distinct among the tokens written by one call; a slot given
- * twice is left holding an unspecified mixture of the two.  No other token's
- * bytes change.  shape->batch and the tables' sizes are checked, not used.
+ * Slots must be distinct among the tokens written by one call (slot_full and
+ * slot_swa name slots of the same group buffers); a slot given twice is left
+ * holding an unspecified mixture of the two.  No other token's bytes change.  shape->batch and the tables' sizes are checked, not used.
  * n_tokens == 0 or n_layers == 0 enqueues nothing.  n_tokens * Hkv <= 2^28.
  */
 gk_status gk_kv4_write(const gk_shape *shape, int32_t layer0, int32_t n_layers, int64_t n_tokens,
@@ -104,9 +104,11 @@ gk_status gk_kv4_read(const gk_shape *shape, int32_t layer0, int32_t n_layers, i
 
 /*
  * gk_kv4_decode_attn_stack -- gk_decode_attn_stack over a 4-bit cache: the
- * same arguments, formulas, results and errors with kv the only difference
- * (k_t, v_t are the values above).  workspace: gk_attn_workspace_bytes /
- * gk_attn_workspace_min_bytes of the shape.
+ * same arguments, formulas and errors with kv the only difference (k_t, v_t are
+ * the values above).  Scores, softmax and sums are fp32; q' and the
+ * probabilities enter the tensor-core products as f16, one rounding each
+ * (2^-11, against 2^-4 and more of a 4-bit K).  workspace:
+ * gk_attn_workspace_bytes / gk_attn_workspace_min_bytes of the shape.
  */
 gk_status gk_kv4_decode_attn_stack(const gk_shape *shape, const void *q, const gk_kv4_cache *kv,
                                    const float *k_scale, const float *v_scale, const float *cos,
@@ -121,7 +123,7 @@ gk_status gk_kv4_decode_attn_stack(const gk_shape *shape, const void *q, const g
  * one new token a row (k_new, v_new [NL, Bt, Hkv, D], slots upd_full and
  * upd_swa) in the planner's launch, then gk_kv4_decode_attn_stack.  Bytes and
  * outputs are those of the two calls.  Inactive rows write nothing and output
- * zeros.
+ * zeros; a row whose slot is GK_KV4_SKIP writes nothing.
  */
 gk_status gk_kv4_decode_step(const gk_shape *shape, const void *q, const void *k_new,
                              const void *v_new, const float *cos, const float *sin,

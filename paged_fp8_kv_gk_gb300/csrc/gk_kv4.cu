@@ -214,15 +214,16 @@ __device__ __forceinline__ LayerScale layer_scale(float s) {
   return {s, exact_reciprocal(s), a >= 0x1p-40f && a <= 0x1p40f ? __frcp_rn(s) : 0.f};
 }
 
-// x / s, correctly rounded, for |x| < 2^60 and r = LayerScale::rcp: two
+// -(x / s), correctly rounded, for |x| < 2^60, nr = -LayerScale::rcp: two
 // corrections by the exact remainder (Markstein), of which the first leaves a
 // quotient within one step and the second rounds it correctly.  For |x| <
 // 2^-100 the remainder may underflow; such a quotient is far below half of the
-// smallest block scale and only its sign counts.
-__device__ __forceinline__ float2 div_by(float2 x, float2 ns, float2 r) {  // ns = -s
-  const float2 q0 = mul2(x, r);
-  const float2 q1 = fma2(fma2(q0, ns, x), r, q0);
-  return fma2(fma2(q1, ns, x), r, q1);
+// smallest block scale and only its sign counts.  Negated, so that a zero
+// quotient comes out of x + q s and q - rem / s with the right sign.
+__device__ __forceinline__ float2 neg_div(float2 x, float2 s, float2 nr) {
+  const float2 q0 = mul2(x, nr);
+  const float2 q1 = fma2(fma2(q0, s, x), nr, q0);
+  return fma2(fma2(q1, s, x), nr, q1);
 }
 
 // Quantise the 16 values x / scale: E4M3 code of the block scale, E2M1 codes.
@@ -238,39 +239,40 @@ __device__ __forceinline__ uint32_t quantise16(float2 (&x)[8], const LayerScale&
   float a = 0.f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) a = max3_abs_nan(a, x[e].x, x[e].y);
+  float2 nu[8];  // -u
   // rounding is monotonic: the largest quotient is that of the largest value
   if (a < 0x1p60f && ls.rcp != 0.f) {
-    const float2 ns = make_float2(-ls.scale, -ls.scale), r = make_float2(ls.rcp, ls.rcp);
+    const float2 s = make_float2(ls.scale, ls.scale), nr = make_float2(-ls.rcp, -ls.rcp);
     if (ls.exact != 0.f) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = mul2(x[e], r);
+      for (int e = 0; e < 8; ++e) nu[e] = mul2(x[e], nr);
       a = fabsf(a * ls.rcp);
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = div_by(x[e], ns, r);
-      a = fabsf(div_by(make_float2(a, a), ns, r).x);
+      for (int e = 0; e < 8; ++e) nu[e] = neg_div(x[e], s, nr);
+      a = fabsf(neg_div(make_float2(a, a), s, nr).x);
     }
-    const float2 six = make_float2(-6.f, -6.f), sixth = make_float2(1.f / 6.f, 1.f / 6.f);
-    a = a < 0x1p60f ? div_by(make_float2(a, a), six, sixth).x : a;
+    const float2 six = make_float2(6.f, 6.f), sixth = make_float2(-1.f / 6.f, -1.f / 6.f);
+    a = a < 0x1p60f ? -neg_div(make_float2(a, a), six, sixth).x : a;
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       // infinities: any value this large has the saturated code, and stays
       // finite through the remainder below
-      x[e].x = fminf(fmaxf(__fdiv_rn(x[e].x, ls.scale), -1e30f), 1e30f);
-      x[e].y = fminf(fmaxf(__fdiv_rn(x[e].y, ls.scale), -1e30f), 1e30f);
+      nu[e].x = fminf(fmaxf(__fdiv_rn(x[e].x, -ls.scale), -1e30f), 1e30f);
+      nu[e].y = fminf(fmaxf(__fdiv_rn(x[e].y, -ls.scale), -1e30f), 1e30f);
     }
     a = __fdiv_rn(__fdiv_rn(a, fabsf(ls.scale)), 6.f);
   }
   const uint32_t sfc = f32x2_to_e4m3x2(a, 0.f) & 0xffu;
   const float sf = f16x2_to_f32x2(e4m3x2_to_f16x2(sfc)).x;
   const float r1 = sf > 0.f ? rcp_approx(sf) : 0.f;  // within 2^-23: enough for the remainder
-  const float2 r = make_float2(r1, r1), nsf = make_float2(-sf, -sf);
+  const float2 nr = make_float2(-r1, -r1), sf2 = make_float2(sf, sf);
   float2 y[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const float2 y0 = mul2(x[e], r);
-    y[e] = fma2(fma2(y0, nsf, x[e]), r, y0);
+    const float2 y0 = mul2(nu[e], nr);
+    y[e] = fma2(fma2(y0, sf2, nu[e]), nr, y0);
   }
   codes = make_uint2(f32x8_to_e2m1x8(y[0], y[1], y[2], y[3]),
                      f32x8_to_e2m1x8(y[4], y[5], y[6], y[7]));

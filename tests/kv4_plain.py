@@ -24,7 +24,7 @@ def quantise(x):
     """fp32 [.., 16 n] (divided by the layer scale) -> (E2M1 codes [.., 16 n], E4M3 scales [.., n]).
     Codes of a block with a NaN are 0 here (any code reads back as NaN there)."""
     x = np.asarray(x, np.float32)
-    blk = x.reshape(*x.shape[:-1], -1, 16)
+    blk = x.reshape(*x.shape[:-1], x.shape[-1] // 16, 16)
     a = np.abs(blk).max(-1)
     nan = np.isnan(a)
     with np.errstate(invalid="ignore", over="ignore"):
@@ -68,7 +68,7 @@ def pack(codes):
 
 
 def unpack(b):
-    return np.stack((b & 15, b >> 4), -1).reshape(*b.shape[:-1], -1)
+    return np.stack((b & 15, b >> 4), -1).reshape(*b.shape[:-1], 2 * b.shape[-1])
 
 
 def write(bufs, sh, k, v, cos, sin, k_scale, v_scale, slot_full, slot_swa, active=None, layer0=0):
@@ -106,12 +106,13 @@ def tokens(buf, slots, Hkv, B, k_scale, v_scale, heads=None):
 def attention(bufs, sh, q, k_scale, v_scale, cos, sin, bt_full, bt_swa, pos, pos_w, active,
               sinks=None, layers=None, rows=None):
     """fp64 [NL, Bt, Hq, D]; q: values of the bf16 input.  layers, rows: the ones to compute (the
-    others are left 0).  Also returns the largest |v| each (layer, row) attends to and its keys."""
+    others are left 0).  Also returns, for each (layer, row), the largest |v| it attends to, its
+    keys, and the largest sum_e |q'_e k_e| / sqrt(D) of its heads and keys."""
     NL, Bt, Hkv, B, W = (sh["num_layers"], sh["batch"], sh["num_kv_heads"], sh["block_size"],
                          sh["window"])
     D, G = sh["head_dim"], sh["num_q_heads"] // Hkv
     out = np.zeros((NL, Bt, Hkv * G, D))
-    vmax, keys = np.zeros((NL, Bt)), np.zeros((NL, Bt))
+    vmax, keys, terms = np.zeros((NL, Bt)), np.zeros((NL, Bt)), np.zeros((NL, Bt))
     for i in (range(NL) if layers is None else layers):
         for b in (range(Bt) if rows is None else rows):
             if not active[b]:
@@ -132,17 +133,22 @@ def attention(bufs, sh, q, k_scale, v_scale, cos, sin, bt_full, bt_swa, pos, pos
                 den = den + np.exp(snk - m)
             out[i, b] = (np.einsum("hgt,thd->hgd", p, v) / den).reshape(-1, D)
             vmax[i, b], keys[i, b] = np.abs(v).max(), len(t)
-    return out, vmax, keys
+            terms[i, b] = np.einsum("hgd,thd->hgt", np.abs(qq), np.abs(k)).max() / np.sqrt(D)
+    return out, vmax, keys, terms
 
 
-def tolerance(vmax, keys):
+def tolerance(vmax, keys, terms):
     """How far the fp32 output may be from the fp64 one, elementwise per (layer, row).
 
-    out = sum p v / sum p with the same rounded p in both sums, so an error d in p moves it by
-    d |v - out| <= 2 d vmax of p's share.  d is a rounding of p to f16 (2^-11; below 2^-14 at most
-    2^-25 absolute, over at most `keys` keys against a sum of at least 1), and the error of the
-    logits: q' as two f16 (2^-22), 64 products summed in fp32 (64 * 2^-24) and ex2 (2^-22), on
-    logits whose absolute products sum to at most 2^6 in log2 units for these inputs: under 2^-11.
-    The fp32 sums over the keys and the combine: keys * 2^-24, far below.  sum: (2^-11 + 2^-11 +
-    2^-25 keys) * 2 vmax."""
-    return (2.0 ** -10 + keys * 2.0 ** -25) * 2 * vmax
+    A logit is sum_e q'_e k_e / sqrt(D).  The kernel rounds q' to f16 (half a step: 2^-11 of each
+    term; q' is normalised so that its largest channel is at least 2^13, and a channel below f16's
+    normal range is off by 2^-25 at most, 2^-38 of that one), rotates q in fp32 and sums 64 products
+    in fp32 (under 2^-17 of the terms together), and exponentiates with ex2 (2^-22) of a score less
+    its reference (fp32: 2^-24 of at most 2^7 where the term still counts).  So p is off by a factor
+    within 1 +- d, d = 1.02 * 2^-11 * terms + 2^-16, and with it
+        out = sum p v / sum p    by    |sum p d (v - out)| / sum p <= 2 d vmax    (to first order).
+    In the numerator p is then rounded to f16: 2^-11 of it, or 2^-25 where p is below 2^-14, against
+    a sum of at least 1 (some key has the reference's score or more): (2^-11 + 2^-25 keys) vmax.
+    The fp32 sums over the keys add 2^-24 keys vmax; the first order above is made safe by 1 + 2 d."""
+    d = 1.02 * 2.0 ** -11 * terms + 2.0 ** -16
+    return vmax * (2 * d * (1 + 2 * d) + 2.0 ** -11 + keys * (2.0 ** -25 + 2.0 ** -24))

@@ -105,6 +105,36 @@ def test_write_bytes(B, Hkv, T, scale):
         assert np.array_equal(got, w), np.argwhere(got != w)[:8].tolist()
 
 
+@pytest.mark.parametrize("scale", [2.0 ** -30, 3e-10, 0.0029, 1.0, 5e9, 1e-30, 2e25, 2.0 ** 100])
+def test_write_extremes(scale):
+    """Values over bf16's whole range, subnormal ones and both zeros among them, and layer scales
+    inside and outside the range of the fast division: bytes as the plain form's."""
+    rng = np.random.default_rng(3)
+    sh = token_shape(NL=2, Hkv=2, B=16, nb=40)
+    T = 300
+    bits = torch.from_numpy(rng.integers(0, 2 ** 15, (2, T, 2, 64)).astype(np.int16))
+    # blocks of one magnitude, of any magnitude, and of a few bits
+    bits[0, ::3] = (bits[0, ::3] & 0x3FF) + torch.from_numpy(
+        rng.integers(0, 31, (T // 3, 2, 1)).astype(np.int16)) * 0x400
+    bits[1, 1::3] &= ~0x1F
+    bits = torch.where((bits & 0x7F80) == 0x7F80, bits & 0x7F00, bits)       # finite
+    x = bits.view(torch.bfloat16) * torch.from_numpy(rng.choice([-1.0, 1.0], bits.shape)).to(
+        torch.bfloat16)
+    x[0, 0] = torch.tensor([0.0, -0.0] * 32, dtype=torch.bfloat16)
+    x = x * (torch.tensor(scale) if 1e-12 < scale < 1e12 else torch.tensor(1.0)).to(torch.bfloat16)
+    x = x.nan_to_num(0.0, 3e38, -3e38).to(torch.bfloat16)
+    slot = rng.permutation(40 * 16)[:T].astype(np.int32)
+    s = np.full(2, scale, np.float32)
+    cache = random_cache(sh, 9)
+    want = [b.copy() for b in flat(cache)]
+    skip = np.full(T, gk.GK_KV4_SKIP, np.int32)
+    for full, swa in ((slot, skip), (skip, slot)):
+        gk.gk_kv4_write(sh, x.cuda(), x.cuda(), None, None, dev(s), dev(s), dev(full), dev(swa), cache)
+        k4.write(want, sh, bf16_np(x), bf16_np(x), None, None, s, s, full, swa)
+        assert np.array_equal(flat(cache)[0], want[0]), np.argwhere(flat(cache)[0] != want[0])[:8]
+    assert gk.gk_read_device_error() == 0
+
+
 def test_write_without_rotation_strides_and_layer_range():
     """K that is rotated already; k and v as slices of a fused projection [n, T, 3 Hkv, 64]; layers
     1 .. 2 of 4 (the two parities, two group buffers); buffers per group."""
@@ -131,21 +161,22 @@ def test_write_without_rotation_strides_and_layer_range():
 
 
 def test_nan_reads_back_as_nan():
+    """A NaN makes the 16 channels of its block NaN and no other."""
     sh = token_shape(Hkv=1, B=16, nb=4)
     k = torch.randn(4, 3, 1, 64).to(torch.bfloat16).cuda()
     v = k.clone()
+    k[1, 0, 0, 63] = float("nan")
     v[2, 1, 0, 20] = float("nan")
-    slot = dev(np.array([0, 17, 40], np.int32))
+    full, swa = dev(np.array([0, 17, 40], np.int32)), dev(np.array([5, 20, 41], np.int32))
     one = torch.ones(4, device="cuda")
     cache = random_cache(sh, 8)
-    gk.gk_kv4_write(sh, k, v, None, None, one, one, slot, slot, cache)
+    gk.gk_kv4_write(sh, k, v, None, None, one, one, full, swa, cache)
     ko, vo = torch.zeros_like(k), torch.zeros_like(k)
-    gk.gk_kv4_read(sh, cache, one, one, slot, slot, ko, vo)
-    nan = torch.zeros_like(vo, dtype=torch.bool)
-    nan[2, 1, 0, 16:32] = True
-    # layers 2 and 3 share slot and buffer here: the later writer's bytes may stand in either
-    assert not torch.isnan(ko).any()
-    assert torch.equal(torch.isnan(vo[:2]), nan[:2])
+    gk.gk_kv4_read(sh, cache, one, one, full, swa, ko, vo)
+    nan_k, nan_v = torch.zeros_like(vo, dtype=torch.bool), torch.zeros_like(vo, dtype=torch.bool)
+    nan_k[1, 0, 0, 48:] = True
+    nan_v[2, 1, 0, 16:32] = True
+    assert torch.equal(torch.isnan(ko), nan_k) and torch.equal(torch.isnan(vo), nan_v)
 
 
 @pytest.mark.parametrize("B,Hkv,T", [(16, 1, 1), (32, 8, 130), (64, 3, 77), (256, 2, 500)])
@@ -256,10 +287,10 @@ class Step:
                             c.bt_swa, c.pos, c.pos_w, c.active, self.sinks, layers, rows)
 
     def check(self, ref=None, out=None, out32=None, layers=None, rows=None):
-        want, vmax, keys = ref or self.reference(layers=layers, rows=rows)
+        want, *size = ref or self.reference(layers=layers, rows=rows)
         sel = np.ix_(range(self.w.num_layers) if layers is None else layers,
                      range(self.w.batch) if rows is None else rows)
-        tol = k4.tolerance(vmax, keys)[sel][..., None, None]
+        tol = k4.tolerance(*size)[sel][..., None, None]
         want = want[sel]
         got = (self.out if out is None else out).double().cpu().numpy()[sel]
         got32 = (self.out32 if out32 is None else out32).double().cpu().numpy()[sel]
@@ -277,6 +308,15 @@ NAMES = ["tiny", "gptoss_small", "ragged_small", "swa_small_peaky", "gk120b_rank
 def test_attention(name, sinks):
     s = Step(gi.get(name), sinks=sinks)
     s.attn()
+    assert gk.gk_read_device_error() == 0
+    s.check()
+
+
+@pytest.mark.parametrize("name", ["max_batch", "max_layers"])
+def test_attention_largest_shapes(name):
+    """8192 rows; 128 layers (64 group buffers)."""
+    s = Step(gi.get(name))
+    s.fused()
     assert gk.gk_read_device_error() == 0
     s.check()
 
@@ -475,9 +515,9 @@ def test_bad_blocks_and_positions_are_reported():
     s.ctl["bt_full"] = dev(bt)
     s.attn()
     assert gk.gk_read_device_error() == gk.GK_DEVERR_BLOCK
-    want, vmax, keys = ref
+    want, *size = ref
     good = [0, 1, 2, 3]
-    lim = k4.tolerance(vmax, keys)[..., None, None]
+    lim = k4.tolerance(*size)[..., None, None]
     d = np.abs(s.out32.double().cpu().numpy() - want)
     assert (d <= lim)[:, good].all() and (d <= lim)[::2].all()
     s.ctl["bt_full"] = dev(s.c.bt_full)
@@ -569,6 +609,49 @@ def test_captured_and_replayed_on_two_streams():
     assert gk.gk_read_device_error() == 0
 
 
+def test_write_attention_read_on_another_stream_and_captured():
+    """The three calls on a stream that is not the current one (`stream=`), then captured together
+    and replayed on new tokens."""
+    s = Step(gi.get("block16_small"))
+    t = s.ctl
+    ko = torch.zeros_like(s.k)
+    vo = torch.zeros_like(s.v)
+    other = torch.cuda.Stream()
+
+    def calls(stream=None):
+        gk.gk_kv4_write(s.sh, s.k, s.v, t["cos"], t["sin"], s.dks, s.dvs, t["upd_full"],
+                        t["upd_swa"], s.cache, active=t["active"], stream=stream)
+        s.attn(stream=stream)
+        gk.gk_kv4_read(s.sh, s.cache, s.dks, s.dvs, t["upd_full"], t["upd_swa"], ko, vo,
+                       active=t["active"], stream=stream)
+
+    def check():
+        assert gk.gk_read_device_error() == 0
+        s.check()
+        bufs = flat(s.cache)
+        for i in range(s.w.num_layers):
+            u = s.c.upd_full if i & 1 else s.c.upd_swa
+            k, v = k4.tokens(bufs[i // 2], u, s.w.num_kv_heads, 16, s.ks[i], s.vs[i])
+            for got, x in ((ko[i], k), (vo[i], v)):
+                d = np.abs(got.double().cpu().numpy() - x)
+                assert (d <= 2.0 ** -8 * np.abs(x) * (1 + 2.0 ** -15)).all()
+
+    torch.cuda.synchronize()
+    calls(other)
+    other.synchronize()
+    check()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        calls()
+    for _ in range(2):
+        s.k.copy_(torch.randn(s.k.shape))
+        s.v.copy_(torch.randn(s.v.shape))
+        s.out.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        check()
+
+
 @pytest.mark.parametrize("fused", [False, True])
 def test_back_to_back_calls_on_one_stream(fused):
     """Alternating inputs with nothing between the calls, one workspace: each call's output is the
@@ -590,7 +673,7 @@ def test_back_to_back_calls_on_one_stream(fused):
         assert torch.equal(o, (a, b)[k % 2].want), k
 
 
-def test_python_refusals():
+def test_python_refusals(monkeypatch):
     sh = token_shape()
     cache = random_cache(sh, 3)
     k = torch.zeros(4, 5, 2, 64, dtype=torch.bfloat16, device="cuda")
@@ -622,5 +705,28 @@ def test_python_refusals():
     refused(gk.GkError, k=x, v=x)
     with pytest.raises(ValueError):
         gk.gk_kv4_read(sh, cache, one, one, i, i, k[:, ::2], k[:, ::2])
+    # every call launches on the current device: tensors of another one are refused
+    s = Step(gi.get("tiny"))
+    monkeypatch.setattr(gk, "_current_device", lambda: 1)
+    refused(ValueError)
+    with pytest.raises(ValueError):
+        gk.gk_kv4_read(sh, cache, one, one, i, i, k, k)
+    for call in (s.attn, s.fused):
+        with pytest.raises(ValueError):
+            call()
+    monkeypatch.undo()
+    # too few values
+    for name in ("cos", "pos", "bt_full", "bt_swa", "upd_swa", "active"):
+        keep = s.ctl[name]
+        s.ctl[name] = keep.reshape(-1)[1:]
+        with pytest.raises(ValueError):
+            s.fused()
+        s.ctl[name] = keep
+    for name in ("q", "out", "k", "dvs"):
+        keep = getattr(s, name)
+        setattr(s, name, keep.reshape(-1)[8:])
+        with pytest.raises(ValueError):
+            s.fused()
+        setattr(s, name, keep)
     torch.cuda.synchronize()
     assert gk.gk_read_device_error() == 0
