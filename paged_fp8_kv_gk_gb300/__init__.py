@@ -166,15 +166,15 @@ class Kv4Cache:
         if self._stacked:
             c.cache = _ptr(bufs, _torch().uint8, "kv")
         else:
-            self._arr = (ctypes.c_void_p * len(self._keep))(
+            arr = (ctypes.c_void_p * len(self._keep))(
                 *[_ptr(t, _torch().uint8, f"kv[{i}]") for i, t in enumerate(self._keep)])
-            c.bufs = ctypes.cast(self._arr, ctypes.c_void_p)
+            c.bufs = ctypes.cast(arr, ctypes.c_void_p)
+            c.pointers = arr      # lives as long as the struct
         self.c = c
 
     def check(self, sh: Shape, dev: Optional[int] = None) -> None:
         """Buffer sizes against the shape, and their device (the C ABI cannot see them)."""
-        groups = sh.num_layers // 2
-        want = sh.num_blocks * sh.num_kv_heads * (sh.block_size // 16) * GK_KV4_TILE_BYTES
+        groups, want = sh.num_layers // 2, _kv4_bytes(sh)
         if self._stacked:
             want *= groups
         elif len(self._keep) < groups:
@@ -225,11 +225,20 @@ def _kv(kv, shape) -> "ctypes._CArgObject":
     return kv.param()
 
 
-def _kv4(kv, shape, dev):
+def _kv4_bytes(sh) -> int:
+    """Bytes of one group buffer."""
+    return sh.num_blocks * sh.num_kv_heads * (sh.block_size // 16) * GK_KV4_TILE_BYTES
+
+
+def _kv4(kv, sh, dev):
+    """The gk_kv4_cache of a Kv4Cache or of its tensors (which the caller holds)."""
+    if hasattr(kv, "data_ptr"):
+        return Kv4CacheC(None, _ptr4(kv, _torch().uint8, "kv", dev,
+                                     sh.num_layers // 2 * _kv4_bytes(sh)))
     if not isinstance(kv, Kv4Cache):
         kv = Kv4Cache(kv)
-    kv.check(shape, dev)
-    return kv
+    kv.check(sh, dev)
+    return kv.c
 
 
 def _current_device() -> int:
@@ -239,11 +248,14 @@ def _current_device() -> int:
 def _ptr4(t, dtype, name, dev, n, allow_none=False):
     """_ptr, of a tensor of at least n values that must lie on device `dev` (the current one: the
     library launches there)."""
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and t.numel() >= n:
+            return t.data_ptr()
+    except AttributeError:      # None or a raw address
+        pass
     if t is None and allow_none:
         return None
     if hasattr(t, "get_device"):
-        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and t.numel() >= n:
-            return t.data_ptr()
         if t.is_cuda and t.get_device() != dev:
             raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is "
                              f"cuda:{dev}")
@@ -688,7 +700,7 @@ def gk_kv4_write(shape, k, v, cos, sin, k_scale, v_scale, slot_full, slot_swa, k
         _ptr4(k_scale, f32, "k_scale", dev, sh.num_layers),
         _ptr4(v_scale, f32, "v_scale", dev, sh.num_layers),
         _ptr4(slot_full, i32, "slot_full", dev, T), _ptr4(slot_swa, i32, "slot_swa", dev, T),
-        _ptr4(active, torch.uint8, "active", dev, T, True), ctypes.byref(kv.c), _stream(stream, k))
+        _ptr4(active, torch.uint8, "active", dev, T, True), ctypes.byref(kv), _stream(stream, k))
     _check(st, "gk_kv4_write")
 
 
@@ -702,7 +714,7 @@ def gk_kv4_read(shape, kv, k_scale, v_scale, slot_full, slot_swa, k_out, v_out, 
     n, T, _ = _kv4_rows(sh, k_out, v_out, ("k_out", "v_out"), dev, True)
     kv = _kv4(kv, sh, dev)
     st = lib().gk_kv4_read(
-        ctypes.byref(sh), int(layer0), n, T, ctypes.byref(kv.c),
+        ctypes.byref(sh), int(layer0), n, T, ctypes.byref(kv),
         _ptr4(k_scale, f32, "k_scale", dev, sh.num_layers),
         _ptr4(v_scale, f32, "v_scale", dev, sh.num_layers),
         _ptr4(slot_full, i32, "slot_full", dev, T), _ptr4(slot_swa, i32, "slot_swa", dev, T),
@@ -719,7 +731,7 @@ def gk_kv4_decode_attn_stack(shape, q, kv, k_scale, v_scale, cos, sin, bt_full, 
     head, mid, tail = _kv4_step_args(sh, dev, q, k_scale, v_scale, cos, sin, bt_full, bt_swa, pos,
                                      pos_w, active, sinks, out, out_f32, workspace)
     kv = _kv4(kv, sh, dev)
-    st = lib().gk_kv4_decode_attn_stack(ctypes.byref(sh), *head, ctypes.byref(kv.c), *mid, *tail,
+    st = lib().gk_kv4_decode_attn_stack(ctypes.byref(sh), *head, ctypes.byref(kv), *mid, *tail,
                                         _stream(stream, q))
     _check(st, "gk_kv4_decode_attn_stack")
 
@@ -733,7 +745,7 @@ def gk_kv4_decode_step(shape, q, k_new, v_new, cos, sin, k_scale, v_scale, upd_f
                                      pos_w, active, sinks, out, out_f32, workspace,
                                      (k_new, v_new, upd_full, upd_swa))
     kv = _kv4(kv, sh, dev)
-    st = lib().gk_kv4_decode_step(ctypes.byref(sh), *head, *mid, ctypes.byref(kv.c), *tail,
+    st = lib().gk_kv4_decode_step(ctypes.byref(sh), *head, *mid, ctypes.byref(kv), *tail,
                                   _stream(stream, q))
     _check(st, "gk_kv4_decode_step")
 

@@ -528,6 +528,7 @@ struct alignas(128) Kv4Ring {
   uint8_t ring[kStages4][kSt4Bytes];
   uint8_t qbuf[kUnitHeadBytes];
   UnitDesc fifo[kFifo4];  // st_begin: first tile; n_st: stages
+  int4 e_nx;              // the next unit's descriptor
 };
 static_assert(sizeof(Kv4Ring) % 128 == 0 && kSt4Bytes % 16 == 0, "16-byte copies");
 constexpr size_t kAttn4Smem = sizeof(Kv4Ring) * kCons;
@@ -549,7 +550,10 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
   // the first unit's descriptor, if there is such a unit, with the header words
   // (any entry of the list otherwise)
   int u_nx = int(blockIdx.x) * kCons + warp, nx_step = 2;
-  int4 e_nx = __ldcg(p.edesc + min(int64_t(fdiv(u_nx, p.fd_planes)), 2 * p.Bt + p.cap - 1));
+  auto copy_desc = [&](int64_t entry) {
+    if (lane == 0) cp_async16(smem_u32(&ws.e_nx), p.edesc + entry);
+  };
+  copy_desc(min(int64_t(fdiv(u_nx, p.fd_planes)), 2 * p.Bt + p.cap - 1));
   const int nU = p.hdr[kHdrNUnits];
   // zero-fill units (inactive rows)
   for (int v = int(blockIdx.x) * kCons + warp, n = p.hdr[kHdrNZero]; v < n;
@@ -582,15 +586,22 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
     return (uint32_t(pb) * blk_tiles + uint32_t(off)) * (kTileBytes / 128);
   };
   // The next unit is fetched in steps, one with each stage issued, so that no
-  // step waits for the one before it: the claim when a unit starts, its
-  // descriptor with the second stage, its first table entries with the third.
+  // step waits for the one before it: the claim when a unit starts; a copy of
+  // its descriptor in the group of the unit's second stage; nothing with the
+  // third; its first table entries with the fourth, which is issued when the
+  // second has been waited for.  `now`: a unit starts before that.
   int32_t ent_nx = 0;
-  auto fetch_next = [&]() {
+  auto fetch_next = [&](bool now) {
     if (nx_step == 1) {
       u_nx = __shfl_sync(kFull, u_nx, 0);  // the claim's answer is lane 0's
-      if (u_nx < nU) e_nx = __ldcg(p.edesc + fdiv(u_nx, p.fd_planes));
-    } else if (u_nx < nU) {
-      ent_nx = load_entry(row_of(e_nx), e_nx.y / kTile + lane, (e_nx.z + kTile - 1) / kTile);
+      if (u_nx < nU) copy_desc(fdiv(u_nx, p.fd_planes));
+    } else if (nx_step == 3 && u_nx < nU) {
+      if (now) {
+        if (lane == 0) cp_async_wait_all();
+        __syncwarp();
+      }
+      const int4 e = ws.e_nx;
+      ent_nx = load_entry(row_of(e), e.y / kTile + lane, (e.z + kTile - 1) / kTile);
     }
     ++nx_step;
   };
@@ -600,7 +611,6 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
   bool q_free = true;   // the q buffer may take the next unit's q
   int pt = 0, pe = 0;   // the producer unit's next and end tile
   const uint8_t* src = nullptr;   // its kv head's tiles of block 0, at this lane's bytes
-  const int32_t* row = nullptr;   // its table row
   uint32_t where = 0;             // lane l: place of tile l of the window
   int w_idx = 0;                  // tiles of the window issued
   int32_t ent = 0;                // lane l: block of tile l of the next window
@@ -615,13 +625,14 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
   auto issue_next = [&]() -> bool {
     if (pt >= pe) {
       if (!q_free || exhausted) return false;  // not free: the buffered q is still to be read
-      while (nx_step < 3) fetch_next();
+      while (nx_step < 4) fetch_next(true);
       const int u = u_nx;
       if (u >= nU) {
         exhausted = true;
         return false;
       }
-      const int4 e = e_nx;
+      const int4 e = ws.e_nx;
+      __syncwarp();
       if (lane == 0) u_nx = atomicAdd(p.queue, 1);
       nx_step = 1;
       const int pl = u - fdiv(u, p.fd_planes) * int(p.fd_planes.d);
@@ -630,9 +641,8 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
       pt = e.y / kTile;
       pe = (e.z + kTile - 1) / kTile;
       src = p.kb[j] + int64_t(kvh) * tpb * kTileBytes + my_off;
-      row = row_of(e);
       where = place(ent_nx, pt + lane);
-      ent = load_entry(row, pt + 32 + lane, pe);
+      ent = load_entry(row_of(e), pt + 32 + lane, pe);
       w_idx = 0;
       if (lane == 0) {
         UnitDesc& d = ws.fifo[f_tail];
@@ -657,10 +667,13 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
         cp_async16(qbuf0 + kQBytes + 16 * lane,
                    (lane < 8 ? p.cosb : p.sinb) + int64_t(e.x) * (kHeadDim / 2) + 4 * (lane & 7));
     } else {
-      if (nx_step < 3) fetch_next();
+      if (nx_step < 4) fetch_next(false);
       if (w_idx == 32) {
         where = place(ent, pt + lane);
-        ent = load_entry(row, pt + 32 + lane, pe);
+        const UnitDesc& du = ws.fifo[f_tail == 0 ? kFifo4 - 1 : f_tail - 1];
+        ent = load_entry((du.layer & 1) ? p.bt_full + int64_t(du.b) * p.MBF
+                                        : p.bt_swa + int64_t(du.b) * p.MBS,
+                         pt + 32 + lane, pe);
         w_idx = 0;
       }
     }
@@ -688,10 +701,9 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
   int left = 0, tok0 = 0;  // the unit's stages left, first token of the next one
   uint32_t c_slot = ring0;  // slot of the next stage to consume
   uint32_t qf[8];  // q' in f16
-  // as in attn_kernel: scores are x * 2^e_h, si_h = 2^-e_h; mr_h the running
-  // reference maximum, which may lag the true one by kLazyLog2
+  // scores are x * 2^e_h (x in log2 units), si_h = 2^-e_h; nb_h is minus the
+  // running reference maximum of x, which may lag the true one by kLazyLog2
   float2 si = make_float2(0.f, 0.f), nb = si;
-  float mr0 = 0.f, mr1 = 0.f, thr0 = 0.f, thr1 = 0.f, vscale = 0.f;
   float o[4][4];
   float2 l01 = make_float2(0.f, 0.f);  // this lane's part of the softmax denominators
   // K rows (g, g + 8) of a tile are its tokens (ktok, ktok + 8); the P that the
@@ -762,7 +774,8 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
       lm0 = fmaxf(lm0, fmaxf(sc[i][0], sc[i][2]));
       lm1 = fmaxf(lm1, fmaxf(sc[i][1], sc[i][3]));
     }
-    if (__any_sync(kFull, lm0 > thr0 || lm1 > thr1)) {
+    const float2 lx = fma2(make_float2(lm0, lm1), si, nb);  // over the reference
+    if (__any_sync(kFull, !(lx.x <= kLazyLog2 && lx.y <= kLazyLog2))) {
       // move the reference to the true running maximum and rescale what was summed
       float w0 = lm0, w1 = lm1;
 #pragma unroll
@@ -770,14 +783,11 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
         w0 = fmaxf(w0, __shfl_xor_sync(kFull, w0, off));
         w1 = fmaxf(w1, __shfl_xor_sync(kFull, w1, off));
       }
-      const float n0 = fmaxf(mr0, w0), n1 = fmaxf(mr1, w1);
-      const float al0 = ex2((mr0 - n0) * si.x), al1 = ex2((mr1 - n1) * si.y);
-      mr0 = n0;
-      mr1 = n1;
-      nb.x = -n0 * si.x;
-      nb.y = -n1 * si.y;
-      thr0 = n0 + kLazyLog2 / si.x;
-      thr1 = n1 + kLazyLog2 / si.y;
+      // nb is minus the reference in log2 units (si is a power of two)
+      const float n0 = fminf(nb.x, -w0 * si.x), n1 = fminf(nb.y, -w1 * si.y);
+      const float al0 = ex2(n0 - nb.x), al1 = ex2(n1 - nb.y);
+      nb.x = n0;
+      nb.y = n1;
       l01.x *= al0;
       l01.y *= al1;
 #pragma unroll
@@ -879,9 +889,7 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
       }
       si.x = __shfl_sync(kFull, finv, 8 * qd);  // heads 2qd and 2qd+1
       si.y = __shfl_sync(kFull, finv, 8 * qd + 4);
-      vscale = p.v_scale[CU.layer];
-      mr0 = mr1 = thr0 = thr1 = -INFINITY;
-      nb.x = nb.y = 0.f;
+      nb.x = nb.y = INFINITY;
       l01 = make_float2(0.f, 0.f);
 #pragma unroll
       for (int m = 0; m < 4; ++m) o[m][0] = o[m][1] = o[m][2] = o[m][3] = 0.f;
@@ -910,8 +918,9 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
             8 * g;
         const float* snk =
             p.sinks ? p.sinks + int64_t(CU.layer) * p.Hq + CU.kvh * kGroup + 2 * qd : nullptr;
-        const float i0 = out_scale(l0, mr0 * si.x, snk, vscale);
-        const float i1 = out_scale(l1, mr1 * si.y, snk ? snk + 1 : nullptr, vscale);
+        const float vscale = __ldg(p.v_scale + CU.layer);
+        const float i0 = out_scale(l0, -nb.x, snk, vscale);
+        const float i1 = out_scale(l1, -nb.y, snk ? snk + 1 : nullptr, vscale);
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
           o[m][0] *= i0;
@@ -943,8 +952,8 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
         const int64_t plane = int64_t(CU.layer >> 1) * p.Hkv + CU.kvh;
         float* rec = p.partials + (plane * p.cap + p.part_base[CU.b] + CU.s) * kPartialFloats;
         if (g == 0) {
-          rec[2 * qd] = mr0 * si.x;  // log2 units
-          rec[2 * qd + 1] = mr1 * si.y;
+          rec[2 * qd] = -nb.x;  // log2 units
+          rec[2 * qd + 1] = -nb.y;
           rec[kGroup + 2 * qd] = l0;
           rec[kGroup + 2 * qd + 1] = l1;
         }
