@@ -81,7 +81,8 @@ size_t gk_kv4_block_bytes(const gk_shape *shape);
  *   active       uint8 [n_tokens] or NULL; 0 skips the token in every layer
  * Slots must be distinct among the tokens written by one call (slot_full and
  * slot_swa name slots of the same group buffers); a slot given twice is left
- * holding an unspecified mixture of the two.  No other token's bytes change.  shape->batch and the tables' sizes are checked, not used.
+ * holding an unspecified mixture of the two.  No other token's bytes change.
+ * shape->batch and the tables' sizes are checked, not used.
  * n_tokens == 0 or n_layers == 0 enqueues nothing.  n_tokens * Hkv <= 2^28.
  */
 gk_status gk_kv4_write(const gk_shape *shape, int32_t layer0, int32_t n_layers, int64_t n_tokens,

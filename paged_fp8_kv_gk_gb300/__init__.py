@@ -10,9 +10,10 @@ The functions carry the C names: ``gk_kv_append``, ``gk_decode_attn_stack``,
 ``gk_attn_workspace_bytes``, ``gk_attn_workspace_min_bytes``,
 ``gk_e4m3_quantize``, ``gk_kv_budget``, ``gk_kv_regions``, ``gk_kv_ingest``,
 ``gk_di_blocks``, ``gk_read_device_error``, ``gk_status_str``, ``gk_abi_version``; and, over a
-4-bit cache (``include/gk_kv4.h``), ``gk_kv4_write``, ``gk_kv4_read``,
-``gk_kv4_decode_attn_stack``, ``gk_kv4_decode_step``, ``gk_kv4_block_bytes``.  Tensors are torch tensors; the stream defaults to torch's
-current stream on the tensors' device.  The cache is a ``KvCache``: per-group
+4-bit cache (``include/gk_kv4.h``; a ``Kv4Cache`` or its tensors, ``new_kv4_cache``),
+``gk_kv4_write``, ``gk_kv4_read``, ``gk_kv4_decode_attn_stack``, ``gk_kv4_decode_step``,
+``gk_kv4_block_bytes``.  Tensors are torch tensors; the stream defaults to torch's current stream
+on the tensors' device.  The cache is a ``KvCache``: per-group
 K and V buffers or stacked ``K_cache`` / ``V_cache``, exactly one of the two,
 with packed-ness read from the K tensors' rank as the "GPT-OSS-120B giga-kernel
 decode" page describes (section "KV-cache layout": ``k.dim() == v.dim() + 1``).

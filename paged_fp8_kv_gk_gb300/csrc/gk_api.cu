@@ -442,8 +442,8 @@ gk_status gk_kv4_write(const gk_shape* shape, int32_t layer0, int32_t n_layers, 
   if (st != GK_OK) return st;
   if (n_layers == 0 || n_tokens == 0) return GK_OK;
   if (!k || !v || !k_scale || !v_scale || !slot_full || !slot_swa || !aligned16(k) ||
-      !aligned16(v) || (layer_stride & 7) || (token_stride & 7) || (cos != nullptr) != (sin != nullptr) ||
-      !aligned16(cos) || !aligned16(sin))
+      !aligned16(v) || (layer_stride & 7) || (token_stride & 7) ||
+      (cos != nullptr) != (sin != nullptr) || !aligned16(cos) || !aligned16(sin))
     return GK_ERR_INVALID_ARG;
   Kv4WriteParams p;
   memset(&p, 0, sizeof(p));

@@ -8,6 +8,10 @@
 //   kv4_attn_kernel        persistent decode attention over 4-bit tiles: the
 //                          same units, split-KV partials and combine as the
 //                          FP8 kernel's, another stage loop.
+//
+// A token of one kv head takes 72 bytes: 2 x 32 of codes, 2 x 4 of block scales.
+// Rates below are bytes read and written once over time, next to 6783 GB/s, the
+// measured rate of a copy.
 #include <cuda_runtime.h>
 
 #include "gk_attn_common.cuh"
@@ -75,7 +79,7 @@ __device__ __forceinline__ uint32_t dup_hi(uint32_t a) {
   return r;
 }
 
-// D(16x8, f32) = A(16x16, f16, row) * B(16x8, f16, col)
+// D(16x8, f32) = A(16x16, f16, row) * B(16x8, f16, col): mma_f16 from zero
 __device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                               uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -285,12 +289,18 @@ constexpr int kTokThreads = 256;
 constexpr int kTokWarps = kTokThreads / 32;
 
 // One warp writes the 8 tokens from 8 tg and kv head h, layers [l0, l1).  Lane
-// (n, blk) has 16 channels of K and of V; its slots and its place in the tiles
-// serve every layer.  The rows come through a ring of kDepth layers in shared
-// memory (`ring`, kRowBytes each), so that the loads of the next layers are in
-// flight without holding registers: the arithmetic needs 80, and 24 warps per
-// SM hide more than 16 with the rows in registers do (121 against 137 us for
-// 8191 tokens of 36 layers, before the ring).
+// (n, blk) has 16 channels of K and of V, one block scale each; its slots and
+// its place in the tiles serve every layer.  The rows come through a ring of
+// kDepth layers in shared memory (`ring`, kRowBytes each), so that the next
+// layer's loads are in flight without holding registers.
+//
+// Bound by issue slots and the arithmetic's latency: about 500 instructions for
+// 8 tokens' K and V, two thirds of them the two exact divisions.  For 8191
+// tokens of 36 layers (387 MB; window layers keep 128 tokens), in us: one
+// thread a block with divisions as the compiler writes them 240; several layers
+// a thread and packed fp32 arithmetic 152; the next layer's rows in registers
+// (128 of them, 16 warps per SM) 137; 80 registers and 24 warps 118; the ring 106
+// (64 registers and 32 warps 119; K and V in different warps 122).
 constexpr int kRowBytes = 2 * kWriteTok * kHeadDim * 2;  // K rows, V rows
 template <int kDepth>
 __device__ __forceinline__ void write_tokens(const Kv4WriteParams& p, int tg, int h, int l0,
@@ -399,7 +409,7 @@ __device__ __forceinline__ void write_tokens(const Kv4WriteParams& p, int tg, in
   }
 }
 
-constexpr int kWriteDepth = 2;
+constexpr int kWriteDepth = 2;  // 3 measures the same
 
 // grid x: (8 tokens, kv head) a warp; grid y: p.seg layers
 __global__ void __launch_bounds__(kTokThreads, 3)
@@ -416,7 +426,10 @@ __global__ void __launch_bounds__(kTokThreads, 3)
 }
 
 // grid x: (4 tokens, kv head) a warp, lane (n, c): channels 8c .. 8c+7 of K and
-// of V; grid y: p.seg layers
+// of V, so that a warp's stores are whole 128-byte rows; grid y: p.seg layers.
+// Four fifths of the traffic are the stores.  Bound by memory: 4 prompts of 8192
+// tokens, 36 layers (1.57 GB) take 260 us, 6050 GB/s; a thread a layer took 394,
+// layers of both kinds in one loop 279.
 __global__ void __launch_bounds__(kTokThreads)
     kv4_read_kernel(const __grid_constant__ Kv4ReadParams p) {
   const int w = int(blockIdx.x) * kTokWarps + (threadIdx.x >> 5);
@@ -465,7 +478,7 @@ __global__ void __launch_bounds__(kTokThreads)
     store8(p.v_out + to, vc, vs, __ldg(p.v_scale + i));
   };
   // a group buffer at a time: its window layer, its full layer
-#pragma unroll 1  // 32 registers: full occupancy outweighs two layers' loads at once
+#pragma unroll 1  // 32 registers: at two layers at once (40) it takes 278 us instead of 260
   for (int i = l0 & ~1; i < l1; i += 2, dst += 2 * out_layer) {
     const uint8_t* buf = p.buf[i >> 1];
     if (ok_s && i >= l0) read_layer(i, buf + win.codes, win, dst);
@@ -502,18 +515,46 @@ __global__ void __launch_bounds__(kPlanThreads)
 // =========================================================================
 // Decode attention
 // =========================================================================
-// One CTA per SM of kCons independent warps; each takes units (layer, row, kv
+// One CTA per SM of kWarps4 independent warps; each takes units (layer, row, kv
 // head, split) from the work counter and streams their tiles through a ring of
 // its own, kStTiles tiles a stage.
+//
+// Arithmetic.  A code times its block scale has at most 6 significant bits and is
+// exact in f16, so K and V enter mma.sync (m16n8k16; N = the 8 heads of the group,
+// M = 16 tokens for Q K^T, 16 channels for P V) as they are stored.  q' is rounded
+// to f16 once, 2^-11 of each term of a score: with a second f16 for the
+// remainder, as over the FP8 cache, attention of the 64-row case took 629 us
+// instead of 557, and K's own rounding is a hundred times coarser.  (Outputs
+// against 64 bits: 2.8e-4 in fp32, 6.1e-4 with q, K and V ~ N(0, 3); the bf16
+// rounding alone is 1.7e-3.)  Scores, reference, sums and outputs are fp32.
+//
+// What bounds it.  At the copy rate an SM sub-partition has about 197 cycles for a
+// tile (16 tokens, 1152 bytes).  The stage loop issues 112 instructions a tile for
+// the products and the softmax -- 32 conversions of a code pair and 32
+// multiplications by a scale among them -- and about 30 for the ring, the units
+// and the loop, and keeps its issue slot 65-70 % busy with the 16 warps that 118
+// registers allow: 220 cycles.  So long rows run at the memory's rate (8 rows of
+// 131072 keys: 10.9 GB in 1613 us, 6750 GB/s; 64 rows of 1024 to 8192: 3.18 GB in 497 us,
+// 6400) and short ones at the issue rate (512 rows of 64 to 512: 2.49 GB in 486 us).
+//
+// Why this form (64-row case): 1152-byte bulk copies issued in the warp, two-tile
+// stages 836 us; the same copies by a producer warp, a lane a warp 722 (a bulk
+// copy takes uniform operands: lanes are served one by one); 16-byte
+// asynchronous copies by the lanes, 15 warps and three stages 651, 16 warps and
+// two stages 628 (14 warps 664, 12 warps 643); one f16 for q' 557; interleaving
+// nibbles by one logic operation, packed fp32, places of 32 tiles at a time 504;
+// the next unit's descriptor in shared memory 497.  20 warps at 96 registers
+// recompute more than they hide (536), and so do two tiles at a time (559).
 constexpr int kStTiles = 4;     // tiles per pipeline stage
 constexpr int kStages4 = 2;     // ring depth per warp
-constexpr int kCons = 16;       // warps
+constexpr int kWarps4 = 16;
 constexpr int kFifo4 = 6;       // unit descriptors in flight per warp (> kStages4 + 1)
 constexpr int kSt4Tok = kStTiles * kTile;
 constexpr uint32_t kSt4Bytes = kStTiles * kTileBytes;
-constexpr int kAttn4Threads = kCons * 32;
-// A warp takes 1.8 us for a stage whatever the others do, so the length of a
-// chunk is the length of the tail: rows may have 16 chunks of 512 keys.
+constexpr int kAttn4Threads = kWarps4 * 32;
+// A warp takes about 1.8 us for a stage, so the length of a chunk is the length
+// of the tail: rows may have 16 chunks of 512 keys (one row of 8192 keys: 43 us
+// for the step; with at most 8 chunks 52, half of the warps without a unit).
 constexpr int kShortMerge4 = 16;
 constexpr int kTileLanes = 32 / kStTiles;              // lanes that copy one tile
 constexpr int kTileCopies = kTileBytes / 16 / kTileLanes;  // 16-byte copies of a lane
@@ -531,7 +572,7 @@ struct alignas(128) Kv4Ring {
   int4 e_nx;              // the next unit's descriptor
 };
 static_assert(sizeof(Kv4Ring) % 128 == 0 && kSt4Bytes % 16 == 0, "16-byte copies");
-constexpr size_t kAttn4Smem = sizeof(Kv4Ring) * kCons;
+constexpr size_t kAttn4Smem = sizeof(Kv4Ring) * kWarps4;
 static_assert(kAttn4Smem <= 227 * 1024, "shared memory of an SM");
 
 __global__ void __launch_bounds__(kAttn4Threads, 1)
@@ -549,15 +590,15 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
   if (p.cap > 0) asm volatile("griddepcontrol.launch_dependents;");
   // the first unit's descriptor, if there is such a unit, with the header words
   // (any entry of the list otherwise)
-  int u_nx = int(blockIdx.x) * kCons + warp, nx_step = 2;
+  int u_nx = int(blockIdx.x) * kWarps4 + warp, nx_step = 2;
   auto copy_desc = [&](int64_t entry) {
     if (lane == 0) cp_async16(smem_u32(&ws.e_nx), p.edesc + entry);
   };
   copy_desc(min(int64_t(fdiv(u_nx, p.fd_planes)), 2 * p.Bt + p.cap - 1));
   const int nU = p.hdr[kHdrNUnits];
   // zero-fill units (inactive rows)
-  for (int v = int(blockIdx.x) * kCons + warp, n = p.hdr[kHdrNZero]; v < n;
-       v += int(gridDim.x) * kCons) {
+  for (int v = int(blockIdx.x) * kWarps4 + warp, n = p.hdr[kHdrNZero]; v < n;
+       v += int(gridDim.x) * kWarps4) {
     const int zr = fdiv(v, p.fd_nl);
     zero_row(p, v - zr * p.NL, p.zero_list[zr], lane);
   }
@@ -576,7 +617,8 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
   auto load_entry = [&](const int32_t* row, int tile, int end) -> int32_t {
     return tile < end ? __ldg(row + fdiv(tile * kTile, p.fd_b)) : 0;
   };
-  // offset of a tile from its kv head's tiles of block 0, in 128 bytes
+  // offset of a tile from its kv head's tiles of block 0, in 128 bytes (32 bits:
+  // half a terabyte of group buffer)
   auto place = [&](int32_t pb, int tile) -> uint32_t {
     if (uint32_t(pb) >= uint32_t(p.nb)) {
       set_error(GK_DEVERR_BLOCK);
@@ -895,7 +937,8 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
       for (int m = 0; m < 4; ++m) o[m][0] = o[m][1] = o[m][2] = o[m][3] = 0.f;
     }
 
-    // a unit's last stage may hold half of its tiles or fewer
+    // a unit's last stage may hold half of its tiles or fewer (512 short rows: 506
+    // us, without the second form 525; 8 rows of 131072 keys: 1632, without 1614)
     if (tok0 + kSt4Tok / 2 < cd.t_end)
       process(Tiles<kStTiles>());
     else
@@ -1015,13 +1058,12 @@ cudaError_t launch_kv4_attention(const PlanParams& plan, const AttnParams& p, cu
   if (e != cudaSuccess) return e;
   Kv4PlanWriteParams pw;
   pw.plan = plan;
-  pw.plan.n_warps = c->sms * kCons;
+  pw.plan.n_warps = c->sms * kWarps4;
   pw.plan.short_merge = kShortMerge4;
   AttnChain ch = {};
   if (write) {
     pw.write = *write;
-    const int64_t warps =
-        int64_t(token_warps(*write, kWriteTok)) * write->n_layers;
+    const int64_t warps = token_warps(*write, kWriteTok) * write->n_layers;
     ch.plan_func = (const void*)kv4_plan_write_kernel;
     ch.plan_arg = &pw;
     ch.plan_grid = unsigned(1 + (warps * 32 + kPlanThreads - 1) / kPlanThreads);
@@ -1036,8 +1078,9 @@ cudaError_t launch_kv4_attention(const PlanParams& plan, const AttnParams& p, cu
 }
 
 // Grid of the write and read kernels: p.seg layers a CTA, as many as leave
-// kTokWaves CTAs per SM, so that a thread's slots, places and rotation serve
-// several layers of a long prompt while a decode step still spreads over the SMs.
+// kTokWaves CTAs per SM, so that a thread's slots and places serve several layers
+// of a long prompt while a decode step still spreads over the SMs (write of 8191
+// tokens: 106 us; at 24 111; 8 and fewer leave the last CTAs alone at the end).
 constexpr int kTokWaves = 16;
 
 template <typename P>
