@@ -100,10 +100,20 @@ __device__ __forceinline__ void plan_body(const PlanParams& p) {
   }
 
   // unit counts and split-record needs of every candidate split length,
-  // one candidate per warp at a time
+  // one candidate per warp at a time; a length above the longest row leaves
+  // every row whole
   for (int k = wid; k < kSplitCands; k += kPlanWarps) {
     const int sh = 9 + k;  // log2 of kMinSplit << k
     const long long S = 1ll << sh;
+    if (S > Lmax) {
+      if (lane == 0) {
+        s_units[k] = NAct;
+        s_remtok[k] = T;
+        s_need[k] = s_full[k] = 0;
+        s_ne[k] = s_maxnf[k] = 0;
+      }
+      continue;
+    }
     long long units = 0, need = 0, full = 0, remtok = 0;
     int ne = 0, maxnf = 0;
     for (int b = lane; b < p.Bt; b += 32) {
@@ -144,14 +154,16 @@ __device__ __forceinline__ void plan_body(const PlanParams& p) {
     // kUnitsPerWarp units per resident warp (uniform long rows need many
     // chunks; mixed rows balance through largest-first order).  Then cap the
     // chunks per row and fit the partial records into the workspace.
-    const long long share = (T * planes) / (warps * 4);
+    // (S < floor(T * planes / (4 warps)), without the division)
     int k = 0;
-    while (k < kSplitCands - 1 && ((long long)kMinSplit << k) < share) ++k;
+    while (k < kSplitCands - 1 &&
+           (((long long)kMinSplit << k) + 1) * (4 * warps) <= T * planes)
+      ++k;
     while (k > 0 && (s_units[k] + NAct) * planes < kUnitsPerWarp * warps) --k;
     // no short chunks that would give a row more than short_merge partials:
     // the per-unit cost of the extra partials outweighs the balance they buy
     while (k < kSplitCands - 1 && ((long long)kMinSplit << k) <= kShortSplit &&
-           (Lmax - 1) / ((long long)kMinSplit << k) + 1 > p.short_merge)
+           ((Lmax - 1) >> (9 + k)) + 1 > p.short_merge)
       ++k;
     if (p.force_split_log >= 0) k = p.force_split_log;  // test hook: a fixed split length
     while (k < kSplitCands - 1 && ((long long)kMinSplit << k) * kMaxSplitsPerRow < Lmax) ++k;
@@ -168,10 +180,11 @@ __device__ __forceinline__ void plan_body(const PlanParams& p) {
     int conv_c = 0, conv_x = 0, conv_p = 0;
     const long long Sk = (long long)kMinSplit << k;
     const long long cunits = s_full[k] * planes;
-    const long long q = cunits / warps, rem = cunits - q * warps;
+    const bool wave = p.force_split_log < 0 && s_ne[k] > 0 && cunits >= warps;
+    const long long q = wave ? cunits / warps : 0, rem = cunits - q * warps;
     const long long gap = (warps - rem) * Sk;                    // idle token slots
     const long long small = (s_remtok[k] + NAct * p.W) * planes;  // work in smaller units
-    if (p.force_split_log < 0 && q >= 1 && rem > 0 && small < gap && s_ne[k] > 0) {
+    if (wave && rem > 0 && small < gap) {
       // cv chunks in all, spread over the eligible rows in row order (fewer
       // if a row would pass kMaxSplitsPerRow chunks or the records the
       // workspace holds)
