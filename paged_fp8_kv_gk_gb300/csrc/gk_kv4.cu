@@ -719,14 +719,14 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
         w_idx = 0;
       }
     }
-    const uint32_t at = __shfl_sync(kFull, where, w_idx + my_tile);
-    if (pt + my_tile < pe) {
-      const uint8_t* s = src + uint64_t(at) * 128u;
-      const uint32_t d = p_slot + my_tile * kTileBytes + my_off;
+    // tiles past the unit's end are filled with zeros (their place is one in
+    // block 0, not read)
+    const uint8_t* s = src + uint64_t(__shfl_sync(kFull, where, w_idx + my_tile)) * 128u;
+    const uint32_t d = p_slot + my_tile * kTileBytes + my_off;
+    const uint32_t bytes = pt + my_tile < pe ? 16u : 0u;
 #pragma unroll
-      for (int i = 0; i < kTileCopies; ++i)
-        cp_async16(d + i * kTileLanes * 16, s + i * kTileLanes * 16);
-    }
+    for (int i = 0; i < kTileCopies; ++i)
+      cp_async16_zfill(d + i * kTileLanes * 16, s + i * kTileLanes * 16, bytes);
     cp_async_commit();
     pt += kStTiles;
     w_idx += kStTiles;
@@ -791,16 +791,19 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
     }
     // ---- online softmax (log2 domain); lane holds heads 2qd (c0,c2), 2qd+1 (c1,c3)
     if (edge) {
-      // V scales of keys outside the range may be anything, NaN included: 0.
-      // Lane l has token l % 16 of every tile, and two of the four blocks.
-      for (int i = 0; i < kT; ++i) {
-        const int t = lane & 15, tok = tok0 + kTile * i + t;
-        if (tok < cd.t_begin || tok >= cd.t_end) {
-          const uint32_t vs = st + i * kTileBytes + kTileVs + 4 * ((t & 7) >> 1) + 2 * (t >> 3) +
-                              (t & 1) + 32 * (lane >> 4);
-          sts8(vs, 0);
-          sts8(vs + 16, 0);
-        }
+      // V scales of a tile's keys outside the range may be anything, NaN
+      // included: 0.  Lane l has token l % 16 of the range's first and last
+      // tiles, and two of the four blocks.
+      const int t = lane & 15, i_end = (cd.t_end - tok0) / kTile;
+      const uint32_t vs = st + kTileVs + 4 * ((t & 7) >> 1) + 2 * (t >> 3) + (t & 1) +
+                          32 * (lane >> 4);
+      if (tok0 + t < cd.t_begin) {
+        sts8(vs, 0);
+        sts8(vs + 16, 0);
+      }
+      if (i_end < kT && tok0 + kTile * i_end + t >= cd.t_end) {
+        sts8(vs + i_end * kTileBytes, 0);
+        sts8(vs + i_end * kTileBytes + 16, 0);
       }
       __syncwarp();
 #pragma unroll
