@@ -283,6 +283,15 @@ __device__ __forceinline__ uint32_t quantise16(float2 (&x)[8], const LayerScale&
   return sfc;
 }
 
+// The write and read grids are programmatic dependents of the kernel before
+// them and touch nothing until it is complete; only then may the next grid
+// launch (its CTAs or a planner's work, which waits for this grid before it
+// ends, so that nothing runs two kernels ahead).
+__device__ __forceinline__ void follow_stream() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+}
+
 constexpr int kWriteTok = 8;  // tokens a warp writes at a time: four lanes each
 constexpr int kReadTok = 4;   // tokens a warp reads at a time: eight lanes each
 constexpr int kTokThreads = 256;
@@ -300,7 +309,7 @@ constexpr int kTokWarps = kTokThreads / 32;
 // thread a block with divisions as the compiler writes them 240; several layers
 // a thread and packed fp32 arithmetic 152; the next layer's rows in registers
 // (128 of them, 16 warps per SM) 137; 80 registers and 24 warps 118; the ring 106
-// (64 registers and 32 warps 119; K and V in different warps 122).
+// (64 registers and 32 warps 119; before the ring, K and V in different warps 122).
 constexpr int kRowBytes = 2 * kWriteTok * kHeadDim * 2;  // K rows, V rows
 template <int kDepth>
 __device__ __forceinline__ void write_tokens(const Kv4WriteParams& p, int tg, int h, int l0,
@@ -414,8 +423,7 @@ constexpr int kWriteDepth = 2;  // 3 measures the same
 // grid x: (8 tokens, kv head) a warp; grid y: p.seg layers
 __global__ void __launch_bounds__(kTokThreads, 3)
     kv4_write_kernel(const __grid_constant__ Kv4WriteParams p) {
-  // the decode-attention planner may launch now (see kv_append_kernel)
-  asm volatile("griddepcontrol.launch_dependents;");
+  follow_stream();
   __shared__ alignas(16) uint8_t rings[kTokWarps][kWriteDepth * kRowBytes];
   const int w = int(blockIdx.x) * kTokWarps + (threadIdx.x >> 5);
   const int tg = w / p.Hkv;
@@ -432,6 +440,7 @@ __global__ void __launch_bounds__(kTokThreads, 3)
 // layers of both kinds in one loop 279.
 __global__ void __launch_bounds__(kTokThreads)
     kv4_read_kernel(const __grid_constant__ Kv4ReadParams p) {
+  follow_stream();
   const int w = int(blockIdx.x) * kTokWarps + (threadIdx.x >> 5);
   const int tg = w / p.Hkv, h = w - tg * p.Hkv;
   const int lane = threadIdx.x & 31, c = lane & 7;
@@ -1094,22 +1103,29 @@ static dim3 token_grid(P& p, int tokens, int sms) {
   return dim3(unsigned(x), unsigned((p.n_layers + p.seg - 1) / p.seg));
 }
 
-cudaError_t launch_kv4_write(Kv4WriteParams& p, cudaStream_t st) {
+template <typename P>
+static cudaError_t launch_tokens(void (*kernel)(P), P& p, int tokens, cudaStream_t st) {
   Kv4Device* c = nullptr;
   const cudaError_t e = kv4_setup(&c);
   if (e != cudaSuccess) return e;
-  const dim3 grid = token_grid(p, kWriteTok, c->sms);
-  kv4_write_kernel<<<grid, kTokThreads, 0, st>>>(p);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = token_grid(p, tokens, c->sms);
+  cfg.blockDim = dim3(kTokThreads);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+cudaError_t launch_kv4_write(Kv4WriteParams& p, cudaStream_t st) {
+  return launch_tokens(kv4_write_kernel, p, kWriteTok, st);
 }
 
 cudaError_t launch_kv4_read(Kv4ReadParams& p, cudaStream_t st) {
-  Kv4Device* c = nullptr;
-  const cudaError_t e = kv4_setup(&c);
-  if (e != cudaSuccess) return e;
-  const dim3 grid = token_grid(p, kReadTok, c->sms);
-  kv4_read_kernel<<<grid, kTokThreads, 0, st>>>(p);
-  return cudaGetLastError();
+  return launch_tokens(kv4_read_kernel, p, kReadTok, st);
 }
 
 cudaError_t read_kv4_error(uint32_t* bits, bool clear) {
