@@ -12,7 +12,10 @@
  * 64, G == 8, B == 16 or a multiple of 32 up to 1024, NL even and <= 128): the
  * layer parity picks table, position and update index, and layers 2j and
  * 2j + 1 share group buffer j.  Everything gk.h says about streams, graph
- * capture, programmatic dependent launch and the device error word holds here.
+ * capture, programmatic dependent launch and the device error word holds here;
+ * the grids of gk_kv4_write and gk_kv4_read may launch early too, touch nothing
+ * before the kernel before them is complete, and open dependent launch then
+ * (they write none of `active`, `pos` and `pos_w`).
  *
  * Layout of group buffer j: uint8 [num_blocks, Hkv, B / 16, GK_KV4_TILE_BYTES],
  * a tile being 16 tokens of one kv head.  Token t of a tile, channel e:

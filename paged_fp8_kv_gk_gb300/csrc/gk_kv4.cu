@@ -480,9 +480,10 @@ __global__ void __launch_bounds__(kTokThreads)
   const int64_t out_layer = int64_t(p.n_tokens) * p.Hkv * kHeadDim;
   int64_t dst = ((l0 & ~1) - p.layer0) * out_layer + (n * p.Hkv + h) * kHeadDim + 8 * c;
   auto read_layer = [&](int i, const uint8_t* codes, const Lane& at, int64_t to) {
-    const uint32_t kc = __ldg(reinterpret_cast<const uint32_t*>(codes));
-    const uint32_t vc = __ldg(reinterpret_cast<const uint32_t*>(codes + kTileV));
-    const uint32_t ks = __ldg(codes + at.ks), vs = __ldg(codes + at.vs);
+    // (from L2: the write before may still be running when this grid launches)
+    const uint32_t kc = __ldcg(reinterpret_cast<const uint32_t*>(codes));
+    const uint32_t vc = __ldcg(reinterpret_cast<const uint32_t*>(codes + kTileV));
+    const uint32_t ks = __ldcg(codes + at.ks), vs = __ldcg(codes + at.vs);
     store8(p.k_out + to, kc, ks, __ldg(p.k_scale + i));
     store8(p.v_out + to, vc, vs, __ldg(p.v_scale + i));
   };
