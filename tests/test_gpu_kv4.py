@@ -673,6 +673,56 @@ def test_back_to_back_calls_on_one_stream(fused):
         assert torch.equal(o, (a, b)[k % 2].want), k
 
 
+@pytest.mark.parametrize("ws", ["minimum", "recommended"])
+def test_mixed_calls_back_to_back(ws):
+    """write, attention, read, fused step, read, ... of two token sets with nothing between the calls
+    and one workspace: every output is the one that the same calls give with a wait after each."""
+    a = Step(gi.get("long_small"), seed=5)
+    b = Step(gi.get("long_small"), seed=6)
+    b.cache, b.dks, b.dvs = a.cache, a.dks, a.dvs
+    b.q = b.q.flip(1).contiguous()
+    b.k, b.v = b.k.flip(2).contiguous(), -b.v
+    if ws == "minimum":
+        a.ws = torch.empty(gk.gk_attn_workspace_min_bytes(a.sh), dtype=torch.uint8, device="cuda")
+    b.ws = a.ws
+    t = a.ctl
+    keep = a.cache.clone()
+
+    def calls(wait):
+        a.cache.copy_(keep)
+        got = []
+        for rep in range(5):
+            for s in (a, b):
+                for fused in (False, True):
+                    out = torch.full_like(s.out, float("nan"))
+                    rows = [torch.full_like(s.k, float("nan")) for _ in range(4)]
+                    torch.cuda.synchronize() if wait else None
+                    read = lambda k, v: gk.gk_kv4_read(  # noqa: E731
+                        s.sh, s.cache, s.dks, s.dvs, t["upd_full"], t["upd_swa"], k, v)
+                    if not fused:
+                        s.write()
+                        torch.cuda.synchronize() if wait else None
+                        read(*rows[:2])
+                        torch.cuda.synchronize() if wait else None
+                        s.attn(out=out, out32=None)
+                    else:
+                        s.fused(out=out, out32=None)
+                        torch.cuda.synchronize() if wait else None
+                        read(*rows[:2])
+                    torch.cuda.synchronize() if wait else None
+                    read(*rows[2:])
+                    got += [out] + rows
+        torch.cuda.synchronize()
+        assert gk.gk_read_device_error() == 0
+        return got
+
+    want = calls(True)
+    assert not torch.equal(want[0], want[10])          # the two sets differ
+    for _ in range(3):
+        for x, y in zip(calls(False), want):
+            assert torch.equal(x, y)
+
+
 def test_python_refusals(monkeypatch):
     sh = token_shape()
     cache = random_cache(sh, 3)
