@@ -566,6 +566,11 @@ constexpr int kAttn4Threads = kWarps4 * 32;
 // of the tail: rows may have 16 chunks of 512 keys (one row of 8192 keys: 43 us
 // for the step; with at most 8 chunks 52, half of the warps without a unit).
 constexpr int kShortMerge4 = 16;
+// The largest probability is 2^7 when the reference is set and at most 2^15 (f16
+// ends at 65504): one of 2^-25 of it, the least that f16 would hold next to 1, is
+// then still rounded to 2^-7 of itself, and many such keys count beside a strong one.
+constexpr float kUpLog2 = 7.f;
+constexpr float kTop = kUpLog2 + kLazyLog2;
 constexpr int kTileLanes = 32 / kStTiles;              // lanes that copy one tile
 constexpr int kTileCopies = kTileBytes / 16 / kTileLanes;  // 16-byte copies of a lane
 static_assert(kTileCopies * kTileLanes * 16 == kTileBytes, "a tile is copied by whole lanes");
@@ -754,7 +759,8 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
   uint32_t c_slot = ring0;  // slot of the next stage to consume
   uint32_t qf[8];  // q' in f16
   // scores are x * 2^e_h (x in log2 units), si_h = 2^-e_h; nb_h is minus the
-  // running reference maximum of x, which may lag the true one by kLazyLog2
+  // running reference of x, kUpLog2 below the maximum when it is set; that may
+  // rise by kLazyLog2 before it is set again
   float2 si = make_float2(0.f, 0.f), nb = si;
   float o[4][4];
   float2 l01 = make_float2(0.f, 0.f);  // this lane's part of the softmax denominators
@@ -830,8 +836,8 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
       lm1 = fmaxf(lm1, fmaxf(sc[i][1], sc[i][3]));
     }
     const float2 lx = fma2(make_float2(lm0, lm1), si, nb);  // over the reference
-    if (__any_sync(kFull, !(lx.x <= kLazyLog2 && lx.y <= kLazyLog2))) {
-      // move the reference to the true running maximum and rescale what was summed
+    if (__any_sync(kFull, !(lx.x <= kTop && lx.y <= kTop))) {
+      // move the reference with the true running maximum and rescale what was summed
       float w0 = lm0, w1 = lm1;
 #pragma unroll
       for (int off = 4; off < 32; off <<= 1) {
@@ -839,7 +845,8 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
         w1 = fmaxf(w1, __shfl_xor_sync(kFull, w1, off));
       }
       // nb is minus the reference in log2 units (si is a power of two)
-      const float n0 = fminf(nb.x, -w0 * si.x), n1 = fminf(nb.y, -w1 * si.y);
+      const float n0 = fminf(nb.x, fmaf(-w0, si.x, kUpLog2));
+      const float n1 = fminf(nb.y, fmaf(-w1, si.y, kUpLog2));
       const float al0 = ex2(n0 - nb.x), al1 = ex2(n1 - nb.y);
       nb.x = n0;
       nb.y = n1;

@@ -723,6 +723,96 @@ def test_mixed_calls_back_to_back(ws):
             assert torch.equal(x, y)
 
 
+def test_weak_keys_beside_a_strong_one():
+    """16383 equal keys, each with 2^-24 to 2^-28 of one other key's probability, in one unit: below
+    f16's steps next to 1, and up to 2^-8 of the output together.
+
+    The output is n e V / (1 + n e), e = 2^-x.  The kernel's e is off by q's rounding to f16 and the
+    factors' (2^-11 of the logit and 2^-16), by p's rounding (2^-25 at most, where the strong key has
+    2^7) and, like the sums over the keys, by the fp32 rounding of 2^-24 a key; the strong key's p
+    and l by 2^-11."""
+    w = gi.get("tiny").replace(name="weak", batch=1, lengths="fixed:16384", num_blocks=None,
+                               scale=None)
+    s = Step(w)
+    sh, c = s.sh, s.c
+    for n in ("cos", "sin"):
+        x = np.full_like(getattr(c, n), float(n == "cos"))
+        setattr(c, n, x)
+        s.ctl[n] = dev(x)
+    s.ks[:], s.vs[:] = 1, 1
+    s.dks, s.dvs = dev(s.ks), dev(s.vs)
+    qs = np.array([22.25, 22.75, 23, 23.25, 23.5, 24, 25, 25.5])
+    s.q.zero_()
+    s.q[..., 0] = dev(qs, torch.bfloat16)
+    s.step["q"] = s.q.cpu()
+    L, at = 16384, 5000
+    t = np.arange(L)
+    skip = np.full(L, gk.GK_KV4_SKIP, np.int32)
+    k = torch.zeros(2, L, 1, 64, dtype=torch.bfloat16)
+    v = torch.ones_like(k)
+    k[:, at, 0, 0] = 6
+    v[:, at] = 0
+    full = (c.bt_full[0].astype(np.int64)[t // 16] * 16 + t % 16).astype(np.int32)
+    gk.gk_kv4_write(sh, k.cuda(), v.cuda(), None, None, s.dks, s.dvs, dev(full), dev(skip), s.cache)
+    space = torch.empty(gk.gk_attn_workspace_min_bytes(sh), dtype=torch.uint8, device="cuda")
+    s.attn(ws=space)
+    assert gk.gk_read_device_error() == 0
+    want = s.reference()[0][1, 0]
+    got = s.out32.double().cpu().numpy()[1, 0]
+    nats = qs * 6 / 8
+    e = np.exp(-nats)
+    rel = 1.1 * (2.0 ** -11 * nats + 2.0 ** -16 + 2.0 ** -25 / (2.0 ** 7 * e) + L * 2.0 ** -24 +
+                 2.0 ** -10)
+    assert (rel < 0.08).all() and (want > 1e-5).all()
+    assert (np.abs(got - want) <= rel[:, None] * want).all(), (got[:, 0] / want[:, 0]).tolist()
+
+
+def test_captured_after_copies_and_a_join():
+    """Each call captured behind a memset, a copy, and a join of two streams: its early launch waits
+    for all of them."""
+    s = Step(gi.get("gptoss_small"), sinks=True)
+    t = s.ctl
+    ko, vo = torch.zeros_like(s.k), torch.zeros_like(s.v)
+    new_k, new_v, new_q = s.k.clone(), s.v.clone(), s.q.clone()
+    keep = s.cache.clone()
+    side = torch.cuda.Stream()
+
+    def calls():
+        s.k.copy_(new_k)                    # a copy before the write
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            s.v.copy_(new_v)
+        main.wait_stream(side)              # a join before the write
+        s.write()
+        ko.zero_()                          # a memset before the read
+        vo.zero_()
+        gk.gk_kv4_read(s.sh, s.cache, s.dks, s.dvs, t["upd_full"], t["upd_swa"], ko, vo,
+                       active=t["active"])
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            s.q.copy_(new_q)
+        s.out.zero_()
+        main.wait_stream(side)              # a join before the attention
+        s.attn(out32=None)
+
+    calls()
+    torch.cuda.synchronize()
+    want = [x.clone() for x in (s.out, ko, vo, s.cache)]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        calls()
+    for _ in range(3):
+        for x in (s.k, s.v, s.q, ko, vo, s.out):
+            x.fill_(float("nan"))
+        s.cache.copy_(keep)
+        g.replay()
+        torch.cuda.synchronize()
+        assert gk.gk_read_device_error() == 0
+        for x, y in zip((s.out, ko, vo, s.cache), want):
+            assert torch.equal(x, y)
+
+
 def test_python_refusals(monkeypatch):
     sh = token_shape()
     cache = random_cache(sh, 3)
