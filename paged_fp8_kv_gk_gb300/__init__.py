@@ -243,7 +243,10 @@ def _kv4(kv, sh, dev):
 
 
 def _current_device() -> int:
-    return _torch()._C._cuda_getDevice()
+    try:
+        return _torch()._C._cuda_getDevice()
+    except RuntimeError:      # no driver: there are CPU tensors only, which are refused by name
+        return 0
 
 
 def _ptr4(t, dtype, name, dev, n, allow_none=False):

@@ -132,6 +132,32 @@ def test_attention_and_step_refusals():
             assert call([(kv_at, ctypes.byref(c))]) == gk.GK_ERR_INVALID_ARG, kw
 
 
+def test_cpu_tensors_are_refused():
+    """By name and as the FP8 calls do, with or without a driver."""
+    sh = _shape()
+    NL, Bt, H, D = sh.num_layers, sh.batch, sh.num_kv_heads, 64
+    kv = torch.zeros(NL, Bt, H, D, dtype=torch.bfloat16)
+    q = torch.zeros(NL, Bt, 8 * H, D, dtype=torch.bfloat16)
+    rope, one = torch.ones(Bt, 32), torch.ones(NL)
+    i, act = torch.zeros(Bt, dtype=torch.int32), torch.ones(Bt, dtype=torch.uint8)
+    bf, bs = (torch.zeros(Bt, n, dtype=torch.int32) for n in (sh.max_blocks_full,
+                                                              sh.max_blocks_swa))
+    ws = torch.zeros(1 << 16, dtype=torch.uint8)
+    cache = torch.zeros(NL // 2 * sh.num_blocks * gk.gk_kv4_block_bytes(sh), dtype=torch.uint8)
+    for call in (
+            lambda c: gk.gk_kv4_write(sh, kv, kv, rope, rope, one, one, i, i, c),
+            lambda c: gk.gk_kv4_read(sh, c, one, one, i, i, kv, kv),
+            lambda c: gk.gk_kv4_decode_attn_stack(sh, q, c, one, one, rope, rope, bf, bs, i, i, act,
+                                                  q, workspace=ws),
+            lambda c: gk.gk_kv4_decode_step(sh, q, kv, kv, rope, rope, one, one, i, i, bf, bs, i, i,
+                                            act, c, q, workspace=ws)):
+        with pytest.raises(ValueError, match="CUDA tensor"):
+            call(cache)
+    for c in (cache, [cache]):
+        with pytest.raises(ValueError, match="CUDA tensor"):
+            gk.Kv4Cache(c)
+
+
 def test_plain_codecs():
     """The plain form's tables and ties."""
     assert E2(0.25) == 0 and E2(0.2500001) == 1 and E2(0.75) == 2 and E2(1.25) == 2
