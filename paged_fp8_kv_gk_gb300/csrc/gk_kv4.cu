@@ -553,7 +553,7 @@ __global__ void __launch_bounds__(kPlanThreads)
 // asynchronous copies by the lanes, 15 warps and three stages 651, 16 warps and
 // two stages 628 (14 warps 664, 12 warps 643); one f16 for q' 557; interleaving
 // nibbles by one logic operation, packed fp32, places of 32 tiles at a time 504;
-// the next unit's descriptor in shared memory 497.  20 warps at 96 registers
+// the next unit's descriptor a word a lane 497.  20 warps at 96 registers
 // recompute more than they hide (536), and so do two tiles at a time (559).
 constexpr int kStTiles = 4;     // tiles per pipeline stage
 constexpr int kStages4 = 2;     // ring depth per warp
@@ -584,7 +584,6 @@ struct alignas(128) Kv4Ring {
   uint8_t ring[kStages4][kSt4Bytes];
   uint8_t qbuf[kUnitHeadBytes];
   UnitDesc fifo[kFifo4];  // st_begin: first tile; n_st: stages
-  int4 e_nx;              // the next unit's descriptor
 };
 static_assert(sizeof(Kv4Ring) % 128 == 0 && kSt4Bytes % 16 == 0, "16-byte copies");
 constexpr size_t kAttn4Smem = sizeof(Kv4Ring) * kWarps4;
@@ -603,13 +602,17 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
   // combine grid may launch now (see attn_kernel in gk_kernels.cu)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (p.cap > 0) asm volatile("griddepcontrol.launch_dependents;");
-  // the first unit's descriptor, if there is such a unit, with the header words
-  // (any entry of the list otherwise)
   int u_nx = int(blockIdx.x) * kWarps4 + warp, nx_step = 2;
-  auto copy_desc = [&](int64_t entry) {
-    if (lane == 0) cp_async16(smem_u32(&ws.e_nx), p.edesc + entry);
+  // lane l holds word l % 4 of the next unit's descriptor; the first one comes, if
+  // there is such a unit, with the header words (any entry of the list otherwise)
+  auto load_desc = [&](int64_t entry) -> int32_t {
+    return __ldcg(reinterpret_cast<const int32_t*>(p.edesc + entry) + (lane & 3));
   };
-  copy_desc(min(int64_t(fdiv(u_nx, p.fd_planes)), 2 * p.Bt + p.cap - 1));
+  auto desc_of = [&](int32_t d) -> int4 {
+    return make_int4(__shfl_sync(kFull, d, 0), __shfl_sync(kFull, d, 1), __shfl_sync(kFull, d, 2),
+                     __shfl_sync(kFull, d, 3));
+  };
+  int32_t d_nx = load_desc(min(int64_t(fdiv(u_nx, p.fd_planes)), 2 * p.Bt + p.cap - 1));
   const int nU = p.hdr[kHdrNUnits];
   // zero-fill units (inactive rows)
   for (int v = int(blockIdx.x) * kWarps4 + warp, n = p.hdr[kHdrNZero]; v < n;
@@ -643,21 +646,16 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
     return (uint32_t(pb) * blk_tiles + uint32_t(off)) * (kTileBytes / 128);
   };
   // The next unit is fetched in steps, one with each stage issued, so that no
-  // step waits for the one before it: the claim when a unit starts; a copy of
-  // its descriptor in the group of the unit's second stage; nothing with the
-  // third; its first table entries with the fourth, which is issued when the
-  // second has been waited for.  `now`: a unit starts before that.
+  // step waits for the one before it: the claim when a unit starts, its
+  // descriptor with the unit's second stage, its first table entries with the
+  // third.  Units of three stages (most windows) then start without a wait.
   int32_t ent_nx = 0;
-  auto fetch_next = [&](bool now) {
+  auto fetch_next = [&]() {
     if (nx_step == 1) {
       u_nx = __shfl_sync(kFull, u_nx, 0);  // the claim's answer is lane 0's
-      if (u_nx < nU) copy_desc(fdiv(u_nx, p.fd_planes));
-    } else if (nx_step == 3 && u_nx < nU) {
-      if (now) {
-        if (lane == 0) cp_async_wait_all();
-        __syncwarp();
-      }
-      const int4 e = ws.e_nx;
+      if (u_nx < nU) d_nx = load_desc(fdiv(u_nx, p.fd_planes));
+    } else if (u_nx < nU) {
+      const int4 e = desc_of(d_nx);
       ent_nx = load_entry(row_of(e), e.y / kTile + lane, (e.z + kTile - 1) / kTile);
     }
     ++nx_step;
@@ -682,14 +680,13 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
   auto issue_next = [&]() -> bool {
     if (pt >= pe) {
       if (!q_free || exhausted) return false;  // not free: the buffered q is still to be read
-      while (nx_step < 4) fetch_next(true);
+      while (nx_step < 3) fetch_next();
       const int u = u_nx;
       if (u >= nU) {
         exhausted = true;
         return false;
       }
-      const int4 e = ws.e_nx;
-      __syncwarp();
+      const int4 e = desc_of(d_nx);
       if (lane == 0) u_nx = atomicAdd(p.queue, 1);
       nx_step = 1;
       const int pl = u - fdiv(u, p.fd_planes) * int(p.fd_planes.d);
@@ -724,7 +721,7 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
         cp_async16(qbuf0 + kQBytes + 16 * lane,
                    (lane < 8 ? p.cosb : p.sinb) + int64_t(e.x) * (kHeadDim / 2) + 4 * (lane & 7));
     } else {
-      if (nx_step < 4) fetch_next(false);
+      if (nx_step < 3) fetch_next();
       if (w_idx == 32) {
         where = place(ent, pt + lane);
         const UnitDesc& du = ws.fifo[f_tail == 0 ? kFifo4 - 1 : f_tail - 1];
