@@ -545,7 +545,7 @@ __global__ void __launch_bounds__(kPlanThreads)
 // and the loop, and keeps its issue slot 65-70 % busy with the 16 warps that 118
 // registers allow: 220 cycles.  So long rows run at the memory's rate (8 rows of
 // 131072 keys: 10.9 GB in 1613 us, 6750 GB/s; 64 rows of 1024 to 8192: 3.18 GB in 497 us,
-// 6400) and short ones at the issue rate (512 rows of 64 to 512: 2.49 GB in 486 us).
+// 6400) and short ones at the issue rate (512 rows of 64 to 512: 2.49 GB in 482 us).
 //
 // Why this form (64-row case): 1152-byte bulk copies issued in the warp, two-tile
 // stages 836 us; the same copies by a producer warp, a lane a warp 722 (a bulk
