@@ -627,6 +627,7 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
   // by a shuffle.
   const int tpb = p.B / kTile;
   const uint32_t blk_tiles = uint32_t(p.Hkv * tpb);
+  auto tiles_of = [](int tokens) -> int { return int(uint32_t(tokens) / kTile); };  // whole tiles
   auto swa_of = [](int4 e) { return ((e.w >> 30) & 1) != 0; };
   auto row_of = [&](int4 e) -> const int32_t* {
     return swa_of(e) ? p.bt_swa + int64_t(e.x) * p.MBS : p.bt_full + int64_t(e.x) * p.MBF;
@@ -656,7 +657,7 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
       if (u_nx < nU) d_nx = load_desc(fdiv(u_nx, p.fd_planes));
     } else if (u_nx < nU) {
       const int4 e = desc_of(d_nx);
-      ent_nx = load_entry(row_of(e), e.y / kTile + lane, (e.z + kTile - 1) / kTile);
+      ent_nx = load_entry(row_of(e), tiles_of(e.y) + lane, tiles_of(e.z + kTile - 1));
     }
     ++nx_step;
   };
@@ -692,11 +693,11 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
       const int pl = u - fdiv(u, p.fd_planes) * int(p.fd_planes.d);
       const int j = fdiv(pl, p.fd_hkv);
       const int kvh = pl - j * p.Hkv, layer = swa_of(e) ? 2 * j : 2 * j + 1;
-      pt = e.y / kTile;
-      pe = (e.z + kTile - 1) / kTile;
+      pt = tiles_of(e.y);
+      pe = tiles_of(e.z + kTile - 1);
       src = p.kb[j] + int64_t(kvh) * tpb * kTileBytes + my_off;
       where = place(ent_nx, pt + lane);
-      ent = load_entry(row_of(e), pt + 32 + lane, pe);
+      if (pe - pt > 32) ent = load_entry(row_of(e), pt + 32 + lane, pe);
       w_idx = 0;
       if (lane == 0) {
         UnitDesc& d = ws.fifo[f_tail];
@@ -708,7 +709,7 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
         d.t_begin = e.y;
         d.t_end = e.z;
         d.st_begin = pt;
-        d.n_st = (pe - pt + kStTiles - 1) / kStTiles;
+        d.n_st = int(uint32_t(pe - pt + kStTiles - 1) / kStTiles);
       }
       f_tail = f_tail == kFifo4 - 1 ? 0 : f_tail + 1;
       q_free = false;
@@ -807,7 +808,7 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
       // V scales of a tile's keys outside the range may be anything, NaN
       // included: 0.  Lane l has token l % 16 of the range's first and last
       // tiles, and two of the four blocks.
-      const int t = lane & 15, i_end = (cd.t_end - tok0) / kTile;
+      const int t = lane & 15, i_end = tiles_of(cd.t_end - tok0);
       const uint32_t vs = st + kTileVs + 4 * ((t & 7) >> 1) + 2 * (t >> 3) + (t & 1) +
                           32 * (lane >> 4);
       if (tok0 + t < cd.t_begin) {
@@ -819,11 +820,14 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
         sts8(vs + i_end * kTileBytes + 16, 0);
       }
       __syncwarp();
+      // (the range begins in the first tile of a stage if in any)
+      const int first = cd.t_begin - tok0 - (g ^ (g >> 2)), end = cd.t_end - tok0 - (g ^ (g >> 2));
+      if (first > 0) sc[0][0] = sc[0][1] = -INFINITY;
+      if (first > 8) sc[0][2] = sc[0][3] = -INFINITY;
 #pragma unroll
       for (int i = 0; i < kT; ++i) {
-        const int t0 = tok0 + kTile * i + (g ^ (g >> 2)), t1 = t0 + 8;
-        if (t0 < cd.t_begin || t0 >= cd.t_end) sc[i][0] = sc[i][1] = -INFINITY;
-        if (t1 < cd.t_begin || t1 >= cd.t_end) sc[i][2] = sc[i][3] = -INFINITY;
+        if (end <= kTile * i) sc[i][0] = sc[i][1] = -INFINITY;
+        if (end <= kTile * i + 8) sc[i][2] = sc[i][3] = -INFINITY;
       }
     }
     float lm0 = fmaxf(sc[0][0], sc[0][2]), lm1 = fmaxf(sc[0][1], sc[0][3]);
@@ -932,7 +936,7 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
 #pragma unroll
       for (int w = 0; w < 8; ++w) {
         r[w] = fma2(bf16x2_to_f32x2(xw[w]), cw[w], mul2(bf16x2_to_f32x2(yw[w] ^ flip), sw[w]));
-        amax = fmaxf(amax, fmaxf(fabsf(r[w].x), fabsf(r[w].y)));
+        amax = max3_abs_nan(amax, r[w].x, r[w].y);
       }
       amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2)) * ck;
