@@ -210,12 +210,12 @@ __device__ __forceinline__ bool token_slot(const P& p, const int32_t* slots, int
 // What divides by a layer scale.
 struct LayerScale {
   float scale;
-  float exact;  // exact_reciprocal(scale)
-  float rcp;    // 1 / scale, correctly rounded; 0 outside 2^-40 .. 2^40
+  float rcp;   // 1 / scale, correctly rounded; 0 outside 2^-40 .. 2^40
+  bool exact;  // rcp is 1 / scale
 };
 __device__ __forceinline__ LayerScale layer_scale(float s) {
   const float a = fabsf(s);
-  return {s, exact_reciprocal(s), a >= 0x1p-40f && a <= 0x1p40f ? __frcp_rn(s) : 0.f};
+  return {s, a >= 0x1p-40f && a <= 0x1p40f ? __frcp_rn(s) : 0.f, exact_reciprocal(s) != 0.f};
 }
 
 // -(x / s), correctly rounded, for |x| < 2^60, nr = -LayerScale::rcp: two
@@ -234,10 +234,10 @@ __device__ __forceinline__ float2 neg_div(float2 x, float2 s, float2 nr) {
 //
 // The codes are those of the exact quotient u / sf, u = x / scale rounded to
 // fp32.  sf has 4 significant bits and a code border t has 3, so u is a border
-// only if it is t * sf exactly; the quotient is refined by one exact remainder,
-// which gives such a quotient exactly and any other within a 2^-45 part of
-// u / sf before its last rounding, hence on its own side of the border (the
-// nearest u to t * sf differs by more than half a step of t).
+// only if it is t * sf exactly.  u is multiplied by 1 / sf in two terms, which
+// leaves u / sf within a 2^-42 part before its one rounding: t exactly for such a
+// u, and for any other its own side of t (the nearest u to t * sf differs by more
+// than half a step of t).  The same holds for a / 6 and the borders of E4M3.
 __device__ __forceinline__ uint32_t quantise16(float2 (&x)[8], const LayerScale& ls,
                                                uint2& codes) {
   float a = 0.f;
@@ -247,7 +247,7 @@ __device__ __forceinline__ uint32_t quantise16(float2 (&x)[8], const LayerScale&
   // rounding is monotonic: the largest quotient is that of the largest value
   if (a < 0x1p60f && ls.rcp != 0.f) {
     const float2 s = make_float2(ls.scale, ls.scale), nr = make_float2(-ls.rcp, -ls.rcp);
-    if (ls.exact != 0.f) {
+    if (ls.exact) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) nu[e] = mul2(x[e], nr);
       a = fabsf(a * ls.rcp);
@@ -256,8 +256,9 @@ __device__ __forceinline__ uint32_t quantise16(float2 (&x)[8], const LayerScale&
       for (int e = 0; e < 8; ++e) nu[e] = neg_div(x[e], s, nr);
       a = fabsf(neg_div(make_float2(a, a), s, nr).x);
     }
-    const float2 six = make_float2(6.f, 6.f), sixth = make_float2(-1.f / 6.f, -1.f / 6.f);
-    a = a < 0x1p60f ? -neg_div(make_float2(a, a), six, sixth).x : a;
+    // a / 6 with one exact remainder
+    const float a0 = a * (1.f / 6.f);
+    if (a < 0x1p60f) a = fmaf(fmaf(a0, -6.f, a), 1.f / 6.f, a0);
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -270,14 +271,13 @@ __device__ __forceinline__ uint32_t quantise16(float2 (&x)[8], const LayerScale&
   }
   const uint32_t sfc = f32x2_to_e4m3x2(a, 0.f) & 0xffu;
   const float sf = f16x2_to_f32x2(e4m3x2_to_f16x2(sfc)).x;
-  const float r1 = sf > 0.f ? rcp_approx(sf) : 0.f;  // within 2^-23: enough for the remainder
-  const float2 nr = make_float2(-r1, -r1), sf2 = make_float2(sf, sf);
+  const float r1 = sf > 0.f ? rcp_approx(sf) : 0.f;  // within 2^-23
+  // 1 / sf = rh + rl, rl with rh's sign, so that a zero keeps its own
+  const float rh = r1 - r1 * 0x1p-21f, rl = fmaf(-sf, rh, 1.f) * r1;
+  const float2 nrh = make_float2(-rh, -rh), nrl = make_float2(-rl, -rl);
   float2 y[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float2 y0 = mul2(nu[e], nr);
-    y[e] = fma2(fma2(y0, sf2, nu[e]), nr, y0);
-  }
+  for (int e = 0; e < 8; ++e) y[e] = fma2(nu[e], nrh, mul2(nu[e], nrl));
   codes = make_uint2(f32x8_to_e2m1x8(y[0], y[1], y[2], y[3]),
                      f32x8_to_e2m1x8(y[4], y[5], y[6], y[7]));
   return sfc;
@@ -303,13 +303,14 @@ constexpr int kTokWarps = kTokThreads / 32;
 // kDepth layers in shared memory (`ring`, kRowBytes each), so that the next
 // layer's loads are in flight without holding registers.
 //
-// Bound by issue slots and the arithmetic's latency: about 500 instructions for
-// 8 tokens' K and V, two thirds of them the two exact divisions.  For 8191
+// Bound by issue slots and the arithmetic's latency: about 480 instructions for
+// 8 tokens' K and V, half of them the two exact divisions.  For 8191
 // tokens of 36 layers (387 MB; window layers keep 128 tokens), in us: one
 // thread a block with divisions as the compiler writes them 240; several layers
 // a thread and packed fp32 arithmetic 152; the next layer's rows in registers
 // (128 of them, 16 warps per SM) 137; 80 registers and 24 warps 118; the ring 106
-// (64 registers and 32 warps 119; before the ring, K and V in different warps 122).
+// (64 registers and 32 warps 119; before the ring, K and V in different warps 122);
+// division by the block scale and by 6 without a second remainder 101.
 constexpr int kRowBytes = 2 * kWriteTok * kHeadDim * 2;  // K rows, V rows
 template <int kDepth>
 __device__ __forceinline__ void write_tokens(const Kv4WriteParams& p, int tg, int h, int l0,
@@ -328,6 +329,7 @@ __device__ __forceinline__ void write_tokens(const Kv4WriteParams& p, int tg, in
   const TokenPlace at_s = place_of(p, max(slot_s, 0), h);
   const int64_t row = n * p.token_stride + h * kHeadDim + 16 * blk;
   LayerScale mk = {}, mv = {};  // lane l: of layer lb + l
+  uint32_t xk = 0, xv = 0;      // bit l: its rcp is exact
   int lb = l0 - 32;
   // the first layer from i on that some lane writes
   auto next_layer = [&](int i) { return ((i & 1) ? any_f : any_s) ? i : i + 1; };
@@ -370,12 +372,14 @@ __device__ __forceinline__ void write_tokens(const Kv4WriteParams& p, int tg, in
         mk = layer_scale(__ldg(p.k_scale + lb + lane));
         mv = layer_scale(__ldg(p.v_scale + lb + lane));
       }
+      xk = __ballot_sync(kFull, mk.exact);
+      xv = __ballot_sync(kFull, mv.exact);
     }
-    auto of_layer = [&](const LayerScale& m) -> LayerScale {
-      return {__shfl_sync(kFull, m.scale, i - lb), __shfl_sync(kFull, m.exact, i - lb),
-              __shfl_sync(kFull, m.rcp, i - lb)};
+    auto of_layer = [&](const LayerScale& m, uint32_t ex) -> LayerScale {
+      return {__shfl_sync(kFull, m.scale, i - lb), __shfl_sync(kFull, m.rcp, i - lb),
+              ((ex >> (i - lb)) & 1u) != 0};
     };
-    const LayerScale sk = of_layer(mk), sv = of_layer(mv);
+    const LayerScale sk = of_layer(mk, xk), sv = of_layer(mv, xv);
     const uint4 k0 = lds128(rows + c0), k1 = lds128(rows + c1);
     const uint32_t kw[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
     float2 x[8];
@@ -1101,7 +1105,7 @@ cudaError_t launch_kv4_attention(const PlanParams& plan, const AttnParams& p, cu
 // Grid of the write and read kernels: p.seg layers a CTA, as many as leave
 // kTokWaves CTAs per SM, so that a thread's slots and places serve several layers
 // of a long prompt while a decode step still spreads over the SMs (write of 8191
-// tokens: 106 us; at 24 111; 8 and fewer leave the last CTAs alone at the end).
+// tokens: 106 us when at 24 it took 111; 8 and fewer leave the last CTAs alone at the end).
 constexpr int kTokWaves = 16;
 
 template <typename P>
