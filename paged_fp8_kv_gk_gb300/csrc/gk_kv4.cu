@@ -14,6 +14,8 @@
 // measured rate of a copy.
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "gk_attn_common.cuh"
 #include "gk_device.cuh"
 #include "gk_internal.h"
@@ -218,16 +220,20 @@ __device__ __forceinline__ LayerScale layer_scale(float s) {
   return {s, a >= 0x1p-40f && a <= 0x1p40f ? __frcp_rn(s) : 0.f, exact_reciprocal(s) != 0.f};
 }
 
-// -(x / s), correctly rounded, for |x| < 2^60, nr = -LayerScale::rcp: two
-// corrections by the exact remainder (Markstein), of which the first leaves a
-// quotient within one step and the second rounds it correctly.  For |x| <
-// 2^-100 the remainder may underflow; such a quotient is far below half of the
-// smallest block scale and only its sign counts.  Negated, so that a zero
-// quotient comes out of x + q s and q - rem / s with the right sign.
-__device__ __forceinline__ float2 neg_div(float2 x, float2 s, float2 nr) {
-  const float2 q0 = mul2(x, nr);
-  const float2 q1 = fma2(fma2(q0, s, x), nr, q0);
-  return fma2(fma2(q1, s, x), nr, q1);
+// -(x / s), correctly rounded, for |x| < 2^60: a quotient by 1 / s in two terms
+// (nh, nl), then one correction by the exact remainder (Markstein) with nr =
+// -RN(1 / s).  The first leaves q0 within 1/2 + 2^-19 of a step of x / s; the
+// second adds the rest up to a part e = |s RN(1 / s) - 1| of it, S 2^-49 of a step
+// at most for s's significand S in [2^23, 2^24).  x / s is at least 1 / (2 S) of a
+// step away from the middle of two floats, and S^2 (1 + 2^-18) < 2^48 for every S
+// below 2^24 - 64; above, even S have an e below 2^-36 and odd ones were checked at
+// every x whose quotient is that near to a middle.  For |x| < 2^-100 the remainder
+// may underflow; such a quotient is far below half of the smallest block scale and
+// only its sign counts.  The terms have one sign and the quotient is negated, so
+// that a zero comes out of x + q0 s and q0 - rem / s with its own.
+__device__ __forceinline__ float2 neg_div(float2 x, float2 s, float2 nr, float2 nh, float2 nl) {
+  const float2 q0 = fma2(x, nh, mul2(x, nl));
+  return fma2(fma2(q0, s, x), nr, q0);
 }
 
 // Quantise the 16 values x / scale: E4M3 code of the block scale, E2M1 codes.
@@ -247,14 +253,17 @@ __device__ __forceinline__ uint32_t quantise16(float2 (&x)[8], const LayerScale&
   // rounding is monotonic: the largest quotient is that of the largest value
   if (a < 0x1p60f && ls.rcp != 0.f) {
     const float2 s = make_float2(ls.scale, ls.scale), nr = make_float2(-ls.rcp, -ls.rcp);
+    // a step or two below 1 / s, and the rest: of one sign
+    const float lh = ls.rcp - ls.rcp * 0x1p-23f, ll = fmaf(-ls.scale, lh, 1.f) * ls.rcp;
+    const float2 nh = make_float2(-lh, -lh), nl = make_float2(-ll, -ll);
     if (ls.exact) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) nu[e] = mul2(x[e], nr);
       a = fabsf(a * ls.rcp);
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) nu[e] = neg_div(x[e], s, nr);
-      a = fabsf(neg_div(make_float2(a, a), s, nr).x);
+      for (int e = 0; e < 8; ++e) nu[e] = neg_div(x[e], s, nr, nh, nl);
+      a = fabsf(neg_div(make_float2(a, a), s, nr, nh, nl).x);
     }
     // a / 6 with one exact remainder
     const float a0 = a * (1.f / 6.f);
@@ -262,8 +271,7 @@ __device__ __forceinline__ uint32_t quantise16(float2 (&x)[8], const LayerScale&
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      // infinities: any value this large has the saturated code, and stays
-      // finite through the remainder below
+      // infinities: any value this large has the saturated code
       nu[e].x = fminf(fmaxf(__fdiv_rn(x[e].x, -ls.scale), -1e30f), 1e30f);
       nu[e].y = fminf(fmaxf(__fdiv_rn(x[e].y, -ls.scale), -1e30f), 1e30f);
     }
@@ -294,8 +302,7 @@ __device__ __forceinline__ void follow_stream() {
 
 constexpr int kWriteTok = 8;  // tokens a warp writes at a time: four lanes each
 constexpr int kReadTok = 4;   // tokens a warp reads at a time: eight lanes each
-constexpr int kTokThreads = 256;
-constexpr int kTokWarps = kTokThreads / 32;
+constexpr int kTokThreads = 128;  // at 256 the write takes 5 us more (8191 tokens), the read 1
 
 // One warp writes the 8 tokens from 8 tg and kv head h, layers [l0, l1).  Lane
 // (n, blk) has 16 channels of K and of V, one block scale each; its slots and
@@ -303,14 +310,15 @@ constexpr int kTokWarps = kTokThreads / 32;
 // kDepth layers in shared memory (`ring`, kRowBytes each), so that the next
 // layer's loads are in flight without holding registers.
 //
-// Bound by issue slots and the arithmetic's latency: about 480 instructions for
+// Bound by issue slots and the arithmetic's latency: about 470 instructions for
 // 8 tokens' K and V, half of them the two exact divisions.  For 8191
 // tokens of 36 layers (387 MB; window layers keep 128 tokens), in us: one
 // thread a block with divisions as the compiler writes them 240; several layers
 // a thread and packed fp32 arithmetic 152; the next layer's rows in registers
 // (128 of them, 16 warps per SM) 137; 80 registers and 24 warps 118; the ring 106
 // (64 registers and 32 warps 119; before the ring, K and V in different warps 122);
-// division by the block scale and by 6 without a second remainder 101.
+// divisions with one remainder or none 99; CTAs of 128 threads 94; the slices of
+// layers of token_grid 92.
 constexpr int kRowBytes = 2 * kWriteTok * kHeadDim * 2;  // K rows, V rows
 template <int kDepth>
 __device__ __forceinline__ void write_tokens(const Kv4WriteParams& p, int tg, int h, int l0,
@@ -425,11 +433,11 @@ __device__ __forceinline__ void write_tokens(const Kv4WriteParams& p, int tg, in
 constexpr int kWriteDepth = 2;  // 3 measures the same
 
 // grid x: (8 tokens, kv head) a warp; grid y: p.seg layers
-__global__ void __launch_bounds__(kTokThreads, 3)
+__global__ void __launch_bounds__(kTokThreads, 6)
     kv4_write_kernel(const __grid_constant__ Kv4WriteParams p) {
   follow_stream();
-  __shared__ alignas(16) uint8_t rings[kTokWarps][kWriteDepth * kRowBytes];
-  const int w = int(blockIdx.x) * kTokWarps + (threadIdx.x >> 5);
+  __shared__ alignas(16) uint8_t rings[kTokThreads / 32][kWriteDepth * kRowBytes];
+  const int w = int(blockIdx.x) * (kTokThreads / 32) + (threadIdx.x >> 5);
   const int tg = w / p.Hkv;
   if (int64_t(tg) * kWriteTok >= p.n_tokens) return;
   const int l0 = p.layer0 + int(blockIdx.y) * p.seg;
@@ -440,12 +448,12 @@ __global__ void __launch_bounds__(kTokThreads, 3)
 // grid x: (4 tokens, kv head) a warp, lane (n, c): channels 8c .. 8c+7 of K and
 // of V, so that a warp's stores are whole 128-byte rows; grid y: p.seg layers.
 // Four fifths of the traffic are the stores.  Bound by memory: 4 prompts of 8192
-// tokens, 36 layers (1.57 GB) take 260 us, 6050 GB/s; a thread a layer took 394,
+// tokens, 36 layers (1.57 GB) take 251 us, 6250 GB/s; a thread a layer took 394,
 // layers of both kinds in one loop 279.
 __global__ void __launch_bounds__(kTokThreads)
     kv4_read_kernel(const __grid_constant__ Kv4ReadParams p) {
   follow_stream();
-  const int w = int(blockIdx.x) * kTokWarps + (threadIdx.x >> 5);
+  const int w = int(blockIdx.x) * (kTokThreads / 32) + (threadIdx.x >> 5);
   const int tg = w / p.Hkv, h = w - tg * p.Hkv;
   const int lane = threadIdx.x & 31, c = lane & 7;
   const int64_t n = int64_t(tg) * kReadTok + (lane >> 3);
@@ -1103,17 +1111,21 @@ cudaError_t launch_kv4_attention(const PlanParams& plan, const AttnParams& p, cu
 }
 
 // Grid of the write and read kernels: p.seg layers a CTA, as many as leave
-// kTokWaves CTAs per SM, so that a thread's slots and places serve several layers
-// of a long prompt while a decode step still spreads over the SMs (write of 8191
-// tokens: 106 us when at 24 it took 111; 8 and fewer leave the last CTAs alone at the end).
-constexpr int kTokWaves = 16;
+// kTokWarps warps per SM, so that a thread's slots and places serve several layers
+// of a long prompt while a decode step still spreads over the SMs; at most two
+// fifths of the layers, so that a long call ends with a third, shorter slice that
+// fills up the last wave.  36 layers: read of 4 x 8192 tokens 251 us (by 12 or 18
+// layers 253 and 256, all 36 at once 264); write of 8191 tokens 92 (by 18 99, by
+// 9 97, by 6 101).
+constexpr int kTokWarps = 128;
 
 template <typename P>
 static dim3 token_grid(P& p, int tokens, int sms) {
-  const int64_t x = (token_warps(p, tokens) + kTokWarps - 1) / kTokWarps;
-  const int64_t seg = x * p.n_layers / (int64_t(sms) * kTokWaves);
-  p.seg = int(seg < 1 ? 1 : seg > p.n_layers ? p.n_layers : seg);
-  return dim3(unsigned(x), unsigned((p.n_layers + p.seg - 1) / p.seg));
+  const int64_t warps = token_warps(p, tokens), per = kTokThreads / 32;
+  const int64_t seg = warps * p.n_layers / (int64_t(sms) * kTokWarps);
+  const int64_t most = std::max(2, 2 * p.n_layers / 5);
+  p.seg = int(std::min(std::max<int64_t>(seg, 1), most));
+  return dim3(unsigned((warps + per - 1) / per), unsigned((p.n_layers + p.seg - 1) / p.seg));
 }
 
 template <typename P>

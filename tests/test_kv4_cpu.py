@@ -1,6 +1,7 @@
 """The 4-bit cache without a GPU: the header's symbols, the host checks, and the
 plain form that the GPU tests compare with."""
 import ctypes
+from fractions import Fraction
 
 import numpy as np
 import pytest
@@ -176,6 +177,37 @@ def test_plain_codecs():
 
 def E2(y):
     return int(k4._nearest_even(np.array([y]), k4.E2M1[:8])[0])
+
+
+def test_quotient_by_a_layer_scale():
+    """The write divides by a layer scale s with one correction, q0 - (q0 s - x) RN(1 / s), of a q0
+    within 1/2 + 2^-19 of a step.  In exact arithmetic, for the significands where the bound of its
+    error does not decide (the largest 64) and some others: at the x whose quotients lie nearest to
+    the middle of two floats, both floats beside the quotient lead to the rounded one."""
+    def rn(v):
+        e = v.numerator.bit_length() - v.denominator.bit_length()
+        e -= v < Fraction(2) ** e
+        return round(v / Fraction(2) ** (e - 23)) * Fraction(2) ** (e - 23)   # ties to even
+
+    n = 0
+    for S in [*range(2 ** 24 - 64, 2 ** 24), 2 ** 23 + 1, 2 ** 23 + 3, 11863283, 13421773, 16000001]:
+        r = rn(Fraction(1, S))
+        xs = set(range(S, min(S + 64, 2 ** 24)))
+        if S & 1:
+            inv = pow(2 ** 25, -1, S)            # 2^25 x = middle * S + d
+            xs |= {d * inv % S for d in range(-15, 16, 2)}
+        for x in xs:
+            x <<= 24 - x.bit_length()
+            q = Fraction(x, S)
+            step = Fraction(2) ** (-23 if q >= 1 else -24)
+            low = q // step * step
+            for q0 in (low, low + step):
+                if abs(q - q0) <= step * (Fraction(1, 2) + Fraction(1, 2 ** 19)):
+                    rem = x - q0 * S
+                    assert rem == 0 or rn(abs(rem)) == abs(rem)
+                    assert rn(q0 + rem * r) == rn(q), (S, x)
+                    n += 1
+    assert n > 1000
 
 
 @pytest.mark.parametrize("B,Hkv", [(16, 1), (32, 3), (96, 2), (1024, 1)])
