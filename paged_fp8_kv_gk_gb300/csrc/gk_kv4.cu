@@ -308,7 +308,8 @@ constexpr int kTokThreads = 128;  // at 256 the write takes 5 us more (8191 toke
 // (n, blk) has 16 channels of K and of V, one block scale each; its slots and
 // its place in the tiles serve every layer.  The rows come through a ring of
 // kDepth layers in shared memory (`ring`, kRowBytes each), so that the next
-// layer's loads are in flight without holding registers.
+// layer's loads are in flight without holding registers; `rope` (kRopeRows) keeps
+// the tokens' cos and sin where kDepth > 1.
 //
 // Bound by issue slots and the arithmetic's latency: about 470 instructions for
 // 8 tokens' K and V, half of them the two exact divisions.  For 8191
@@ -318,11 +319,13 @@ constexpr int kTokThreads = 128;  // at 256 the write takes 5 us more (8191 toke
 // (128 of them, 16 warps per SM) 137; 80 registers and 24 warps 118; the ring 106
 // (64 registers and 32 warps 119; before the ring, K and V in different warps 122);
 // divisions with one remainder or none 99; CTAs of 128 threads 94; the slices of
-// layers of token_grid 92.
+// layers of token_grid 92; cos and sin in shared memory instead of L1 and 28 warps
+// 87 (32 warps spill: 106).
 constexpr int kRowBytes = 2 * kWriteTok * kHeadDim * 2;  // K rows, V rows
+constexpr int kRopeRows = 2 * kWriteTok * kHeadDim / 2 * 4;  // cos, sin
 template <int kDepth>
 __device__ __forceinline__ void write_tokens(const Kv4WriteParams& p, int tg, int h, int l0,
-                                             int l1, uint8_t* ring) {
+                                             int l1, uint8_t* ring, uint8_t* rope) {
   const int lane = threadIdx.x & 31, blk = lane & 3;
   const int64_t n = int64_t(tg) * kWriteTok + (lane >> 2);
   int slot_f, slot_s;
@@ -359,6 +362,18 @@ __device__ __forceinline__ void write_tokens(const Kv4WriteParams& p, int tg, in
     cp_async_commit();
   };
   int i = next_layer(l0), ahead = i, st = 0, st_ahead = 0;
+  if (i >= l1) return;
+  // cos and sin of the 8 tokens, in the order in which the lanes read them (with
+  // the first layer's rows; several layers only)
+  constexpr bool kKeep = kDepth > 1;
+  const uint32_t cs0 = kKeep ? smem_u32(rope) + (2 * tok + (blk & 1)) * 16 : 0;
+  if (kKeep && rotate && blk < 2) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      cp_async16(cs0 + 512 * q, p.cosb + rope_at + 4 * q);
+      cp_async16(cs0 + 512 * q + 256, p.sinb + rope_at + 4 * q);
+    }
+  }
 #pragma unroll
   for (int k = 0; k < kDepth - 1; ++k) {
     load(ahead, k);
@@ -396,14 +411,14 @@ __device__ __forceinline__ void write_tokens(const Kv4WriteParams& p, int tg, in
     if (rotate) {
       // rotate-half, the pair's other half two blocks away: every operation
       // rounded on its own, as in the FP8 append (x - y s = x + (-y) s).  cos
-      // and sin come from L1 for every layer: 32 registers for them would cost
-      // a third of the resident warps.
+      // and sin come from shared memory for every layer: 32 registers for them
+      // would cost a third of the resident warps.
       const uint4 y0 = lds128(rows + (c0 ^ 64u)), y1 = lds128(rows + (c1 ^ 64u));
       const uint32_t yw[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const float4 c4 = ldg_nc_f4(p.cosb + rope_at + 4 * q);
-        const float4 s4 = ldg_nc_f4(p.sinb + rope_at + 4 * q);
+        const float4 c4 = kKeep ? lds_f4(cs0 + 512 * q) : ldg_nc_f4(p.cosb + rope_at + 4 * q);
+        const float4 s4 = kKeep ? lds_f4(cs0 + 512 * q + 256) : ldg_nc_f4(p.sinb + rope_at + 4 * q);
         x[2 * q] = add2(mul2(x[2 * q], make_float2(c4.x, c4.y)),
                         mul2(bf16x2_to_f32x2(yw[2 * q] ^ flip), make_float2(s4.x, s4.y)));
         x[2 * q + 1] = add2(mul2(x[2 * q + 1], make_float2(c4.z, c4.w)),
@@ -433,16 +448,17 @@ __device__ __forceinline__ void write_tokens(const Kv4WriteParams& p, int tg, in
 constexpr int kWriteDepth = 2;  // 3 measures the same
 
 // grid x: (8 tokens, kv head) a warp; grid y: p.seg layers
-__global__ void __launch_bounds__(kTokThreads, 6)
+__global__ void __launch_bounds__(kTokThreads, 7)
     kv4_write_kernel(const __grid_constant__ Kv4WriteParams p) {
   follow_stream();
   __shared__ alignas(16) uint8_t rings[kTokThreads / 32][kWriteDepth * kRowBytes];
+  __shared__ alignas(16) uint8_t ropes[kTokThreads / 32][kRopeRows];
   const int w = int(blockIdx.x) * (kTokThreads / 32) + (threadIdx.x >> 5);
   const int tg = w / p.Hkv;
   if (int64_t(tg) * kWriteTok >= p.n_tokens) return;
   const int l0 = p.layer0 + int(blockIdx.y) * p.seg;
   write_tokens<kWriteDepth>(p, tg, w - tg * p.Hkv, l0, min(l0 + p.seg, p.layer0 + p.n_layers),
-                            rings[threadIdx.x >> 5]);
+                            rings[threadIdx.x >> 5], ropes[threadIdx.x >> 5]);
 }
 
 // grid x: (4 tokens, kv head) a warp, lane (n, c): channels 8c .. 8c+7 of K and
@@ -531,7 +547,7 @@ __global__ void __launch_bounds__(kPlanThreads)
   if (i >= p.write.n_layers) return;
   __shared__ alignas(16) uint8_t rings[kPlanThreads / 32][kRowBytes];
   write_tokens<1>(p.write, tg, r - tg * p.write.Hkv, p.write.layer0 + i, p.write.layer0 + i + 1,
-                  rings[threadIdx.x >> 5]);
+                  rings[threadIdx.x >> 5], nullptr);
 }
 
 // =========================================================================
@@ -1115,8 +1131,8 @@ cudaError_t launch_kv4_attention(const PlanParams& plan, const AttnParams& p, cu
 // of a long prompt while a decode step still spreads over the SMs; at most two
 // fifths of the layers, so that a long call ends with a third, shorter slice that
 // fills up the last wave.  36 layers: read of 4 x 8192 tokens 251 us (by 12 or 18
-// layers 253 and 256, all 36 at once 264); write of 8191 tokens 92 (by 18 99, by
-// 9 97, by 6 101).
+// layers 253 and 256, all 36 at once 264); write of 8191 tokens 92 when by 18 it
+// took 99, by 9 97, by 6 101.
 constexpr int kTokWarps = 128;
 
 template <typename P>
