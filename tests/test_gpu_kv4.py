@@ -218,6 +218,43 @@ def test_read_values(B, Hkv, T):
             assert torch.equal(torch.nan_to_num(got.cpu()), torch.nan_to_num(w))
 
 
+@pytest.mark.parametrize("NL,T,layer0,n", [(12, 20001, 1, 11), (24, 4099, 0, 24), (6, 9000, 3, 1)])
+def test_long_prompts_over_many_layers(NL, T, layer0, n):
+    """A prompt so long that a warp keeps its tokens for several layers: the same bytes and values as
+    by calls of one layer each, of few tokens each (which the tests above compare with the plain
+    form); window layers keep the last tokens, with inactive tokens in between."""
+    Hkv, B = 8, 32
+    sh = token_shape(NL=NL, Hkv=Hkv, B=B, nb=-(-2 * T // B))
+    g = torch.Generator(device="cuda").manual_seed(T)
+    k, v = (torch.randn(n, T, Hkv, 64, generator=g, device="cuda").to(torch.bfloat16)
+            for _ in range(2))
+    ang = torch.rand(T, 32, generator=g, device="cuda") * 100
+    cos, sin = ang.cos(), ang.sin()
+    ks, vs = torch.rand(2, NL, generator=g, device="cuda") + 0.01
+    ks[::3] = 0.5
+    slots = torch.randperm(sh["num_blocks"] * B, generator=g, device="cuda").int()
+    sf, ss = slots[:T].clone(), slots[T:2 * T].clone()
+    ss[:T // 2] = gk.GK_KV4_SKIP
+    active = (torch.rand(T, generator=g, device="cuda") < 0.9).to(torch.uint8)
+    caches = [random_cache(sh, 12) for _ in range(2)]
+    outs = [torch.full((2,) + k.shape, 3.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    gk.gk_kv4_write(sh, k, v, cos, sin, ks, vs, sf, ss, caches[0], active=active, layer0=layer0)
+    gk.gk_kv4_read(sh, caches[0], ks, vs, sf, ss, outs[0][0], outs[0][1], active=active,
+                   layer0=layer0)
+    for i in range(n):
+        for t in range(0, T, 1000):
+            at = slice(t, min(t + 1000, T))
+            gk.gk_kv4_write(sh, k[i:i + 1, at], v[i:i + 1, at], cos[at], sin[at], ks, vs, sf[at],
+                            ss[at], caches[1], active=active[at], layer0=layer0 + i)
+            part = outs[1][:, i:i + 1, at].contiguous()
+            gk.gk_kv4_read(sh, caches[1], ks, vs, sf[at], ss[at], part[0], part[1],
+                           active=active[at], layer0=layer0 + i)
+            outs[1][:, i:i + 1, at] = part
+    assert gk.gk_read_device_error() == 0
+    assert torch.equal(*caches) and torch.equal(*outs)
+    assert (outs[0] == 3.0).any() and (outs[0] != 3.0).any()
+
+
 def test_empty_calls():
     sh = token_shape()
     cache = random_cache(sh, 3)
