@@ -850,6 +850,55 @@ def test_captured_after_copies_and_a_join():
             assert torch.equal(x, y)
 
 
+def test_early_launches_wait_for_other_streams():
+    """Tokens, positions and q that another stream writes late, behind an event that the calls' stream
+    waits for while the library's kernel before it has opened dependent launch already."""
+    s = Step(gi.get("gptoss_small"))
+    t = s.ctl
+    ko, vo = torch.zeros_like(s.k), torch.zeros_like(s.v)
+    keep, late = s.cache.clone(), {n: x.clone() for n, x in
+                                   (("k", s.k), ("v", s.v), ("q", s.q), ("pos", t["pos"]),
+                                    ("active", t["active"]))}
+    here = {"k": s.k, "v": s.v, "q": s.q, "pos": t["pos"], "active": t["active"]}
+    main, side = torch.cuda.current_stream(), torch.cuda.Stream()
+
+    def calls(wait, fused):
+        s.cache.copy_(keep)
+        for x in here.values():
+            x.zero_()
+        torch.cuda.synchronize()
+
+        def write_late(names):
+            with torch.cuda.stream(side):
+                torch.cuda._sleep(4000000)          # 2 ms
+                for n in names:
+                    here[n].copy_(late[n])
+            # a kernel that opens dependent launch, then the wait for the other stream
+            gk.gk_kv4_read(s.sh, s.cache, s.dks, s.dvs, t["upd_full"], t["upd_swa"], ko, vo)
+            main.wait_stream(side)
+            if wait:
+                torch.cuda.synchronize()
+
+        s.out.fill_(float("nan"))
+        if fused:
+            write_late(("k", "v", "q", "pos", "active"))
+            s.fused(out32=None)
+        else:
+            write_late(("k", "v", "active"))
+            s.write()
+            write_late(("q", "pos"))
+            s.attn(out32=None)
+        torch.cuda.synchronize()
+        return [x.clone() for x in (s.out, s.cache)]
+
+    for fused in (False, True):
+        want = calls(True, fused)
+        assert torch.isfinite(want[0]).all() and want[0].any()
+        for x, y in zip(calls(False, fused), want):
+            assert torch.equal(x, y)
+    assert gk.gk_read_device_error() == 0
+
+
 def test_python_refusals(monkeypatch):
     sh = token_shape()
     cache = random_cache(sh, 3)
