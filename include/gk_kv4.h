@@ -125,8 +125,9 @@ gk_status gk_kv4_decode_attn_stack(const gk_shape *shape, const void *q, const g
 /*
  * gk_kv4_decode_step -- the whole decode step in two launches: gk_kv4_write of
  * one new token a row (k_new, v_new [NL, Bt, Hkv, D], slots upd_full and
- * upd_swa) in the planner's launch, then gk_kv4_decode_attn_stack.  Bytes and
- * outputs are those of the two calls.  Inactive rows write nothing and output
+ * upd_swa) in the planner's launch, then gk_kv4_decode_attn_stack (and, as
+ * there, a combine grid when rows are split).  Bytes and outputs are those of the
+ * two calls.  Inactive rows write nothing and output
  * zeros; a row whose slot is GK_KV4_SKIP writes nothing.
  */
 gk_status gk_kv4_decode_step(const gk_shape *shape, const void *q, const void *k_new,
