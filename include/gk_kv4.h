@@ -9,9 +9,10 @@
  * (No counterpart on the pages: an addition of this library.)
  *
  * Conventions, argument layouts and supported shapes are those of gk.h (D ==
- * 64, G == 8, B == 16 or a multiple of 32 up to 1024, NL even and <= 128): the
- * layer parity picks table, position and update index, and layers 2j and
- * 2j + 1 share group buffer j.  Everything gk.h says about streams, graph
+ * 64, G == 8, B == 16 or a multiple of 32 up to 1024, NL even and <= 128), and a
+ * group buffer holds at most 2^39 bytes (GK_ERR_UNSUPPORTED above): the layer
+ * parity picks table, position and update index, and layers 2j and 2j + 1 share
+ * group buffer j.  Everything gk.h says about streams, graph
  * capture, programmatic dependent launch and the device error word holds here;
  * the grids of gk_kv4_write and gk_kv4_read may launch early too, touch nothing
  * before the kernel before them is complete, and open dependent launch then
@@ -44,7 +45,7 @@ extern "C" {
  * gk_kv4_cache -- per-group or stacked, exactly one of the two (as gk_kv_cache):
  *   per-group: bufs[j] (HOST array of NL/2 DEVICE pointers) is group buffer j;
  *   stacked:   cache (DEVICE pointer) holds the NL/2 group buffers back to back.
- * All 16-byte aligned.  Offsets are 64-bit throughout.
+ * All 16-byte aligned.
  */
 typedef struct {
     void *const *bufs;

@@ -83,6 +83,18 @@ static int64_t kv4_block_bytes(const gk_shape& s) {
   return int64_t(s.num_kv_heads) * (s.block_size / 16) * GK_KV4_TILE_BYTES;
 }
 
+// check_shape for the 4-bit cache.  Its attention keeps a tile's place in a group
+// buffer as a 32-bit count of 128 bytes, so a buffer ends at 2^39 bytes; write
+// and read, whose offsets are 64-bit, refuse what the attention could not reach.
+static gk_status check_kv4_shape(const gk_shape* s) {
+  const gk_status st = check_shape(s);
+  if (st != GK_OK) return st;
+  const uint64_t tiles = uint64_t(s->num_blocks) * uint64_t(s->block_size / 16);  // < 2^27 a head
+  return tiles * uint64_t(s->num_kv_heads) * (GK_KV4_TILE_BYTES / 128) > (uint64_t(1) << 32)
+             ? GK_ERR_UNSUPPORTED
+             : GK_OK;
+}
+
 // The 4-bit cache descriptor -> group buffer pointers, exactly one form.
 static gk_status resolve_kv4(const gk_shape& s, const gk_kv4_cache* kv, uint8_t** buf) {
   if (!kv || (kv->bufs != nullptr) == (kv->cache != nullptr)) return GK_ERR_INVALID_ARG;
@@ -227,7 +239,7 @@ static gk_status decode_attention(const gk_shape* shape, const void* q, const gk
                                   float* out_f32, void* workspace, size_t ws_bytes, void* stream,
                                   const AppendInputs* app, int force_split_log = -1,
                                   const gk_kv4_cache* kv4 = nullptr) {
-  gk_status st = check_shape(shape);
+  gk_status st = kv4 ? check_kv4_shape(shape) : check_shape(shape);
   if (st != GK_OK) return st;
   if (!q || !k_scale || !v_scale || !cos || !sin || !bt_full || !bt_swa ||
       !pos || !pos_w || !active || !out)
@@ -420,13 +432,13 @@ gk_status gk_kv4_decode_step(const gk_shape* shape, const void* q, const void* k
 }
 
 size_t gk_kv4_block_bytes(const gk_shape* shape) {
-  return check_shape(shape) == GK_OK ? size_t(kv4_block_bytes(*shape)) : 0;
+  return check_kv4_shape(shape) == GK_OK ? size_t(kv4_block_bytes(*shape)) : 0;
 }
 
 // Checks that gk_kv4_write and gk_kv4_read share.
 static gk_status check_kv4_tokens(const gk_shape* shape, int32_t layer0, int32_t n_layers,
                                   int64_t n_tokens) {
-  const gk_status st = check_shape(shape);
+  const gk_status st = check_kv4_shape(shape);
   if (st != GK_OK) return st;
   if (layer0 < 0 || n_layers < 0 || layer0 > shape->num_layers - n_layers || n_tokens < 0)
     return GK_ERR_INVALID_ARG;

@@ -665,7 +665,7 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
     return tile < end ? __ldg(row + fdiv(tile * kTile, p.fd_b)) : 0;
   };
   // offset of a tile from its kv head's tiles of block 0, in 128 bytes (32 bits:
-  // half a terabyte of group buffer)
+  // the calls refuse group buffers above 2^39 bytes)
   auto place = [&](int32_t pb, int tile) -> uint32_t {
     if (uint32_t(pb) >= uint32_t(p.nb)) {
       set_error(GK_DEVERR_BLOCK);

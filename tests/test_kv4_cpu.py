@@ -235,3 +235,29 @@ def test_plain_write_then_read():
             a = np.abs(x.reshape(-1, 16)).max(-1, keepdims=True)
             # the widest code step is 2 of 6, the scale is off by at most 1/16
             assert np.all(np.abs(got - x).reshape(-1, 16) <= a / 6 * (1 + 2 ** -4) + 1e-9)
+
+
+@no_device
+def test_group_buffers_above_512_gib_are_refused():
+    """The attention holds a tile's place as a 32-bit count of 128 bytes: a shape whose group buffer
+    is larger than 2^39 bytes is refused by every call, the largest one below it by none."""
+    L = gk.lib()
+    f = ctypes.c_void_p(FAKE)
+    kvs, keep = _cache(form="per_group")
+    kv = ctypes.byref(kvs)
+    for B, Hkv in ((16, 8), (32, 8), (96, 40), (1024, 8), (16, 2 ** 20), (1024, 2 ** 27)):
+        most = 2 ** 39 // (72 * B * Hkv)
+        over = dict(block_size=B, num_kv_heads=Hkv, num_q_heads=8 * Hkv, batch=1,
+                    max_blocks_full=1, max_blocks_swa=-(-(128 + 2 * B - 2) // B))
+        for nb, fits in ((most, True), (most + 1, False), (2 ** 31 // B - 1, False)):
+            if nb < 1 or nb * B >= 2 ** 31:
+                continue
+            sh = _shape(num_blocks=nb, **over)
+            s, need = ctypes.byref(sh), 1 << 50
+            got = [L.gk_kv4_write(s, 0, 4, 1, f, f, 512, 512, f, f, f, f, f, f, f, kv, None),
+                   L.gk_kv4_read(s, 0, 4, 1, kv, f, f, f, f, f, f, f, None),
+                   L.gk_kv4_decode_attn_stack(s, f, kv, *[f] * 9, None, f, None, f, need, None),
+                   L.gk_kv4_decode_step(s, *[f] * 14, None, kv, f, None, f, need, None)]
+            assert all((x != gk.GK_ERR_UNSUPPORTED) == fits for x in got), (B, Hkv, nb, got)
+            assert (L.gk_kv4_block_bytes(s) == 72 * B * Hkv) == fits
+            assert L.gk_attn_workspace_min_bytes(s) > 0     # the FP8 cache takes such a shape
