@@ -25,6 +25,7 @@
 #include "gk_attn_common.cuh"
 #include "gk_device.cuh"
 #include "gk_internal.h"
+#include "gk_once.h"
 
 namespace gk {
 
@@ -1032,13 +1033,11 @@ cudaError_t launch_wait_timeout(uint64_t limit_ns, cudaStream_t st) {
 // Launchers
 // =========================================================================
 struct DeviceCache {
-  int dev = -1;
   int sms = 0;
   int attn_blocks_per_sm = 0;  // of the selected path
   bool fma = false;            // GK_ATTN_PATH=fma selects the FMA comparison path
-  bool attrs_set = false;
 };
-static DeviceCache g_cache[64];
+static PerDevice<DeviceCache, 64> g_cache;
 
 // Attention instantiations, index = fma * 2 + plain_k.
 static const void* const kAttnKernels[4] = {
@@ -1050,14 +1049,13 @@ cudaError_t plan_setup() {
                               int(2 * kMaxBatch * sizeof(int32_t)));
 }
 
-static cudaError_t device_setup(DeviceCache** out) {
+static cudaError_t device_setup(const DeviceCache** out) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  DeviceCache& c = g_cache[dev];
-  if (!c.attrs_set) {
-    e = cudaDeviceGetAttribute(&c.sms, cudaDevAttrMultiProcessorCount, dev);
+  if (dev < 0 || dev >= g_cache.devices) return cudaErrorInvalidDevice;
+  return g_cache.get<cudaError_t>(dev, out, [dev](DeviceCache& c) -> cudaError_t {
+    cudaError_t e = cudaDeviceGetAttribute(&c.sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
     const char* path = getenv("GK_ATTN_PATH");
     c.fma = path != nullptr && strcmp(path, "fma") == 0;
@@ -1083,15 +1081,12 @@ static cudaError_t device_setup(DeviceCache** out) {
                              int(2 * kMaxBatch * sizeof(int32_t)));
     if (e != cudaSuccess) return e;
     if (c.attn_blocks_per_sm < 1) c.attn_blocks_per_sm = 1;
-    c.dev = dev;
-    c.attrs_set = true;
-  }
-  *out = &c;
-  return cudaSuccess;
+    return cudaSuccess;
+  });
 }
 
 int attention_resident_warps() {
-  DeviceCache* c = nullptr;
+  const DeviceCache* c = nullptr;
   if (device_setup(&c) != cudaSuccess) return 0;
   return c->sms * c->attn_blocks_per_sm * kWarps;
 }
@@ -1108,7 +1103,7 @@ cudaError_t launch_append(const AppendParams& p, cudaStream_t st) {
 cudaError_t launch_quantize(const float* x, float scale, uint8_t* codes, int64_t n,
                             cudaStream_t st) {
   if (n <= 0) return cudaSuccess;
-  DeviceCache* c = nullptr;
+  const DeviceCache* c = nullptr;
   cudaError_t e = device_setup(&c);
   if (e != cudaSuccess) return e;
   const int threads = 256;
@@ -1120,7 +1115,7 @@ cudaError_t launch_quantize(const float* x, float scale, uint8_t* codes, int64_t
 
 cudaError_t launch_attention(const PlanParams& plan, const AttnParams& p, cudaStream_t st,
                              const AppendParams* app) {
-  DeviceCache* c = nullptr;
+  const DeviceCache* c = nullptr;
   cudaError_t e = device_setup(&c);
   if (e != cudaSuccess) return e;
   PlanParams pp = plan;

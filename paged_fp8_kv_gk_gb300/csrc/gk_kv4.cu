@@ -19,6 +19,7 @@
 #include "gk_attn_common.cuh"
 #include "gk_device.cuh"
 #include "gk_internal.h"
+#include "gk_once.h"
 #include "../../include/gk_kv4.h"
 
 namespace gk {
@@ -1067,18 +1068,16 @@ __global__ void __launch_bounds__(kAttn4Threads, 1)
 // =========================================================================
 struct Kv4Device {
   int sms = 0;
-  bool set = false;
 };
-static Kv4Device g_kv4_dev[64];
+static PerDevice<Kv4Device, 64> g_kv4_dev;
 
-static cudaError_t kv4_setup(Kv4Device** out) {
+static cudaError_t kv4_setup(const Kv4Device** out) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  Kv4Device& c = g_kv4_dev[dev];
-  if (!c.set) {
-    e = cudaDeviceGetAttribute(&c.sms, cudaDevAttrMultiProcessorCount, dev);
+  if (dev < 0 || dev >= g_kv4_dev.devices) return cudaErrorInvalidDevice;
+  return g_kv4_dev.get<cudaError_t>(dev, out, [dev](Kv4Device& c) -> cudaError_t {
+    cudaError_t e = cudaDeviceGetAttribute(&c.sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(kv4_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              int(kAttn4Smem));
@@ -1086,12 +1085,8 @@ static cudaError_t kv4_setup(Kv4Device** out) {
     e = cudaFuncSetAttribute(kv4_plan_write_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              int(2 * kMaxBatch * sizeof(int32_t)));
     if (e != cudaSuccess) return e;
-    e = plan_setup();
-    if (e != cudaSuccess) return e;
-    c.set = true;
-  }
-  *out = &c;
-  return cudaSuccess;
+    return plan_setup();
+  });
 }
 
 // Warps of the write and read kernels for one layer.
@@ -1102,7 +1097,7 @@ static int64_t token_warps(const P& p, int tokens) {
 
 cudaError_t launch_kv4_attention(const PlanParams& plan, const AttnParams& p, cudaStream_t st,
                                  const Kv4WriteParams* write) {
-  Kv4Device* c = nullptr;
+  const Kv4Device* c = nullptr;
   const cudaError_t e = kv4_setup(&c);
   if (e != cudaSuccess) return e;
   Kv4PlanWriteParams pw;
@@ -1146,7 +1141,7 @@ static dim3 token_grid(P& p, int tokens, int sms) {
 
 template <typename P>
 static cudaError_t launch_tokens(void (*kernel)(P), P& p, int tokens, cudaStream_t st) {
-  Kv4Device* c = nullptr;
+  const Kv4Device* c = nullptr;
   const cudaError_t e = kv4_setup(&c);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
