@@ -6,6 +6,7 @@
 #define GK_TESTING_H
 
 #include "gk.h"
+#include "gk_kv4.h"
 
 #ifdef __cplusplus
 extern "C" {
@@ -42,6 +43,17 @@ gk_status gk_selftest_decode_attn_split(const gk_shape *shape, const void *q,
                                         const uint8_t *active, const float *sinks, void *out,
                                         float *out_f32, void *workspace, size_t ws_bytes,
                                         int32_t split_tokens, void *stream);
+
+/* gk_selftest_kv4_decode_attn_split -- the same of gk_kv4_decode_attn_stack. */
+gk_status gk_selftest_kv4_decode_attn_split(const gk_shape *shape, const void *q,
+                                            const gk_kv4_cache *kv, const float *k_scale,
+                                            const float *v_scale, const float *cos,
+                                            const float *sin, const int32_t *bt_full,
+                                            const int32_t *bt_swa, const int32_t *pos,
+                                            const int32_t *pos_w, const uint8_t *active,
+                                            const float *sinks, void *out, float *out_f32,
+                                            void *workspace, size_t ws_bytes,
+                                            int32_t split_tokens, void *stream);
 
 #ifdef __cplusplus
 }

@@ -333,6 +333,8 @@ def lib(build_if_needed: bool = True) -> ctypes.CDLL:
                                                    ctypes.POINTER(ctypes.c_uint32)]
             L.gk_selftest_decode_attn_split.restype = ctypes.c_int
             L.gk_selftest_decode_attn_split.argtypes = [sp] + [vp] * 15 + [sz, i32, vp]
+            L.gk_selftest_kv4_decode_attn_split.restype = ctypes.c_int
+            L.gk_selftest_kv4_decode_attn_split.argtypes = [sp] + [vp] * 15 + [sz, i32, vp]
             L.gk_read_device_error.restype = ctypes.c_int
             L.gk_read_device_error.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32), ctypes.c_int]
             _lib = L
@@ -782,6 +784,20 @@ def gk_selftest_decode_attn_split(shape, q, kv: KvCache, k_scale, v_scale, cos, 
         _ptr(workspace, torch.uint8, "workspace"), int(workspace.numel()), int(split_tokens),
         _stream(stream, q))
     _check(st, "gk_selftest_decode_attn_split")
+
+
+def gk_selftest_kv4_decode_attn_split(shape, q, kv, k_scale, v_scale, cos, sin, bt_full, bt_swa,
+                                      pos, pos_w, active, out, out_f32, workspace,
+                                      split_tokens: int, stream=None, sinks=None) -> None:
+    """Test hook (include/gk_testing.h): gk_kv4_decode_attn_stack with the split-KV chunk length
+    fixed to `split_tokens` (a power of two >= 512)."""
+    sh, dev = _as_shape(shape), _current_device()
+    head, mid, tail = _kv4_step_args(sh, dev, q, k_scale, v_scale, cos, sin, bt_full, bt_swa, pos,
+                                     pos_w, active, sinks, out, out_f32, workspace)
+    kv = _kv4(kv, sh, dev)
+    st = lib().gk_selftest_kv4_decode_attn_split(ctypes.byref(sh), *head, ctypes.byref(kv), *mid,
+                                                 *tail, int(split_tokens), _stream(stream, q))
+    _check(st, "gk_selftest_kv4_decode_attn_split")
 
 
 def new_workspace(shape, device="cuda"):

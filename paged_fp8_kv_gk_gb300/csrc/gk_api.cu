@@ -639,6 +639,13 @@ gk_status gk_e4m3_quantize(const float* x, float scale, uint8_t* codes, int64_t 
              : GK_ERR_CUDA;
 }
 
+// log2(split_tokens / kMinSplit), or -1 for a length that the hooks refuse.
+static int split_log(int32_t split_tokens) {
+  for (int k = 0; k < 22; ++k)
+    if ((kMinSplit << k) == split_tokens) return k;
+  return -1;
+}
+
 gk_status gk_selftest_decode_attn_split(const gk_shape* shape, const void* q,
                                         const gk_kv_cache* kv, const float* k_scale,
                                         const float* v_scale, const float* cos, const float* sin,
@@ -647,12 +654,26 @@ gk_status gk_selftest_decode_attn_split(const gk_shape* shape, const void* q,
                                         const uint8_t* active, const float* sinks, void* out,
                                         float* out_f32, void* workspace, size_t ws_bytes,
                                         int32_t split_tokens, void* stream) {
-  int k = -1;
-  for (int c = 0; c < 22; ++c)
-    if ((kMinSplit << c) == split_tokens) k = c;
+  const int k = split_log(split_tokens);
   if (k < 0) return GK_ERR_INVALID_ARG;
   return decode_attention(shape, q, kv, k_scale, v_scale, cos, sin, bt_full, bt_swa, pos, pos_w,
                           active, sinks, out, out_f32, workspace, ws_bytes, stream, nullptr, k);
+}
+
+gk_status gk_selftest_kv4_decode_attn_split(const gk_shape* shape, const void* q,
+                                            const gk_kv4_cache* kv, const float* k_scale,
+                                            const float* v_scale, const float* cos,
+                                            const float* sin, const int32_t* bt_full,
+                                            const int32_t* bt_swa, const int32_t* pos,
+                                            const int32_t* pos_w, const uint8_t* active,
+                                            const float* sinks, void* out, float* out_f32,
+                                            void* workspace, size_t ws_bytes,
+                                            int32_t split_tokens, void* stream) {
+  const int k = split_log(split_tokens);
+  if (k < 0 || !kv) return GK_ERR_INVALID_ARG;
+  return decode_attention(shape, q, nullptr, k_scale, v_scale, cos, sin, bt_full, bt_swa, pos,
+                          pos_w, active, sinks, out, out_f32, workspace, ws_bytes, stream, nullptr,
+                          k, kv);
 }
 
 gk_status gk_selftest_wait_timeout(uint64_t limit_ns, void* stream, uint32_t* bits) {

@@ -261,3 +261,16 @@ def test_group_buffers_above_512_gib_are_refused():
             assert all((x != gk.GK_ERR_UNSUPPORTED) == fits for x in got), (B, Hkv, nb, got)
             assert (L.gk_kv4_block_bytes(s) == 72 * B * Hkv) == fits
             assert L.gk_attn_workspace_min_bytes(s) > 0     # the FP8 cache takes such a shape
+
+
+@no_device
+def test_split_hook_validates_the_length_and_the_cache():
+    L = gk.lib()
+    f = ctypes.c_void_p(FAKE)
+    kvs, keep = _cache()
+    args = [*[f] * 9, None, f, None, f, 1 << 30]
+    for bad in (0, -512, 256, 513, 1000, 3 << 9, 512 << 22):
+        assert L.gk_selftest_kv4_decode_attn_split(ctypes.byref(_shape()), f, ctypes.byref(kvs),
+                                                   *args, bad, None) == gk.GK_ERR_INVALID_ARG, bad
+    assert L.gk_selftest_kv4_decode_attn_split(ctypes.byref(_shape()), f, None, *args, 512,
+                                               None) == gk.GK_ERR_INVALID_ARG
