@@ -225,3 +225,133 @@ def test_plans(cache):
         seen_pieces += p["pieces"] > 0
         seen_splits += p["records"] > 0
     assert seen_pieces >= 3 and seen_splits >= 15, (seen_pieces, seen_splits)
+
+
+# ---------------------------------------------------------------- written bytes
+@pytest.mark.parametrize("name", ["max_batch", "max_layers", "max_block"])
+def test_fused_bytes_of_the_largest_shapes(name):
+    """Every byte of the cache after a fused step of 8192 rows, of 128 layers, of 1024-token blocks:
+    the new tokens' are the plain form's, the others are those that were there."""
+    s = Step(gi.get(name))
+    want = [x.copy() for x in flat(s.cache)]
+    k4.write(want, s.sh, bf16_np(s.step["k_new"]), bf16_np(s.step["v_new"]), s.c.cos, s.c.sin, s.ks,
+             s.vs, s.c.upd_full, s.c.upd_swa, s.c.active)
+    s.fused()
+    assert gk.gk_read_device_error() == 0
+    for got, x in zip(flat(s.cache), want):
+        assert np.array_equal(got, x)
+    check_rows(s, layers=sorted({0, 1, s.w.num_layers - 2, s.w.num_layers - 1}),
+               rows=range(0, s.w.batch, max(1, s.w.batch // 64)))
+
+
+@pytest.mark.parametrize("fused", [False, True])
+def test_written_bytes_beyond_4_gib(fused):
+    """A group buffer of 4.95 GB with the tokens in its last blocks: the bytes there are the plain
+    form's, those at the same offsets modulo 2^32 and 2^31 stay; K and V read back; the attention."""
+    nb, H, B, T = 8400, 8, 1024, 3
+    w = gi.get("max_block").replace(name="far", num_layers=2, num_q_heads=8 * H, num_kv_heads=H,
+                                    num_blocks=nb, seed=91)
+    s = Step(w, cache=torch.empty(1, nb, H, B // 16, gk.GK_KV4_TILE_BYTES, dtype=torch.uint8,
+                                  device="cuda"))
+    bb = gk.gk_kv4_block_bytes(s.sh)
+    used = np.unique(np.concatenate(s.c.full_blocks + s.c.swa_blocks))
+    base = nb - 1 - len(used)
+    assert base * bb > 2 ** 32
+    move = np.full(nb, nb - 1)
+    move[used] = np.arange(base, nb - 1)
+    for n in ("bt_full", "bt_swa"):
+        setattr(s.c, n, move[getattr(s.c, n)].astype(np.int32))
+    for n in ("upd_full", "upd_swa"):
+        u = getattr(s.c, n)
+        setattr(s.c, n, (move[u // B] * B + u % B).astype(np.int32))
+    s.ctl.update({n: torch.as_tensor(getattr(s.c, n)).cuda()
+                  for n in ("bt_full", "bt_swa", "upd_full", "upd_swa")})
+    blocks = s.cache[0].view(nb, bb)
+    small = gpu_cache(w.replace(num_blocks=None), 3)[0].reshape(-1, bb)[:len(used)]
+    blocks[base:nb - 1] = small
+    # what a write with a truncated offset would touch
+    near = sorted({(base * bb - wrap) // bb + k for wrap in (2 ** 31, 2 ** 32)
+                   for k in range(-1, len(used) + 2)} & set(range(base)))
+    blocks[near] = 0x5A
+    want = [small.cpu().numpy().reshape(-1).copy()]
+    shift = {n: (getattr(s.c, n) - base * B).astype(np.int64) for n in ("upd_full", "upd_swa")}
+    k4.write(want, {**s.sh, "num_blocks": len(used)}, bf16_np(s.step["k_new"]),
+             bf16_np(s.step["v_new"]), s.c.cos, s.c.sin, s.ks, s.vs, shift["upd_full"],
+             shift["upd_swa"], s.c.active)
+    assert not np.array_equal(want[0], small.cpu().numpy().reshape(-1))
+    if fused:
+        s.fused()
+    else:
+        s.write()
+        s.attn()
+    assert gk.gk_read_device_error() == 0
+    assert np.array_equal(blocks[base:nb - 1].cpu().numpy().reshape(-1), want[0])
+    assert bool((blocks[near] == 0x5A).all())
+    ko = torch.zeros(2, T, H, 64, dtype=torch.bfloat16, device="cuda")
+    vo = torch.zeros_like(ko)
+    gk.gk_kv4_read(s.sh, s.cache, s.dks, s.dvs, s.ctl["upd_full"], s.ctl["upd_swa"], ko, vo)
+    for i in range(2):
+        k, v = k4.tokens(want[0], shift["upd_full" if i else "upd_swa"], H, B, s.ks[i], s.vs[i])
+        for got, x in ((ko[i], k), (vo[i], v)):
+            got = got.double().cpu().numpy()
+            assert (np.abs(got - x) <= 2.0 ** -8 * np.abs(x) * (1 + 2.0 ** -15)).all()
+    check_rows(s)
+
+
+@pytest.mark.parametrize("T,layers", [(5, 4), (300, 4), (4100, 1)])
+@pytest.mark.parametrize("scale", [0.0029, 0.125])
+def test_rotated_extremes(T, layers, scale):
+    """K and V over bf16's whole range through the rotation: infinities, both zeros, subnormal and
+    huge values whose sum overflows, NaN; angles with cos or sin zero or one among them.  Block
+    scales are the plain form's byte for byte, codes wherever the block is not NaN (there any code
+    reads back as NaN), and no byte of another token changes."""
+    rng = np.random.default_rng(T)
+    H, B = 2, 32
+    sh = dict(num_layers=layers + layers % 2, batch=1, num_q_heads=8 * H, num_kv_heads=H,
+              head_dim=64, block_size=B, num_blocks=-(-2 * T // B) + 1, window=128,
+              max_blocks_full=4, max_blocks_swa=6)
+    NL = sh["num_layers"]
+    bits = rng.integers(0, 2 ** 16, (2, layers, T, H, 64)).astype(np.uint16)
+    special = np.array([0x0000, 0x8000, 0x7F80, 0xFF80, 0x7F7F, 0xFF7F, 0x0001, 0x8001, 0x7FC0],
+                       np.uint16)
+    # tokens of ordinary values, each with some special ones; the others of any value
+    calm = rng.random((2, layers, T, 1, 1)) < 0.7
+    mild = torch.randn(bits.shape, generator=torch.Generator().manual_seed(T)).to(torch.bfloat16)
+    bits = np.where(calm, mild.view(torch.int16).numpy().view(np.uint16), bits)
+    few = rng.random(bits.shape) < 0.01
+    bits = np.where(few, rng.choice(special[:-1], bits.shape), bits)
+    # NaN: a few, no more (a rotated NaN takes two blocks)
+    nan = ((bits & 0x7F80) == 0x7F80) & ((bits & 0x7F) != 0)
+    bits = np.where(nan & (rng.random(bits.shape) < 0.98), bits & 0x7F00, bits)
+    bits[0, 0, 0, 0, 0] = bits[1, -1, -1, -1, -1] = 0x7FC0
+    x = torch.from_numpy(bits.astype(np.uint16).view(np.int16)).view(torch.bfloat16)
+    ang = rng.uniform(-3000, 3000, (T, 32))
+    cos, sin = np.cos(ang).astype(np.float32), np.sin(ang).astype(np.float32)
+    axis = rng.random((T, 32)) < 0.2
+    turn = rng.integers(0, 4, (T, 32))
+    cos = np.where(axis, np.array([1, 0, -1, 0], np.float32)[turn], cos)
+    sin = np.where(axis, np.array([0, 1, 0, -1], np.float32)[turn], sin)
+    slots = rng.permutation(sh["num_blocks"] * B)[:2 * T].astype(np.int32)
+    s = np.full(NL, scale, np.float32)
+    cache = torch.randint(0, 256, (NL // 2, sh["num_blocks"], H, B // 16, gk.GK_KV4_TILE_BYTES),
+                          generator=torch.Generator().manual_seed(1), dtype=torch.uint8).cuda()
+    before = flat(cache)
+    want = [b.copy() for b in before]
+    k, v = x[0].cuda(), x[1].cuda()
+    to = lambda a: torch.as_tensor(a).cuda()  # noqa: E731
+    gk.gk_kv4_write(sh, k, v, to(cos), to(sin), to(s), to(s), to(slots[:T]), to(slots[T:]), cache,
+                    layer0=NL - layers)
+    assert gk.gk_read_device_error() == 0
+    k4.write(want, sh, bf16_np(k), bf16_np(v), cos, sin, s, s, slots[:T], slots[T:],
+             layer0=NL - layers)
+    got, nans = flat(cache), 0
+    for i in range(NL - layers, NL):
+        # codes of NaN blocks take the kernel's value
+        at = k4.addresses(slots[:T] if i & 1 else slots[T:], np.arange(H), H, B)
+        for codes, scales in ((at[0], at[2]), (at[1], at[3])):
+            nan = codes[np.repeat(want[i // 2][scales] == 0x7F, 8, -1)]
+            want[i // 2][nan] = got[i // 2][nan]
+            nans += nan.size
+    for g, w in zip(got, want):
+        assert np.array_equal(g, w), np.argwhere(g != w)[:8].tolist()
+    assert 0 < nans < 0.2 * T * layers * H * 64
