@@ -2,6 +2,10 @@
 many chunks, and chunks are cut for the last wave: every row's error within the bound of
 tests/kv4_norms.py (which sees sixteen keys that are left out), the plan as tests/plan_plain.py has
 it."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -355,3 +359,67 @@ def test_rotated_extremes(T, layers, scale):
     for g, w in zip(got, want):
         assert np.array_equal(g, w), np.argwhere(g != w)[:8].tolist()
     assert 0 < nans < 0.2 * T * layers * H * 64
+
+
+# ---------------------------------------------------------------- windows, first calls in a capture
+@pytest.mark.parametrize("window", [1, 2, 15, 16, 17, 129, 1000, 5000])
+@pytest.mark.parametrize("block", [16, 96])
+def test_windows(window, block):
+    """Windows of one key, of a tile and one more or less, of more tiles than a table window of 32,
+    and longer than every row."""
+    w = gi.get("gptoss_small").replace(name="windows", window=window, block_size=block,
+                                       lengths="fixed:1,16,33,1001,2047,4999", seed=45)
+    s = Step(w, sinks=window % 2 == 0)
+    want = [x.copy() for x in flat(s.cache)]
+    k4.write(want, s.sh, bf16_np(s.step["k_new"]), bf16_np(s.step["v_new"]), s.c.cos, s.c.sin, s.ks,
+             s.vs, s.c.upd_full, s.c.upd_swa, s.c.active)
+    s.fused()
+    assert gk.gk_read_device_error() == 0
+    for got, x in zip(flat(s.cache), want):
+        assert np.array_equal(got, x)
+    check_rows(s)
+    s.check()
+
+
+CAPTURE = r"""
+import torch
+import gk_inputs as gi
+import paged_fp8_kv_gk_gb300 as gk
+from test_gpu_kv4 import Step
+
+s = Step(gi.get("gptoss_small"))
+keep, ko, vo = s.cache.clone(), torch.zeros_like(s.k), torch.zeros_like(s.v)
+torch.cuda.synchronize()
+
+def calls():
+    s.write()
+    gk.gk_kv4_read(s.sh, s.cache, s.dks, s.dvs, s.ctl["upd_full"], s.ctl["upd_swa"], ko, vo)
+    s.attn()
+    s.fused()
+
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    calls()
+s.cache.copy_(keep)
+s.out.fill_(float("nan"))
+g.replay()
+torch.cuda.synchronize()
+got = [x.clone() for x in (s.out, s.out32, s.cache, ko, vo)]
+s.cache.copy_(keep)
+calls()
+torch.cuda.synchronize()
+assert gk.gk_read_device_error() == 0
+assert torch.isfinite(s.out).all()
+for x, y in zip(got, (s.out, s.out32, s.cache, ko, vo)):
+    assert torch.equal(x, y)
+print("capture ok")
+"""
+
+
+def test_first_calls_are_captured():
+    """A process whose first calls of the library are captured into a graph."""
+    here = os.path.dirname(os.path.abspath(__file__))
+    env = {**os.environ, "PYTHONPATH": os.pathsep.join([here, os.path.dirname(here)])}
+    run = subprocess.run([sys.executable, "-c", CAPTURE], capture_output=True, text=True,
+                         timeout=300, env=env)
+    assert run.returncode == 0 and "capture ok" in run.stdout, run.stderr[-3000:]
