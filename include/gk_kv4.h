@@ -53,7 +53,8 @@ typedef struct {
 } gk_kv4_cache;
 
 /* Bytes of one block of one group buffer (K and V), num_kv_heads * B * 72; a
- * pool of `available` bytes holds available / (NL/2 * block_bytes) blocks.
+ * pool of `available` bytes (gk_kv_budget's available_bytes; its num_blocks
+ * counts blocks of the FP8 cache) holds available / (NL/2 * block_bytes) blocks.
  * 0 for an invalid or unsupported shape (num_blocks, batch and the table sizes
  * are checked like everywhere). */
 size_t gk_kv4_block_bytes(const gk_shape *shape);
@@ -112,7 +113,9 @@ gk_status gk_kv4_read(const gk_shape *shape, int32_t layer0, int32_t n_layers, i
  * same arguments, formulas and errors with kv the only difference (k_t, v_t are
  * the values above).  Scores, softmax and sums are fp32; q' and the
  * probabilities enter the tensor-core products as f16, one rounding each
- * (2^-11, against 2^-4 and more of a 4-bit K).  workspace:
+ * (2^-11, against 2^-4 and more of a 4-bit K; gk.h's call keeps two terms of
+ * q').  The softmax's denominator sums the probabilities in fp32 as they are
+ * before that rounding.  workspace:
  * gk_attn_workspace_bytes / gk_attn_workspace_min_bytes of the shape.
  */
 gk_status gk_kv4_decode_attn_stack(const gk_shape *shape, const void *q, const gk_kv4_cache *kv,

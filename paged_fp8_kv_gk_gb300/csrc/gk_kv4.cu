@@ -312,9 +312,12 @@ constexpr int kTokThreads = 128;  // at 256 the write takes 5 us more (8191 toke
 // layer's loads are in flight without holding registers; `rope` (kRopeRows) keeps
 // the tokens' cos and sin where kDepth > 1.
 //
-// Bound by issue slots and the arithmetic's latency: about 470 instructions for
-// 8 tokens' K and V, half of them the two exact divisions.  For 8191
-// tokens of 36 layers (387 MB; window layers keep 128 tokens), in us: one
+// Bound by issue slots and the arithmetic's latency: 540 instructions for 8
+// tokens' K and V, 104 of them the packed products and FMAs of the two exact
+// divisions.  A call of one layer has nothing to load ahead and shares nothing
+// between layers: 36 of them take 300 us where one call of 36 takes 86 (K rotated
+// already: 248).  For 8191 tokens of 36 layers (393 MB; window layers keep 128
+// tokens), in us: one
 // thread a block with divisions as the compiler writes them 240; several layers
 // a thread and packed fp32 arithmetic 152; the next layer's rows in registers
 // (128 of them, 16 warps per SM) 137; 80 registers and 24 warps 118; the ring 106
@@ -565,16 +568,21 @@ __global__ void __launch_bounds__(kPlanThreads)
 // remainder, as over the FP8 cache, attention of the 64-row case took 629 us
 // instead of 557, and K's own rounding is a hundred times coarser.  (Outputs
 // against 64 bits: 2.8e-4 in fp32, 6.1e-4 with q, K and V ~ N(0, 3); the bf16
-// rounding alone is 1.7e-3.)  Scores, reference, sums and outputs are fp32.
+// rounding alone is 1.7e-3.)  Scores, reference, sums and outputs are fp32.  The
+// denominator sums the probabilities before their rounding to f16 (the FP8 kernel
+// sums the rounded ones): of the rounded ones the errors are 1 to 4 % lower
+// (4.07e-4 instead of 4.21e-4 over the peaky workload) and the calls 1.4 to 2.8 %
+// longer, four conversions a tile.
 //
 // What bounds it.  At the copy rate an SM sub-partition has about 197 cycles for a
 // tile (16 tokens, 1152 bytes).  The stage loop issues 112 instructions a tile for
 // the products and the softmax -- 32 conversions of a code pair and 32
-// multiplications by a scale among them -- and about 30 for the ring, the units
-// and the loop, and keeps its issue slot 65-70 % busy with the 16 warps that 118
-// registers allow: 220 cycles.  So long rows run at the memory's rate (8 rows of
-// 131072 keys: 10.9 GB in 1613 us, 6750 GB/s; 64 rows of 1024 to 8192: 3.18 GB in 497 us,
-// 6400) and short ones at the issue rate (512 rows of 64 to 512: 2.49 GB in 482 us).
+// multiplications by a scale among them -- and about 38 for the ring, the units
+// and the loop (150 in all by the counter), and keeps its issue slot 65-70 % busy
+// with the 16 warps that 116 registers allow: 220 cycles.  So long rows run at the
+// memory's rate (whole calls, planner and combine among them: 8 rows of 131072 keys,
+// 10.9 GB in 1614 us, 6750 GB/s; 64 rows of 1024 to 8192, 3.18 GB in 493 us, 6450) and
+// short ones at the issue rate (512 rows of 64 to 512: 2.49 GB in 476 us).
 //
 // Why this form (64-row case): 1152-byte bulk copies issued in the warp, two-tile
 // stages 836 us; the same copies by a producer warp, a lane a warp 722 (a bulk
@@ -582,7 +590,7 @@ __global__ void __launch_bounds__(kPlanThreads)
 // asynchronous copies by the lanes, 15 warps and three stages 651, 16 warps and
 // two stages 628 (14 warps 664, 12 warps 643); one f16 for q' 557; interleaving
 // nibbles by one logic operation, packed fp32, places of 32 tiles at a time 504;
-// the next unit's descriptor a word a lane 497.  20 warps at 96 registers
+// the next unit's descriptor a word a lane 497, edge masks by one compare 495.  20 warps at 96 registers
 // recompute more than they hide (536), and so do two tiles at a time (559).
 constexpr int kStTiles = 4;     // tiles per pipeline stage
 constexpr int kStages4 = 2;     // ring depth per warp
