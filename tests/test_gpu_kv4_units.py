@@ -423,3 +423,84 @@ def test_first_calls_are_captured():
     run = subprocess.run([sys.executable, "-c", CAPTURE], capture_output=True, text=True,
                          timeout=300, env=env)
     assert run.returncode == 0 and "capture ok" in run.stdout, run.stderr[-3000:]
+
+
+# ---------------------------------------------------------------- largest calls, shared workspaces
+@pytest.mark.parametrize("block,ws", [(16, "recommended"), (1024, "recommended"), (96, "minimum")])
+def test_a_row_of_a_million_keys(block, ws):
+    """1048583 keys beside rows of 5 and 70000, one kv head: 64 chunks of the long row, or one unit of
+    16385 stages."""
+    w = gi.get("gk120b_rank_small").replace(name="million", num_layers=2, batch=3, block_size=block,
+                                            lengths="fixed:5,1048583,70000", seed=46)
+    s = Step(w, cache=gpu_cache(w, 9), sinks=True)
+    if ws == "minimum":
+        s.ws = torch.empty(gk.gk_attn_workspace_min_bytes(s.sh), dtype=torch.uint8, device="cuda")
+    s.attn()
+    assert gk.gk_read_device_error() == 0
+    assert (header(s)[6] > 0) == (ws == "recommended")
+    check_rows(s)
+
+
+def test_most_tokens_of_a_call():
+    """2^28 tokens of one kv head written in a call (all but a few left out; one row of K and V for
+    all of them, by a stride of 0), 2^28 + 1 refused; 2^26 + 3 read, offsets beyond 2^32 elements."""
+    sh = dict(num_layers=2, batch=1, num_q_heads=8, num_kv_heads=1, head_dim=64, block_size=16,
+              num_blocks=4, window=128, max_blocks_full=4, max_blocks_swa=9)
+    T, n = 2 ** 28, 2 ** 26 + 3
+    at = [0, 7, 8, 12345678, n - 1, 2 ** 27 + 1, T - 9, T - 1]
+    slots = np.array([3, 0, 63, 20, 17, 40, 33, 48], np.int32)
+    slot = torch.full((T,), gk.GK_KV4_SKIP, dtype=torch.int32, device="cuda")
+    slot[torch.as_tensor(at)] = torch.as_tensor(slots).cuda()
+    skip = torch.full_like(slot, gk.GK_KV4_SKIP)
+    row = torch.randn(2, 64, generator=torch.Generator().manual_seed(4)).to(torch.bfloat16)
+    k, v = (x.cuda().view(1, 1, 1, 64).expand(1, T, 1, 64) for x in row)
+    one = torch.ones(2, device="cuda")
+    cache = torch.full((1, 4, 1, 1, gk.GK_KV4_TILE_BYTES), 0x11, dtype=torch.uint8, device="cuda")
+    want = [x.copy() for x in flat(cache)]
+    gk.gk_kv4_write(sh, k, v, None, None, one, one, slot, skip, cache, layer0=1)
+    assert gk.gk_read_device_error() == 0
+    x = row.float().numpy()
+    k4.write(want, sh, *(np.broadcast_to(r, (1, 8, 1, 64)) for r in x), None, None,
+             np.ones(2, np.float32), np.ones(2, np.float32), slots, None, layer0=1)
+    assert np.array_equal(flat(cache)[0], want[0])
+    more = torch.full((T + 1,), gk.GK_KV4_SKIP, dtype=torch.int32, device="cuda")
+    with pytest.raises(gk.GkError) as e:
+        gk.gk_kv4_write(sh, *(r.cuda().view(1, 1, 1, 64).expand(1, T + 1, 1, 64) for r in row), None,
+                        None, one, one, more, more, cache, layer0=1)
+    assert e.value.status == gk.GK_ERR_UNSUPPORTED
+    del more, k, v
+    ko = torch.zeros(1, n, 1, 64, dtype=torch.bfloat16, device="cuda")
+    vo = torch.zeros_like(ko)
+    gk.gk_kv4_read(sh, cache, one, one, slot[:n], skip[:n], ko, vo, layer0=1)
+    assert gk.gk_read_device_error() == 0
+    here = [a for a in at if a < n]
+    wk, wv = k4.tokens(want[0], slots[:len(here)], 1, 16, 1, 1)
+    for got, values in ((ko, wk), (vo, wv)):
+        assert torch.equal(got[0, here].cpu(), torch.as_tensor(values).float().to(torch.bfloat16))
+        got[0, here] = 0
+        assert not any(bool(part.any()) for part in got.view(-1).split(2 ** 30))
+
+
+def test_two_graphs_share_a_workspace():
+    """Two fused steps captured with one workspace, replayed in turn with nothing between them."""
+    a, b = Step(gi.get("long_small"), seed=11, sinks=True), Step(gi.get("ragged_small"), seed=12)
+    ws = a.ws if a.ws.numel() > b.ws.numel() else b.ws
+    graphs = []
+    for s in (a, b):
+        s.ws = ws
+        s.fused(out32=None)
+        torch.cuda.synchronize()
+        s.want = s.out.clone()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            s.fused(out32=None)
+        graphs.append(g)
+    for s in (a, b):
+        s.out.fill_(float("nan"))
+    torch.cuda.synchronize()
+    for rep in range(6):
+        for g in graphs if rep % 2 else graphs[::-1]:
+            g.replay()
+    torch.cuda.synchronize()
+    assert gk.gk_read_device_error() == 0
+    assert torch.equal(a.out, a.want) and torch.equal(b.out, b.want)
