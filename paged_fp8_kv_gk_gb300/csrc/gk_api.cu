@@ -31,7 +31,10 @@ static gk_status check_shape(const gk_shape* s) {
   if (s->max_blocks_swa < need_swa) return GK_ERR_INVALID_ARG;
   // flat slots (block * B + offset) are int32
   if (int64_t(s->num_blocks) * s->block_size > INT32_MAX) return GK_ERR_UNSUPPORTED;
-  if (int64_t(s->max_blocks_full) * s->block_size > INT32_MAX / 2) return GK_ERR_UNSUPPORTED;
+  // so are positions and the tables' lengths in tokens
+  if (int64_t(s->max_blocks_full) * s->block_size > INT32_MAX / 2 ||
+      int64_t(s->max_blocks_swa) * s->block_size > INT32_MAX / 2)
+    return GK_ERR_UNSUPPORTED;
   return GK_OK;
 }
 

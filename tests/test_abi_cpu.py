@@ -239,3 +239,23 @@ def test_split_hook_exported_and_validates_the_length():
                                              *([FAKE] * 9), None, FAKE, None, FAKE, 1 << 30, bad,
                                              None)
         assert st == gk.GK_ERR_INVALID_ARG, bad
+
+
+@no_device
+def test_window_tables_of_2_30_tokens_are_refused():
+    """A window table row of more than INT32_MAX / 2 tokens, like a full one, is refused: its length
+    in tokens is an int32 in the planner."""
+    L = gk.lib()
+    base = dict(num_layers=4, batch=1, num_q_heads=8, num_kv_heads=1, head_dim=64, block_size=32,
+                num_blocks=8, window=128, max_blocks_full=4, max_blocks_swa=6)
+    for key in ("max_blocks_full", "max_blocks_swa"):
+        for blocks, ok in ((2 ** 25 - 1, True), (2 ** 25, False), (2 ** 26, False),
+                           (2 ** 26 + 2, False), (2 ** 31 - 1, False)):
+            sh = gk.Shape.make(**{**base, key: blocks})
+            assert (L.gk_attn_workspace_min_bytes(ctypes.byref(sh)) > 0) == ok, (key, blocks)
+            assert (L.gk_kv4_block_bytes(ctypes.byref(sh)) > 0) == ok, (key, blocks)
+    wide = gk.Shape.make(**{**base, "window": 2 ** 31 - 1, "max_blocks_swa": 2 ** 26 + 2})
+    kvs, arrs = _kv_struct()
+    st = L.gk_decode_attn_stack(ctypes.byref(wide), FAKE, ctypes.byref(kvs), *([FAKE] * 9), None,
+                                FAKE, None, FAKE, 1 << 30, None)
+    assert st == gk.GK_ERR_UNSUPPORTED
