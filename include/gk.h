@@ -71,7 +71,8 @@
  *                     V byte (pb, h, t, e) = ((pb*Hkv + h)*B + t)*D + e
  * Supported shapes: D == 64, G == 8, B == 16 or a multiple of 32 up to 1024,
  * NL even and <= 128, Bt <= 8192, slots (num_blocks * B) within int32 and rows of
- * either table below 2^30 tokens.  Other shapes return GK_ERR_UNSUPPORTED.
+ * either table below 2^30 tokens, NL * Hkv * Bt < 2^31.  Other shapes return
+ * GK_ERR_UNSUPPORTED.
  */
 #ifndef GK_H
 #define GK_H

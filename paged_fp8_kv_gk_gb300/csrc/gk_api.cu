@@ -35,6 +35,9 @@ static gk_status check_shape(const gk_shape* s) {
   if (int64_t(s->max_blocks_full) * s->block_size > INT32_MAX / 2 ||
       int64_t(s->max_blocks_swa) * s->block_size > INT32_MAX / 2)
     return GK_ERR_UNSUPPORTED;
+  // and work units: a full and a window one for each (layer pair, kv head, row)
+  if (int64_t(s->num_layers / 2) * s->num_kv_heads * 2 * s->batch > INT32_MAX)
+    return GK_ERR_UNSUPPORTED;
   return GK_OK;
 }
 

@@ -259,3 +259,26 @@ def test_window_tables_of_2_30_tokens_are_refused():
     st = L.gk_decode_attn_stack(ctypes.byref(wide), FAKE, ctypes.byref(kvs), *([FAKE] * 9), None,
                                 FAKE, None, FAKE, 1 << 30, None)
     assert st == gk.GK_ERR_UNSUPPORTED
+
+
+def test_more_work_units_than_an_int32_are_refused():
+    """Two units for each (layer pair, kv head, row) at least, counted in int32: a shape beyond that
+    is refused (2^26 kv heads of 128 layers once divided by zero on the host)."""
+    L = gk.lib()
+    for layers, heads, batch, ok in ((4, 2 ** 28, 2, True), (4, 2 ** 28, 3, False),
+                                     (128, 2 ** 24 - 1, 1, True), (128, 2 ** 24, 1, False),
+                                     (128, 2 ** 26, 1, False), (128, 2047, 8192, True),
+                                     (128, 2048, 8192, False), (128, 2 ** 28 - 1, 8192, False)):
+        sh = gk.Shape.make(num_layers=layers, batch=batch, num_q_heads=8 * heads if heads < 2 ** 28
+                           else 2 ** 31 - 8, num_kv_heads=heads if heads < 2 ** 28 else 2 ** 28 - 1,
+                           head_dim=64, block_size=16, num_blocks=1, window=1, max_blocks_full=1,
+                           max_blocks_swa=2)
+        s = ctypes.byref(sh)
+        assert (L.gk_attn_workspace_min_bytes(s) > 0) == ok, (layers, heads, batch)
+        assert (L.gk_kv4_block_bytes(s) > 0) == ok, (layers, heads, batch)
+        if not ok:
+            kvs, arrs = _kv_struct()
+            kv4 = gk.Kv4CacheC(None, FAKE)
+            for fn, kv in ((L.gk_decode_attn_stack, kvs), (L.gk_kv4_decode_attn_stack, kv4)):
+                assert fn(s, FAKE, ctypes.byref(kv), *[FAKE] * 9, None, FAKE, None, FAKE, 1 << 40,
+                          None) == gk.GK_ERR_UNSUPPORTED
