@@ -540,8 +540,9 @@ gk_status gk_kv_budget(uint64_t total_bytes, uint64_t used_bytes, double gmu, do
     if (shape->num_layers < 2 || (shape->num_layers & 1) || shape->num_kv_heads < 1 ||
         shape->block_size < 1 || shape->head_dim < 1)
       return GK_ERR_INVALID_ARG;
-    const uint64_t per_block = uint64_t(shape->num_layers / 2) * 2 * uint64_t(shape->num_kv_heads) *
-                               uint64_t(shape->block_size) * uint64_t(shape->head_dim);
+    // four int32 factors: up to 2^124
+    const unsigned __int128 per_block = (unsigned __int128)(shape->num_layers / 2) * 2 *
+                                        shape->num_kv_heads * shape->block_size * shape->head_dim;
     *num_blocks = int64_t(available / per_block);
     too_small = too_small || *num_blocks < 2;
   }

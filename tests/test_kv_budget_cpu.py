@@ -81,3 +81,13 @@ def test_invalid_arguments():
                          (0.9, 0.3, -1.0)):
         assert L.gk_kv_budget(10, 0, gmu, cap, mn, None, ctypes.byref(a), None) == gk.GK_ERR_INVALID_ARG
     assert L.gk_kv_budget(10, 0, 0.9, 0.3, 0.0, None, None, None) == gk.GK_ERR_INVALID_ARG
+
+
+def test_blocks_of_any_size():
+    """A block of more than 2^64 bytes (its size once wrapped to 0, a division by zero): none fits."""
+    for big in (dict(num_kv_heads=16, block_size=2 ** 30, head_dim=2 ** 30),
+                dict(num_kv_heads=2 ** 31 - 1, block_size=2 ** 31 - 1, head_dim=2 ** 31 - 1)):
+        shape = dict(num_layers=2, batch=1, num_q_heads=8, num_blocks=1, window=1,
+                     max_blocks_full=1, max_blocks_swa=1, **big)
+        st, available, blocks = gk.gk_kv_budget(2 ** 38, 0, 0.9, shape=shape)
+        assert (st, blocks) == (gk.GK_ERR_BUDGET, 0) and available > 2 ** 34
