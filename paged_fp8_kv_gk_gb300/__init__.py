@@ -12,7 +12,9 @@ The functions carry the C names: ``gk_kv_append``, ``gk_decode_attn_stack``,
 ``gk_di_blocks``, ``gk_read_device_error``, ``gk_status_str``, ``gk_abi_version``; and, over a
 4-bit cache (``include/gk_kv4.h``; a ``Kv4Cache`` or its tensors, ``new_kv4_cache``),
 ``gk_kv4_write``, ``gk_kv4_read``, ``gk_kv4_decode_attn_stack``, ``gk_kv4_decode_step``,
-``gk_kv4_block_bytes``.  Tensors are torch tensors; the stream defaults to torch's current stream
+``gk_kv4_block_bytes``; and, for a prompt's pass (``include/gk_prompt.h``), ``gk_rope_table``,
+``gk_rope``, ``gk_kv_write``, ``gk_kv_read``, ``gk_prompt_plan_bytes``, ``gk_prompt_plan``,
+``gk_prompt_attn`` (plans: ``new_prompt_plan``).  Tensors are torch tensors; the stream defaults to torch's current stream
 on the tensors' device.  The cache is a ``KvCache``: per-group
 K and V buffers or stacked ``K_cache`` / ``V_cache``, exactly one of the two,
 with packed-ness read from the K tensors' rank as the "GPT-OSS-120B giga-kernel
@@ -34,9 +36,13 @@ GK_DEVERR_SLOT, GK_DEVERR_BLOCK, GK_DEVERR_POS, GK_DEVERR_TIMEOUT, GK_DEVERR_PLA
     GK_DEVERR_INGEST = 0x1, 0x2, 0x4, 0x8, 0x10, 0x20
 GK_K_PACKED, GK_K_PLAIN = 0, 1
 GK_KV4_TILE_BYTES, GK_KV4_SKIP = 1152, -1
+GK_KV_SKIP, GK_DEVERR_SEQ = -1, 0x40
+GK_ROPE_PLAIN, GK_ROPE_LINEAR, GK_ROPE_YARN = 0, 1, 2
+GK_ROPE_HALF, GK_ROPE_INTERLEAVED = 0, 1
 
 HEADER = os.path.join(_build.INCLUDE, "gk.h")
 KV4_HEADER = os.path.join(_build.INCLUDE, "gk_kv4.h")
+PROMPT_HEADER = os.path.join(_build.INCLUDE, "gk_prompt.h")
 
 _lock = threading.Lock()
 _lib = None
@@ -58,6 +64,30 @@ class Shape(ctypes.Structure):
     @classmethod
     def make(cls, **kw) -> "Shape":
         return cls(**{k: int(v) for k, v in kw.items()})
+
+
+class RopeParams(ctypes.Structure):
+    """gk_rope_params; ``make`` takes the scaling by name ("none", "linear", "yarn") or number."""
+    _fields_ = [("rot_dim", ctypes.c_int32), ("scaling", ctypes.c_int32)] + [
+        (n, ctypes.c_double) for n in ("theta", "factor", "original_context", "beta_fast",
+                                       "beta_slow")]
+    SCALING = {"none": GK_ROPE_PLAIN, "linear": GK_ROPE_LINEAR, "yarn": GK_ROPE_YARN}
+
+    @classmethod
+    def make(cls, rot_dim, theta, scaling="none", factor=1.0, original_context=4096.0,
+             beta_fast=32.0, beta_slow=1.0) -> "RopeParams":
+        if scaling in cls.SCALING:
+            scaling = cls.SCALING[scaling]
+        elif isinstance(scaling, str):
+            raise ValueError(f"scaling {scaling!r}: one of {sorted(cls.SCALING)}")
+        return cls(int(rot_dim), int(scaling), float(theta), float(factor),
+                   float(original_context), float(beta_fast), float(beta_slow))
+
+
+class Prompt(ctypes.Structure):
+    """gk_prompt: all int32."""
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "num_seqs", "num_q_heads", "num_kv_heads", "head_dim", "window", "q_tokens", "k_tokens")]
 
 
 class KvRegion(ctypes.Structure):
@@ -328,6 +358,21 @@ def lib(build_if_needed: bool = True) -> ctypes.CDLL:
             L.gk_kv4_decode_attn_stack.argtypes = [sp] + [vp] * 15 + [sz, vp]
             L.gk_kv4_decode_step.restype = ctypes.c_int
             L.gk_kv4_decode_step.argtypes = [sp] + [vp] * 19 + [sz, vp]
+            L.gk_rope_table.restype = ctypes.c_int
+            L.gk_rope_table.argtypes = [ctypes.POINTER(RopeParams), i64] + [vp] * 4
+            L.gk_rope.restype = ctypes.c_int
+            L.gk_rope.argtypes = [i64, i32, i32, i32, i32, vp, i64, vp, vp, vp, i64, vp]
+            L.gk_kv_write.restype = ctypes.c_int
+            L.gk_kv_write.argtypes = [sp, i32, i32, i64, vp, vp, i64, i64] + [vp] * 9
+            L.gk_kv_read.restype = ctypes.c_int
+            L.gk_kv_read.argtypes = [sp, i32, i32, i64] + [vp] * 9
+            pp = ctypes.POINTER(Prompt)
+            L.gk_prompt_plan_bytes.restype = sz
+            L.gk_prompt_plan_bytes.argtypes = [pp]
+            L.gk_prompt_plan.restype = ctypes.c_int
+            L.gk_prompt_plan.argtypes = [pp, vp, vp, vp, sz, vp]
+            L.gk_prompt_attn.restype = ctypes.c_int
+            L.gk_prompt_attn.argtypes = [pp, vp, sz, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp]
             L.gk_selftest_wait_timeout.restype = ctypes.c_int
             L.gk_selftest_wait_timeout.argtypes = [ctypes.c_uint64, vp,
                                                    ctypes.POINTER(ctypes.c_uint32)]
@@ -754,6 +799,179 @@ def gk_kv4_decode_step(shape, q, k_new, v_new, cos, sin, k_scale, v_scale, upd_f
     st = lib().gk_kv4_decode_step(ctypes.byref(sh), *head, *mid, ctypes.byref(kv), *tail,
                                   _stream(stream, q))
     _check(st, "gk_kv4_decode_step")
+
+
+# --------------------------------------------------------------- a prompt's pass
+def gk_rope_table(params, pos, cos, sin, stream=None) -> None:
+    """cos and sin, fp32 [n, rot_dim / 2], of the positions `pos` (int32 [n]).  params: a RopeParams
+    or its fields (rot_dim, theta, scaling "none", "linear" or "yarn", factor, ...)."""
+    torch = _torch()
+    dev = _current_device()
+    if not isinstance(params, RopeParams):
+        params = RopeParams.make(**params)
+    n = pos.numel()
+    want = n * params.rot_dim // 2
+    st = lib().gk_rope_table(
+        ctypes.byref(params), n, _ptr4(pos, torch.int32, "pos", dev, n),
+        _ptr4(cos, torch.float32, "cos", dev, want), _ptr4(sin, torch.float32, "sin", dev, want),
+        _stream(stream, pos))
+    _check(st, "gk_rope_table")
+
+
+def _heads(t, name, dev, heads=None, dim=None):
+    """Checks of a bf16 [tokens, heads, channels] tensor with contiguous heads, as slices of a fused
+    projection are; returns (tokens, heads, channels, token stride)."""
+    if t.dtype is not _torch().bfloat16:
+        raise TypeError(f"{name}: expected {_torch().bfloat16}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (no CPU path)")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+    if t.dim() != 3 or (heads is not None and t.shape[1:] != (heads, dim)):
+        raise ValueError(f"{name} must be [tokens, "
+                         f"{'heads, channels' if heads is None else f'{heads}, {dim}'}]")
+    T, H, D = t.shape
+    if t.numel() and ((D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D)):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return T, H, D, t.stride(0) if T > 1 else H * D
+
+
+def gk_rope(x, cos, sin, out, layout="half", stream=None) -> None:
+    """Rotate the heads of x by cos and sin (fp32 [n, rot_dim / 2]; channels from rot_dim on are
+    copied) into out, which may be x.  x, out: bf16 [n, heads, head_dim], the heads of a token
+    contiguous, tokens of any stride that is a multiple of 8.  layout: "half" (pairs e, e +
+    rot_dim / 2) or "interleaved" (pairs 2e, 2e + 1)."""
+    torch = _torch()
+    dev = _current_device()
+    n, H, D, xs = _heads(x, "x", dev)
+    m, _, _, os_ = _heads(out, "out", dev, H, D)
+    if m != n:
+        raise ValueError(f"out has {m} tokens, x has {n}")
+    if layout not in ("half", "interleaved"):
+        raise ValueError(f"layout {layout!r}: 'half' or 'interleaved'")
+    if cos.dim() != 2 or cos.shape[0] != n or sin.shape != cos.shape:
+        raise ValueError(f"cos and sin must be [{n}, rot_dim / 2]")
+    rot = 2 * cos.shape[1]
+    st = lib().gk_rope(
+        n, H, D, rot, GK_ROPE_HALF if layout == "half" else GK_ROPE_INTERLEAVED, x.data_ptr(), xs,
+        _ptr4(cos, torch.float32, "cos", dev, 0), _ptr4(sin, torch.float32, "sin", dev, 0),
+        out.data_ptr(), os_, _stream(stream, x))
+    _check(st, "gk_rope")
+
+
+def _kv_on(kv, sh, dev):
+    """_kv, of a cache on device `dev` (the current one: the library launches there)."""
+    c = _kv(kv, sh)
+    for t in kv._keep[0] + kv._keep[1]:
+        if not isinstance(t, int) and t.get_device() != dev:
+            raise ValueError(f"a cache buffer is on cuda:{t.get_device()}, the current device is "
+                             f"cuda:{dev}")
+    return c
+
+
+def gk_kv_write(shape, k, v, cos, sin, k_scale, v_scale, slot_full, slot_swa, kv: KvCache,
+                active=None, layer0: int = 0, stream=None) -> None:
+    """Rotate, quantise and write the K and V of tokens into the FP8 cache.
+
+    k, v: bf16 [n_layers, n_tokens, kv, 64] of layers layer0 ..; the heads of a token are
+    contiguous, layers and tokens may have any stride that is a multiple of 8.  cos, sin: fp32
+    [n_tokens, 32], or both None for K that is rotated already.  slot_full, slot_swa: int32
+    [n_tokens], GK_KV_SKIP to leave a token out."""
+    torch = _torch()
+    f32, i32 = torch.float32, torch.int32
+    sh, dev = _as_shape(shape), _current_device()
+    n, T, (ls, ts) = _kv4_rows(sh, k, v, ("k", "v"), dev, False)
+    rope = T * sh.head_dim // 2
+    st = lib().gk_kv_write(
+        ctypes.byref(sh), int(layer0), n, T, k.data_ptr(), v.data_ptr(), ls, ts,
+        _ptr4(cos, f32, "cos", dev, rope, True), _ptr4(sin, f32, "sin", dev, rope, True),
+        _ptr4(k_scale, f32, "k_scale", dev, sh.num_layers),
+        _ptr4(v_scale, f32, "v_scale", dev, sh.num_layers),
+        _ptr4(slot_full, i32, "slot_full", dev, T), _ptr4(slot_swa, i32, "slot_swa", dev, T),
+        _ptr4(active, torch.uint8, "active", dev, T, True), _kv_on(kv, sh, dev),
+        _stream(stream, k))
+    _check(st, "gk_kv_write")
+
+
+def gk_kv_read(shape, kv: KvCache, k_scale, v_scale, slot_full, slot_swa, k_out, v_out,
+               active=None, layer0: int = 0, stream=None) -> None:
+    """The values at the given slots of the FP8 cache, as bf16 [n_layers, n_tokens, kv, 64]
+    (contiguous) of layers layer0 ..; the rows of skipped tokens are left as they were."""
+    torch = _torch()
+    f32, i32 = torch.float32, torch.int32
+    sh, dev = _as_shape(shape), _current_device()
+    n, T, _ = _kv4_rows(sh, k_out, v_out, ("k_out", "v_out"), dev, True)
+    st = lib().gk_kv_read(
+        ctypes.byref(sh), int(layer0), n, T, _kv_on(kv, sh, dev),
+        _ptr4(k_scale, f32, "k_scale", dev, sh.num_layers),
+        _ptr4(v_scale, f32, "v_scale", dev, sh.num_layers),
+        _ptr4(slot_full, i32, "slot_full", dev, T), _ptr4(slot_swa, i32, "slot_swa", dev, T),
+        _ptr4(active, torch.uint8, "active", dev, T, True), k_out.data_ptr(), v_out.data_ptr(),
+        _stream(stream, k_out))
+    _check(st, "gk_kv_read")
+
+
+def _as_prompt(prompt) -> Prompt:
+    if isinstance(prompt, Prompt):
+        return prompt
+    try:
+        return Prompt(**prompt)
+    except TypeError:      # values that are not plain ints
+        return Prompt(**{k: int(v) for k, v in prompt.items()})
+
+
+def gk_prompt_plan_bytes(prompt) -> int:
+    return int(lib().gk_prompt_plan_bytes(ctypes.byref(_as_prompt(prompt))))
+
+
+def new_prompt_plan(prompt, device="cuda"):
+    """Room for the plan of a prompt's attention (gk_prompt_plan fills it)."""
+    import torch
+    n = gk_prompt_plan_bytes(prompt)
+    if n == 0:
+        raise GkError(GK_ERR_UNSUPPORTED, "gk_prompt_plan_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def gk_prompt_plan(prompt, q_start, k_start, plan, stream=None) -> None:
+    """Work out the tiles of a prompt's attention from the sequences' starts (int32 [num_seqs + 1] on
+    the device), for every layer with these sequences and this window.  prompt: a Prompt or its
+    fields."""
+    torch = _torch()
+    pr, dev = _as_prompt(prompt), _current_device()
+    st = lib().gk_prompt_plan(
+        ctypes.byref(pr), _ptr4(q_start, torch.int32, "q_start", dev, pr.num_seqs + 1),
+        _ptr4(k_start, torch.int32, "k_start", dev, pr.num_seqs + 1),
+        _ptr4(plan, torch.uint8, "plan", dev, 1), plan.numel(), _stream(stream, q_start))
+    _check(st, "gk_prompt_plan")
+
+
+def gk_prompt_attn(prompt, plan, q, k, v, out, out_f32=None, sinks=None, stream=None) -> None:
+    """Causal attention of packed sequences, one layer, along a plan of gk_prompt_plan.
+
+    q: bf16 [q_tokens, q heads, 64]; k, v: bf16 [k_tokens, kv heads, 64]; the heads of a token are
+    contiguous, tokens may have any stride that is a multiple of 8.  out (bf16) and out_f32 are
+    contiguous; their rows outside every sequence are left as they were.  sinks: fp32 [q heads]."""
+    torch = _torch()
+    pr, dev = _as_prompt(prompt), _current_device()
+    Hq, H, D = pr.num_q_heads, pr.num_kv_heads, pr.head_dim
+    strides = []
+    for t, name, rows, heads in ((q, "q", pr.q_tokens, Hq), (k, "k", pr.k_tokens, H),
+                                 (v, "v", pr.k_tokens, H)):
+        T, _, _, s = _heads(t, name, dev, heads, D)
+        if T < rows:
+            raise ValueError(f"{name} has {T} tokens, the prompt {rows}")
+        strides.append(s)
+    if sinks is not None and sinks.numel() != Hq:
+        raise ValueError(f"sinks must hold num_q_heads = {Hq} values")
+    n = pr.q_tokens * Hq * D
+    st = lib().gk_prompt_attn(
+        ctypes.byref(pr), _ptr4(plan, torch.uint8, "plan", dev, 1), plan.numel(), q.data_ptr(),
+        strides[0], k.data_ptr(), strides[1], v.data_ptr(), strides[2],
+        _ptr4(sinks, torch.float32, "sinks", dev, 1, True),
+        _ptr4(out, torch.bfloat16, "out", dev, n),
+        _ptr4(out_f32, torch.float32, "out_f32", dev, n, True), _stream(stream, q))
+    _check(st, "gk_prompt_attn")
 
 
 def gk_selftest_wait_timeout(limit_ns: int, stream=None) -> int:

@@ -1,10 +1,12 @@
 // gk_api.cu -- extern "C" entry points declared in include/gk.h: argument
 // validation, workspace layout and kernel launches.  No allocation.
 #include <cuda_runtime.h>
+#include <math.h>
 #include <string.h>
 
 #include "gk_internal.h"
 #include "../../include/gk_kv4.h"
+#include "../../include/gk_prompt.h"
 #include "../../include/gk_testing.h"
 
 namespace gk {
@@ -155,6 +157,25 @@ WsLayout ws_layout(const gk_shape& s, size_t ws_bytes) {
   cap = cap + 2 < cmax_of(s) ? cap + 2 : cmax_of(s);
   place(cap);
   while (cap > 0 && L.total > ws_bytes) place(--cap);
+  return L;
+}
+
+PromptLayout prompt_layout(const gk_prompt& s) {
+  PromptLayout L;
+  L.tile_tokens = kPromptRows / (s.num_q_heads / s.num_kv_heads);
+  // a sequence's last tile may be short; every tile has a token
+  L.tiles = int64_t(s.q_tokens) / L.tile_tokens + s.num_seqs;
+  if (L.tiles > s.q_tokens) L.tiles = s.q_tokens;
+  // Keys are split only where whole tiles would leave slots empty or the last wave
+  // thin; two waves of parts at most (a record is 33 KB: 21 MB).
+  L.max_recs = L.tiles * s.num_kv_heads < 2 * kPromptSlots ? 640 / s.num_kv_heads : 0;
+  if (L.max_recs < 2 || s.k_tokens <= 4 * kPromptKeys) L.max_recs = 0;
+  L.max_items = L.tiles + L.max_recs;
+  L.items = kPromptHdrWords * sizeof(int32_t);
+  L.splits = align256(L.items + size_t(L.max_items) * 2 * sizeof(int4));
+  // a split tile has two records at least
+  L.records = align256(L.splits + size_t(L.max_recs / 2) * sizeof(int4));
+  L.total = align256(L.records + size_t(L.max_recs) * s.num_kv_heads * kPromptRecFloats * sizeof(float));
   return L;
 }
 
@@ -441,10 +462,9 @@ size_t gk_kv4_block_bytes(const gk_shape* shape) {
   return check_kv4_shape(shape) == GK_OK ? size_t(kv4_block_bytes(*shape)) : 0;
 }
 
-// Checks that gk_kv4_write and gk_kv4_read share.
-static gk_status check_kv4_tokens(const gk_shape* shape, int32_t layer0, int32_t n_layers,
-                                  int64_t n_tokens) {
-  const gk_status st = check_kv4_shape(shape);
+// Checks that the write and the read of given tokens share (`st`: the shape's).
+static gk_status check_tokens(gk_status st, const gk_shape* shape, int32_t layer0,
+                              int32_t n_layers, int64_t n_tokens) {
   if (st != GK_OK) return st;
   if (layer0 < 0 || n_layers < 0 || layer0 > shape->num_layers - n_layers || n_tokens < 0)
     return GK_ERR_INVALID_ARG;
@@ -456,7 +476,7 @@ gk_status gk_kv4_write(const gk_shape* shape, int32_t layer0, int32_t n_layers, 
                        const float* cos, const float* sin, const float* k_scale,
                        const float* v_scale, const int32_t* slot_full, const int32_t* slot_swa,
                        const uint8_t* active, const gk_kv4_cache* kv, void* stream) {
-  gk_status st = check_kv4_tokens(shape, layer0, n_layers, n_tokens);
+  gk_status st = check_tokens(check_kv4_shape(shape), shape, layer0, n_layers, n_tokens);
   if (st != GK_OK) return st;
   if (n_layers == 0 || n_tokens == 0) return GK_OK;
   if (!k || !v || !k_scale || !v_scale || !slot_full || !slot_swa || !aligned16(k) ||
@@ -493,7 +513,7 @@ gk_status gk_kv4_read(const gk_shape* shape, int32_t layer0, int32_t n_layers, i
                       const gk_kv4_cache* kv, const float* k_scale, const float* v_scale,
                       const int32_t* slot_full, const int32_t* slot_swa, const uint8_t* active,
                       void* k_out, void* v_out, void* stream) {
-  gk_status st = check_kv4_tokens(shape, layer0, n_layers, n_tokens);
+  gk_status st = check_tokens(check_kv4_shape(shape), shape, layer0, n_layers, n_tokens);
   if (st != GK_OK) return st;
   if (n_layers == 0 || n_tokens == 0) return GK_OK;
   if (!k_out || !v_out || !k_scale || !v_scale || !slot_full || !slot_swa || !aligned16(k_out) ||
@@ -520,6 +540,264 @@ gk_status gk_kv4_read(const gk_shape* shape, int32_t layer0, int32_t n_layers, i
   p.B = shape->block_size;
   p.nb = shape->num_blocks;
   return launch_kv4_read(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GK_OK : GK_ERR_CUDA;
+}
+
+gk_status gk_kv_write(const gk_shape* shape, int32_t layer0, int32_t n_layers, int64_t n_tokens,
+                      const void* k, const void* v, int64_t layer_stride, int64_t token_stride,
+                      const float* cos, const float* sin, const float* k_scale,
+                      const float* v_scale, const int32_t* slot_full, const int32_t* slot_swa,
+                      const uint8_t* active, const gk_kv_cache* kv, void* stream) {
+  gk_status st = check_tokens(check_shape(shape), shape, layer0, n_layers, n_tokens);
+  if (st != GK_OK) return st;
+  if (n_layers == 0 || n_tokens == 0) return GK_OK;
+  if (!k || !v || !k_scale || !v_scale || !slot_full || !slot_swa || !aligned16(k) ||
+      !aligned16(v) || (layer_stride & 7) || (token_stride & 7) ||
+      (cos != nullptr) != (sin != nullptr) || !aligned16(cos) || !aligned16(sin))
+    return GK_ERR_INVALID_ARG;
+  KvWriteParams p;
+  memset(&p, 0, sizeof(p));
+  st = resolve_kv(*shape, kv, p.kb, p.vb, &p.k_packed);
+  if (st != GK_OK) return st;
+  p.k = static_cast<const uint16_t*>(k);
+  p.v = static_cast<const uint16_t*>(v);
+  p.layer_stride = layer_stride;
+  p.token_stride = token_stride;
+  p.cosb = cos;
+  p.sinb = sin;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.slot_full = slot_full;
+  p.slot_swa = slot_swa;
+  p.active = active;
+  p.layer0 = layer0;
+  p.n_layers = n_layers;
+  p.n_tokens = int(n_tokens);
+  p.fd_b = make_fastdiv(uint32_t(shape->block_size));
+  p.Hkv = shape->num_kv_heads;
+  p.B = shape->block_size;
+  p.nb = shape->num_blocks;
+  return launch_kv_write(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GK_OK : GK_ERR_CUDA;
+}
+
+gk_status gk_kv_read(const gk_shape* shape, int32_t layer0, int32_t n_layers, int64_t n_tokens,
+                     const gk_kv_cache* kv, const float* k_scale, const float* v_scale,
+                     const int32_t* slot_full, const int32_t* slot_swa, const uint8_t* active,
+                     void* k_out, void* v_out, void* stream) {
+  gk_status st = check_tokens(check_shape(shape), shape, layer0, n_layers, n_tokens);
+  if (st != GK_OK) return st;
+  if (n_layers == 0 || n_tokens == 0) return GK_OK;
+  if (!k_out || !v_out || !k_scale || !v_scale || !slot_full || !slot_swa || !aligned16(k_out) ||
+      !aligned16(v_out))
+    return GK_ERR_INVALID_ARG;
+  KvReadParams p;
+  memset(&p, 0, sizeof(p));
+  uint8_t* kb[kMaxGroups];
+  uint8_t* vb[kMaxGroups];
+  st = resolve_kv(*shape, kv, kb, vb, &p.k_packed);
+  if (st != GK_OK) return st;
+  for (int j = 0; j < shape->num_layers / 2; ++j) {
+    p.kb[j] = kb[j];
+    p.vb[j] = vb[j];
+  }
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.slot_full = slot_full;
+  p.slot_swa = slot_swa;
+  p.active = active;
+  p.k_out = static_cast<uint16_t*>(k_out);
+  p.v_out = static_cast<uint16_t*>(v_out);
+  p.layer0 = layer0;
+  p.n_layers = n_layers;
+  p.n_tokens = int(n_tokens);
+  p.fd_b = make_fastdiv(uint32_t(shape->block_size));
+  p.Hkv = shape->num_kv_heads;
+  p.B = shape->block_size;
+  p.nb = shape->num_blocks;
+  return launch_kv_read(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GK_OK : GK_ERR_CUDA;
+}
+
+gk_status gk_rope_table(const gk_rope_params* params, int64_t n, const int32_t* pos, float* cos,
+                        float* sin, void* stream) {
+  // comparisons that a NaN fails
+  if (!params || n < 0 || !(params->theta > 1.0) || !isfinite(params->theta) ||
+      params->rot_dim < 2 || (params->rot_dim & 1))
+    return GK_ERR_INVALID_ARG;
+  const gk_rope_params& r = *params;
+  const int half = r.rot_dim / 2;
+  double low = 0, high = 1;
+  switch (r.scaling) {
+    case GK_ROPE_PLAIN: break;
+    case GK_ROPE_LINEAR:
+      if (!(r.factor > 0.0) || !isfinite(r.factor)) return GK_ERR_INVALID_ARG;
+      break;
+    case GK_ROPE_YARN: {
+      if (!(r.factor >= 1.0) || !isfinite(r.factor) || !(r.original_context > 0.0) ||
+          !isfinite(r.original_context) || !(r.beta_slow > 0.0) ||
+          !(r.beta_fast > r.beta_slow) || !isfinite(r.beta_fast))
+        return GK_ERR_INVALID_ARG;
+      auto pair = [&](double beta) {
+        return half * ::log(r.original_context / (beta * 2 * M_PI)) / ::log(r.theta);
+      };
+      low = fmax(pair(r.beta_fast), 0.0);
+      high = fmin(pair(r.beta_slow), double(r.rot_dim - 1));
+      break;
+    }
+    default: return GK_ERR_INVALID_ARG;
+  }
+  if ((r.rot_dim & 15) || half > kMaxRopePairs || n > (int64_t(1) << 28)) return GK_ERR_UNSUPPORTED;
+  if (n == 0) return GK_OK;
+  if (!pos || !cos || !sin || (reinterpret_cast<uintptr_t>(pos) & 3u) || !aligned16(cos) ||
+      !aligned16(sin))
+    return GK_ERR_INVALID_ARG;
+  RopeTableParams p;
+  memset(&p, 0, sizeof(p));
+  p.pos = pos;
+  p.cosb = cos;
+  p.sinb = sin;
+  p.n = n;
+  p.half = half;
+  p.scale = r.scaling == GK_ROPE_YARN ? float(0.1 * ::log(r.factor) + 1.0) : 1.f;
+  for (int e = 0; e < half; ++e) {
+    double f = pow(r.theta, -double(e) / half);
+    if (r.scaling == GK_ROPE_LINEAR) f /= r.factor;
+    if (r.scaling == GK_ROPE_YARN) {
+      const double slow = fmin(fmax((e - low) / fmax(high - low, 1e-3), 0.0), 1.0);
+      f = f * (1 - slow) + f / r.factor * slow;
+    }
+    const double turns = fmod(f / (2 * M_PI), 1.0);
+    p.freq[e] = uint64_t(ldexp(turns, 64));
+  }
+  return launch_rope_table(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GK_OK
+                                                                               : GK_ERR_CUDA;
+}
+
+gk_status gk_rope(int64_t n, int32_t num_heads, int32_t head_dim, int32_t rot_dim, int32_t layout,
+                  const void* x, int64_t x_stride, const float* cos, const float* sin, void* out,
+                  int64_t out_stride, void* stream) {
+  if (n < 0 || num_heads < 1 || head_dim < 2 || rot_dim < 2 || rot_dim > head_dim ||
+      (layout != GK_ROPE_HALF && layout != GK_ROPE_INTERLEAVED))
+    return GK_ERR_INVALID_ARG;
+  if ((head_dim & 15) || (rot_dim & 15) || head_dim > 2 * kMaxRopePairs || num_heads > 65535 ||
+      n > (int64_t(1) << 28))
+    return GK_ERR_UNSUPPORTED;
+  if (n == 0) return GK_OK;
+  const int64_t row = int64_t(num_heads) * head_dim;
+  if (!x || !out || !cos || !sin || !aligned16(x) || !aligned16(out) || !aligned16(cos) ||
+      !aligned16(sin) || (x_stride & 7) || (out_stride & 7) ||
+      (n > 1 && (x_stride < row || out_stride < row)) ||
+      (n > 1 && x == out && x_stride != out_stride))
+    return GK_ERR_INVALID_ARG;
+  RopeParams p;
+  p.x = static_cast<const uint16_t*>(x);
+  p.out = static_cast<uint16_t*>(out);
+  p.cosb = cos;
+  p.sinb = sin;
+  p.n = n;
+  p.x_stride = x_stride;
+  p.out_stride = out_stride;
+  p.heads = num_heads;
+  p.head_dim = head_dim;
+  p.rot_dim = rot_dim;
+  p.interleaved = layout == GK_ROPE_INTERLEAVED;
+  p.chunks = head_dim / 16;
+  return launch_rope(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GK_OK : GK_ERR_CUDA;
+}
+
+static gk_status check_prompt(const gk_prompt* s) {
+  if (!s || s->num_seqs < 1 || s->num_q_heads < 1 || s->num_kv_heads < 1 || s->head_dim < 1 ||
+      s->window < 0 || s->q_tokens < 0 || s->k_tokens < 0 || s->num_q_heads % s->num_kv_heads != 0)
+    return GK_ERR_INVALID_ARG;
+  if (s->head_dim != kHeadDim || s->num_q_heads / s->num_kv_heads > kPromptRows ||
+      s->num_seqs > kPromptMaxSeqs || s->q_tokens > (1 << 28) || s->k_tokens > (1 << 28))
+    return GK_ERR_UNSUPPORTED;
+  // a CTA for each item and kv head
+  return prompt_layout(*s).max_items * s->num_kv_heads > INT32_MAX ? GK_ERR_UNSUPPORTED : GK_OK;
+}
+
+// Window in keys: none reaches further than any key.
+static int prompt_window(const gk_prompt& s) {
+  return s.window == 0 || s.window > (1 << 29) ? 1 << 29 : s.window;
+}
+
+size_t gk_prompt_plan_bytes(const gk_prompt* prompt) {
+  return check_prompt(prompt) == GK_OK ? prompt_layout(*prompt).total : 0;
+}
+
+gk_status gk_prompt_plan(const gk_prompt* prompt, const int32_t* q_start, const int32_t* k_start,
+                         void* plan, size_t plan_bytes, void* stream) {
+  const gk_status st = check_prompt(prompt);
+  if (st != GK_OK) return st;
+  if (!q_start || !k_start || (reinterpret_cast<uintptr_t>(q_start) & 3u) ||
+      (reinterpret_cast<uintptr_t>(k_start) & 3u))
+    return GK_ERR_INVALID_ARG;
+  const PromptLayout L = prompt_layout(*prompt);
+  if (!plan || (reinterpret_cast<uintptr_t>(plan) & 255u) || plan_bytes < L.total)
+    return GK_ERR_WORKSPACE;
+  uint8_t* ws = static_cast<uint8_t*>(plan);
+  PromptPlanParams p;
+  p.q_start = q_start;
+  p.k_start = k_start;
+  p.hdr = reinterpret_cast<int32_t*>(ws);
+  p.items = reinterpret_cast<int4*>(ws + L.items);
+  p.splits = reinterpret_cast<int4*>(ws + L.splits);
+  p.max_items = L.max_items;
+  p.max_recs = L.max_recs;
+  p.num_seqs = prompt->num_seqs;
+  p.Hkv = prompt->num_kv_heads;
+  p.W = prompt_window(*prompt);
+  p.q_tokens = prompt->q_tokens;
+  p.k_tokens = prompt->k_tokens;
+  p.tile_tokens = L.tile_tokens;
+  return launch_prompt_plan(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GK_OK
+                                                                                : GK_ERR_CUDA;
+}
+
+gk_status gk_prompt_attn(const gk_prompt* prompt, void* plan, size_t plan_bytes, const void* q,
+                         int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                         int64_t v_stride, const float* sinks, void* out, float* out_f32,
+                         void* stream) {
+  const gk_status st = check_prompt(prompt);
+  if (st != GK_OK) return st;
+  const gk_prompt& s = *prompt;
+  if (s.q_tokens == 0) return GK_OK;
+  const int64_t q_row = int64_t(s.num_q_heads) * kHeadDim, k_row = int64_t(s.num_kv_heads) * kHeadDim;
+  // k and v of no token may be null
+  if (!q || !out || (s.k_tokens > 0 && (!k || !v)) || !aligned16(q) || !aligned16(k) ||
+      !aligned16(v) || !aligned16(out) || !aligned16(out_f32) ||
+      (reinterpret_cast<uintptr_t>(sinks) & 3u) || (q_stride & 7) || (k_stride & 7) ||
+      (v_stride & 7) || (s.q_tokens > 1 && q_stride < q_row) ||
+      (s.k_tokens > 1 && (k_stride < k_row || v_stride < k_row)))
+    return GK_ERR_INVALID_ARG;
+  const PromptLayout L = prompt_layout(s);
+  if (!plan || (reinterpret_cast<uintptr_t>(plan) & 255u) || plan_bytes < L.total)
+    return GK_ERR_WORKSPACE;
+  uint8_t* ws = static_cast<uint8_t*>(plan);
+  PromptAttnParams p;
+  memset(&p, 0, sizeof(p));
+  p.q = static_cast<const uint16_t*>(q);
+  p.k = static_cast<const uint16_t*>(k);
+  p.v = static_cast<const uint16_t*>(v);
+  p.sinks = sinks;
+  p.out = static_cast<uint16_t*>(out);
+  p.out_f32 = out_f32;
+  p.hdr = reinterpret_cast<const int32_t*>(ws);
+  p.items = reinterpret_cast<const int4*>(ws + L.items);
+  p.splits = reinterpret_cast<const int4*>(ws + L.splits);
+  p.records = reinterpret_cast<float*>(ws + L.records);
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.max_items = L.max_items;
+  p.max_recs = L.max_recs;
+  p.Hq = s.num_q_heads;
+  p.Hkv = s.num_kv_heads;
+  p.G = s.num_q_heads / s.num_kv_heads;
+  p.W = prompt_window(s);
+  p.q_tokens = s.q_tokens;
+  p.k_tokens = s.k_tokens;
+  p.tile_tokens = L.tile_tokens;
+  return launch_prompt_attn(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GK_OK
+                                                                                : GK_ERR_CUDA;
 }
 
 gk_status gk_kv_budget(uint64_t total_bytes, uint64_t used_bytes, double gmu, double cap_fraction,
@@ -699,7 +977,11 @@ gk_status gk_read_device_error(void* stream, uint32_t* bits, int clear) {
   if (read_ingest_error(&ingest_bits, clear != 0) != cudaSuccess) return GK_ERR_CUDA;
   uint32_t kv4_bits = 0;
   if (read_kv4_error(&kv4_bits, clear != 0) != cudaSuccess) return GK_ERR_CUDA;
-  *bits |= ingest_bits | kv4_bits;
+  uint32_t tokens_bits = 0, prompt_bits = 0;
+  if (read_tokens_error(&tokens_bits, clear != 0) != cudaSuccess ||
+      read_prompt_error(&prompt_bits, clear != 0) != cudaSuccess)
+    return GK_ERR_CUDA;
+  *bits |= ingest_bits | kv4_bits | tokens_bits | prompt_bits;
   return *bits ? GK_ERR_DEVICE_BOUNDS : GK_OK;
 }
 

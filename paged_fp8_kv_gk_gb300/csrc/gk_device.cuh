@@ -195,6 +195,20 @@ __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
   return r;
 }
 
+// Four finite fp32 -> four E4M3 codes (a.x -> low byte), as above.
+__device__ __forceinline__ uint32_t f32x4_to_e4m3x4(float2 a, float2 b) {
+  uint32_t d;
+  asm("{\n"
+      " .reg .b16 l, h;\n"
+      " cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n"
+      " cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n"
+      " mov.b32 %0, {l, h};\n"
+      "}\n"
+      : "=r"(d)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
 __device__ __forceinline__ float bf16lo_to_f32(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16hi_to_f32(uint32_t w) {
   return __uint_as_float(w & 0xffff0000u);

@@ -8,6 +8,7 @@
 #include <stdint.h>
 
 #include "../../include/gk.h"
+#include "../../include/gk_prompt.h"
 
 namespace gk {
 
@@ -178,6 +179,107 @@ struct Kv4ReadParams {
   FastDiv fd_b;
 };
 
+struct KvWriteParams {
+  const uint16_t* k;
+  const uint16_t* v;
+  int64_t layer_stride, token_stride;  // elements
+  const float* cosb;  // null with sinb: K is rotated already
+  const float* sinb;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* slot_full;
+  const int32_t* slot_swa;
+  const uint8_t* active;  // or null
+  uint8_t* kb[kMaxGroups];
+  uint8_t* vb[kMaxGroups];
+  int k_packed, layer0, n_layers, n_tokens, Hkv, B, nb;
+  int seg;  // layers a CTA takes (set by the launcher)
+  FastDiv fd_b;
+};
+
+struct KvReadParams {
+  const uint8_t* kb[kMaxGroups];
+  const uint8_t* vb[kMaxGroups];
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* slot_full;
+  const int32_t* slot_swa;
+  const uint8_t* active;  // or null
+  uint16_t* k_out;
+  uint16_t* v_out;
+  int k_packed, layer0, n_layers, n_tokens, Hkv, B, nb;
+  int seg;  // layers a CTA takes (set by the launcher)
+  FastDiv fd_b;
+};
+
+constexpr int kMaxRopePairs = 128;
+
+struct RopeTableParams {
+  const int32_t* pos;
+  float* cosb;
+  float* sinb;
+  int64_t n;
+  int half;     // R / 2
+  float scale;  // of both outputs
+  uint64_t freq[kMaxRopePairs];  // turns a position, times 2^64, modulo 2^64
+};
+
+struct RopeParams {
+  const uint16_t* x;
+  uint16_t* out;
+  const float* cosb;
+  const float* sinb;
+  int64_t n, x_stride, out_stride;
+  int heads, head_dim, rot_dim, interleaved;
+  int chunks;  // head_dim / 16
+};
+
+// A prompt's attention.  A tile is up to kPromptRows / G tokens of one sequence
+// (G = Hq / Hkv): its rows are (token, q head of one kv head).  An item is a tile
+// with a run of its keys; the plan lists the items, longest first.
+constexpr int kPromptRows = 128;      // rows of a tile
+constexpr int kPromptKeys = 128;      // keys of a step
+constexpr int kPromptSlots = 2 * 152; // CTAs that a GB300 runs at a time
+constexpr int kPromptMaxSeqs = 8192;
+constexpr int kPromptHdrWords = 64;
+// results of a split item for one kv head: m[128], l[128], o[128][64]
+constexpr int kPromptRecFloats = kPromptRows * (2 + kHeadDim);
+
+struct PromptLayout {
+  size_t items, splits, records, total;
+  int64_t tiles;     // most tiles
+  int64_t max_items;
+  int64_t max_recs;  // items of split tiles (0: nothing is split)
+  int tile_tokens;
+};
+PromptLayout prompt_layout(const gk_prompt& s);
+
+struct PromptPlanParams {
+  const int32_t* q_start;
+  const int32_t* k_start;
+  int32_t* hdr;   // 0: items, 1: split tiles
+  int4* items;    // two an item: (q0, tokens, own key of q0, first key), (end key, record or -1)
+  int4* splits;   // a split tile: (q0, tokens, first record, records)
+  int64_t max_items, max_recs;
+  int num_seqs, Hkv, W, q_tokens, k_tokens, tile_tokens;
+};
+
+struct PromptAttnParams {
+  const uint16_t* q;
+  const uint16_t* k;
+  const uint16_t* v;
+  const float* sinks;
+  uint16_t* out;
+  float* out_f32;
+  const int32_t* hdr;
+  const int4* items;
+  const int4* splits;
+  float* records;
+  int64_t q_stride, k_stride, v_stride;  // elements
+  int64_t max_items, max_recs;
+  int Hq, Hkv, G, W, q_tokens, k_tokens, tile_tokens;
+};
+
 // Launchers (gk_kernels.cu).  They return the launch status.
 cudaError_t launch_append(const AppendParams& p, cudaStream_t st);
 cudaError_t launch_quantize(const float* x, float scale, uint8_t* codes, int64_t n, cudaStream_t st);
@@ -214,5 +316,17 @@ cudaError_t launch_kv4_read(Kv4ReadParams& p, cudaStream_t st);
 cudaError_t launch_kv4_attention(const PlanParams& plan, const AttnParams& p, cudaStream_t st,
                                  const Kv4WriteParams* write);
 cudaError_t read_kv4_error(uint32_t* bits, bool clear);
+// gk_tokens.cu: given tokens of the FP8 cache, with its own device error word.
+cudaError_t launch_kv_write(KvWriteParams& p, cudaStream_t st);
+cudaError_t launch_kv_read(KvReadParams& p, cudaStream_t st);
+cudaError_t read_tokens_error(uint32_t* bits, bool clear);
+// gk_prompt.cu: planner, attention and joining of split tiles, with their own
+// device error word.
+cudaError_t launch_prompt_plan(const PromptPlanParams& p, cudaStream_t st);
+cudaError_t launch_prompt_attn(const PromptAttnParams& p, cudaStream_t st);
+cudaError_t read_prompt_error(uint32_t* bits, bool clear);
+// gk_rope.cu
+cudaError_t launch_rope_table(const RopeTableParams& p, cudaStream_t st);
+cudaError_t launch_rope(const RopeParams& p, cudaStream_t st);
 
 }  // namespace gk

@@ -16,7 +16,7 @@
 
 #include <algorithm>
 
-#include "gk_attn_common.cuh"
+#include "gk_token.cuh"
 #include "gk_device.cuh"
 #include "gk_internal.h"
 #include "gk_once.h"
@@ -115,50 +115,6 @@ __device__ __forceinline__ uint32_t f32x8_to_e2m1x8(float2 a, float2 b, float2 c
   return r;
 }
 
-// a * b + c in both components.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 r;
-  asm("{\n"
-      " .reg .b64 a, b, c;\n"
-      " mov.b64 a, {%2, %3};\n"
-      " mov.b64 b, {%4, %5};\n"
-      " mov.b64 c, {%6, %7};\n"
-      " fma.rn.f32x2 a, a, b, c;\n"
-      " mov.b64 {%0, %1}, a;\n"
-      "}\n"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return r;
-}
-
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 r;
-  asm("{\n"
-      " .reg .b64 a, b;\n"
-      " mov.b64 a, {%2, %3};\n"
-      " mov.b64 b, {%4, %5};\n"
-      " mul.rn.f32x2 a, a, b;\n"
-      " mov.b64 {%0, %1}, a;\n"
-      "}\n"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return r;
-}
-
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 r;
-  asm("{\n"
-      " .reg .b64 a, b;\n"
-      " mov.b64 a, {%2, %3};\n"
-      " mov.b64 b, {%4, %5};\n"
-      " add.rn.f32x2 a, a, b;\n"
-      " mov.b64 {%0, %1}, a;\n"
-      "}\n"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return r;
-}
-
 // The low nibble of every byte from a, the high one from b.
 __device__ __forceinline__ uint32_t low_nibbles(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -166,21 +122,10 @@ __device__ __forceinline__ uint32_t low_nibbles(uint32_t a, uint32_t b) {
   return r;
 }
 
-// max(|a|, |b|, |c|), NaN when one of them is.
-__device__ __forceinline__ float max3_abs_nan(float a, float b, float c) {
-  float r;
-  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
 __device__ __forceinline__ float rcp_approx(float x) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
-}
-
-__device__ __forceinline__ float2 bf16x2_to_f32x2(uint32_t w) {
-  return make_float2(bf16lo_to_f32(w), bf16hi_to_f32(w));
 }
 
 // =========================================================================
@@ -208,33 +153,6 @@ __device__ __forceinline__ bool token_slot(const P& p, const int32_t* slots, int
   if (slot != GK_KV4_SKIP) set_error(GK_DEVERR_SLOT);
   slot = GK_KV4_SKIP;
   return false;
-}
-
-// What divides by a layer scale.
-struct LayerScale {
-  float scale;
-  float rcp;   // 1 / scale, correctly rounded; 0 outside 2^-40 .. 2^40
-  bool exact;  // rcp is 1 / scale
-};
-__device__ __forceinline__ LayerScale layer_scale(float s) {
-  const float a = fabsf(s);
-  return {s, a >= 0x1p-40f && a <= 0x1p40f ? __frcp_rn(s) : 0.f, exact_reciprocal(s) != 0.f};
-}
-
-// -(x / s), correctly rounded, for |x| < 2^60: a quotient by 1 / s in two terms
-// (nh, nl), then one correction by the exact remainder (Markstein) with nr =
-// -RN(1 / s).  The first leaves q0 within 1/2 + 2^-19 of a step of x / s; the
-// second adds the rest up to a part e = |s RN(1 / s) - 1| of it, S 2^-49 of a step
-// at most for s's significand S in [2^23, 2^24).  x / s is at least 1 / (2 S) of a
-// step away from the middle of two floats, and S^2 (1 + 2^-18) < 2^48 for every S
-// below 2^24 - 64; above, even S have an e below 2^-36 and odd ones were checked at
-// every x whose quotient is that near to a middle.  For |x| < 2^-100 the remainder
-// may underflow; such a quotient is far below half of the smallest block scale and
-// only its sign counts.  The terms have one sign and the quotient is negated, so
-// that a zero comes out of x + q0 s and q0 - rem / s with its own.
-__device__ __forceinline__ float2 neg_div(float2 x, float2 s, float2 nr, float2 nh, float2 nl) {
-  const float2 q0 = fma2(x, nh, mul2(x, nl));
-  return fma2(fma2(q0, s, x), nr, q0);
 }
 
 // Quantise the 16 values x / scale: E4M3 code of the block scale, E2M1 codes.
@@ -290,15 +208,6 @@ __device__ __forceinline__ uint32_t quantise16(float2 (&x)[8], const LayerScale&
   codes = make_uint2(f32x8_to_e2m1x8(y[0], y[1], y[2], y[3]),
                      f32x8_to_e2m1x8(y[4], y[5], y[6], y[7]));
   return sfc;
-}
-
-// The write and read grids are programmatic dependents of the kernel before
-// them and touch nothing until it is complete; only then may the next grid
-// launch (its CTAs or a planner's work, which waits for this grid before it
-// ends, so that nothing runs two kernels ahead).
-__device__ __forceinline__ void follow_stream() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;");
 }
 
 constexpr int kWriteTok = 8;  // tokens a warp writes at a time: four lanes each

@@ -1,0 +1,225 @@
+"""Attention of packed prompts on the GPU against the plain form in 64 bits (tests/prompt_plain.py),
+within the tolerance that it derives."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import paged_fp8_kv_gk_gb300 as gk
+import prompt_plain as pp
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+    gk.lib()
+    gk.gk_read_device_error(clear=True)
+
+
+def i32(a):
+    return torch.tensor([int(x) for x in a], dtype=torch.int32, device="cuda")
+
+
+class Case:
+    def __init__(self, nq, nk, Hkv=1, G=8, window=0, sinks=False, pad=0, fused=False, seed=0, spread=1.0):
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+
+        def randn(*size):
+            return torch.randn(size, generator=gen, device="cuda").to(torch.bfloat16)
+        Hq = Hkv * G
+        self.qs = np.concatenate(([0], np.cumsum(nq))).tolist()
+        self.ks = np.concatenate(([0], np.cumsum(nk))).tolist()
+        Tq, Tk = self.qs[-1] + pad, self.ks[-1] + pad
+        if fused:
+            assert list(nq) == list(nk)
+            qkv = randn(Tq, Hq + 2 * Hkv, 64)
+            self.q, self.k, self.v = qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:]
+        else:
+            self.q, self.k, self.v = randn(Tq, Hq, 64), randn(Tk, Hkv, 64), randn(Tk, Hkv, 64)
+        if spread != 1.0:
+            self.q.mul_(spread)
+        self.sinks = torch.randn(Hq, generator=gen, device="cuda") * 3 if sinks else None
+        self.window = window
+        self.prompt = dict(num_seqs=len(nq), num_q_heads=Hq, num_kv_heads=Hkv, head_dim=64,
+                           window=window, q_tokens=Tq, k_tokens=Tk)
+        self.plan = gk.new_prompt_plan(self.prompt)
+        gk.gk_prompt_plan(self.prompt, i32(self.qs), i32(self.ks), self.plan)
+
+    def run(self, plan=None):
+        size = (self.prompt["q_tokens"], self.prompt["num_q_heads"], 64)
+        out = torch.full(size, 7.0, dtype=torch.bfloat16, device="cuda")
+        f32 = torch.full(size, 7.0, device="cuda")
+        gk.gk_prompt_attn(self.prompt, self.plan if plan is None else plan, self.q, self.k, self.v,
+                          out, f32, sinks=self.sinks)
+        return out, f32
+
+    def check(self, out=None, f32=None):
+        if out is None:
+            out, f32 = self.run()
+        assert gk.gk_read_device_error() == 0
+        want, tol = pp.attention(self.q, self.k, self.v, self.qs, self.ks, self.window, self.sinks)
+        n = self.qs[-1]
+        assert (out[n:] == 7).all() and (f32[n:] == 7).all()      # padding: left as it was
+        out, f32, want, tol = out[:n].double(), f32[:n].double(), want[:n], tol[:n]
+        nan = want.isnan()
+        assert (f32.isnan() | f32.isinf())[nan].all() and f32[~nan].isfinite().all()
+        d = (f32 - want).abs()
+        worst = (d / tol)[~nan]
+        assert (d <= tol)[~nan].all(), (float(worst.max()), (d > tol).nonzero()[:6].tolist())
+        d = (out - want).abs() - 2.0 ** -8 * (want.abs() + tol)    # and half a step of the output
+        assert (d <= tol)[~nan].all()
+        return float(worst.max()) if worst.numel() else 0.0
+
+
+@pytest.mark.parametrize("n", [1, 2, 15, 16, 17, 31, 33, 127, 128, 129, 143, 144, 145, 257, 500])
+@pytest.mark.parametrize("window", [0, 1, 20, 128])
+def test_one_sequence(n, window):
+    Case([n], [n], window=window, sinks=n % 2 == 0, fused=True, pad=3, seed=n).check()
+
+
+@pytest.mark.parametrize("G", [1, 2, 3, 5, 6, 7, 8, 16, 48, 64, 128])
+@pytest.mark.parametrize("Hkv", [1, 3])
+def test_groups(G, Hkv):
+    """Heads that do not divide a tile's rows, one head, and a token that fills the tile."""
+    Case([1, 70, 33], [5, 70, 290], Hkv=Hkv, G=G, window=40 * (G & 1), sinks=True, seed=G).check()
+
+
+def test_ragged_batch():
+    rng = np.random.default_rng(1)
+    n = rng.integers(0, 300, 40)
+    n[[0, 7, 8, 39]] = 0
+    Case(n, n, Hkv=2, sinks=True, pad=61, fused=True).check()
+
+
+@pytest.mark.parametrize("window", [0, 1, 100, 128, 1000, 5000])
+def test_context_in_front(window):
+    """Queries that are the last tokens of longer keys, one token among them, and more queries than
+    keys (the first ones see nothing: zeros), and sequences without keys or without queries."""
+    nq = [1, 8, 129, 0, 20, 3, 1, 64]
+    nk = [1, 1000, 2049, 50, 7, 0, 4097, 64]
+    c = Case(nq, nk, Hkv=2, window=window, sinks=window == 128, seed=window)
+    c.check()
+    out, f32 = c.run()
+    q0 = c.qs[4]
+    assert (out[q0:q0 + 13] == 0).all() and (f32[c.qs[5]:c.qs[6]] == 0).all()
+
+
+@pytest.mark.parametrize("nq,nk,Hkv", [(1, 30000, 1), (8, 8184, 8), (5, 65536, 2), (40, 20011, 1)])
+def test_split_keys(nq, nk, Hkv):
+    """Few queries over long contexts: the keys are split over the GPU and joined."""
+    c = Case([nq, 1], [nk, 700], Hkv=Hkv, sinks=True, seed=nq)
+    assert c.plan.numel() > 1 << 20
+    c.check()
+    c = Case([nq, 2], [nk, 9001], Hkv=Hkv, window=3000, seed=nq)
+    c.check()
+
+
+@pytest.mark.parametrize("spread", [0.0, 8.0, 40.0])
+def test_peaked_scores(spread):
+    """All scores alike, and scores so far apart that the maximum moves and dominates."""
+    Case([300, 40], [300, 1500], Hkv=1, sinks=True, seed=3, spread=spread).check()
+
+
+def test_rising_scores():
+    """A maximum that rises by more than 2^8 at every step of keys."""
+    c = Case([200], [2000], Hkv=1, seed=5)
+    c.k.copy_((torch.arange(2000, device="cuda").float()[:, None, None] / 200).expand_as(c.k))
+    c.q.fill_(1.0)
+    c.check()
+    c.q.fill_(-1.0)
+    c.check()
+
+
+def test_long_prompt():
+    c = Case([3001], [3001], Hkv=1, sinks=True, fused=True, seed=8)
+    c.check()
+
+
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+def test_values_of_unseen_keys(value):
+    """K and V of keys that a row does not see (other sequences', padding, later tokens of its own, or
+    before its window) do not reach it; V that it sees does."""
+    nq, nk = [40, 50, 200], [40, 300, 200]
+    for window in (0, 64):
+        c = Case(nq, nk, Hkv=2, window=window, pad=20, seed=2)
+        c.k[c.ks[-1]:] = value
+        c.v[c.ks[-1]:] = value
+        c.k[:40] = value                # a whole sequence
+        c.v[:40] = value
+        c.v[c.ks[2] + 77, 1] = value    # one token of the last
+        c.v[c.ks[2] + 140, 0, 5] = value
+        out, f32 = c.run()
+        q2 = c.qs[2]
+        assert f32[40:q2].isfinite().all()
+        assert f32[q2:q2 + 77, 8:].isfinite().all() and not f32[q2 + 77, 8:].isfinite().any()
+        assert f32[q2:q2 + 140, :8].isfinite().all()
+        if window:
+            assert f32[q2 + 77 + 64:, 8:].isfinite().all()
+        c.k[:40] = 0                    # the formula has no value for it
+        c.v[:40] = 0
+        c.check()
+
+
+def test_strides_beyond_32_bits():
+    """Tokens so far apart that offsets pass 2^31 elements."""
+    if torch.cuda.mem_get_info()[0] < 20 << 30:
+        pytest.skip("memory")
+    n, stride = 600, 1 << 22
+    wide = torch.empty(n, stride, dtype=torch.bfloat16, device="cuda")
+    c = Case([n], [n], Hkv=1, sinks=True, seed=4)
+    for name, at in (("q", 0), ("k", 512), ("v", 1024)):
+        t = getattr(c, name)
+        view = wide[:, at:at + t[0].numel()].view(n, t.shape[1], 64)
+        view.copy_(t)
+        setattr(c, name, view)
+    assert n * stride > 2 ** 31
+    c.check()
+
+
+def test_bad_ranges():
+    """Starts that descend or leave the buffers: nothing is written, the error bit is set."""
+    base = Case([10, 10], [10, 10], Hkv=1)
+    for qs, ks in (([0, 10, 21], [0, 10, 20]), ([0, 11, 10], [0, 10, 20]), ([-1, 10, 20], [0, 10, 20]),
+                   ([0, 10, 20], [0, 10, 21]), ([0, 10, 20], [0, 21, 20]), ([0, 10, 20], [-5, 10, 20])):
+        gk.gk_prompt_plan(base.prompt, i32(qs), i32(ks), base.plan)
+        out, f32 = base.run()
+        assert gk.gk_read_device_error() == gk.GK_DEVERR_SEQ
+        assert (out == 7).all() and (f32 == 7).all()
+
+
+def test_streams_graph_and_reuse():
+    """One plan for several layers; another stream; a captured pass replayed on new values gives the
+    bits of an eager call; a plan filled again for other sequences."""
+    c = Case([50, 8], [50, 5000], Hkv=2, sinks=True, seed=6)
+    a, _ = c.run()
+    b, _ = c.run()
+    assert torch.equal(a, b)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        e, _ = c.run()
+    s.synchronize()
+    assert torch.equal(a, e)
+    out = torch.zeros_like(a)
+    qs, ks = i32(c.qs), i32(c.ks)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        gk.gk_prompt_plan(c.prompt, qs, ks, c.plan)
+        gk.gk_prompt_attn(c.prompt, c.plan, c.q, c.k, c.v, out, sinks=c.sinks)
+    for _ in range(3):
+        c.q.normal_()
+        c.v.normal_()
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, c.run()[0])
+    # other sequences of the same sizes on the same plan
+    c.qs, c.ks = [0, 8, 58], [0, 3000, 5050]
+    gk.gk_prompt_plan(c.prompt, i32(c.qs), i32(c.ks), c.plan)
+    c.check()
+    assert gk.gk_read_device_error() == 0
