@@ -22,7 +22,7 @@ INCLUDE = os.path.join(ROOT, "include")
 SOURCES = ["gk_kernels.cu", "gk_api.cu", "gk_noalloc.cu", "gk_ingest.cu", "gk_kv4.cu",
            "gk_tokens.cu", "gk_rope.cu", "gk_prompt.cu"]
 HEADERS = ["gk_device.cuh", "gk_internal.h", "gk_plan.cuh", "gk_attn_common.cuh", "gk_once.h",
-           "gk_token.cuh"]
+           "gk_token.cuh", "gk_tcgen05.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2",
               "--expt-relaxed-constexpr", "-Xptxas", "-v"]

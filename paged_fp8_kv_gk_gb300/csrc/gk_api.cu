@@ -768,6 +768,10 @@ gk_status gk_prompt_attn(const gk_prompt* prompt, void* plan, size_t plan_bytes,
       (v_stride & 7) || (s.q_tokens > 1 && q_stride < q_row) ||
       (s.k_tokens > 1 && (k_stride < k_row || v_stride < k_row)))
     return GK_ERR_INVALID_ARG;
+  // a tensor map's strides end at 2^40 bytes
+  if (q_stride >= (int64_t(1) << 39) || k_stride >= (int64_t(1) << 39) ||
+      v_stride >= (int64_t(1) << 39))
+    return GK_ERR_UNSUPPORTED;
   const PromptLayout L = prompt_layout(s);
   if (!plan || (reinterpret_cast<uintptr_t>(plan) & 255u) || plan_bytes < L.total)
     return GK_ERR_WORKSPACE;

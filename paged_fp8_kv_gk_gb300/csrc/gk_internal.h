@@ -2,6 +2,7 @@
 // the host API (gk_api.cu) and the kernels (gk_kernels.cu).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <vector_types.h>
 #include <stddef.h>
@@ -265,6 +266,7 @@ struct PromptPlanParams {
 };
 
 struct PromptAttnParams {
+  CUtensorMap q_map, k_map, v_map;  // [tokens, heads, 64] (set by the launcher)
   const uint16_t* q;
   const uint16_t* k;
   const uint16_t* v;
@@ -323,7 +325,7 @@ cudaError_t read_tokens_error(uint32_t* bits, bool clear);
 // gk_prompt.cu: planner, attention and joining of split tiles, with their own
 // device error word.
 cudaError_t launch_prompt_plan(const PromptPlanParams& p, cudaStream_t st);
-cudaError_t launch_prompt_attn(const PromptAttnParams& p, cudaStream_t st);
+cudaError_t launch_prompt_attn(PromptAttnParams& p, cudaStream_t st);
 cudaError_t read_prompt_error(uint32_t* bits, bool clear);
 // gk_rope.cu
 cudaError_t launch_rope_table(const RopeTableParams& p, cudaStream_t st);

@@ -2,14 +2,16 @@
 //
 //   prompt_plan_kernel  lists the items (tiles of queries with a run of keys),
 //                       longest first.
-//   prompt_rows_kernel  attention, a warp a row.
+//   prompt_attn_kernel  attention of one item and kv head a CTA.
 //   prompt_join_kernel  joins the parts of tiles whose keys are split.
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 
 #include <algorithm>
 
 #include "gk_internal.h"
 #include "gk_once.h"
+#include "gk_tcgen05.cuh"
 #include "gk_token.cuh"
 
 namespace gk {
@@ -268,36 +270,367 @@ __device__ __forceinline__ void store_row(const PromptAttnParams& p, int64_t tok
   if (p.out_f32) *reinterpret_cast<float2*>(p.out_f32 + at) = y;
 }
 
-constexpr int kRowThreads = 256;
+// =========================================================================
+// Attention
+// =========================================================================
+// A CTA has one tile of 128 rows (16 tokens of 8 heads, say) and a run of keys, 128
+// a step.  Warps 0-3: a thread a row, the softmax.  Warp 4 copies, warp 5 issues the
+// products:
+//   S = Q K^T  128 x 128 x 64  both operands in shared memory, fp32 in tensor memory
+//   O += P V   128 x 64 x 128  P, bf16, in tensor memory; V in shared memory, MN-major
+// A row's scores are loaded into registers as soon as they are there, so that the
+// next step's S is computed while this one's exponentials are; two CTAs an SM fill
+// each other's gaps.
+constexpr int kAttnThreads = 192;
+constexpr int kPromptStages = 3;
+constexpr int kTileBytes = kPromptRows * kHeadDim * 2;  // Q, and one step of K or of V: 16 KB
+constexpr int kTmemColumns = 256;                       // S 128, O 64, P 64
+constexpr int kTmemO = 128, kTmemP = 192;
+constexpr float kLazyScore = kLazyLog2 / kScoreLog2;    // kLazyLog2 in units of q.k
 
-__global__ void __launch_bounds__(kRowThreads)
-    prompt_rows_kernel(const __grid_constant__ PromptAttnParams p) {
+struct PromptSmem {
+  alignas(1024) uint8_t q[kTileBytes];
+  uint8_t k[kPromptStages][kTileBytes];
+  uint8_t v[kPromptStages][kTileBytes];
+  uint64_t q_full, k_full[kPromptStages], v_full[kPromptStages], k_free[kPromptStages],
+      v_free[kPromptStages];
+  uint64_t s_full, s_free, p_full, o_full;
+  uint32_t tmem;
+};
+static_assert(kPromptKeys * kHeadDim * 2 == kTileBytes, "a step of K is as large as Q");
+static_assert(sizeof(PromptSmem) <= 115712, "two CTAs an SM");
+
+struct Phase {  // place in a ring of barriers, and the parity of its next phase
+  int at = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next(int n) {
+    if (++at == n) {
+      at = 0;
+      parity ^= 1;
+    }
+  }
+};
+
+// Waits for a barrier's phase; false, with the error bit set, after kWaitLimitNs.
+__device__ __forceinline__ bool prompt_wait(uint64_t& bar, uint32_t parity) {
+  if (mbar_wait_bounded(smem_u32(&bar), parity, kWaitLimitNs)) return true;
+  atomicOr(&g_prompt_error, GK_DEVERR_TIMEOUT);
+  return false;
+}
+
+// The same by a whole warp, which goes on or gives up together.
+__device__ __forceinline__ bool warp_wait(uint64_t& bar, uint32_t parity) {
+  return __all_sync(kFull, prompt_wait(bar, parity));
+}
+
+// Whether one of the keys [a, b) has a V that is not finite (a warp).
+__device__ __forceinline__ bool any_not_finite(const PromptAttnParams& p, int a, int b, int h) {
+  bool bad = false;
+  for (int t = a; t < b; ++t) {
+    const uint32_t w = __ldcg(reinterpret_cast<const uint32_t*>(
+        p.v + int64_t(t) * p.v_stride + h * kHeadDim + 2 * (threadIdx.x & 31)));
+    bad = bad || (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+  }
+  return __any_sync(kFull, bad);
+}
+
+__device__ __forceinline__ void store_part(const PromptAttnParams& p, const Item& it, int h, int r,
+                                           int lane, const RowResult& y) {
+  float* rec = p.records + (int64_t(it.rec) * p.Hkv + h) * kPromptRecFloats;
+  if (lane == 0) {
+    rec[r] = y.m;
+    rec[kPromptRows + r] = y.l;
+  }
+  *reinterpret_cast<float2*>(rec + 2 * kPromptRows + r * kHeadDim + 2 * lane) = y.o;
+}
+
+__global__ void __launch_bounds__(kAttnThreads, 2)
+    prompt_attn_kernel(const __grid_constant__ PromptAttnParams p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  PromptSmem& sm = *reinterpret_cast<PromptSmem*>(smem_raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   follow_stream();
-  __shared__ alignas(16) float qs[kRowThreads / 32][kHeadDim];
   const int i = int(blockIdx.x) / p.Hkv, h = int(blockIdx.x) - i * p.Hkv;
   if (i >= __ldcg(p.hdr)) return;
   const Item it = load_item(p, i);
-  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int r = w; r < it.n * p.G; r += kRowThreads / 32) {
-    const int t = r / p.G, g = r - t * p.G, head = h * p.G + g;
-    const uint32_t qw = __ldcg(reinterpret_cast<const uint32_t*>(
-        p.q + int64_t(it.q0 + t) * p.q_stride + head * kHeadDim + 2 * lane));
-    __syncwarp();
-    *reinterpret_cast<float2*>(&qs[w][2 * lane]) = bf16x2_to_f32x2(qw);
-    __syncwarp();
-    const RowResult y = attend_row(p, seen_keys(p, it, t), h, qs[w]);
-    if (it.rec < 0) {
-      store_row(p, it.q0 + t, head, lane, y.m, y.l, y.o);
-    } else {
-      float* rec = p.records + (int64_t(it.rec) * p.Hkv + h) * kPromptRecFloats;
-      if (lane == 0) {
-        rec[r] = y.m;
-        rec[kPromptRows + r] = y.l;
+  const int steps = (it.k_end - it.k_lo + kPromptKeys - 1) / kPromptKeys;
+  if (steps == 0) {  // no key: zeros (such a tile is not split)
+    for (int r = warp; r < it.n * p.G; r += kAttnThreads / 32)
+      store_row(p, it.q0 + r / p.G, h * p.G + r % p.G, lane, 0.f, 0.f, make_float2(0.f, 0.f));
+    return;
+  }
+  if (warp == 4) {
+    if (lane == 0) {
+      mbar_init(smem_u32(&sm.q_full), 1);
+      for (int s = 0; s < kPromptStages; ++s) {
+        mbar_init(smem_u32(&sm.k_full[s]), 1);
+        mbar_init(smem_u32(&sm.v_full[s]), 1);
+        mbar_init(smem_u32(&sm.k_free[s]), 1);
+        mbar_init(smem_u32(&sm.v_free[s]), 1);
       }
-      *reinterpret_cast<float2*>(rec + 2 * kPromptRows + r * kHeadDim + 2 * lane) = y.o;
+      mbar_init(smem_u32(&sm.s_full), 1);
+      mbar_init(smem_u32(&sm.s_free), 4);
+      mbar_init(smem_u32(&sm.p_full), 4);
+      mbar_init(smem_u32(&sm.o_full), 1);
+      mbar_init_fence();
+    }
+  } else if (warp == 5) {
+    tmem_alloc<kTmemColumns>(smem_u32(&sm.tmem));
+  }
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  const uint32_t tmem = sm.tmem;
+
+  if (warp == 4) {
+    if (lane == 0) {
+      mbar_arrive_expect_tx(smem_u32(&sm.q_full), uint32_t(p.tile_tokens * p.G) * kHeadDim * 2);
+      tma_load_3d(smem_u32(sm.q), &p.q_map, 0, h * p.G, it.q0, smem_u32(&sm.q_full));
+      Phase s;
+      int j = 0;
+      for (; j < steps; ++j) {
+        const int t = it.k_lo + j * kPromptKeys;
+        // the first round finds the stages free
+        if (!prompt_wait(sm.k_free[s.at], s.parity ^ 1)) break;
+        mbar_arrive_expect_tx(smem_u32(&sm.k_full[s.at]), kTileBytes);
+        tma_load_3d(smem_u32(sm.k[s.at]), &p.k_map, 0, h, t, smem_u32(&sm.k_full[s.at]));
+        if (!prompt_wait(sm.v_free[s.at], s.parity ^ 1)) break;
+        mbar_arrive_expect_tx(smem_u32(&sm.v_full[s.at]), kTileBytes);
+        tma_load_3d(smem_u32(sm.v[s.at]), &p.v_map, 0, h, t, smem_u32(&sm.v_full[s.at]));
+        s.next(kPromptStages);
+      }
+      // gave up: its copies have landed before the CTA ends
+      for (int x = j < steps ? max(j - kPromptStages, 0) : steps; x <= min(j, steps - 1); ++x) {
+        const uint32_t parity = uint32_t(x / kPromptStages) & 1;
+        mbar_wait_bounded(smem_u32(&sm.k_full[x % kPromptStages]), parity, kWaitLimitNs);
+        mbar_wait_bounded(smem_u32(&sm.v_full[x % kPromptStages]), parity, kWaitLimitNs);
+      }
+    }
+  } else if (warp == 5) {
+    if (lane == 0) {
+      constexpr uint32_t kS = bf16_idesc(kPromptRows, kPromptKeys, false);
+      constexpr uint32_t kO = bf16_idesc(kPromptRows, kHeadDim, true);
+      const uint64_t qd = sw128_desc(smem_u32(sm.q));
+      auto scores = [&](int stage) {
+        const uint64_t kd = sw128_desc(smem_u32(sm.k[stage]));
+#pragma unroll
+        for (int c = 0; c < kHeadDim / 16; ++c) mma_ss(tmem, qd + 2 * c, kd + 2 * c, kS, c > 0);
+        mma_commit(smem_u32(&sm.k_free[stage]));
+        mma_commit(smem_u32(&sm.s_full));
+      };
+      Phase k, v;
+      bool ok = prompt_wait(sm.q_full, 0) && prompt_wait(sm.k_full[0], 0);
+      if (ok) {
+        tmem_fence_after();
+        scores(0);
+        k.next(kPromptStages);
+      }
+      for (int j = 0; ok && j < steps; ++j) {
+        if (j + 1 < steps) {
+          ok = prompt_wait(sm.k_full[k.at], k.parity) && prompt_wait(sm.s_free, j & 1);
+          if (!ok) break;
+          tmem_fence_after();
+          scores(k.at);
+          k.next(kPromptStages);
+        }
+        ok = prompt_wait(sm.v_full[v.at], v.parity) && prompt_wait(sm.p_full, j & 1);
+        if (!ok) break;
+        tmem_fence_after();
+        const uint64_t vd = sw128_desc(smem_u32(sm.v[v.at]));
+#pragma unroll
+        for (int c = 0; c < kPromptKeys / 16; ++c)
+          mma_ts(tmem + kTmemO, tmem + kTmemP + 8 * c, vd + 128 * c, kO, j > 0 || c > 0);
+        mma_commit(smem_u32(&sm.v_free[v.at]));
+        mma_commit(smem_u32(&sm.o_full));
+        v.next(kPromptStages);
+      }
+      if (!ok) {  // gave up: its products are complete before the tensor memory is freed
+        mma_commit(smem_u32(&sm.q_full));
+        mbar_wait_bounded(smem_u32(&sm.q_full), 1, kWaitLimitNs);
+      }
+    }
+  } else {
+    const int r = threadIdx.x;  // row of the tile
+    const int token = r / p.G;
+    const bool valid = token < it.n && r < p.tile_tokens * p.G;
+    const int2 seen = seen_keys(p, it, min(token, it.n - 1));
+    // steps that every row sees whole
+    const int whole_lo = it.diag + it.n - p.W, whole_hi = min(it.diag + 1, it.k_end) - kPromptKeys;
+    const uint32_t lanes = tmem + (uint32_t(warp) << 21);  // lane 32 warp
+    float m = -INFINITY;  // reference maximum, units of q.k
+    float2 sum = make_float2(0.f, 0.f);
+    Phase v;
+    bool ok = true;
+    for (int j = 0; j < steps; ++j) {
+      const int t0 = it.k_lo + j * kPromptKeys;
+      if (!(ok = warp_wait(sm.s_full, j & 1))) break;
+      tmem_fence_after();
+      uint32_t s[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(lanes + 32 * c, s[c]);
+      tmem_wait_ld();
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_landed(s[c]);
+      tmem_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.s_free));
+      if (t0 < whole_lo || t0 > whole_hi) {
+        const uint32_t first = uint32_t(seen.x - t0), n = uint32_t(max(seen.y - seen.x, 0));
+#pragma unroll
+        for (int c = 0; c < 128; ++c)
+          if (uint32_t(c) - first >= n) s[c >> 5][c & 31] = __float_as_uint(-INFINITY);
+      }
+      float top[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        top[c] = __uint_as_float(s[c][0]);
+#pragma unroll
+        for (int e = 1; e < 31; e += 2)
+          top[c] = fmaxf(top[c], fmaxf(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])));
+        top[c] = fmaxf(top[c], __uint_as_float(s[c][31]));
+      }
+      const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+      // P of the step before has been used, and O is up to it
+      if (j > 0 && !(ok = warp_wait(sm.o_full, (j - 1) & 1))) break;
+      tmem_fence_after();
+      if (j == 0) {
+        m = most;
+      } else if (__any_sync(kFull, most > m + kLazyScore)) {
+        // probabilities would pass 2^8: a new reference, and O and the sum in its units
+        const float to = fmaxf(m, most);
+        const float f = to == m ? 1.f : ex2((m - to) * kScoreLog2);
+        m = to;
+        sum.x *= f;
+        sum.y *= f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t o[16];
+          tmem_ld16(lanes + kTmemO + 16 * c, o);
+          tmem_wait_ld();
+          tmem_landed(o);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+          tmem_st16(lanes + kTmemO + 16 * c, o);
+        }
+      }
+      const float ref = m == -INFINITY ? 0.f : -m * kScoreLog2;
+      const float2 scale = make_float2(kScoreLog2, kScoreLog2), shift = make_float2(ref, ref);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t pr[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float2 x = fma2(make_float2(__uint_as_float(s[c][2 * e]), __uint_as_float(s[c][2 * e + 1])),
+                                scale, shift);
+          const float2 y = make_float2(ex2(x.x), ex2(x.y));
+          sum = add2(sum, y);
+          pr[e] = f32x2_to_bf16x2(y.x, y.y);
+        }
+        tmem_st16(lanes + kTmemP + 16 * c, pr);
+      }
+      if (t0 + kPromptKeys > it.k_end) {
+        // keys behind the item's: whatever V is there (other sequences, padding), zero
+        // times it must be zero
+        if (!(ok = warp_wait(sm.v_full[v.at], v.parity))) break;
+        if (t0 + r >= it.k_end) {
+          uint4* row = reinterpret_cast<uint4*>(sm.v[v.at] + r * (kHeadDim * 2));
+#pragma unroll
+          for (int c = 0; c < 8; ++c) row[c] = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_shared();
+      }
+      v.next(kPromptStages);
+      tmem_wait_st();
+      tmem_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.p_full));
+    }
+    if (ok && warp_wait(sm.o_full, (steps - 1) & 1)) {
+      tmem_fence_after();
+      uint32_t o[2][32];
+      tmem_ld32(lanes + kTmemO, o[0]);
+      tmem_ld32(lanes + kTmemO + 32, o[1]);
+      tmem_wait_ld();
+      tmem_landed(o[0]);
+      tmem_landed(o[1]);
+      const float l = sum.x + sum.y;
+      float size = 0.f;
+#pragma unroll
+      for (int c = 0; c < 64; c += 2)
+        size = max3_abs_nan(size, __uint_as_float(o[c >> 5][c & 31]), __uint_as_float(o[c >> 5][(c & 31) + 1]));
+      // Zero times an unseen key's infinity or NaN, if it is not a seen key's: such rows
+      // are computed again from the keys that they see.
+      uint32_t again = __ballot_sync(kFull, valid && !(size < INFINITY));
+      uint32_t done = 0;
+      float* qs = reinterpret_cast<float*>(sm.q) + warp * kHeadDim;  // Q has been used
+      while (again) {
+        const int x = __ffs(again) - 1, rr = 32 * warp + x, tt = rr / p.G;
+        again &= again - 1;
+        const int2 keys = seen_keys(p, it, tt);
+        if (!any_not_finite(p, it.k_lo, min(keys.x, it.k_end), h) &&
+            !any_not_finite(p, max(keys.y, it.k_lo), it.k_end, h))
+          continue;
+        const int head = h * p.G + rr - tt * p.G;
+        const uint32_t qw = __ldcg(reinterpret_cast<const uint32_t*>(
+            p.q + int64_t(it.q0 + tt) * p.q_stride + head * kHeadDim + 2 * lane));
+        __syncwarp();
+        *reinterpret_cast<float2*>(qs + 2 * lane) = bf16x2_to_f32x2(qw);
+        __syncwarp();
+        const RowResult y = attend_row(p, keys, h, qs);
+        if (it.rec < 0)
+          store_row(p, it.q0 + tt, head, lane, y.m, y.l, y.o);
+        else
+          store_part(p, it, h, rr, lane, y);
+        done |= 1u << x;
+      }
+      if (valid && !((done >> lane) & 1u)) {
+        const float ml = m * kScoreLog2;
+        if (it.rec >= 0) {
+          float* rec = p.records + (int64_t(it.rec) * p.Hkv + h) * kPromptRecFloats;
+          rec[r] = ml;
+          rec[kPromptRows + r] = l;
+          uint4* to = reinterpret_cast<uint4*>(rec + 2 * kPromptRows + r * kHeadDim);
+#pragma unroll
+          for (int c = 0; c < 16; ++c)
+            to[c] = make_uint4(o[c >> 3][4 * (c & 7)], o[c >> 3][4 * (c & 7) + 1], o[c >> 3][4 * (c & 7) + 2],
+                               o[c >> 3][4 * (c & 7) + 3]);
+        } else {
+          const int head = h * p.G + r - token * p.G;
+          const int64_t at = (int64_t(it.q0 + token) * p.Hq + head) * kHeadDim;
+          const float f = l == 0.f ? 0.f : out_scale(l, ml, p.sinks ? p.sinks + head : nullptr, 1.f);
+          uint4* to = reinterpret_cast<uint4*>(p.out + at);
+#pragma unroll
+          for (int c = 0; c < 64; ++c)
+            o[c >> 5][c & 31] =
+                l == 0.f ? 0u : __float_as_uint(__uint_as_float(o[c >> 5][c & 31]) * f);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int a = 8 * c + 2 * e;
+              w[e] = f32x2_to_bf16x2(__uint_as_float(o[a >> 5][a & 31]), __uint_as_float(o[a >> 5][(a & 31) + 1]));
+            }
+            to[c] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          if (p.out_f32) {
+            uint4* to32 = reinterpret_cast<uint4*>(p.out_f32 + at);
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+              to32[c] = make_uint4(o[c >> 3][4 * (c & 7)], o[c >> 3][4 * (c & 7) + 1],
+                                   o[c >> 3][4 * (c & 7) + 2], o[c >> 3][4 * (c & 7) + 3]);
+          }
+        }
+      }
     }
   }
+  tmem_fence_before();
+  __syncthreads();
+  __syncwarp();
+  if (warp == 5) tmem_dealloc<kTmemColumns>(tmem);
 }
+
+constexpr int kRowThreads = 256;
 
 // One warp a row of a split tile: the parts in order.
 __global__ void __launch_bounds__(kRowThreads)
@@ -335,15 +668,54 @@ __global__ void __launch_bounds__(kRowThreads)
 // =========================================================================
 // Launchers
 // =========================================================================
+struct PromptDevice {
+  PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+};
+static PerDevice<PromptDevice, 64> g_prompt_dev;
+
+static cudaError_t prompt_setup(const PromptDevice** out) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= g_prompt_dev.devices) return cudaErrorInvalidDevice;
+  return g_prompt_dev.get<cudaError_t>(dev, out, [](PromptDevice& d) -> cudaError_t {
+    cudaDriverEntryPointQueryResult found;
+    void* f = nullptr;
+    cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000,
+                                                     cudaEnableDefault, &found);
+    if (e != cudaSuccess) return e;
+    if (found != cudaDriverEntryPointSuccess || !f) return cudaErrorNotSupported;
+    d.encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    return cudaFuncSetAttribute(prompt_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                int(sizeof(PromptSmem)));
+  });
+}
+
+// [tokens, heads, 64] bf16, boxes of box_tokens x box_heads rows of 128 bytes, swizzled.
+static bool encode_map(const PromptDevice& d, CUtensorMap* map, const void* base, int tokens,
+                       int heads, int64_t stride, int box_tokens, int box_heads) {
+  const cuuint64_t dims[3] = {kHeadDim, cuuint64_t(heads), cuuint64_t(tokens)};
+  // the stride of one token is never used, but checked
+  const cuuint64_t strides[2] = {kHeadDim * 2, tokens > 1 ? cuuint64_t(stride) * 2
+                                                          : cuuint64_t(heads) * kHeadDim * 2};
+  const cuuint32_t box[3] = {kHeadDim, cuuint32_t(box_heads), cuuint32_t(box_tokens)};
+  const cuuint32_t ones[3] = {1, 1, 1};
+  return d.encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
+                  box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <typename P>
 static cudaError_t launch(void (*kernel)(P), const P& p, unsigned grid, unsigned threads,
-                          cudaStream_t st) {
+                          size_t smem, cudaStream_t st) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
@@ -351,17 +723,25 @@ static cudaError_t launch(void (*kernel)(P), const P& p, unsigned grid, unsigned
 }
 
 cudaError_t launch_prompt_plan(const PromptPlanParams& p, cudaStream_t st) {
-  return launch(prompt_plan_kernel, p, 1, kPromptPlanThreads, st);
+  return launch(prompt_plan_kernel, p, 1, kPromptPlanThreads, 0, st);
 }
 
-cudaError_t launch_prompt_attn(const PromptAttnParams& p, cudaStream_t st) {
-  const cudaError_t e =
-      launch(prompt_rows_kernel, p, unsigned(p.max_items * p.Hkv), kRowThreads, st);
+cudaError_t launch_prompt_attn(PromptAttnParams& p, cudaStream_t st) {
+  const PromptDevice* d = nullptr;
+  cudaError_t e = prompt_setup(&d);
+  if (e != cudaSuccess) return e;
+  bool ok = encode_map(*d, &p.q_map, p.q, p.q_tokens, p.Hq, p.q_stride, p.tile_tokens, p.G);
+  // without keys no item copies any
+  if (p.k_tokens > 0)
+    ok = ok && encode_map(*d, &p.k_map, p.k, p.k_tokens, p.Hkv, p.k_stride, kPromptKeys, 1) &&
+         encode_map(*d, &p.v_map, p.v, p.k_tokens, p.Hkv, p.v_stride, kPromptKeys, 1);
+  if (!ok) return cudaErrorInvalidValue;
+  e = launch(prompt_attn_kernel, p, unsigned(p.max_items * p.Hkv), kAttnThreads, sizeof(PromptSmem), st);
   if (e != cudaSuccess || p.max_recs == 0) return e;
   // most rows of split tiles: half of the records, or the tiles
   const int64_t rows = std::min(p.max_recs / 2, p.max_items - p.max_recs) * p.Hkv * kPromptRows;
   return launch(prompt_join_kernel, p, unsigned((rows + kRowThreads / 32 - 1) / (kRowThreads / 32)),
-                kRowThreads, st);
+                kRowThreads, 0, st);
 }
 
 cudaError_t read_prompt_error(uint32_t* bits, bool clear) {
