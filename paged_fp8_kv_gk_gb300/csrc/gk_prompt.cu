@@ -270,6 +270,12 @@ __device__ __forceinline__ void store_row(const PromptAttnParams& p, int64_t tok
   if (p.out_f32) *reinterpret_cast<float2*>(p.out_f32 + at) = y;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // =========================================================================
 // Attention
 // =========================================================================
@@ -313,6 +319,9 @@ struct Phase {  // place in a ring of barriers, and the parity of its next phase
 
 // Waits for a barrier's phase; false, with the error bit set, after kWaitLimitNs.
 __device__ __forceinline__ bool prompt_wait(uint64_t& bar, uint32_t parity) {
+  // waits here last a microsecond; the clock is read for the limit only behind that
+  for (int tries = 0; tries < 4096; ++tries)
+    if (mbar_try_wait(smem_u32(&bar), parity)) return true;
   if (mbar_wait_bounded(smem_u32(&bar), parity, kWaitLimitNs)) return true;
   atomicOr(&g_prompt_error, GK_DEVERR_TIMEOUT);
   return false;
@@ -348,7 +357,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
     prompt_attn_kernel(const __grid_constant__ PromptAttnParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   PromptSmem& sm = *reinterpret_cast<PromptSmem*>(smem_raw);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   follow_stream();
   const int i = int(blockIdx.x) / p.Hkv, h = int(blockIdx.x) - i * p.Hkv;
   if (i >= __ldcg(p.hdr)) return;
@@ -383,71 +392,84 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
   const uint32_t tmem = sm.tmem;
 
   if (warp == 4) {
-    if (lane == 0) {
+    const bool one = elect_one();
+    if (one) {
       mbar_arrive_expect_tx(smem_u32(&sm.q_full), uint32_t(p.tile_tokens * p.G) * kHeadDim * 2);
       tma_load_3d(smem_u32(sm.q), &p.q_map, 0, h * p.G, it.q0, smem_u32(&sm.q_full));
-      Phase s;
-      int j = 0;
-      for (; j < steps; ++j) {
-        const int t = it.k_lo + j * kPromptKeys;
-        // the first round finds the stages free
-        if (!prompt_wait(sm.k_free[s.at], s.parity ^ 1)) break;
+    }
+    Phase s;
+    int j = 0;
+    for (; j < steps; ++j) {
+      const int t = it.k_lo + j * kPromptKeys;
+      // the first round finds the stages free
+      if (!warp_wait(sm.k_free[s.at], s.parity ^ 1)) break;
+      if (one) {
         mbar_arrive_expect_tx(smem_u32(&sm.k_full[s.at]), kTileBytes);
         tma_load_3d(smem_u32(sm.k[s.at]), &p.k_map, 0, h, t, smem_u32(&sm.k_full[s.at]));
-        if (!prompt_wait(sm.v_free[s.at], s.parity ^ 1)) break;
+      }
+      if (!warp_wait(sm.v_free[s.at], s.parity ^ 1)) break;
+      if (one) {
         mbar_arrive_expect_tx(smem_u32(&sm.v_full[s.at]), kTileBytes);
         tma_load_3d(smem_u32(sm.v[s.at]), &p.v_map, 0, h, t, smem_u32(&sm.v_full[s.at]));
-        s.next(kPromptStages);
       }
-      // gave up: its copies have landed before the CTA ends
-      for (int x = j < steps ? max(j - kPromptStages, 0) : steps; x <= min(j, steps - 1); ++x) {
-        const uint32_t parity = uint32_t(x / kPromptStages) & 1;
-        mbar_wait_bounded(smem_u32(&sm.k_full[x % kPromptStages]), parity, kWaitLimitNs);
-        mbar_wait_bounded(smem_u32(&sm.v_full[x % kPromptStages]), parity, kWaitLimitNs);
-      }
+      s.next(kPromptStages);
+    }
+    // gave up: its copies have landed before the CTA ends
+    for (int x = j < steps ? max(j - kPromptStages, 0) : steps; x <= min(j, steps - 1); ++x) {
+      const uint32_t parity = uint32_t(x / kPromptStages) & 1;
+      mbar_wait_bounded(smem_u32(&sm.k_full[x % kPromptStages]), parity, kWaitLimitNs);
+      mbar_wait_bounded(smem_u32(&sm.v_full[x % kPromptStages]), parity, kWaitLimitNs);
     }
   } else if (warp == 5) {
-    if (lane == 0) {
-      constexpr uint32_t kS = bf16_idesc(kPromptRows, kPromptKeys, false);
-      constexpr uint32_t kO = bf16_idesc(kPromptRows, kHeadDim, true);
-      const uint64_t qd = sw128_desc(smem_u32(sm.q));
-      auto scores = [&](int stage) {
-        const uint64_t kd = sw128_desc(smem_u32(sm.k[stage]));
+    // The whole warp runs this and one elected lane issues: in a branch of one lane the
+    // compiler cannot see that the operands are uniform, and a product takes 45 to 90
+    // cycles to issue where the tensor cores need 32 or 64 for it.
+    constexpr uint32_t kS = bf16_idesc(kPromptRows, kPromptKeys, false);
+    constexpr uint32_t kO = bf16_idesc(kPromptRows, kHeadDim, true);
+    const uint64_t qd = sw128_desc(smem_u32(sm.q));
+    const uint64_t kd0 = sw128_desc(smem_u32(sm.k[0])), vd0 = sw128_desc(smem_u32(sm.v[0]));
+    auto scores = [&](int stage) {
+      const uint64_t kd = kd0 + uint64_t(stage * (kTileBytes >> 4));
+      if (elect_one()) {
 #pragma unroll
         for (int c = 0; c < kHeadDim / 16; ++c) mma_ss(tmem, qd + 2 * c, kd + 2 * c, kS, c > 0);
         mma_commit(smem_u32(&sm.k_free[stage]));
         mma_commit(smem_u32(&sm.s_full));
-      };
-      Phase k, v;
-      bool ok = prompt_wait(sm.q_full, 0) && prompt_wait(sm.k_full[0], 0);
-      if (ok) {
-        tmem_fence_after();
-        scores(0);
-        k.next(kPromptStages);
       }
-      for (int j = 0; ok && j < steps; ++j) {
-        if (j + 1 < steps) {
-          ok = prompt_wait(sm.k_full[k.at], k.parity) && prompt_wait(sm.s_free, j & 1);
-          if (!ok) break;
-          tmem_fence_after();
-          scores(k.at);
-          k.next(kPromptStages);
-        }
-        ok = prompt_wait(sm.v_full[v.at], v.parity) && prompt_wait(sm.p_full, j & 1);
+      __syncwarp();
+    };
+    Phase k, v;
+    bool ok = warp_wait(sm.q_full, 0) && warp_wait(sm.k_full[0], 0);
+    if (ok) {
+      tmem_fence_after();
+      scores(0);
+      k.next(kPromptStages);
+    }
+    for (int j = 0; ok && j < steps; ++j) {
+      if (j + 1 < steps) {
+        ok = warp_wait(sm.k_full[k.at], k.parity) && warp_wait(sm.s_free, j & 1);
         if (!ok) break;
         tmem_fence_after();
-        const uint64_t vd = sw128_desc(smem_u32(sm.v[v.at]));
+        scores(k.at);
+        k.next(kPromptStages);
+      }
+      ok = warp_wait(sm.v_full[v.at], v.parity) && warp_wait(sm.p_full, j & 1);
+      if (!ok) break;
+      tmem_fence_after();
+      const uint64_t vd = vd0 + uint64_t(v.at * (kTileBytes >> 4));
+      if (elect_one()) {
 #pragma unroll
         for (int c = 0; c < kPromptKeys / 16; ++c)
           mma_ts(tmem + kTmemO, tmem + kTmemP + 8 * c, vd + 128 * c, kO, j > 0 || c > 0);
         mma_commit(smem_u32(&sm.v_free[v.at]));
         mma_commit(smem_u32(&sm.o_full));
-        v.next(kPromptStages);
       }
-      if (!ok) {  // gave up: its products are complete before the tensor memory is freed
-        mma_commit(smem_u32(&sm.q_full));
-        mbar_wait_bounded(smem_u32(&sm.q_full), 1, kWaitLimitNs);
-      }
+      __syncwarp();
+      v.next(kPromptStages);
+    }
+    if (!ok) {  // gave up: its products are complete before the tensor memory is freed
+      if (elect_one()) mma_commit(smem_u32(&sm.q_full));
+      mbar_wait_bounded(smem_u32(&sm.q_full), 1, kWaitLimitNs);
     }
   } else {
     const int r = threadIdx.x;  // row of the tile
@@ -486,7 +508,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
         top[c] = __uint_as_float(s[c][0]);
 #pragma unroll
         for (int e = 1; e < 31; e += 2)
-          top[c] = fmaxf(top[c], fmaxf(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])));
+          top[c] = max3(top[c], __uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
         top[c] = fmaxf(top[c], __uint_as_float(s[c][31]));
       }
       const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));

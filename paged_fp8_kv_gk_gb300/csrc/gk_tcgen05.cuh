@@ -6,6 +6,19 @@
 
 namespace gk {
 
+// True in one lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n"
+      " .reg .pred p;\n"
+      " elect.sync _|p, 0xffffffff;\n"
+      " selp.u32 %0, 1, 0, p;\n"
+      "}\n"
+      : "=r"(r));
+  return r != 0;
+}
+
 // ---------------------------------------------------------------- tensor memory
 // A whole warp; columns a power of two from 32 to 512.  The address is written to
 // shared memory at `dst`.

@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kTokThreads)
     for (int q = 0; q < 4; ++q) now[q] = rows[q];
     const int next = next_layer(i + 1);
     load(next);
-    const LayerScale sk = layer_scale(__ldcg(p.k_scale + i)), sv = layer_scale(__ldcg(p.v_scale + i));
+    const LayerScale sk = layer_scale(p.k_scale[i]), sv = layer_scale(p.v_scale[i]);
     const uint32_t aw[4] = {now[0].x, now[0].y, now[0].z, now[0].w};
     const uint32_t bw[4] = {now[1].x, now[1].y, now[1].z, now[1].w};
     float2 x[8];
@@ -245,8 +245,8 @@ __global__ void __launch_bounds__(kTokThreads)
       kc = __ldcg(reinterpret_cast<const uint2*>(kb + row + 8 * c));
     }
     const uint2 vc = __ldcg(reinterpret_cast<const uint2*>(p.vb[i >> 1] + row + 8 * c));
-    store8(p.k_out + to, kc, __ldcg(p.k_scale + i));
-    store8(p.v_out + to, vc, __ldcg(p.v_scale + i));
+    store8(p.k_out + to, kc, p.k_scale[i]);
+    store8(p.v_out + to, vc, p.v_scale[i]);
   };
   // a group buffer at a time: its window layer, its full layer
 #pragma unroll 1
