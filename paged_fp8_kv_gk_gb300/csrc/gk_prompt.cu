@@ -276,6 +276,13 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
+__device__ __forceinline__ float max32(const uint32_t (&s)[32]) {
+  float top = __uint_as_float(s[0]);
+#pragma unroll
+  for (int e = 1; e < 31; e += 2) top = max3(top, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+  return fmaxf(top, __uint_as_float(s[31]));
+}
+
 // =========================================================================
 // Attention
 // =========================================================================
@@ -319,9 +326,10 @@ struct Phase {  // place in a ring of barriers, and the parity of its next phase
 
 // Waits for a barrier's phase; false, with the error bit set, after kWaitLimitNs.
 __device__ __forceinline__ bool prompt_wait(uint64_t& bar, uint32_t parity) {
-  // waits here last a microsecond; the clock is read for the limit only behind that
-  for (int tries = 0; tries < 4096; ++tries)
-    if (mbar_try_wait(smem_u32(&bar), parity)) return true;
+  // Asleep between tries: a warp that polls takes the issue slots of the softmax warp
+  // beside it (its steps took 2250 cycles where the others' took 1400).
+  for (int tries = 0; tries < 64; ++tries)
+    if (mbar_try_wait_for(smem_u32(&bar), parity, 20000)) return true;
   if (mbar_wait_bounded(smem_u32(&bar), parity, kWaitLimitNs)) return true;
   atomicOr(&g_prompt_error, GK_DEVERR_TIMEOUT);
   return false;
@@ -502,28 +510,18 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
         for (int c = 0; c < 128; ++c)
           if (uint32_t(c) - first >= n) s[c >> 5][c & 31] = __float_as_uint(-INFINITY);
       }
-      float top[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        top[c] = __uint_as_float(s[c][0]);
-#pragma unroll
-        for (int e = 1; e < 31; e += 2)
-          top[c] = max3(top[c], __uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
-        top[c] = fmaxf(top[c], __uint_as_float(s[c][31]));
-      }
-      const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-      // P of the step before has been used, and O is up to it
-      if (j > 0 && !(ok = warp_wait(sm.o_full, (j - 1) & 1))) break;
-      tmem_fence_after();
+      const float most = fmaxf(fmaxf(max32(s[0]), max32(s[1])), fmaxf(max32(s[2]), max32(s[3])));
       if (j == 0) {
         m = most;
       } else if (__any_sync(kFull, most > m + kLazyScore)) {
-        // probabilities would pass 2^8: a new reference, and O and the sum in its units
+        // probabilities would pass 2^kLazyLog2: a new reference, and O and the sum in its units
         const float to = fmaxf(m, most);
         const float f = to == m ? 1.f : ex2((m - to) * kScoreLog2);
         m = to;
         sum.x *= f;
         sum.y *= f;
+        if (!(ok = warp_wait(sm.o_full, (j - 1) & 1))) break;
+        tmem_fence_after();
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t o[16];
@@ -537,19 +535,24 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
       }
       const float ref = m == -INFINITY ? 0.f : -m * kScoreLog2;
       const float2 scale = make_float2(kScoreLog2, kScoreLog2), shift = make_float2(ref, ref);
+      uint32_t pr[4][16];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        uint32_t pr[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const float2 x = fma2(make_float2(__uint_as_float(s[c][2 * e]), __uint_as_float(s[c][2 * e + 1])),
                                 scale, shift);
           const float2 y = make_float2(ex2(x.x), ex2(x.y));
           sum = add2(sum, y);
-          pr[e] = f32x2_to_bf16x2(y.x, y.y);
+          pr[c][e] = f32x2_to_bf16x2(y.x, y.y);
         }
-        tmem_st16(lanes + kTmemP + 16 * c, pr);
       }
+      // P of the step before has been used: waited for as late as possible (before the
+      // exponentials, it adds the product's time to every step's)
+      if (j > 0 && !(ok = warp_wait(sm.o_full, (j - 1) & 1))) break;
+      tmem_fence_after();
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_st16(lanes + kTmemP + 16 * c, pr[c]);
       if (t0 + kPromptKeys > it.k_end) {
         // keys behind the item's: whatever V is there (other sequences, padding), zero
         // times it must be zero
