@@ -287,26 +287,35 @@ __device__ __forceinline__ float max32(const uint32_t (&s)[32]) {
 // Attention
 // =========================================================================
 // A CTA has one tile of 128 rows (16 tokens of 8 heads, say) and a run of keys, 128
-// a step.  Warps 0-3: a thread a row, the softmax.  Warp 4 copies, warp 5 issues the
+// a step.  Warps 0-3 do the softmax, a thread a row.  Warp 4 copies, warp 5 issues the
 // products:
 //   S = Q K^T  128 x 128 x 64  both operands in shared memory, fp32 in tensor memory
 //   O += P V   128 x 64 x 128  P, bf16, in tensor memory; V in shared memory, MN-major
-// A row's scores are loaded into registers as soon as they are there, so that the
-// next step's S is computed while this one's exponentials are; two CTAs an SM fill
-// each other's gaps.
-constexpr int kAttnThreads = 192;
-constexpr int kPromptStages = 3;
+// A row's scores are loaded into registers as soon as they are there, so that the next
+// step's S is computed while this one's exponentials are; two CTAs an SM fill each
+// other's gaps.
+//
+// The softmax's reference R of a row (log2 units; p = 2^(s - R)) is the largest score
+// of the first step plus kHeadroom (every row sees a key of its first step, or none at
+// all), and no step after it looks for a maximum: p and the sums are floats (bf16 in P,
+// with a float's exponents), as exact at 2^60 as at 1.  After a step whose sum passes
+// kLargest the row takes a new R, and O and the sum are scaled to it.  A row that
+// overflows all the same (a score 54 or more above all before it, and then values of
+// 2^60) is computed again by attend_row, as are rows with unseen infinities or NaN.
+constexpr int kSoftWarps = 4;
+constexpr int kAttnThreads = 32 * (kSoftWarps + 2);
+constexpr int kKStages = 3, kVStages = 2;               // V is needed a softmax later than K
 constexpr int kTileBytes = kPromptRows * kHeadDim * 2;  // Q, and one step of K or of V: 16 KB
 constexpr int kTmemColumns = 256;                       // S 128, O 64, P 64
 constexpr int kTmemO = 128, kTmemP = 192;
-constexpr float kLazyScore = kLazyLog2 / kScoreLog2;    // kLazyLog2 in units of q.k
+constexpr float kHeadroom = 24.f;
+constexpr float kLargest = 0x1p30f;  // of a row's sum of a step
 
 struct PromptSmem {
   alignas(1024) uint8_t q[kTileBytes];
-  uint8_t k[kPromptStages][kTileBytes];
-  uint8_t v[kPromptStages][kTileBytes];
-  uint64_t q_full, k_full[kPromptStages], v_full[kPromptStages], k_free[kPromptStages],
-      v_free[kPromptStages];
+  uint8_t k[kKStages][kTileBytes];
+  uint8_t v[kVStages][kTileBytes];
+  uint64_t q_full, k_full[kKStages], v_full[kVStages], k_free[kKStages], v_free[kVStages];
   uint64_t s_full, s_free, p_full, o_full;
   uint32_t tmem;
 };
@@ -324,15 +333,20 @@ struct Phase {  // place in a ring of barriers, and the parity of its next phase
   }
 };
 
-// Waits for a barrier's phase; false, with the error bit set, after kWaitLimitNs.
+// Waits for a barrier's phase; false, with the error bit set, after kWaitTries tries
+// (a tenth of a second at least; waits here last a microsecond).  The loop is short
+// because it is in the way of straight code: with a clock read for the limit, each wait
+// took 200 cycles even where the phase was complete.
+constexpr int kWaitTries = 1 << 24;
 __device__ __forceinline__ bool prompt_wait(uint64_t& bar, uint32_t parity) {
-  // Asleep between tries: a warp that polls takes the issue slots of the softmax warp
-  // beside it (its steps took 2250 cycles where the others' took 1400).
-  for (int tries = 0; tries < 64; ++tries)
-    if (mbar_try_wait_for(smem_u32(&bar), parity, 20000)) return true;
-  if (mbar_wait_bounded(smem_u32(&bar), parity, kWaitLimitNs)) return true;
-  atomicOr(&g_prompt_error, GK_DEVERR_TIMEOUT);
-  return false;
+  const uint32_t at = smem_u32(&bar);
+  int tries = kWaitTries;
+  while (!mbar_try_wait(at, parity))
+    if (--tries == 0) {
+      atomicOr(&g_prompt_error, GK_DEVERR_TIMEOUT);
+      return false;
+    }
+  return true;
 }
 
 // The same by a whole warp, which goes on or gives up together.
@@ -376,22 +390,24 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
       store_row(p, it.q0 + r / p.G, h * p.G + r % p.G, lane, 0.f, 0.f, make_float2(0.f, 0.f));
     return;
   }
-  if (warp == 4) {
+  if (warp == kSoftWarps) {
     if (lane == 0) {
       mbar_init(smem_u32(&sm.q_full), 1);
-      for (int s = 0; s < kPromptStages; ++s) {
+      for (int s = 0; s < kKStages; ++s) {
         mbar_init(smem_u32(&sm.k_full[s]), 1);
-        mbar_init(smem_u32(&sm.v_full[s]), 1);
         mbar_init(smem_u32(&sm.k_free[s]), 1);
+      }
+      for (int s = 0; s < kVStages; ++s) {
+        mbar_init(smem_u32(&sm.v_full[s]), 1);
         mbar_init(smem_u32(&sm.v_free[s]), 1);
       }
       mbar_init(smem_u32(&sm.s_full), 1);
-      mbar_init(smem_u32(&sm.s_free), 4);
-      mbar_init(smem_u32(&sm.p_full), 4);
+      mbar_init(smem_u32(&sm.s_free), kSoftWarps);
+      mbar_init(smem_u32(&sm.p_full), kSoftWarps);
       mbar_init(smem_u32(&sm.o_full), 1);
       mbar_init_fence();
     }
-  } else if (warp == 5) {
+  } else if (warp == kSoftWarps + 1) {
     tmem_alloc<kTmemColumns>(smem_u32(&sm.tmem));
   }
   tmem_fence_before();
@@ -399,36 +415,40 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
   tmem_fence_after();
   const uint32_t tmem = sm.tmem;
 
-  if (warp == 4) {
+  if (warp == kSoftWarps) {
     const bool one = elect_one();
     if (one) {
       mbar_arrive_expect_tx(smem_u32(&sm.q_full), uint32_t(p.tile_tokens * p.G) * kHeadDim * 2);
       tma_load_3d(smem_u32(sm.q), &p.q_map, 0, h * p.G, it.q0, smem_u32(&sm.q_full));
     }
-    Phase s;
-    int j = 0;
-    for (; j < steps; ++j) {
-      const int t = it.k_lo + j * kPromptKeys;
-      // the first round finds the stages free
-      if (!warp_wait(sm.k_free[s.at], s.parity ^ 1)) break;
+    // K a step ahead of V; the first round finds the stages free
+    int nk = 0, nv = 0;
+    auto load = [&](uint64_t& free, uint64_t& full, uint8_t* to, const CUtensorMap* map, int n, int stages) {
+      if (!warp_wait(free, uint32_t(n / stages) & 1 ^ 1)) return false;
       if (one) {
-        mbar_arrive_expect_tx(smem_u32(&sm.k_full[s.at]), kTileBytes);
-        tma_load_3d(smem_u32(sm.k[s.at]), &p.k_map, 0, h, t, smem_u32(&sm.k_full[s.at]));
+        mbar_arrive_expect_tx(smem_u32(&full), kTileBytes);
+        tma_load_3d(smem_u32(to), map, 0, h, it.k_lo + n * kPromptKeys, smem_u32(&full));
       }
-      if (!warp_wait(sm.v_free[s.at], s.parity ^ 1)) break;
-      if (one) {
-        mbar_arrive_expect_tx(smem_u32(&sm.v_full[s.at]), kTileBytes);
-        tma_load_3d(smem_u32(sm.v[s.at]), &p.v_map, 0, h, t, smem_u32(&sm.v_full[s.at]));
+      return true;
+    };
+    while (nv < steps) {
+      if (nk < steps && nk < nv + 2) {
+        const int at = nk % kKStages;
+        if (!load(sm.k_free[at], sm.k_full[at], sm.k[at], &p.k_map, nk, kKStages)) break;
+        ++nk;
+      } else {
+        const int at = nv % kVStages;
+        if (!load(sm.v_free[at], sm.v_full[at], sm.v[at], &p.v_map, nv, kVStages)) break;
+        ++nv;
       }
-      s.next(kPromptStages);
     }
-    // gave up: its copies have landed before the CTA ends
-    for (int x = j < steps ? max(j - kPromptStages, 0) : steps; x <= min(j, steps - 1); ++x) {
-      const uint32_t parity = uint32_t(x / kPromptStages) & 1;
-      mbar_wait_bounded(smem_u32(&sm.k_full[x % kPromptStages]), parity, kWaitLimitNs);
-      mbar_wait_bounded(smem_u32(&sm.v_full[x % kPromptStages]), parity, kWaitLimitNs);
+    if (nv < steps) {  // gave up: its copies have landed before the CTA ends
+      for (int x = max(nk - kKStages, 0); x < nk; ++x)
+        mbar_wait_bounded(smem_u32(&sm.k_full[x % kKStages]), uint32_t(x / kKStages) & 1, kWaitLimitNs);
+      for (int x = max(nv - kVStages, 0); x < nv; ++x)
+        mbar_wait_bounded(smem_u32(&sm.v_full[x % kVStages]), uint32_t(x / kVStages) & 1, kWaitLimitNs);
     }
-  } else if (warp == 5) {
+  } else if (warp == kSoftWarps + 1) {
     // The whole warp runs this and one elected lane issues: in a branch of one lane the
     // compiler cannot see that the operands are uniform, and a product takes 45 to 90
     // cycles to issue where the tensor cores need 32 or 64 for it.
@@ -451,7 +471,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
     if (ok) {
       tmem_fence_after();
       scores(0);
-      k.next(kPromptStages);
+      k.next(kKStages);
     }
     for (int j = 0; ok && j < steps; ++j) {
       if (j + 1 < steps) {
@@ -459,7 +479,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
         if (!ok) break;
         tmem_fence_after();
         scores(k.at);
-        k.next(kPromptStages);
+        k.next(kKStages);
       }
       ok = warp_wait(sm.v_full[v.at], v.parity) && warp_wait(sm.p_full, j & 1);
       if (!ok) break;
@@ -473,7 +493,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
         mma_commit(smem_u32(&sm.o_full));
       }
       __syncwarp();
-      v.next(kPromptStages);
+      v.next(kVStages);
     }
     if (!ok) {  // gave up: its products are complete before the tensor memory is freed
       if (elect_one()) mma_commit(smem_u32(&sm.q_full));
@@ -487,7 +507,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
     // steps that every row sees whole
     const int whole_lo = it.diag + it.n - p.W, whole_hi = min(it.diag + 1, it.k_end) - kPromptKeys;
     const uint32_t lanes = tmem + (uint32_t(warp) << 21);  // lane 32 warp
-    float m = -INFINITY;  // reference maximum, units of q.k
+    float R = 0.f, scale_o = 1.f;
+    bool scale_due = false, over = false;
     float2 sum = make_float2(0.f, 0.f);
     Phase v;
     bool ok = true;
@@ -504,56 +525,64 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
       tmem_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sm.s_free));
-      if (t0 < whole_lo || t0 > whole_hi) {
+      if (__builtin_expect(t0 < whole_lo || t0 > whole_hi, 0)) {
         const uint32_t first = uint32_t(seen.x - t0), n = uint32_t(max(seen.y - seen.x, 0));
 #pragma unroll
         for (int c = 0; c < 128; ++c)
           if (uint32_t(c) - first >= n) s[c >> 5][c & 31] = __float_as_uint(-INFINITY);
       }
-      const float most = fmaxf(fmaxf(max32(s[0]), max32(s[1])), fmaxf(max32(s[2]), max32(s[3])));
-      if (j == 0) {
-        m = most;
-      } else if (__any_sync(kFull, most > m + kLazyScore)) {
-        // probabilities would pass 2^kLazyLog2: a new reference, and O and the sum in its units
-        const float to = fmaxf(m, most);
-        const float f = to == m ? 1.f : ex2((m - to) * kScoreLog2);
-        m = to;
-        sum.x *= f;
-        sum.y *= f;
-        if (!(ok = warp_wait(sm.o_full, (j - 1) & 1))) break;
-        tmem_fence_after();
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t o[16];
-          tmem_ld16(lanes + kTmemO + 16 * c, o);
-          tmem_wait_ld();
-          tmem_landed(o);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-          tmem_st16(lanes + kTmemO + 16 * c, o);
-        }
+      if (__builtin_expect(j == 0, 0)) {
+        const float top = fmaxf(fmaxf(max32(s[0]), max32(s[1])), fmaxf(max32(s[2]), max32(s[3])));
+        if (fabsf(top) < INFINITY) R = fmaf(top, kScoreLog2, kHeadroom);
       }
-      const float ref = m == -INFINITY ? 0.f : -m * kScoreLog2;
-      const float2 scale = make_float2(kScoreLog2, kScoreLog2), shift = make_float2(ref, ref);
-      uint32_t pr[4][16];
+      const float2 scale = make_float2(kScoreLog2, kScoreLog2), shift = make_float2(-R, -R);
+      float2 part = make_float2(0.f, 0.f);
+      uint32_t pr[2][32];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float2 x = fma2(make_float2(__uint_as_float(s[c][2 * e]), __uint_as_float(s[c][2 * e + 1])),
-                                scale, shift);
-          const float2 y = make_float2(ex2(x.x), ex2(x.y));
-          sum = add2(sum, y);
-          pr[c][e] = f32x2_to_bf16x2(y.x, y.y);
-        }
+      for (int e = 0; e < 64; ++e) {
+        const uint32_t* se = &s[e >> 4][(2 * e) & 31];
+        const float2 x = fma2(make_float2(__uint_as_float(se[0]), __uint_as_float(se[1])), scale, shift);
+        const float2 y = make_float2(ex2(x.x), ex2(x.y));
+        part = add2(part, y);
+        pr[e >> 5][e & 31] = f32x2_to_bf16x2(y.x, y.y);
       }
       // P of the step before has been used: waited for as late as possible (before the
       // exponentials, it adds the product's time to every step's)
-      if (j > 0 && !(ok = warp_wait(sm.o_full, (j - 1) & 1))) break;
-      tmem_fence_after();
+      if (j > 0) {
+        if (!(ok = warp_wait(sm.o_full, (j - 1) & 1))) break;
+        tmem_fence_after();
+      }
+      tmem_st32(lanes + kTmemP, pr[0]);
+      tmem_st32(lanes + kTmemP + 32, pr[1]);
+      if (__builtin_expect(scale_due, 0)) {
+        scale_due = false;
+#pragma unroll 1
+        for (int c = 0; c < kHeadDim; c += 32) {
+          uint32_t o[32];
+          tmem_ld32(lanes + kTmemO + c, o);
+          tmem_wait_ld();
+          tmem_landed(o);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_st16(lanes + kTmemP + 16 * c, pr[c]);
-      if (t0 + kPromptKeys > it.k_end) {
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * scale_o);
+          tmem_st32(lanes + kTmemO + c, o);
+        }
+      }
+      sum = add2(sum, part);
+      const float total = part.x + part.y;
+      if (__builtin_expect(__any_sync(kFull, total > kLargest), 0)) {
+        over = over || total > kLargest * kLargest;
+        if (j + 1 < steps) {
+          // at most by 2^100, a normal float
+          const float up = fminf(kHeadroom + float(int(__float_as_uint(total) >> 23) - 127), 100.f);
+          const float to = total > kLargest ? R + up : R;
+          scale_o = ex2(R - to);
+          R = to;
+          sum.x *= scale_o;
+          sum.y *= scale_o;
+          scale_due = true;
+        }
+      }
+      if (__builtin_expect(t0 + kPromptKeys > it.k_end, 0)) {
         // keys behind the item's: whatever V is there (other sequences, padding), zero
         // times it must be zero
         if (!(ok = warp_wait(sm.v_full[v.at], v.parity))) break;
@@ -564,7 +593,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
         }
         fence_proxy_async_shared();
       }
-      v.next(kPromptStages);
+      v.next(kVStages);
       tmem_wait_st();
       tmem_fence_before();
       __syncwarp();
@@ -579,20 +608,20 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
       tmem_landed(o[0]);
       tmem_landed(o[1]);
       const float l = sum.x + sum.y;
-      float size = 0.f;
+      float size = fabsf(l);
 #pragma unroll
       for (int c = 0; c < 64; c += 2)
         size = max3_abs_nan(size, __uint_as_float(o[c >> 5][c & 31]), __uint_as_float(o[c >> 5][(c & 31) + 1]));
-      // Zero times an unseen key's infinity or NaN, if it is not a seen key's: such rows
-      // are computed again from the keys that they see.
-      uint32_t again = __ballot_sync(kFull, valid && !(size < INFINITY));
-      uint32_t done = 0;
+      // Zero times an unseen key's infinity or NaN, if it is not a seen key's, or an
+      // overflow: such rows are computed again from the keys that they see.
+      uint32_t todo = __ballot_sync(kFull, valid && !(size < INFINITY)), done = 0;
+      const uint32_t sure = __ballot_sync(kFull, over);
       float* qs = reinterpret_cast<float*>(sm.q) + warp * kHeadDim;  // Q has been used
-      while (again) {
-        const int x = __ffs(again) - 1, rr = 32 * warp + x, tt = rr / p.G;
-        again &= again - 1;
+      while (todo) {
+        const int x = __ffs(todo) - 1, rr = 32 * warp + x, tt = rr / p.G;
+        todo &= todo - 1;
         const int2 keys = seen_keys(p, it, tt);
-        if (!any_not_finite(p, it.k_lo, min(keys.x, it.k_end), h) &&
+        if (!((sure >> x) & 1) && !any_not_finite(p, it.k_lo, min(keys.x, it.k_end), h) &&
             !any_not_finite(p, max(keys.y, it.k_lo), it.k_end, h))
           continue;
         const int head = h * p.G + rr - tt * p.G;
@@ -609,10 +638,9 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
         done |= 1u << x;
       }
       if (valid && !((done >> lane) & 1u)) {
-        const float ml = m * kScoreLog2;
         if (it.rec >= 0) {
           float* rec = p.records + (int64_t(it.rec) * p.Hkv + h) * kPromptRecFloats;
-          rec[r] = ml;
+          rec[r] = l == 0.f ? -INFINITY : R;
           rec[kPromptRows + r] = l;
           uint4* to = reinterpret_cast<uint4*>(rec + 2 * kPromptRows + r * kHeadDim);
 #pragma unroll
@@ -622,12 +650,11 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
         } else {
           const int head = h * p.G + r - token * p.G;
           const int64_t at = (int64_t(it.q0 + token) * p.Hq + head) * kHeadDim;
-          const float f = l == 0.f ? 0.f : out_scale(l, ml, p.sinks ? p.sinks + head : nullptr, 1.f);
+          const float f = l == 0.f ? 0.f : out_scale(l, R, p.sinks ? p.sinks + head : nullptr, 1.f);
           uint4* to = reinterpret_cast<uint4*>(p.out + at);
 #pragma unroll
           for (int c = 0; c < 64; ++c)
-            o[c >> 5][c & 31] =
-                l == 0.f ? 0u : __float_as_uint(__uint_as_float(o[c >> 5][c & 31]) * f);
+            o[c >> 5][c & 31] = l == 0.f ? 0u : __float_as_uint(__uint_as_float(o[c >> 5][c & 31]) * f);
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
             uint32_t w[4];
@@ -652,7 +679,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
   tmem_fence_before();
   __syncthreads();
   __syncwarp();
-  if (warp == 5) tmem_dealloc<kTmemColumns>(tmem);
+  if (warp == kSoftWarps + 1) tmem_dealloc<kTmemColumns>(tmem);
 }
 
 constexpr int kRowThreads = 256;
