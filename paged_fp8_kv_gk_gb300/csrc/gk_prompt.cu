@@ -211,9 +211,8 @@ struct RowResult {
 };
 
 // One row by one warp, 32 keys at a time: a key a lane for the scores, two channels
-// a lane for the sums.  Only keys that the row sees are read.  q: the row, in shared
-// memory (64 floats of the warp's own).
-__device__ __noinline__ RowResult attend_row(const PromptAttnParams& p, int2 keys, int h, const float* q) {
+// a lane for the sums.  Only keys that the row sees are read.
+__device__ __noinline__ RowResult attend_row(const PromptAttnParams& p, int2 keys, int h, const uint16_t* q) {
   const int lane = threadIdx.x & 31;
   RowResult r = {-INFINITY, 0.f, make_float2(0.f, 0.f)};
   for (int t0 = keys.x; t0 < keys.y; t0 += 32) {
@@ -224,12 +223,11 @@ __device__ __noinline__ RowResult attend_row(const PromptAttnParams& p, int2 key
       float2 a = make_float2(0.f, 0.f);
       for (int c = 0; c < kHeadDim; c += 8) {
         const uint4 w = __ldcg(reinterpret_cast<const uint4*>(kr + c));
-        const float4 q0 = *reinterpret_cast<const float4*>(q + c);
-        const float4 q1 = *reinterpret_cast<const float4*>(q + c + 4);
-        a = fma2(bf16x2_to_f32x2(w.x), make_float2(q0.x, q0.y), a);
-        a = fma2(bf16x2_to_f32x2(w.y), make_float2(q0.z, q0.w), a);
-        a = fma2(bf16x2_to_f32x2(w.z), make_float2(q1.x, q1.y), a);
-        a = fma2(bf16x2_to_f32x2(w.w), make_float2(q1.z, q1.w), a);
+        const uint4 x = *reinterpret_cast<const uint4*>(q + c);
+        a = fma2(bf16x2_to_f32x2(w.x), bf16x2_to_f32x2(x.x), a);
+        a = fma2(bf16x2_to_f32x2(w.y), bf16x2_to_f32x2(x.y), a);
+        a = fma2(bf16x2_to_f32x2(w.z), bf16x2_to_f32x2(x.z), a);
+        a = fma2(bf16x2_to_f32x2(w.w), bf16x2_to_f32x2(x.w), a);
       }
       s = (a.x + a.y) * kScoreLog2;
     }
@@ -286,22 +284,26 @@ __device__ __forceinline__ float max32(const uint32_t (&s)[32]) {
 // =========================================================================
 // Attention
 // =========================================================================
-// A CTA has one tile of 128 rows (16 tokens of 8 heads, say) and a run of keys, 128
-// a step.  Warps 0-3 do the softmax, a thread a row.  Warp 4 copies, warp 5 issues the
+// An item is a tile of 128 rows (16 tokens of 8 heads, say) and a run of keys, 128
+// a step, for one kv head.  Warps 0-3 do the softmax, a thread a row.  Warp 4 copies, warp 5 issues the
 // products:
 //   S = Q K^T  128 x 128 x 64  both operands in shared memory, fp32 in tensor memory
 //   O += P V   128 x 64 x 128  P, bf16, in tensor memory; V in shared memory, MN-major
 // A row's scores are loaded into registers as soon as they are there, so that the next
 // step's S is computed while this one's exponentials are; two CTAs an SM fill each
-// other's gaps.
+// other's gaps.  The grid is what the GPU holds at a time; a CTA takes items in turns
+// through the plan (there and back, so that long and short ones even out) and its warps
+// run on from one to the next: Q, K and V of the next item are copied and its first S
+// computed while this one's last exponentials and its output are.
 //
 // The softmax's reference R of a row (log2 units; p = 2^(s - R)) is the largest score
 // of the first step plus kHeadroom (every row sees a key of its first step, or none at
 // all), and no step after it looks for a maximum: p and the sums are floats (bf16 in P,
-// with a float's exponents), as exact at 2^60 as at 1.  After a step whose sum passes
-// kLargest the row takes a new R, and O and the sum are scaled to it.  A row that
-// overflows all the same (a score 54 or more above all before it, and then values of
-// 2^60) is computed again by attend_row, as are rows with unseen infinities or NaN.
+// with a float's exponents), as exact at 2^60 as at 1.  Every fourth step, a row whose
+// sum has passed kLargest takes a new R, and O and the sum are scaled to it.  A row that
+// overflows all the same (a score 54 or more above all up to the last such step, and
+// then values of 2^60) is computed again by attend_row, as are rows with unseen
+// infinities or NaN.
 constexpr int kSoftWarps = 4;
 constexpr int kAttnThreads = 32 * (kSoftWarps + 2);
 constexpr int kKStages = 3, kVStages = 2;               // V is needed a softmax later than K
@@ -309,15 +311,19 @@ constexpr int kTileBytes = kPromptRows * kHeadDim * 2;  // Q, and one step of K 
 constexpr int kTmemColumns = 256;                       // S 128, O 64, P 64
 constexpr int kTmemO = 128, kTmemP = 192;
 constexpr float kHeadroom = 24.f;
-constexpr float kLargest = 0x1p30f;  // of a row's sum of a step
+constexpr float kLargest = 0x1p30f;  // of a row's sum
 
 struct PromptSmem {
-  alignas(1024) uint8_t q[kTileBytes];
+  alignas(1024) uint8_t q[2][kTileBytes];
   uint8_t k[kKStages][kTileBytes];
   uint8_t v[kVStages][kTileBytes];
-  uint64_t q_full, k_full[kKStages], v_full[kVStages], k_free[kKStages], v_free[kVStages];
+  uint64_t q_full[2], q_free[2], k_full[kKStages], v_full[kVStages], k_free[kKStages],
+      v_free[kVStages];
   uint64_t s_full, s_free, p_full, o_full;
   uint32_t tmem;
+  int failed;  // a wait gave up
+  // a softmax warp's item and the one after it, as in the plan: out of its registers
+  alignas(16) int item[kSoftWarps][2][8];
 };
 static_assert(kPromptKeys * kHeadDim * 2 == kTileBytes, "a step of K is as large as Q");
 static_assert(sizeof(PromptSmem) <= 115712, "two CTAs an SM");
@@ -325,33 +331,52 @@ static_assert(sizeof(PromptSmem) <= 115712, "two CTAs an SM");
 struct Phase {  // place in a ring of barriers, and the parity of its next phase
   int at = 0;
   uint32_t parity = 0;
-  __device__ __forceinline__ void next(int n) {
-    if (++at == n) {
+  template <int kN>
+  __device__ __forceinline__ void next() {
+    if (++at == kN) {
       at = 0;
       parity ^= 1;
     }
   }
 };
 
-// Waits for a barrier's phase; false, with the error bit set, after kWaitTries tries
-// (a tenth of a second at least; waits here last a microsecond).  The loop is short
-// because it is in the way of straight code: with a clock read for the limit, each wait
-// took 200 cycles even where the phase was complete.
-constexpr int kWaitTries = 1 << 24;
-__device__ __forceinline__ bool prompt_wait(uint64_t& bar, uint32_t parity) {
-  const uint32_t at = smem_u32(&bar);
-  int tries = kWaitTries;
-  while (!mbar_try_wait(at, parity))
-    if (--tries == 0) {
-      atomicOr(&g_prompt_error, GK_DEVERR_TIMEOUT);
-      return false;
-    }
-  return true;
+// The places in the plan that a CTA takes, (item, kv head): every grid's width, there
+// and back.
+struct Turn {
+  int n, at, round = 0;
+  __device__ __forceinline__ Turn(const PromptAttnParams& p) : n(__ldcg(p.hdr) * p.Hkv) { next(); }
+  __device__ __forceinline__ bool more() const { return at < n; }
+  __device__ __forceinline__ void next() {
+    const int g = int(gridDim.x);
+    at = round * g + (round & 1 ? g - 1 - int(blockIdx.x) : int(blockIdx.x));
+    ++round;
+  }
+};
+__device__ __forceinline__ int item_steps(const Item& it) {
+  return (it.k_end - it.k_lo + kPromptKeys - 1) / kPromptKeys;
 }
 
-// The same by a whole warp, which goes on or gives up together.
-__device__ __forceinline__ bool warp_wait(uint64_t& bar, uint32_t parity) {
-  return __all_sync(kFull, prompt_wait(bar, parity));
+// Waits for a barrier's phase.  After kWaitTries tries (a tenth of a second at least;
+// waits here last a microsecond) the CTA is marked as failed and goes on, so that its
+// warps stay together: it waits for nothing from then on, writes no output, and ends
+// once its copies have had time to land.  The loop in the way is short: with a clock
+// read for the limit, a vote and a way out, each wait took 200 cycles even where the
+// phase was complete.
+constexpr int kWaitTries = 1 << 24;
+__device__ __noinline__ void prompt_wait_long(uint32_t bar, uint32_t parity, volatile int* failed) {
+  for (int tries = 0; tries < kWaitTries && !*failed; ++tries)
+    if (mbar_try_wait(bar, parity)) return;
+  *failed = 1;
+  atomicOr(&g_prompt_error, GK_DEVERR_TIMEOUT);
+}
+__device__ __forceinline__ void prompt_wait(PromptSmem& sm, uint64_t& bar, uint32_t parity) {
+  const uint32_t at = smem_u32(&bar);
+  int tries = 4096;
+  while (!mbar_try_wait(at, parity))
+    if (--tries == 0) {
+      prompt_wait_long(at, parity, &sm.failed);
+      break;
+    }
 }
 
 // Whether one of the keys [a, b) has a V that is not finite (a warp).
@@ -380,19 +405,12 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   PromptSmem& sm = *reinterpret_cast<PromptSmem*>(smem_raw);
   const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  follow_stream();
-  const int i = int(blockIdx.x) / p.Hkv, h = int(blockIdx.x) - i * p.Hkv;
-  if (i >= __ldcg(p.hdr)) return;
-  const Item it = load_item(p, i);
-  const int steps = (it.k_end - it.k_lo + kPromptKeys - 1) / kPromptKeys;
-  if (steps == 0) {  // no key: zeros (such a tile is not split)
-    for (int r = warp; r < it.n * p.G; r += kAttnThreads / 32)
-      store_row(p, it.q0 + r / p.G, h * p.G + r % p.G, lane, 0.f, 0.f, make_float2(0.f, 0.f));
-    return;
-  }
   if (warp == kSoftWarps) {
     if (lane == 0) {
-      mbar_init(smem_u32(&sm.q_full), 1);
+      for (int s = 0; s < 2; ++s) {
+        mbar_init(smem_u32(&sm.q_full[s]), 1);
+        mbar_init(smem_u32(&sm.q_free[s]), 1);
+      }
       for (int s = 0; s < kKStages; ++s) {
         mbar_init(smem_u32(&sm.k_full[s]), 1);
         mbar_init(smem_u32(&sm.k_free[s]), 1);
@@ -406,6 +424,10 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
       mbar_init(smem_u32(&sm.p_full), kSoftWarps);
       mbar_init(smem_u32(&sm.o_full), 1);
       mbar_init_fence();
+      sm.failed = 0;
+      tma_prefetch_map(&p.q_map);
+      tma_prefetch_map(&p.k_map);
+      tma_prefetch_map(&p.v_map);
     }
   } else if (warp == kSoftWarps + 1) {
     tmem_alloc<kTmemColumns>(smem_u32(&sm.tmem));
@@ -414,39 +436,43 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
   __syncthreads();
   tmem_fence_after();
   const uint32_t tmem = sm.tmem;
+  follow_stream();
+  Turn turn(p);
 
   if (warp == kSoftWarps) {
     const bool one = elect_one();
-    if (one) {
-      mbar_arrive_expect_tx(smem_u32(&sm.q_full), uint32_t(p.tile_tokens * p.G) * kHeadDim * 2);
-      tma_load_3d(smem_u32(sm.q), &p.q_map, 0, h * p.G, it.q0, smem_u32(&sm.q_full));
-    }
-    // K a step ahead of V; the first round finds the stages free
-    int nk = 0, nv = 0;
-    auto load = [&](uint64_t& free, uint64_t& full, uint8_t* to, const CUtensorMap* map, int n, int stages) {
-      if (!warp_wait(free, uint32_t(n / stages) & 1 ^ 1)) return false;
+    Phase q, k, v;
+    // the first round finds the places free
+    auto load = [&](uint64_t& free, uint64_t& full, uint32_t parity, uint8_t* to, const CUtensorMap* map,
+                    uint32_t bytes, int head, int token) {
+      prompt_wait(sm, free, parity ^ 1);
       if (one) {
-        mbar_arrive_expect_tx(smem_u32(&full), kTileBytes);
-        tma_load_3d(smem_u32(to), map, 0, h, it.k_lo + n * kPromptKeys, smem_u32(&full));
+        mbar_arrive_expect_tx(smem_u32(&full), bytes);
+        tma_load_3d(smem_u32(to), map, 0, head, token, smem_u32(&full));
       }
-      return true;
+      __syncwarp();
     };
-    while (nv < steps) {
-      if (nk < steps && nk < nv + 2) {
-        const int at = nk % kKStages;
-        if (!load(sm.k_free[at], sm.k_full[at], sm.k[at], &p.k_map, nk, kKStages)) break;
-        ++nk;
-      } else {
-        const int at = nv % kVStages;
-        if (!load(sm.v_free[at], sm.v_full[at], sm.v[at], &p.v_map, nv, kVStages)) break;
-        ++nv;
+    for (; turn.more(); turn.next()) {
+      const int i = turn.at / p.Hkv, h = turn.at - i * p.Hkv;
+      const Item it = load_item(p, i);
+      const int steps = item_steps(it), k_lo = it.k_lo;
+      if (steps == 0) continue;
+      load(sm.q_free[q.at], sm.q_full[q.at], q.parity, sm.q[q.at], &p.q_map,
+           uint32_t(p.tile_tokens * p.G) * kHeadDim * 2, h * p.G, it.q0);
+      q.next<2>();
+      // K a step ahead of V
+      auto load_k = [&](int j) {
+        load(sm.k_free[k.at], sm.k_full[k.at], k.parity, sm.k[k.at], &p.k_map, kTileBytes, h,
+             k_lo + j * kPromptKeys);
+        k.next<kKStages>();
+      };
+      load_k(0);
+      for (int j = 0; j < steps; ++j) {
+        if (j + 1 < steps) load_k(j + 1);
+        load(sm.v_free[v.at], sm.v_full[v.at], v.parity, sm.v[v.at], &p.v_map, kTileBytes, h,
+             k_lo + j * kPromptKeys);
+        v.next<kVStages>();
       }
-    }
-    if (nv < steps) {  // gave up: its copies have landed before the CTA ends
-      for (int x = max(nk - kKStages, 0); x < nk; ++x)
-        mbar_wait_bounded(smem_u32(&sm.k_full[x % kKStages]), uint32_t(x / kKStages) & 1, kWaitLimitNs);
-      for (int x = max(nv - kVStages, 0); x < nv; ++x)
-        mbar_wait_bounded(smem_u32(&sm.v_full[x % kVStages]), uint32_t(x / kVStages) & 1, kWaitLimitNs);
     }
   } else if (warp == kSoftWarps + 1) {
     // The whole warp runs this and one elected lane issues: in a branch of one lane the
@@ -454,152 +480,206 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
     // cycles to issue where the tensor cores need 32 or 64 for it.
     constexpr uint32_t kS = bf16_idesc(kPromptRows, kPromptKeys, false);
     constexpr uint32_t kO = bf16_idesc(kPromptRows, kHeadDim, true);
-    const uint64_t qd = sw128_desc(smem_u32(sm.q));
-    const uint64_t kd0 = sw128_desc(smem_u32(sm.k[0])), vd0 = sw128_desc(smem_u32(sm.v[0]));
-    auto scores = [&](int stage) {
-      const uint64_t kd = kd0 + uint64_t(stage * (kTileBytes >> 4));
+    const uint64_t qd0 = sw128_desc(smem_u32(sm.q[0])), kd0 = sw128_desc(smem_u32(sm.k[0])),
+                   vd0 = sw128_desc(smem_u32(sm.v[0]));
+    Phase q, k, v;
+    uint32_t s_parity = 1, p_parity = 0;  // S is free at first
+    // S of the next step in turn, `left` steps of its item counting itself
+    auto scores = [&](int left, bool first) {
+      if (first) prompt_wait(sm, sm.q_full[q.at], q.parity);
+      prompt_wait(sm, sm.k_full[k.at], k.parity);
+      prompt_wait(sm, sm.s_free, s_parity);
+      s_parity ^= 1;
+      tmem_fence_after();
+      const uint64_t qd = qd0 + uint64_t(q.at * (kTileBytes >> 4)), kd = kd0 + uint64_t(k.at * (kTileBytes >> 4));
       if (elect_one()) {
 #pragma unroll
         for (int c = 0; c < kHeadDim / 16; ++c) mma_ss(tmem, qd + 2 * c, kd + 2 * c, kS, c > 0);
-        mma_commit(smem_u32(&sm.k_free[stage]));
+        mma_commit(smem_u32(&sm.k_free[k.at]));
+        if (left == 1) mma_commit(smem_u32(&sm.q_free[q.at]));
         mma_commit(smem_u32(&sm.s_full));
       }
       __syncwarp();
+      k.next<kKStages>();
+      if (left == 1) q.next<2>();
     };
-    Phase k, v;
-    bool ok = warp_wait(sm.q_full, 0) && warp_wait(sm.k_full[0], 0);
-    if (ok) {
-      tmem_fence_after();
-      scores(0);
-      k.next(kKStages);
-    }
-    for (int j = 0; ok && j < steps; ++j) {
-      if (j + 1 < steps) {
-        ok = warp_wait(sm.k_full[k.at], k.parity) && warp_wait(sm.s_free, j & 1);
-        if (!ok) break;
+    // keys of the next item that has any; 0: no more
+    auto next_item = [&]() -> int {
+      int keys = 0;
+      for (; turn.more() && keys == 0; turn.next()) {
+        const Item it = load_item(p, turn.at / p.Hkv);
+        keys = it.k_end - it.k_lo;
+      }
+      return keys;
+    };
+    auto steps_of = [](int keys) { return (keys + kPromptKeys - 1) / kPromptKeys; };
+    int next = next_item();
+    if (next) scores(steps_of(next), true);
+    while (next) {
+      const int n = next, steps = steps_of(n);
+      next = next_item();  // its first S follows this one's last
+      for (int j = 0; j < steps; ++j) {
+        if (j + 1 < steps)
+          scores(steps - j - 1, false);
+        else if (next)
+          scores(steps_of(next), true);
+        prompt_wait(sm, sm.v_full[v.at], v.parity);
+        prompt_wait(sm, sm.p_full, p_parity);
+        p_parity ^= 1;
         tmem_fence_after();
-        scores(k.at);
-        k.next(kKStages);
-      }
-      ok = warp_wait(sm.v_full[v.at], v.parity) && warp_wait(sm.p_full, j & 1);
-      if (!ok) break;
-      tmem_fence_after();
-      const uint64_t vd = vd0 + uint64_t(v.at * (kTileBytes >> 4));
-      if (elect_one()) {
+        const uint64_t vd = vd0 + uint64_t(v.at * (kTileBytes >> 4));
+        const int keys = n - j * kPromptKeys;
+        if (elect_one()) {
 #pragma unroll
-        for (int c = 0; c < kPromptKeys / 16; ++c)
-          mma_ts(tmem + kTmemO, tmem + kTmemP + 8 * c, vd + 128 * c, kO, j > 0 || c > 0);
-        mma_commit(smem_u32(&sm.v_free[v.at]));
-        mma_commit(smem_u32(&sm.o_full));
+          for (int c = 0; c < kPromptKeys / 16; ++c)
+            if (16 * c < keys)
+              mma_ts(tmem + kTmemO, tmem + kTmemP + 8 * c, vd + 128 * c, kO, j > 0 || c > 0);
+          mma_commit(smem_u32(&sm.v_free[v.at]));
+          mma_commit(smem_u32(&sm.o_full));
+        }
+        __syncwarp();
+        v.next<kVStages>();
       }
-      __syncwarp();
-      v.next(kVStages);
-    }
-    if (!ok) {  // gave up: its products are complete before the tensor memory is freed
-      if (elect_one()) mma_commit(smem_u32(&sm.q_full));
-      mbar_wait_bounded(smem_u32(&sm.q_full), 1, kWaitLimitNs);
     }
   } else {
     const int r = threadIdx.x;  // row of the tile
-    const int token = r / p.G;
-    const bool valid = token < it.n && r < p.tile_tokens * p.G;
-    const int2 seen = seen_keys(p, it, min(token, it.n - 1));
-    // steps that every row sees whole
-    const int whole_lo = it.diag + it.n - p.W, whole_hi = min(it.diag + 1, it.k_end) - kPromptKeys;
     const uint32_t lanes = tmem + (uint32_t(warp) << 21);  // lane 32 warp
-    float R = 0.f, scale_o = 1.f;
-    bool scale_due = false, over = false;
-    float2 sum = make_float2(0.f, 0.f);
-    Phase v;
-    bool ok = true;
-    for (int j = 0; j < steps; ++j) {
-      const int t0 = it.k_lo + j * kPromptKeys;
-      if (!(ok = warp_wait(sm.s_full, j & 1))) break;
-      tmem_fence_after();
-      uint32_t s[4][32];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(lanes + 32 * c, s[c]);
-      tmem_wait_ld();
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_landed(s[c]);
-      tmem_fence_before();
+    uint32_t count = 0;  // steps so far: the parities of all barriers
+    auto fetch = [&](int place) {
+      if (turn.more() && lane < 2)
+        cp_async16(smem_u32(&sm.item[warp][place][4 * lane]), p.items + 2 * (turn.at / p.Hkv) + lane);
+    };
+    fetch(0);
+    for (int place = 0; turn.more(); place ^= 1) {
+      const int h = turn.at % p.Hkv;
+      cp_async_wait_all();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sm.s_free));
-      if (__builtin_expect(t0 < whole_lo || t0 > whole_hi, 0)) {
-        const uint32_t first = uint32_t(seen.x - t0), n = uint32_t(max(seen.y - seen.x, 0));
-#pragma unroll
-        for (int c = 0; c < 128; ++c)
-          if (uint32_t(c) - first >= n) s[c >> 5][c & 31] = __float_as_uint(-INFINITY);
+      const volatile int* kept = sm.item[warp][place];
+      auto item = [&]() -> Item { return {kept[0], kept[1], kept[2], kept[3], kept[4], kept[5]}; };
+      turn.next();
+      fetch(place ^ 1);
+      const Item at_first = item();
+      const int steps = item_steps(at_first);
+      if (steps == 0) {  // no key: zeros (such a tile is not split)
+        for (int x = warp; x < at_first.n * p.G; x += kSoftWarps)
+          store_row(p, at_first.q0 + x / p.G, h * p.G + x % p.G, lane, 0.f, 0.f, make_float2(0.f, 0.f));
+        continue;
       }
-      if (__builtin_expect(j == 0, 0)) {
-        const float top = fmaxf(fmaxf(max32(s[0]), max32(s[1])), fmaxf(max32(s[2]), max32(s[3])));
-        if (fabsf(top) < INFINITY) R = fmaf(top, kScoreLog2, kHeadroom);
-      }
-      const float2 scale = make_float2(kScoreLog2, kScoreLog2), shift = make_float2(-R, -R);
-      float2 part = make_float2(0.f, 0.f);
-      uint32_t pr[2][32];
-#pragma unroll
-      for (int e = 0; e < 64; ++e) {
-        const uint32_t* se = &s[e >> 4][(2 * e) & 31];
-        const float2 x = fma2(make_float2(__uint_as_float(se[0]), __uint_as_float(se[1])), scale, shift);
-        const float2 y = make_float2(ex2(x.x), ex2(x.y));
-        part = add2(part, y);
-        pr[e >> 5][e & 31] = f32x2_to_bf16x2(y.x, y.y);
-      }
-      // P of the step before has been used: waited for as late as possible (before the
-      // exponentials, it adds the product's time to every step's)
-      if (j > 0) {
-        if (!(ok = warp_wait(sm.o_full, (j - 1) & 1))) break;
+      // steps that every row sees whole
+      const int whole_lo = at_first.diag + at_first.n - p.W;
+      const int whole_hi = min(at_first.diag + 1, at_first.k_end) - kPromptKeys;
+      float R = 0.f, scale_o = 1.f;
+      bool scale_due = false, over = false;
+      float2 sum = make_float2(0.f, 0.f);
+      int t0 = at_first.k_lo;
+      for (int j = 0; j < steps; ++j, ++count, t0 += kPromptKeys) {
+        prompt_wait(sm, sm.s_full, count & 1);
         tmem_fence_after();
-      }
-      tmem_st32(lanes + kTmemP, pr[0]);
-      tmem_st32(lanes + kTmemP + 32, pr[1]);
-      if (__builtin_expect(scale_due, 0)) {
-        scale_due = false;
+        uint32_t s[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(lanes + 32 * c, s[c]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_landed(s[c]);
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.s_free));
+        int keys = kPromptKeys;  // of the step
+        if (__builtin_expect(t0 < whole_lo || t0 > whole_hi, 0)) {
+          const Item it = item();
+          keys = it.k_end - t0;
+          const int2 seen = seen_keys(p, it, min(r / p.G, it.n - 1));
+          const uint32_t first = uint32_t(seen.x - t0), n = uint32_t(max(seen.y - seen.x, 0));
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (t0 + 32 * c < whole_lo || t0 + 32 * c - (kPromptKeys - 32) > whole_hi) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (uint32_t(32 * c + e) - first >= n) s[c][e] = __float_as_uint(-INFINITY);
+            }
+        }
+        if (__builtin_expect(j == 0, 0)) {
+          const float top = fmaxf(fmaxf(max32(s[0]), max32(s[1])), fmaxf(max32(s[2]), max32(s[3])));
+          if (fabsf(top) < INFINITY) R = fmaf(top, kScoreLog2, kHeadroom);
+        }
+        const float2 scale = make_float2(kScoreLog2, kScoreLog2), shift = make_float2(-R, -R);
+        auto probabilities = [&](uint32_t s0, uint32_t s1) -> uint32_t {
+          const float2 x = fma2(make_float2(__uint_as_float(s0), __uint_as_float(s1)), scale, shift);
+          const float2 y = make_float2(ex2(x.x), ex2(x.y));
+          sum = add2(sum, y);
+          return f32x2_to_bf16x2(y.x, y.y);
+        };
+        // P of the step before has been used: waited for as late as possible (before the
+        // exponentials, it adds the product's time to every step's)
+        auto p_free = [&]() {
+          if (j > 0) {
+            prompt_wait(sm, sm.o_full, (count - 1) & 1);
+            tmem_fence_after();
+          }
+        };
+        if (__builtin_expect(keys > 32, 1)) {
+          uint32_t pr[2][32];
+#pragma unroll
+          for (int e = 0; e < 64; ++e) pr[e >> 5][e & 31] = probabilities(s[e >> 4][2 * e & 31], s[e >> 4][(2 * e & 31) + 1]);
+          p_free();
+          tmem_st32(lanes + kTmemP, pr[0]);
+          tmem_st32(lanes + kTmemP + 32, pr[1]);
+        } else {  // the last few keys of a window or a prompt; the product takes no more
+          uint32_t pr[32];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            pr[e] = probabilities(s[0][2 * e], s[0][2 * e + 1]);
+            pr[16 + e] = 0;
+          }
+          p_free();
+          tmem_st32(lanes + kTmemP, pr);
+        }
+        if (__builtin_expect(scale_due, 0)) {
+          scale_due = false;
 #pragma unroll 1
-        for (int c = 0; c < kHeadDim; c += 32) {
-          uint32_t o[32];
-          tmem_ld32(lanes + kTmemO + c, o);
-          tmem_wait_ld();
-          tmem_landed(o);
+          for (int c = 0; c < kHeadDim; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(lanes + kTmemO + c, o);
+            tmem_wait_ld();
+            tmem_landed(o);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * scale_o);
-          tmem_st32(lanes + kTmemO + c, o);
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * scale_o);
+            tmem_st32(lanes + kTmemO + c, o);
+          }
         }
-      }
-      sum = add2(sum, part);
-      const float total = part.x + part.y;
-      if (__builtin_expect(__any_sync(kFull, total > kLargest), 0)) {
-        over = over || total > kLargest * kLargest;
-        if (j + 1 < steps) {
-          // at most by 2^100, a normal float
-          const float up = fminf(kHeadroom + float(int(__float_as_uint(total) >> 23) - 127), 100.f);
-          const float to = total > kLargest ? R + up : R;
-          scale_o = ex2(R - to);
-          R = to;
-          sum.x *= scale_o;
-          sum.y *= scale_o;
-          scale_due = true;
+        if ((j & 3) == 3) {
+          const float total = sum.x + sum.y;
+          if (__builtin_expect(__any_sync(kFull, total > kLargest), 0)) {
+            over = over || total > kLargest * kLargest;
+            if (j + 1 < steps) {
+              // at most by 2^100, a normal float
+              const float up = fminf(kHeadroom + float(int(__float_as_uint(total) >> 23) - 127), 100.f);
+              const float to = total > kLargest ? R + up : R;
+              scale_o = ex2(R - to);
+              R = to;
+              sum.x *= scale_o;
+              sum.y *= scale_o;
+              scale_due = true;
+            }
+          }
         }
-      }
-      if (__builtin_expect(t0 + kPromptKeys > it.k_end, 0)) {
-        // keys behind the item's: whatever V is there (other sequences, padding), zero
-        // times it must be zero
-        if (!(ok = warp_wait(sm.v_full[v.at], v.parity))) break;
-        if (t0 + r >= it.k_end) {
-          uint4* row = reinterpret_cast<uint4*>(sm.v[v.at] + r * (kHeadDim * 2));
+        if (__builtin_expect(keys < kPromptKeys, 0)) {
+          // keys behind the item's, up to the 16 that a product takes: whatever V is there
+          // (other sequences, padding), zero times it must be zero
+          prompt_wait(sm, sm.v_full[count % kVStages], count / kVStages & 1);
+          if (r >= keys && r < keys + 15) {
+            uint4* row = reinterpret_cast<uint4*>(sm.v[count % kVStages] + r * (kHeadDim * 2));
 #pragma unroll
-          for (int c = 0; c < 8; ++c) row[c] = make_uint4(0, 0, 0, 0);
+            for (int c = 0; c < 8; ++c) row[c] = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_shared();
         }
-        fence_proxy_async_shared();
+        tmem_wait_st();
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.p_full));
       }
-      v.next(kVStages);
-      tmem_wait_st();
-      tmem_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sm.p_full));
-    }
-    if (ok && warp_wait(sm.o_full, (steps - 1) & 1)) {
+      prompt_wait(sm, sm.o_full, (count - 1) & 1);
       tmem_fence_after();
       uint32_t o[2][32];
       tmem_ld32(lanes + kTmemO, o[0]);
@@ -607,6 +687,11 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
       tmem_wait_ld();
       tmem_landed(o[0]);
       tmem_landed(o[1]);
+      tmem_fence_before();  // the next item's P lets its first product write here
+      if (__any_sync(kFull, *reinterpret_cast<volatile int*>(&sm.failed))) continue;
+      const Item it = item();
+      const int token = r / p.G, head = h * p.G + r - token * p.G;
+      const bool valid = token < it.n && r < p.tile_tokens * p.G;
       const float l = sum.x + sum.y;
       float size = fabsf(l);
 #pragma unroll
@@ -615,27 +700,24 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
       // Zero times an unseen key's infinity or NaN, if it is not a seen key's, or an
       // overflow: such rows are computed again from the keys that they see.
       uint32_t todo = __ballot_sync(kFull, valid && !(size < INFINITY)), done = 0;
-      const uint32_t sure = __ballot_sync(kFull, over);
-      float* qs = reinterpret_cast<float*>(sm.q) + warp * kHeadDim;  // Q has been used
-      while (todo) {
-        const int x = __ffs(todo) - 1, rr = 32 * warp + x, tt = rr / p.G;
-        todo &= todo - 1;
-        const int2 keys = seen_keys(p, it, tt);
-        if (!((sure >> x) & 1) && !any_not_finite(p, it.k_lo, min(keys.x, it.k_end), h) &&
-            !any_not_finite(p, max(keys.y, it.k_lo), it.k_end, h))
-          continue;
-        const int head = h * p.G + rr - tt * p.G;
-        const uint32_t qw = __ldcg(reinterpret_cast<const uint32_t*>(
-            p.q + int64_t(it.q0 + tt) * p.q_stride + head * kHeadDim + 2 * lane));
-        __syncwarp();
-        *reinterpret_cast<float2*>(qs + 2 * lane) = bf16x2_to_f32x2(qw);
-        __syncwarp();
-        const RowResult y = attend_row(p, keys, h, qs);
-        if (it.rec < 0)
-          store_row(p, it.q0 + tt, head, lane, y.m, y.l, y.o);
-        else
-          store_part(p, it, h, rr, lane, y);
-        done |= 1u << x;
+      if (__builtin_expect(todo != 0, 0)) {
+        const uint32_t sure = __ballot_sync(kFull, over || l > kLargest * kLargest);
+        while (todo) {
+          const int x = __ffs(todo) - 1, rr = 32 * warp + x, tt = rr / p.G;
+          todo &= todo - 1;
+          const int2 keys = seen_keys(p, it, tt);
+          if (!((sure >> x) & 1) && !any_not_finite(p, it.k_lo, min(keys.x, it.k_end), h) &&
+              !any_not_finite(p, max(keys.y, it.k_lo), it.k_end, h))
+            continue;
+          const int hh = h * p.G + rr - tt * p.G;
+          const RowResult y =
+              attend_row(p, keys, h, p.q + int64_t(it.q0 + tt) * p.q_stride + hh * kHeadDim);
+          if (it.rec < 0)
+            store_row(p, it.q0 + tt, hh, lane, y.m, y.l, y.o);
+          else
+            store_part(p, it, h, rr, lane, y);
+          done |= 1u << x;
+        }
       }
       if (valid && !((done >> lane) & 1u)) {
         if (it.rec >= 0) {
@@ -648,7 +730,6 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
             to[c] = make_uint4(o[c >> 3][4 * (c & 7)], o[c >> 3][4 * (c & 7) + 1], o[c >> 3][4 * (c & 7) + 2],
                                o[c >> 3][4 * (c & 7) + 3]);
         } else {
-          const int head = h * p.G + r - token * p.G;
           const int64_t at = (int64_t(it.q0 + token) * p.Hq + head) * kHeadDim;
           const float f = l == 0.f ? 0.f : out_scale(l, R, p.sinks ? p.sinks + head : nullptr, 1.f);
           uint4* to = reinterpret_cast<uint4*>(p.out + at);
@@ -675,6 +756,10 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
         }
       }
     }
+  }
+  if (*reinterpret_cast<volatile int*>(&sm.failed)) {  // copies and products in flight
+    const uint64_t since = globaltimer_ns();
+    while (globaltimer_ns() - since < 10000000) __nanosleep(1000);
   }
   tmem_fence_before();
   __syncthreads();
@@ -722,6 +807,7 @@ __global__ void __launch_bounds__(kRowThreads)
 // =========================================================================
 struct PromptDevice {
   PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+  int sms = 0;
 };
 static PerDevice<PromptDevice, 64> g_prompt_dev;
 
@@ -730,7 +816,7 @@ static cudaError_t prompt_setup(const PromptDevice** out) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= g_prompt_dev.devices) return cudaErrorInvalidDevice;
-  return g_prompt_dev.get<cudaError_t>(dev, out, [](PromptDevice& d) -> cudaError_t {
+  return g_prompt_dev.get<cudaError_t>(dev, out, [dev](PromptDevice& d) -> cudaError_t {
     cudaDriverEntryPointQueryResult found;
     void* f = nullptr;
     cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000,
@@ -738,6 +824,8 @@ static cudaError_t prompt_setup(const PromptDevice** out) {
     if (e != cudaSuccess) return e;
     if (found != cudaDriverEntryPointSuccess || !f) return cudaErrorNotSupported;
     d.encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
     return cudaFuncSetAttribute(prompt_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 int(sizeof(PromptSmem)));
   });
@@ -788,7 +876,8 @@ cudaError_t launch_prompt_attn(PromptAttnParams& p, cudaStream_t st) {
     ok = ok && encode_map(*d, &p.k_map, p.k, p.k_tokens, p.Hkv, p.k_stride, kPromptKeys, 1) &&
          encode_map(*d, &p.v_map, p.v, p.k_tokens, p.Hkv, p.v_stride, kPromptKeys, 1);
   if (!ok) return cudaErrorInvalidValue;
-  e = launch(prompt_attn_kernel, p, unsigned(p.max_items * p.Hkv), kAttnThreads, sizeof(PromptSmem), st);
+  const int64_t grid = std::min(p.max_items * p.Hkv, int64_t(2) * d->sms);
+  e = launch(prompt_attn_kernel, p, unsigned(grid), kAttnThreads, sizeof(PromptSmem), st);
   if (e != cudaSuccess || p.max_recs == 0) return e;
   // most rows of split tiles: half of the records, or the tiles
   const int64_t rows = std::min(p.max_recs / 2, p.max_items - p.max_recs) * p.Hkv * kPromptRows;
