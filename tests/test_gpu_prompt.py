@@ -88,6 +88,31 @@ def test_groups(G, Hkv):
     Case([1, 70, 33], [5, 70, 290], Hkv=Hkv, G=G, window=40 * (G & 1), sinks=True, seed=G).check()
 
 
+@pytest.mark.parametrize("Hkv,G,nq,ctx", [(8, 16, [1217], 0), (8, 16, [700, 650], 300), (64, 1, [2561], 0),
+                                         (32, 2, [1700, 900, 9], 130), (8, 48, [305], 77), (8, 128, [163], 0),
+                                         (13, 7, [1900], 0), (8, 8, [1303, 1200, 40], 513)])
+@pytest.mark.parametrize("window", [0, 1, 128, 700])
+def test_long_sequences(Hkv, G, nq, ctx, window):
+    """Items of two tiles, as long sequences have them: both halves filled, one empty, a last step that
+    only the second half sees, windows that begin behind the second half's first step."""
+    c = Case(nq, [n + ctx for n in nq], Hkv=Hkv, G=G, window=window, sinks=G == 16, pad=3, seed=G)
+    assert c.plan.numel() < 1 << 20         # no room for parts: two tiles
+    c.check()
+
+
+def test_long_sequences_of_odd_values():
+    """NaN and infinities behind, before and between; scores far apart; the first queries without keys."""
+    c = Case([1290, 64], [1217, 64], Hkv=8, G=16, sinks=True, seed=4, pad=9, spread=30.0)
+    c.k[c.ks[-1]:] = math.nan
+    c.v[c.ks[-1]:] = math.nan
+    c.v[800, 3] = math.inf
+    c.v[1216, 5, 7] = math.nan
+    c.check()
+    out, f32 = c.run()
+    assert (f32[:73] == 0).all()
+    assert f32[73:873].isfinite().all() and f32[1290:1354].isfinite().all()
+
+
 def test_ragged_batch():
     rng = np.random.default_rng(1)
     n = rng.integers(0, 300, 40)
