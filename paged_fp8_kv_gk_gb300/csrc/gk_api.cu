@@ -160,25 +160,16 @@ WsLayout ws_layout(const gk_shape& s, size_t ws_bytes) {
   return L;
 }
 
-// Tiles of an item: two where the sequences are long enough to fill them and there are
-// eight items an SM or more to even out.
-static int prompt_tiles(const gk_prompt& s, int tile_tokens) {
-  const int64_t pairs = int64_t(s.q_tokens) / (2 * tile_tokens);
-  return pairs >= 4 * int64_t(s.num_seqs) && pairs * s.num_kv_heads >= 4 * kPromptSlots ? 2 : 1;
-}
-
 PromptLayout prompt_layout(const gk_prompt& s) {
   PromptLayout L;
   L.tile_tokens = kPromptRows / (s.num_q_heads / s.num_kv_heads);
   // a sequence's last tile may be short; every tile has a token
-  L.tiles_per_item = prompt_tiles(s, L.tile_tokens);
-  const int item_tokens = L.tile_tokens * L.tiles_per_item;
-  L.tiles = int64_t(s.q_tokens) / item_tokens + s.num_seqs;
+  L.tiles = int64_t(s.q_tokens) / L.tile_tokens + s.num_seqs;
   if (L.tiles > s.q_tokens) L.tiles = s.q_tokens;
   // Keys are split only where whole tiles would leave slots empty or the last wave
   // thin; two waves of parts at most (a record is 33 KB: 21 MB).
   L.max_recs = L.tiles * s.num_kv_heads < 2 * kPromptSlots ? 640 / s.num_kv_heads : 0;
-  if (L.max_recs < 2 || s.k_tokens <= 4 * kPromptKeys || L.tiles_per_item > 1) L.max_recs = 0;
+  if (L.max_recs < 2 || s.k_tokens <= 4 * kPromptKeys) L.max_recs = 0;
   L.max_items = L.tiles + L.max_recs;
   L.items = kPromptHdrWords * sizeof(int32_t);
   L.splits = align256(L.items + size_t(L.max_items) * 2 * sizeof(int4));
@@ -756,7 +747,7 @@ gk_status gk_prompt_plan(const gk_prompt* prompt, const int32_t* q_start, const 
   p.W = prompt_window(*prompt);
   p.q_tokens = prompt->q_tokens;
   p.k_tokens = prompt->k_tokens;
-  p.item_tokens = L.tile_tokens * L.tiles_per_item;
+  p.tile_tokens = L.tile_tokens;
   return launch_prompt_plan(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GK_OK
                                                                                 : GK_ERR_CUDA;
 }
@@ -809,7 +800,6 @@ gk_status gk_prompt_attn(const gk_prompt* prompt, void* plan, size_t plan_bytes,
   p.q_tokens = s.q_tokens;
   p.k_tokens = s.k_tokens;
   p.tile_tokens = L.tile_tokens;
-  p.tiles = L.tiles_per_item;
   p.fd_g = make_fastdiv(uint32_t(p.G));
   return launch_prompt_attn(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GK_OK
                                                                                 : GK_ERR_CUDA;

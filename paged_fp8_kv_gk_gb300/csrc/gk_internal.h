@@ -236,8 +236,8 @@ struct RopeParams {
 };
 
 // A prompt's attention.  A tile is up to kPromptRows / G tokens of one sequence
-// (G = Hq / Hkv): its rows are (token, q head of one kv head).  An item is a tile, or
-// two, with a run of its keys; the plan lists the items, longest first.
+// (G = Hq / Hkv): its rows are (token, q head of one kv head).  An item is a tile
+// with a run of its keys; the plan lists the items, longest first.
 constexpr int kPromptRows = 128;      // rows of a tile
 constexpr int kPromptKeys = 128;      // keys of a step
 constexpr int kPromptSlots = 2 * 152; // CTAs that a GB300 runs at a time
@@ -248,11 +248,10 @@ constexpr int kPromptRecFloats = kPromptRows * (2 + kHeadDim);
 
 struct PromptLayout {
   size_t items, splits, records, total;
-  int64_t tiles;     // most items before splitting
+  int64_t tiles;     // most tiles
   int64_t max_items;
   int64_t max_recs;  // items of split tiles (0: nothing is split)
-  int tile_tokens;   // of a tile
-  int tiles_per_item;  // 2: no item is split
+  int tile_tokens;
 };
 PromptLayout prompt_layout(const gk_prompt& s);
 
@@ -263,7 +262,7 @@ struct PromptPlanParams {
   int4* items;    // two an item: (q0, tokens, own key of q0, first key), (end key, record or -1)
   int4* splits;   // a split tile: (q0, tokens, first record, records)
   int64_t max_items, max_recs;
-  int num_seqs, Hkv, W, q_tokens, k_tokens, item_tokens;
+  int num_seqs, Hkv, W, q_tokens, k_tokens, tile_tokens;
 };
 
 struct PromptAttnParams {
@@ -281,7 +280,6 @@ struct PromptAttnParams {
   int64_t q_stride, k_stride, v_stride;  // elements
   int64_t max_items, max_recs;
   int Hq, Hkv, G, W, q_tokens, k_tokens, tile_tokens;
-  int tiles;  // of an item
   FastDiv fd_g;
 };
 

@@ -8,6 +8,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "gk_internal.h"
 #include "gk_once.h"
@@ -65,7 +66,7 @@ __global__ void __launch_bounds__(kPromptPlanThreads)
   __shared__ int count[kBuckets];
   __shared__ int warps[32];
   __shared__ int longest, steps_of[kCandidates], recs_of[kCandidates], part, n_splits, n_recs;
-  const int tid = threadIdx.x, T = p.item_tokens;
+  const int tid = threadIdx.x, T = p.tile_tokens;
   int tiles = 0;
   bool bad = false;
   for (int s0 = 0; s0 < p.num_seqs; s0 += kPromptPlanThreads) {
@@ -284,57 +285,50 @@ __device__ __forceinline__ float max32(const uint32_t (&s)[32]) {
 // =========================================================================
 // Attention
 // =========================================================================
-// A tile is 128 rows: (token, q head of one kv head), 16 tokens of 8 heads, say.  An
-// item is kTiles tiles one behind the other with a run of keys, 128 a step, for one kv
-// head.  Four warps a tile do its softmax, a thread a row; one warp copies, one issues
-// the products:
+// An item is a tile of 128 rows (16 tokens of 8 heads, say) and a run of keys, 128
+// a step, for one kv head.  Warps 0-3 do the softmax, a thread a row.  Warp 4 copies, warp 5 issues the
+// products:
 //   S = Q K^T  128 x 128 x 64  both operands in shared memory, fp32 in tensor memory
 //   O += P V   128 x 64 x 128  P, bf16, in tensor memory; V in shared memory, MN-major
 // A row's scores are loaded into registers as soon as they are there, so that the next
-// step's S is computed while this one's exponentials are.  The grid is what the GPU
-// holds at a time; a CTA takes items in turns through the plan (there and back, so that
-// long and short ones even out) and its warps run on from one to the next: Q, K and V of
-// the next item are copied and its first S computed while this one's last exponentials
-// and its output are.
-//
-// Exponentials bound the step: 4 cycles for 32 of them, 512 a warp and step, as many as
-// the tensor cores need for a tile's products.  Two tiles share an SM, so that one's
-// exponentials run while the other waits, loads and stores.  Left to themselves (two
-// CTAs an SM, kTiles = 1) both fall into step and contend: 930 cycles a tile and step.
-// With kTiles = 2 one CTA has both and they take turns (Turns below), and share K and V.
-// kTiles = 1 is for few or short sequences: half the rows to fill, twice the items.
+// step's S is computed while this one's exponentials are; two CTAs an SM fill each
+// other's gaps.  The grid is what the GPU holds at a time; a CTA takes items in turns
+// through the plan (there and back, so that long and short ones even out) and its warps
+// run on from one to the next: Q, K and V of the next item are copied and its first S
+// computed while this one's last exponentials and its output are.
 //
 // The softmax's reference R of a row (log2 units; p = 2^(s - R)) is the largest score
-// of the first step in which it sees a key, plus kHeadroom, and no step after it looks
-// for a maximum: p and the sums are floats (bf16 in P, with a float's exponents), as
-// exact at 2^60 as at 1.  Every fourth step, a row whose sum has passed kLargest takes a
-// new R, and O and the sum are scaled to it.  A row that overflows all the same (a score
-// 54 or more above all up to the last such step, and then values of 2^60) is computed
-// again by attend_row, as are rows with unseen infinities or NaN.
-constexpr int kTileBytes = kPromptRows * kHeadDim * 2;  // Q of a tile, a step of K or of V: 16 KB
-constexpr int kTileColumns = 256;                       // of tensor memory: S 128, O 64, P 64
+// of the first step plus kHeadroom (every row sees a key of its first step, or none at
+// all), and no step after it looks for a maximum: p and the sums are floats (bf16 in P,
+// with a float's exponents), as exact at 2^60 as at 1.  Every kCheckSteps steps, a row
+// whose sum has passed kLargest takes a new R, and O and the sum are scaled to it.  A row
+// that overflows all the same (a score 54 or more above all up to the last check, and
+// then values of 2^60) is computed again by attend_row, as are rows with unseen
+// infinities or NaN.
+constexpr int kSoftWarps = 4;
+constexpr int kAttnThreads = 32 * (kSoftWarps + 2);
+constexpr int kKStages = 3, kVStages = 2;               // V is needed a softmax later than K
+constexpr int kTileBytes = kPromptRows * kHeadDim * 2;  // Q, and one step of K or of V: 16 KB
+constexpr int kTmemColumns = 256;                       // S 128, O 64, P 64
 constexpr int kTmemO = 128, kTmemP = 192;
 constexpr float kHeadroom = 24.f;
 constexpr float kLargest = 0x1p30f;  // of a row's sum
+constexpr int kCheckSteps = 16;
 
-template <int kTiles>
 struct PromptSmem {
-  static constexpr int kWarps = 4 * kTiles;             // of the softmax
-  static constexpr int kStages = kTiles == 1 ? 2 : 4;   // of K and of V
-  alignas(1024) uint8_t q[2][kTiles][kTileBytes];
-  uint8_t k[kStages][kTileBytes];
-  uint8_t v[kStages][kTileBytes];
-  uint8_t out[kWarps][32 * kHeadDim * 2];               // a warp's rows on their way out
-  uint64_t q_full[2], q_free[2], k_full[kStages], v_full[kStages], k_free[kStages], v_free[kStages];
-  uint64_t s_full[kTiles], s_free[kTiles], p_full[kTiles], o_full[kTiles];
+  alignas(1024) uint8_t q[2][kTileBytes];
+  uint8_t k[kKStages][kTileBytes];
+  uint8_t v[kVStages][kTileBytes];
+  uint64_t q_full[2], q_free[2], k_full[kKStages], v_full[kVStages], k_free[kKStages],
+      v_free[kVStages];
+  uint64_t s_full, s_free, p_full, o_full;
   uint32_t tmem;
   int failed;  // a wait gave up
   // a softmax warp's item and the one after it, as in the plan: out of its registers
-  alignas(16) int item[kWarps][2][8];
+  alignas(16) int item[kSoftWarps][2][8];
 };
 static_assert(kPromptKeys * kHeadDim * 2 == kTileBytes, "a step of K is as large as Q");
-static_assert(sizeof(PromptSmem<1>) <= 115712, "two CTAs an SM");
-static_assert(sizeof(PromptSmem<2>) <= 227 * 1024, "one CTA an SM");
+static_assert(sizeof(PromptSmem) <= 115712, "two CTAs an SM");
 
 struct Phase {  // place in a ring of barriers, and the parity of its next phase
   int at = 0;
@@ -350,9 +344,9 @@ struct Phase {  // place in a ring of barriers, and the parity of its next phase
 
 // The places in the plan that a CTA takes, (item, kv head): every grid's width, there
 // and back.
-struct Places {
+struct Turn {
   int n, at, round = 0;
-  __device__ __forceinline__ Places(const PromptAttnParams& p) : n(__ldcg(p.hdr) * p.Hkv) { next(); }
+  __device__ __forceinline__ Turn(const PromptAttnParams& p) : n(__ldcg(p.hdr) * p.Hkv) { next(); }
   __device__ __forceinline__ bool more() const { return at < n; }
   __device__ __forceinline__ void next() {
     const int g = int(gridDim.x);
@@ -364,28 +358,23 @@ __device__ __forceinline__ int item_steps(const Item& it) {
   return (it.k_end - it.k_lo + kPromptKeys - 1) / kPromptKeys;
 }
 
-// Waits for a barrier's phase.  After kWaitTries tries (a tenth of a second at least;
-// waits here last a microsecond) the CTA is marked as failed and goes on, so that its
-// warps stay together: it waits for nothing from then on, writes no output, and ends
-// once its copies have had time to land.  The loop in the way is short: with a clock
-// read for the limit, a vote and a way out, each wait took 200 cycles even where the
-// phase was complete.
-constexpr int kWaitTries = 1 << 24;
-__device__ __noinline__ void prompt_wait_long(uint32_t bar, uint32_t parity, volatile int* failed) {
-  for (int tries = 0; tries < kWaitTries && !*failed; ++tries)
-    if (mbar_try_wait(bar, parity)) return;
-  *failed = 1;
-  atomicOr(&g_prompt_error, GK_DEVERR_TIMEOUT);
-}
-template <typename Smem>
-__device__ __forceinline__ void prompt_wait(Smem& sm, uint64_t& bar, uint32_t parity) {
+// Waits for a barrier's phase.  After kWaitTries tries (10 ms and more; waits here last
+// a microsecond) the CTA is marked as failed and goes on, so that its warps stay
+// together; from the next item on it does nothing, and it ends once its copies have had
+// time to land.  No clock, no vote and no call here: each of them cost the loops around
+// it 4 % and more.
+constexpr int kWaitTries = 1 << 20;
+__device__ __forceinline__ void prompt_wait(PromptSmem& sm, uint64_t& bar, uint32_t parity) {
   const uint32_t at = smem_u32(&bar);
-  int tries = 4096;
+  int tries = kWaitTries;
   while (!mbar_try_wait(at, parity))
     if (--tries == 0) {
-      prompt_wait_long(at, parity, &sm.failed);
+      *reinterpret_cast<volatile int*>(&sm.failed) = 1;
       break;
     }
+}
+__device__ __forceinline__ bool gave_up(PromptSmem& sm) {
+  return __any_sync(kFull, *reinterpret_cast<volatile int*>(&sm.failed));
 }
 
 // Whether one of the keys [a, b) has a V that is not finite (a warp).
@@ -409,43 +398,29 @@ __device__ __forceinline__ void store_part(const PromptAttnParams& p, const Item
   *reinterpret_cast<float2*>(rec + 2 * kPromptRows + r * kHeadDim + 2 * lane) = y.o;
 }
 
-// Two tiles' exponentials in turns: tile `t` waits for its turn, and passes it on.
-__device__ __forceinline__ void await_turn(int t) {
-  asm volatile("bar.sync %0, 256;" ::"r"(t + 1) : "memory");
-}
-__device__ __forceinline__ void pass_turn(int t) {
-  asm volatile("bar.arrive %0, 256;" ::"r"(2 - t) : "memory");
-}
-
-template <int kTiles>
-constexpr int kAttnThreads = 32 * (PromptSmem<kTiles>::kWarps + 2);
-
-template <int kTiles>
-__global__ void __launch_bounds__(kAttnThreads<kTiles>, kTiles == 1 ? 2 : 1)
+__global__ void __launch_bounds__(kAttnThreads, 2)
     prompt_attn_kernel(const __grid_constant__ PromptAttnParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  using Smem = PromptSmem<kTiles>;
-  Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
-  constexpr int kSoftWarps = Smem::kWarps, kStages = Smem::kStages;
+  PromptSmem& sm = *reinterpret_cast<PromptSmem*>(smem_raw);
   const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (warp == kSoftWarps) {
     if (lane == 0) {
       for (int s = 0; s < 2; ++s) {
         mbar_init(smem_u32(&sm.q_full[s]), 1);
-        mbar_init(smem_u32(&sm.q_free[s]), 1);
+        mbar_init(smem_u32(&sm.q_free[s]), 1 + kSoftWarps);
       }
-      for (int s = 0; s < kStages; ++s) {
+      for (int s = 0; s < kKStages; ++s) {
         mbar_init(smem_u32(&sm.k_full[s]), 1);
         mbar_init(smem_u32(&sm.k_free[s]), 1);
+      }
+      for (int s = 0; s < kVStages; ++s) {
         mbar_init(smem_u32(&sm.v_full[s]), 1);
         mbar_init(smem_u32(&sm.v_free[s]), 1);
       }
-      for (int t = 0; t < kTiles; ++t) {
-        mbar_init(smem_u32(&sm.s_full[t]), 1);
-        mbar_init(smem_u32(&sm.s_free[t]), 4);
-        mbar_init(smem_u32(&sm.p_full[t]), 4);
-        mbar_init(smem_u32(&sm.o_full[t]), 1);
-      }
+      mbar_init(smem_u32(&sm.s_full), 1);
+      mbar_init(smem_u32(&sm.s_free), kSoftWarps);
+      mbar_init(smem_u32(&sm.p_full), kSoftWarps);
+      mbar_init(smem_u32(&sm.o_full), 1);
       mbar_init_fence();
       sm.failed = 0;
       tma_prefetch_map(&p.q_map);
@@ -453,54 +428,48 @@ __global__ void __launch_bounds__(kAttnThreads<kTiles>, kTiles == 1 ? 2 : 1)
       tma_prefetch_map(&p.v_map);
     }
   } else if (warp == kSoftWarps + 1) {
-    tmem_alloc<kTiles * kTileColumns>(smem_u32(&sm.tmem));
+    tmem_alloc<kTmemColumns>(smem_u32(&sm.tmem));
   }
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
   const uint32_t tmem = sm.tmem;
   follow_stream();
-  Places turn(p);
+  Turn turn(p);
 
   if (warp == kSoftWarps) {
     const bool one = elect_one();
     Phase q, k, v;
     // the first round finds the places free
     auto load = [&](uint64_t& free, uint64_t& full, uint32_t parity, uint8_t* to, const CUtensorMap* map,
-                    int head, int token) {
+                    uint32_t bytes, int head, int token) {
       prompt_wait(sm, free, parity ^ 1);
       if (one) {
-        mbar_arrive_expect_tx(smem_u32(&full), kTileBytes);
+        mbar_arrive_expect_tx(smem_u32(&full), bytes);
         tma_load_3d(smem_u32(to), map, 0, head, token, smem_u32(&full));
       }
       __syncwarp();
     };
-    for (; turn.more(); turn.next()) {
+    for (; turn.more() && !gave_up(sm); turn.next()) {
       const int i = turn.at / p.Hkv, h = turn.at - i * p.Hkv;
       const Item it = load_item(p, i);
       const int steps = item_steps(it), k_lo = it.k_lo;
       if (steps == 0) continue;
-      prompt_wait(sm, sm.q_free[q.at], q.parity ^ 1);
-      if (one) {
-        const int tiles = kTiles == 1 || it.n <= p.tile_tokens ? 1 : 2;
-        mbar_arrive_expect_tx(smem_u32(&sm.q_full[q.at]),
-                              uint32_t(tiles * p.tile_tokens * p.G) * kHeadDim * 2);
-        for (int t = 0; t < tiles; ++t)
-          tma_load_3d(smem_u32(sm.q[q.at][t]), &p.q_map, 0, h * p.G, it.q0 + t * p.tile_tokens,
-                      smem_u32(&sm.q_full[q.at]));
-      }
-      __syncwarp();
+      load(sm.q_free[q.at], sm.q_full[q.at], q.parity, sm.q[q.at], &p.q_map,
+           uint32_t(p.tile_tokens * p.G) * kHeadDim * 2, h * p.G, it.q0);
       q.next<2>();
       // K a step ahead of V
       auto load_k = [&](int j) {
-        load(sm.k_free[k.at], sm.k_full[k.at], k.parity, sm.k[k.at], &p.k_map, h, k_lo + j * kPromptKeys);
-        k.next<kStages>();
+        load(sm.k_free[k.at], sm.k_full[k.at], k.parity, sm.k[k.at], &p.k_map, kTileBytes, h,
+             k_lo + j * kPromptKeys);
+        k.next<kKStages>();
       };
       load_k(0);
       for (int j = 0; j < steps; ++j) {
         if (j + 1 < steps) load_k(j + 1);
-        load(sm.v_free[v.at], sm.v_full[v.at], v.parity, sm.v[v.at], &p.v_map, h, k_lo + j * kPromptKeys);
-        v.next<kStages>();
+        load(sm.v_free[v.at], sm.v_full[v.at], v.parity, sm.v[v.at], &p.v_map, kTileBytes, h,
+             k_lo + j * kPromptKeys);
+        v.next<kVStages>();
       }
     }
   } else if (warp == kSoftWarps + 1) {
@@ -509,93 +478,76 @@ __global__ void __launch_bounds__(kAttnThreads<kTiles>, kTiles == 1 ? 2 : 1)
     // cycles to issue where the tensor cores need 32 or 64 for it.
     constexpr uint32_t kS = bf16_idesc(kPromptRows, kPromptKeys, false);
     constexpr uint32_t kO = bf16_idesc(kPromptRows, kHeadDim, true);
-    const uint64_t qd0 = sw128_desc(smem_u32(sm.q[0][0])), kd0 = sw128_desc(smem_u32(sm.k[0])),
+    const uint64_t qd0 = sw128_desc(smem_u32(sm.q[0])), kd0 = sw128_desc(smem_u32(sm.k[0])),
                    vd0 = sw128_desc(smem_u32(sm.v[0]));
     Phase q, k, v;
-    uint32_t s_parity[kTiles], p_parity[kTiles];  // S is free at first
-#pragma unroll
-    for (int t = 0; t < kTiles; ++t) s_parity[t] = 1, p_parity[t] = 0;
-    // S of the tiles in the next step in turn, the last of its item or not
-    auto scores = [&](int tiles, bool first, bool last) {
+    uint32_t s_parity = 1, p_parity = 0;  // S is free at first
+    // S of the next step in turn, `left` steps of its item counting itself
+    auto scores = [&](int left, bool first) {
       if (first) prompt_wait(sm, sm.q_full[q.at], q.parity);
       prompt_wait(sm, sm.k_full[k.at], k.parity);
-      const uint64_t kd = kd0 + uint64_t(k.at * (kTileBytes >> 4));
+      prompt_wait(sm, sm.s_free, s_parity);
+      s_parity ^= 1;
+      tmem_fence_after();
+      const uint64_t qd = qd0 + uint64_t(q.at * (kTileBytes >> 4)), kd = kd0 + uint64_t(k.at * (kTileBytes >> 4));
+      if (elect_one()) {
 #pragma unroll
-      for (int t = 0; t < kTiles; ++t) {
-        if (t >= tiles) break;
-        prompt_wait(sm, sm.s_free[t], s_parity[t]);
-        s_parity[t] ^= 1;
+        for (int c = 0; c < kHeadDim / 16; ++c) mma_ss(tmem, qd + 2 * c, kd + 2 * c, kS, c > 0);
+        mma_commit(smem_u32(&sm.k_free[k.at]));
+        if (left == 1) mma_commit(smem_u32(&sm.q_free[q.at]));
+        mma_commit(smem_u32(&sm.s_full));
+      }
+      __syncwarp();
+      k.next<kKStages>();
+      if (left == 1) q.next<2>();
+    };
+    // keys of the next item that has any; 0: no more
+    auto next_item = [&]() -> int {
+      int keys = 0;
+      for (; turn.more() && keys == 0; turn.next()) {
+        const Item it = load_item(p, turn.at / p.Hkv);
+        keys = it.k_end - it.k_lo;
+      }
+      return keys;
+    };
+    auto steps_of = [](int keys) { return (keys + kPromptKeys - 1) / kPromptKeys; };
+    int next = next_item();
+    if (next) scores(steps_of(next), true);
+    while (next && !gave_up(sm)) {
+      const int n = next, steps = steps_of(n);
+      next = next_item();  // its first S follows this one's last
+      for (int j = 0; j < steps; ++j) {
+        if (j + 1 < steps)
+          scores(steps - j - 1, false);
+        else if (next)
+          scores(steps_of(next), true);
+        prompt_wait(sm, sm.v_full[v.at], v.parity);
+        prompt_wait(sm, sm.p_full, p_parity);
+        p_parity ^= 1;
         tmem_fence_after();
-        const uint64_t qd = qd0 + uint64_t((q.at * kTiles + t) * (kTileBytes >> 4));
+        const uint64_t vd = vd0 + uint64_t(v.at * (kTileBytes >> 4));
+        const int keys = n - j * kPromptKeys;
         if (elect_one()) {
 #pragma unroll
-          for (int c = 0; c < kHeadDim / 16; ++c)
-            mma_ss(tmem + t * kTileColumns, qd + 2 * c, kd + 2 * c, kS, c > 0);
-          if (t + 1 == tiles) {
-            mma_commit(smem_u32(&sm.k_free[k.at]));
-            if (last) mma_commit(smem_u32(&sm.q_free[q.at]));
-          }
-          mma_commit(smem_u32(&sm.s_full[t]));
+          for (int c = 0; c < kPromptKeys / 16; ++c)
+            if (16 * c < keys)
+              mma_ts(tmem + kTmemO, tmem + kTmemP + 8 * c, vd + 128 * c, kO, j > 0 || c > 0);
+          mma_commit(smem_u32(&sm.v_free[v.at]));
+          mma_commit(smem_u32(&sm.o_full));
         }
         __syncwarp();
-      }
-      k.next<kStages>();
-      if (last) q.next<2>();
-    };
-    // the next item that has keys: their number (0: no more items) and its tokens
-    auto next_item = [&]() -> int2 {
-      int2 r = make_int2(0, 0);
-      for (; turn.more() && r.x == 0; turn.next()) {
-        const Item it = load_item(p, turn.at / p.Hkv);
-        r = make_int2(it.k_end - it.k_lo, it.n);
-      }
-      return r;
-    };
-    auto tiles_of = [&](int n) { return kTiles == 1 || n <= p.tile_tokens ? 1 : 2; };
-    int2 next = next_item();
-    if (next.x) scores(tiles_of(next.y), true, next.x <= kPromptKeys);
-    while (next.x) {
-      const int keys = next.x, n = next.y, tiles = tiles_of(n);
-      next = next_item();  // its first S follows this one's last
-      for (int left = keys; left > 0; left -= kPromptKeys) {
-        if (left > kPromptKeys)
-          scores(tiles, false, left <= 2 * kPromptKeys);
-        else if (next.x)
-          scores(tiles_of(next.y), true, next.x <= kPromptKeys);
-        prompt_wait(sm, sm.v_full[v.at], v.parity);
-        const uint64_t vd = vd0 + uint64_t(v.at * (kTileBytes >> 4));
-#pragma unroll
-        for (int t = 0; t < kTiles; ++t) {
-          if (t >= tiles) break;
-          prompt_wait(sm, sm.p_full[t], p_parity[t]);
-          p_parity[t] ^= 1;
-          tmem_fence_after();
-          // the first tile of two ends before the second one's tokens
-          const int of_tile = left - (t + 1 < tiles ? n - p.tile_tokens : 0);
-          if (elect_one()) {
-            const uint32_t d = tmem + t * kTileColumns;
-#pragma unroll
-            for (int c = 0; c < kPromptKeys / 16; ++c)
-              if (16 * c < of_tile)
-                mma_ts(d + kTmemO, d + kTmemP + 8 * c, vd + 128 * c, kO, left < keys || c > 0);
-            if (t + 1 == tiles) mma_commit(smem_u32(&sm.v_free[v.at]));
-            mma_commit(smem_u32(&sm.o_full[t]));
-          }
-          __syncwarp();
-        }
-        v.next<kStages>();
+        v.next<kVStages>();
       }
     }
   } else {
-    const int tile = warp >> 2, r = threadIdx.x & 127;  // row of the tile
-    const int token = tile * p.tile_tokens + fdiv(r, p.fd_g);  // of the item
-    const uint32_t lanes = tmem + tile * kTileColumns + (uint32_t(warp & 3) << 21);  // lane 32 (warp % 4)
-    uint32_t all = 0, mine = 0;  // steps so far, and those with a share of this tile: barriers' parities
+    const int r = threadIdx.x;  // row of the tile
+    const int token = fdiv(r, p.fd_g);
+    const uint32_t lanes = tmem + (uint32_t(warp) << 21);  // lane 32 warp
+    uint32_t count = 0, items = 0;  // steps and items so far: the parities of all barriers
     auto fetch = [&](int place) {
       if (turn.more() && lane < 2)
         cp_async16(smem_u32(&sm.item[warp][place][4 * lane]), p.items + 2 * (turn.at / p.Hkv) + lane);
     };
-    if (kTiles == 2 && tile == 1) pass_turn(1);
     fetch(0);
     for (int place = 0; turn.more(); place ^= 1) {
       const int h = turn.at % p.Hkv;
@@ -608,27 +560,21 @@ __global__ void __launch_bounds__(kAttnThreads<kTiles>, kTiles == 1 ? 2 : 1)
       const Item at_first = item();
       const int steps = item_steps(at_first);
       if (steps == 0) {  // no key: zeros (such a tile is not split)
-        for (int x = warp; x < at_first.n * p.G; x += kSoftWarps)
-          store_row(p, at_first.q0 + x / p.G, h * p.G + x % p.G, lane, 0.f, 0.f, make_float2(0.f, 0.f));
+        for (int x = warp; x < at_first.n * p.G; x += kSoftWarps) {
+          const int t = fdiv(x, p.fd_g);
+          store_row(p, at_first.q0 + t, h * p.G + x - t * p.G, lane, 0.f, 0.f, make_float2(0.f, 0.f));
+        }
         continue;
       }
-      const bool two = kTiles == 2 && at_first.n > p.tile_tokens;
-      if (tile == 1 && !two) {
-        all += steps;
-        continue;
-      }
-      // steps that every row of the tile sees whole
-      const int t_lo = tile * p.tile_tokens, t_hi = min(t_lo + p.tile_tokens, at_first.n);
-      const int whole_lo = at_first.diag + t_hi - p.W;
-      const int whole_hi = min(at_first.diag + t_lo + 1, at_first.k_end) - kPromptKeys;
-      float R = 0.f, scale_o = 1.f;
-      bool scale_due = false, over = false;
-      bool has = false;    // the row has a reference
-      bool fresh = true;   // one of the warp's rows may have none
+      // steps [whole_lo, whole_end) are seen whole by every row
+      const int whole_lo = max(at_first.diag + at_first.n - p.W - at_first.k_lo + kPromptKeys - 1, 0) / kPromptKeys;
+      const int whole_end = max(min(at_first.diag + 1, at_first.k_end) - at_first.k_lo, 0) / kPromptKeys;
+      float R = 0.f;
+      bool over = false;
       float2 sum = make_float2(0.f, 0.f);
-      int t0 = at_first.k_lo;
-      for (int j = 0; j < steps; ++j, ++all, ++mine, t0 += kPromptKeys) {
-        prompt_wait(sm, sm.s_full[tile], mine & 1);
+      auto step = [&](int j, auto whole) {
+        constexpr bool kWhole = decltype(whole)::value;
+        prompt_wait(sm, sm.s_full, count & 1);
         tmem_fence_after();
         uint32_t s[4][32];
 #pragma unroll
@@ -638,31 +584,27 @@ __global__ void __launch_bounds__(kAttnThreads<kTiles>, kTiles == 1 ? 2 : 1)
         for (int c = 0; c < 4; ++c) tmem_landed(s[c]);
         tmem_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sm.s_free[tile]));
-        int keys = kPromptKeys, behind = kPromptKeys;  // the step's of the tile, of the item
-        if (__builtin_expect(t0 < whole_lo || t0 > whole_hi, 0)) {
+        if (lane == 0) mbar_arrive(smem_u32(&sm.s_free));
+        int keys = kPromptKeys;  // of the step
+        if (!kWhole) {
           const Item it = item();
-          behind = it.k_end - t0;
-          keys = min(it.k_end, it.diag + min((tile + 1) * p.tile_tokens, it.n)) - t0;
+          const int t0 = it.k_lo + j * kPromptKeys;
+          keys = it.k_end - t0;
           const int2 seen = seen_keys(p, it, min(token, it.n - 1));
           const uint32_t first = uint32_t(seen.x - t0), n = uint32_t(max(seen.y - seen.x, 0));
+          const int lo = it.diag + it.n - p.W - t0, hi = min(it.diag + 1 - t0, keys) - 32;
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            if (t0 + 32 * c < whole_lo || t0 + 32 * c - (kPromptKeys - 32) > whole_hi) {
+            if (32 * c < lo || 32 * c > hi) {
 #pragma unroll
               for (int e = 0; e < 32; ++e)
                 if (uint32_t(32 * c + e) - first >= n) s[c][e] = __float_as_uint(-INFINITY);
             }
-        }
-        if (__builtin_expect(fresh, 0)) {
-          const float top = fmaxf(fmaxf(max32(s[0]), max32(s[1])), fmaxf(max32(s[2]), max32(s[3])));
-          if (!has && !(top == -INFINITY)) {
-            has = true;
-            R = top < INFINITY ? fmaf(top, kScoreLog2, kHeadroom) : 0.f;
+          if (j == 0) {
+            const float top = fmaxf(fmaxf(max32(s[0]), max32(s[1])), fmaxf(max32(s[2]), max32(s[3])));
+            if (fabsf(top) < INFINITY) R = fmaf(top, kScoreLog2, kHeadroom);
           }
-          fresh = __any_sync(kFull, !has);
         }
-        if (kTiles == 2 && two) await_turn(tile);
         const float2 scale = make_float2(kScoreLog2, kScoreLog2), shift = make_float2(-R, -R);
         auto probabilities = [&](uint32_t s0, uint32_t s1) -> uint32_t {
           const float2 x = fma2(make_float2(__uint_as_float(s0), __uint_as_float(s1)), scale, shift);
@@ -673,16 +615,15 @@ __global__ void __launch_bounds__(kAttnThreads<kTiles>, kTiles == 1 ? 2 : 1)
         // P of the step before has been used: waited for as late as possible (before the
         // exponentials, it adds the product's time to every step's)
         auto p_free = [&]() {
-          if (j > 0) {
-            prompt_wait(sm, sm.o_full[tile], (mine - 1) & 1);
+          if (kWhole || j > 0) {
+            prompt_wait(sm, sm.o_full, (count - 1) & 1);
             tmem_fence_after();
           }
         };
-        if (__builtin_expect(keys > 32, 1)) {
+        if (kWhole || keys > 32) {
           uint32_t pr[2][32];
 #pragma unroll
           for (int e = 0; e < 64; ++e) pr[e >> 5][e & 31] = probabilities(s[e >> 4][2 * e & 31], s[e >> 4][(2 * e & 31) + 1]);
-          if (kTiles == 2 && two) pass_turn(tile);
           p_free();
           tmem_st32(lanes + kTmemP, pr[0]);
           tmem_st32(lanes + kTmemP + 32, pr[1]);
@@ -693,45 +634,15 @@ __global__ void __launch_bounds__(kAttnThreads<kTiles>, kTiles == 1 ? 2 : 1)
             pr[e] = probabilities(s[0][2 * e], s[0][2 * e + 1]);
             pr[16 + e] = 0;
           }
-          if (kTiles == 2 && two) pass_turn(tile);
           p_free();
           tmem_st32(lanes + kTmemP, pr);
         }
-        if (__builtin_expect(scale_due, 0)) {
-          scale_due = false;
-#pragma unroll 1
-          for (int c = 0; c < kHeadDim; c += 32) {
-            uint32_t o[32];
-            tmem_ld32(lanes + kTmemO + c, o);
-            tmem_wait_ld();
-            tmem_landed(o);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * scale_o);
-            tmem_st32(lanes + kTmemO + c, o);
-          }
-        }
-        if ((j & 3) == 3) {
-          const float total = sum.x + sum.y;
-          if (__builtin_expect(__any_sync(kFull, total > kLargest), 0)) {
-            over = over || total > kLargest * kLargest;
-            if (j + 1 < steps) {
-              // at most by 2^100, a normal float
-              const float up = fminf(kHeadroom + float(int(__float_as_uint(total) >> 23) - 127), 100.f);
-              const float to = total > kLargest ? R + up : R;
-              scale_o = ex2(R - to);
-              R = to;
-              sum.x *= scale_o;
-              sum.y *= scale_o;
-              scale_due = true;
-            }
-          }
-        }
-        if (__builtin_expect(behind < kPromptKeys, 0)) {
+        if (!kWhole && keys < kPromptKeys) {
           // keys behind the item's, up to the 16 that a product takes: whatever V is there
           // (other sequences, padding), zero times it must be zero
-          prompt_wait(sm, sm.v_full[all % kStages], all / kStages & 1);
-          if (r >= behind && r < behind + 15) {
-            uint4* row = reinterpret_cast<uint4*>(sm.v[all % kStages] + r * (kHeadDim * 2));
+          prompt_wait(sm, sm.v_full[count % kVStages], count / kVStages & 1);
+          if (r >= keys && r < keys + 15) {
+            uint4* row = reinterpret_cast<uint4*>(sm.v[count % kVStages] + r * (kHeadDim * 2));
 #pragma unroll
             for (int c = 0; c < 8; ++c) row[c] = make_uint4(0, 0, 0, 0);
           }
@@ -740,9 +651,45 @@ __global__ void __launch_bounds__(kAttnThreads<kTiles>, kTiles == 1 ? 2 : 1)
         tmem_wait_st();
         tmem_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[tile]));
+        if (lane == 0) mbar_arrive(smem_u32(&sm.p_full));
+        ++count;
+      };
+      step(0, std::false_type());
+      for (int j = 1; j < steps;) {
+        // runs of whole steps in a loop of their own, without the rare cases' code
+        const int end = min(whole_end, j + kCheckSteps);
+        if (j >= whole_lo && j < end) {
+          do step(j, std::true_type()); while (++j < end);
+        } else {
+          step(j, std::false_type());
+          ++j;
+        }
+        const float total = sum.x + sum.y;
+        if (j < steps && __any_sync(kFull, total > kLargest)) {
+          over = over || total > kLargest * kLargest;
+          // at most by 2^100, a normal float
+          const float up = fminf(kHeadroom + float(int(__float_as_uint(total) >> 23) - 127), 100.f);
+          const float to = total > kLargest ? R + up : R;
+          const float f = ex2(R - to);
+          R = to;
+          sum.x *= f;
+          sum.y *= f;
+          prompt_wait(sm, sm.o_full, (count - 1) & 1);
+          tmem_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < kHeadDim; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(lanes + kTmemO + c, o);
+            tmem_wait_ld();
+            tmem_landed(o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st32(lanes + kTmemO + c, o);
+          }
+          tmem_wait_st();
+        }
       }
-      prompt_wait(sm, sm.o_full[tile], (mine - 1) & 1);
+      prompt_wait(sm, sm.o_full, (count - 1) & 1);
       tmem_fence_after();
       uint32_t o[2][32];
       tmem_ld32(lanes + kTmemO, o[0]);
@@ -751,7 +698,7 @@ __global__ void __launch_bounds__(kAttnThreads<kTiles>, kTiles == 1 ? 2 : 1)
       tmem_landed(o[0]);
       tmem_landed(o[1]);
       tmem_fence_before();  // the next item's P lets its first product write here
-      if (__any_sync(kFull, *reinterpret_cast<volatile int*>(&sm.failed))) continue;
+      if (gave_up(sm)) break;
       const Item it = item();
       const bool valid = token < it.n && r < p.tile_tokens * p.G;
       const float l = sum.x + sum.y;
@@ -765,8 +712,7 @@ __global__ void __launch_bounds__(kAttnThreads<kTiles>, kTiles == 1 ? 2 : 1)
       if (__builtin_expect(todo != 0, 0)) {
         const uint32_t sure = __ballot_sync(kFull, over || l > kLargest * kLargest);
         while (todo) {
-          const int x = __ffs(todo) - 1, rr = 32 * (warp & 3) + x, of_tile = fdiv(rr, p.fd_g);
-          const int tt = tile * p.tile_tokens + of_tile, hh = h * p.G + rr - of_tile * p.G;
+          const int x = __ffs(todo) - 1, rr = 32 * warp + x, tt = fdiv(rr, p.fd_g), hh = h * p.G + rr - tt * p.G;
           todo &= todo - 1;
           const int2 keys = seen_keys(p, it, tt);
           if (!((sure >> x) & 1) && !any_not_finite(p, it.k_lo, min(keys.x, it.k_end), h) &&
@@ -781,9 +727,10 @@ __global__ void __launch_bounds__(kAttnThreads<kTiles>, kTiles == 1 ? 2 : 1)
           done |= 1u << x;
         }
       }
-      const bool mine_to_store = valid && !((done >> lane) & 1u);
-      if (kTiles == 1 && it.rec >= 0) {
-        if (mine_to_store) {
+      const bool stores = valid && !((done >> lane) & 1u);
+      const uint32_t q_at = items++ & 1;
+      if (it.rec >= 0) {
+        if (stores) {
           float* rec = p.records + (int64_t(it.rec) * p.Hkv + h) * kPromptRecFloats;
           rec[r] = l == 0.f ? -INFINITY : R;
           rec[kPromptRows + r] = l;
@@ -793,58 +740,60 @@ __global__ void __launch_bounds__(kAttnThreads<kTiles>, kTiles == 1 ? 2 : 1)
             to[c] = make_uint4(o[c >> 3][4 * (c & 7)], o[c >> 3][4 * (c & 7) + 1], o[c >> 3][4 * (c & 7) + 2],
                                o[c >> 3][4 * (c & 7) + 3]);
         }
-        continue;
-      }
-      const int head = h * p.G + r - (token - tile * p.tile_tokens) * p.G;
-      const float f = l == 0.f || !valid ? 0.f : out_scale(l, R, p.sinks ? p.sinks + head : nullptr, 1.f);
+      } else {
+        const int head = h * p.G + r - token * p.G;
+        const float f = l == 0.f || !valid ? 0.f : out_scale(l, R, p.sinks ? p.sinks + head : nullptr, 1.f);
 #pragma unroll
-      for (int c = 0; c < 64; ++c)
-        o[c >> 5][c & 31] = l == 0.f ? 0u : __float_as_uint(__uint_as_float(o[c >> 5][c & 31]) * f);
-      if (p.out_f32 && mine_to_store) {
-        uint4* to32 = reinterpret_cast<uint4*>(p.out_f32 + (int64_t(it.q0 + token) * p.Hq + head) * kHeadDim);
+        for (int c = 0; c < 64; ++c)
+          o[c >> 5][c & 31] = l == 0.f ? 0u : __float_as_uint(__uint_as_float(o[c >> 5][c & 31]) * f);
+        if (p.out_f32 && stores) {
+          uint4* to32 = reinterpret_cast<uint4*>(p.out_f32 + (int64_t(it.q0 + token) * p.Hq + head) * kHeadDim);
 #pragma unroll
-        for (int c = 0; c < 16; ++c)
-          to32[c] = make_uint4(o[c >> 3][4 * (c & 7)], o[c >> 3][4 * (c & 7) + 1], o[c >> 3][4 * (c & 7) + 2],
-                               o[c >> 3][4 * (c & 7) + 3]);
-      }
-      // Through shared memory, so that eight lanes store a row's 128 bytes together: a row
-      // a lane, in pieces of 16 bytes, took 4700 cycles an item.  Row x's piece c lies at
-      // piece c ^ (x % 8).
-      uint8_t* stage = sm.out[warp];
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        uint32_t w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int a = 8 * c + 2 * e;
-          w[e] = f32x2_to_bf16x2(__uint_as_float(o[a >> 5][a & 31]), __uint_as_float(o[a >> 5][(a & 31) + 1]));
+          for (int c = 0; c < 16; ++c)
+            to32[c] = make_uint4(o[c >> 3][4 * (c & 7)], o[c >> 3][4 * (c & 7) + 1], o[c >> 3][4 * (c & 7) + 2],
+                                 o[c >> 3][4 * (c & 7) + 3]);
         }
-        *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-      const uint32_t rows = __ballot_sync(kFull, mine_to_store);
-      __syncwarp();
+        // Through Q's place, which the item's products have read, so that eight lanes store
+        // a row's 128 bytes together: a row a lane, in pieces of 16 bytes, took 4700 cycles
+        // an item.  Row x's piece c lies at piece c ^ (x % 8).
+        uint8_t* stage = sm.q[q_at] + warp * (32 * kHeadDim * 2);
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        const int x = 4 * c + (lane >> 3), piece = lane & 7;
-        if ((rows >> x) & 1u) {
-          const int rr = 32 * (warp & 3) + x, of_tile = fdiv(rr, p.fd_g);
-          const int64_t at = int64_t(it.q0 + tile * p.tile_tokens + of_tile) * p.Hq + h * p.G + rr - of_tile * p.G;
-          *reinterpret_cast<uint4*>(p.out + at * kHeadDim + 8 * piece) =
-              *reinterpret_cast<const uint4*>(stage + x * 128 + ((piece ^ (x & 7)) << 4));
+        for (int c = 0; c < 8; ++c) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int a = 8 * c + 2 * e;
+            w[e] = f32x2_to_bf16x2(__uint_as_float(o[a >> 5][a & 31]), __uint_as_float(o[a >> 5][(a & 31) + 1]));
+          }
+          *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
+        const uint32_t rows = __ballot_sync(kFull, stores);
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const int x = 4 * c + (lane >> 3), piece = lane & 7;
+          if ((rows >> x) & 1u) {
+            const int rr = 32 * warp + x, t = fdiv(rr, p.fd_g);
+            const int64_t at = int64_t(it.q0 + t) * p.Hq + h * p.G + rr - t * p.G;
+            *reinterpret_cast<uint4*>(p.out + at * kHeadDim + 8 * piece) =
+                *reinterpret_cast<const uint4*>(stage + x * 128 + ((piece ^ (x & 7)) << 4));
+          }
+        }
+        fence_proxy_async_shared();  // before a copy writes there again
       }
       __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.q_free[q_at]));
     }
-    if (kTiles == 2 && tile == 0) await_turn(0);  // the last one passed
   }
   if (*reinterpret_cast<volatile int*>(&sm.failed)) {  // copies and products in flight
+    if (threadIdx.x == 0) atomicOr(&g_prompt_error, GK_DEVERR_TIMEOUT);
     const uint64_t since = globaltimer_ns();
     while (globaltimer_ns() - since < 10000000) __nanosleep(1000);
   }
   tmem_fence_before();
   __syncthreads();
   __syncwarp();
-  if (warp == kSoftWarps + 1) tmem_dealloc<kTiles * kTileColumns>(tmem);
+  if (warp == kSoftWarps + 1) tmem_dealloc<kTmemColumns>(tmem);
 }
 
 constexpr int kRowThreads = 256;
@@ -906,11 +855,8 @@ static cudaError_t prompt_setup(const PromptDevice** out) {
     d.encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
     e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(prompt_attn_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             int(sizeof(PromptSmem<1>)));
-    if (e != cudaSuccess) return e;
-    return cudaFuncSetAttribute(prompt_attn_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                int(sizeof(PromptSmem<2>)));
+    return cudaFuncSetAttribute(prompt_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                int(sizeof(PromptSmem)));
   });
 }
 
@@ -959,12 +905,8 @@ cudaError_t launch_prompt_attn(PromptAttnParams& p, cudaStream_t st) {
     ok = ok && encode_map(*d, &p.k_map, p.k, p.k_tokens, p.Hkv, p.k_stride, kPromptKeys, 1) &&
          encode_map(*d, &p.v_map, p.v, p.k_tokens, p.Hkv, p.v_stride, kPromptKeys, 1);
   if (!ok) return cudaErrorInvalidValue;
-  const int64_t places = p.max_items * p.Hkv;
-  if (p.tiles == 2)
-    return launch(prompt_attn_kernel<2>, p, unsigned(std::min(places, int64_t(d->sms))), kAttnThreads<2>,
-                  sizeof(PromptSmem<2>), st);
-  e = launch(prompt_attn_kernel<1>, p, unsigned(std::min(places, int64_t(2) * d->sms)), kAttnThreads<1>,
-             sizeof(PromptSmem<1>), st);
+  const int64_t grid = std::min(p.max_items * p.Hkv, int64_t(2) * d->sms);
+  e = launch(prompt_attn_kernel, p, unsigned(grid), kAttnThreads, sizeof(PromptSmem), st);
   if (e != cudaSuccess || p.max_recs == 0) return e;
   // most rows of split tiles: half of the records, or the tiles
   const int64_t rows = std::min(p.max_recs / 2, p.max_items - p.max_recs) * p.Hkv * kPromptRows;
