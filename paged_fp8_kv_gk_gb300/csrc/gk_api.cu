@@ -801,6 +801,7 @@ gk_status gk_prompt_attn(const gk_prompt* prompt, void* plan, size_t plan_bytes,
   p.k_tokens = s.k_tokens;
   p.tile_tokens = L.tile_tokens;
   p.fd_g = make_fastdiv(uint32_t(p.G));
+  p.fd_hkv = make_fastdiv(uint32_t(p.Hkv));
   return launch_prompt_attn(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GK_OK
                                                                                 : GK_ERR_CUDA;
 }

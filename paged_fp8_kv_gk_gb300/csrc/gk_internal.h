@@ -280,7 +280,7 @@ struct PromptAttnParams {
   int64_t q_stride, k_stride, v_stride;  // elements
   int64_t max_items, max_recs;
   int Hq, Hkv, G, W, q_tokens, k_tokens, tile_tokens;
-  FastDiv fd_g;
+  FastDiv fd_g, fd_hkv;
 };
 
 // Launchers (gk_kernels.cu).  They return the launch status.

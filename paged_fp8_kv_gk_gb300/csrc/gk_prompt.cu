@@ -358,20 +358,21 @@ __device__ __forceinline__ int item_steps(const Item& it) {
   return (it.k_end - it.k_lo + kPromptKeys - 1) / kPromptKeys;
 }
 
-// Waits for a barrier's phase.  After kWaitTries tries (10 ms and more; waits here last
-// a microsecond) the CTA is marked as failed and goes on, so that its warps stay
+// Waits for a barrier's phase.  After 4 kWaitRounds tries (10 ms and more; waits here
+// last a microsecond) the CTA is marked as failed and goes on, so that its warps stay
 // together; from the next item on it does nothing, and it ends once its copies have had
-// time to land.  No clock, no vote and no call here: each of them cost the loops around
-// it 4 % and more.
-constexpr int kWaitTries = 1 << 20;
+// time to land.  No clock, no vote, no call here, and no count between the tries: a
+// warp that polls shares its scheduler with the softmax, and each of these cost 4 to 12 %.
+constexpr int kWaitRounds = 1 << 18;
 __device__ __forceinline__ void prompt_wait(PromptSmem& sm, uint64_t& bar, uint32_t parity) {
   const uint32_t at = smem_u32(&bar);
-  int tries = kWaitTries;
-  while (!mbar_try_wait(at, parity))
-    if (--tries == 0) {
-      *reinterpret_cast<volatile int*>(&sm.failed) = 1;
-      break;
-    }
+#pragma unroll 1
+  for (int n = 0; n < kWaitRounds; ++n) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (mbar_try_wait(at, parity)) return;
+  }
+  *reinterpret_cast<volatile int*>(&sm.failed) = 1;
 }
 __device__ __forceinline__ bool gave_up(PromptSmem& sm) {
   return __any_sync(kFull, *reinterpret_cast<volatile int*>(&sm.failed));
@@ -451,7 +452,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
       __syncwarp();
     };
     for (; turn.more() && !gave_up(sm); turn.next()) {
-      const int i = turn.at / p.Hkv, h = turn.at - i * p.Hkv;
+      const int i = fdiv(turn.at, p.fd_hkv), h = turn.at - i * p.Hkv;
       const Item it = load_item(p, i);
       const int steps = item_steps(it), k_lo = it.k_lo;
       if (steps == 0) continue;
@@ -505,7 +506,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
     auto next_item = [&]() -> int {
       int keys = 0;
       for (; turn.more() && keys == 0; turn.next()) {
-        const Item it = load_item(p, turn.at / p.Hkv);
+        const Item it = load_item(p, fdiv(turn.at, p.fd_hkv));
         keys = it.k_end - it.k_lo;
       }
       return keys;
@@ -546,11 +547,11 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
     uint32_t count = 0, items = 0;  // steps and items so far: the parities of all barriers
     auto fetch = [&](int place) {
       if (turn.more() && lane < 2)
-        cp_async16(smem_u32(&sm.item[warp][place][4 * lane]), p.items + 2 * (turn.at / p.Hkv) + lane);
+        cp_async16(smem_u32(&sm.item[warp][place][4 * lane]), p.items + 2 * fdiv(turn.at, p.fd_hkv) + lane);
     };
     fetch(0);
     for (int place = 0; turn.more(); place ^= 1) {
-      const int h = turn.at % p.Hkv;
+      const int h = turn.at - fdiv(turn.at, p.fd_hkv) * p.Hkv;
       cp_async_wait_all();
       __syncwarp();
       const volatile int* kept = sm.item[warp][place];
@@ -591,17 +592,22 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
           const int t0 = it.k_lo + j * kPromptKeys;
           keys = it.k_end - t0;
           const int2 seen = seen_keys(p, it, min(token, it.n - 1));
-          const uint32_t first = uint32_t(seen.x - t0), n = uint32_t(max(seen.y - seen.x, 0));
+          auto below = [](int n) -> uint32_t {  // bits below n
+            return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1;
+          };
           const int lo = it.diag + it.n - p.W - t0, hi = min(it.diag + 1 - t0, keys) - 32;
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            if (32 * c < lo || 32 * c > hi) {
+            if ((c == 0 || keys > 32) && (32 * c < lo || 32 * c > hi)) {
+              const int at = t0 + 32 * c;
+              const uint32_t sees = below(seen.y - at) & ~below(seen.x - at);
 #pragma unroll
               for (int e = 0; e < 32; ++e)
-                if (uint32_t(32 * c + e) - first >= n) s[c][e] = __float_as_uint(-INFINITY);
+                if (!(sees & (1u << e))) s[c][e] = __float_as_uint(-INFINITY);
             }
           if (j == 0) {
-            const float top = fmaxf(fmaxf(max32(s[0]), max32(s[1])), fmaxf(max32(s[2]), max32(s[3])));
+            float top = max32(s[0]);
+            if (keys > 32) top = fmaxf(fmaxf(top, max32(s[1])), fmaxf(max32(s[2]), max32(s[3])));
             if (fabsf(top) < INFINITY) R = fmaf(top, kScoreLog2, kHeadroom);
           }
         }
@@ -744,8 +750,12 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
         const int head = h * p.G + r - token * p.G;
         const float f = l == 0.f || !valid ? 0.f : out_scale(l, R, p.sinks ? p.sinks + head : nullptr, 1.f);
 #pragma unroll
-        for (int c = 0; c < 64; ++c)
-          o[c >> 5][c & 31] = l == 0.f ? 0u : __float_as_uint(__uint_as_float(o[c >> 5][c & 31]) * f);
+        for (int c = 0; c < 64; ++c) o[c >> 5][c & 31] = __float_as_uint(__uint_as_float(o[c >> 5][c & 31]) * f);
+        if (__any_sync(kFull, l == 0.f)) {  // no key seen: zeros, whatever the product made of them
+#pragma unroll
+          for (int c = 0; c < 64; ++c)
+            if (l == 0.f) o[c >> 5][c & 31] = 0;
+        }
         if (p.out_f32 && stores) {
           uint4* to32 = reinterpret_cast<uint4*>(p.out_f32 + (int64_t(it.q0 + token) * p.Hq + head) * kHeadDim);
 #pragma unroll
@@ -768,16 +778,15 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
           *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
         const uint32_t rows = __ballot_sync(kFull, stores);
+        uint16_t* out = p.out + ((int64_t(it.q0) * p.Hq + h * p.G) * kHeadDim + 8 * (lane & 7));
+        const int64_t token_step = int64_t(p.Hq - p.G) * kHeadDim;
         __syncwarp();
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-          const int x = 4 * c + (lane >> 3), piece = lane & 7;
-          if ((rows >> x) & 1u) {
-            const int rr = 32 * warp + x, t = fdiv(rr, p.fd_g);
-            const int64_t at = int64_t(it.q0 + t) * p.Hq + h * p.G + rr - t * p.G;
-            *reinterpret_cast<uint4*>(p.out + at * kHeadDim + 8 * piece) =
-                *reinterpret_cast<const uint4*>(stage + x * 128 + ((piece ^ (x & 7)) << 4));
-          }
+          const int x = 4 * c + (lane >> 3), rr = 32 * warp + x;
+          if ((rows >> x) & 1u)
+            *reinterpret_cast<uint4*>(out + (fdiv(rr, p.fd_g) * token_step + rr * kHeadDim)) =
+                *reinterpret_cast<const uint4*>(stage + x * 128 + (((lane & 7) ^ (x & 7)) << 4));
         }
         fence_proxy_async_shared();  // before a copy writes there again
       }
