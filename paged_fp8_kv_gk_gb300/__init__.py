@@ -145,6 +145,11 @@ class KvCache:
         self.per_group = per_group
         self.k_layout = int(k_layout)
         self._keep = (ks, vs)
+        held = [t for t in ks + vs if not isinstance(t, int)]
+        # of the tensors: the smallest one's bytes, and their device (-1: several)
+        self._bytes = min((t.numel() * t.element_size() for t in held), default=None)
+        devs = {t.get_device() for t in held}
+        self._dev = None if not devs else devs.pop() if len(devs) == 1 else -1
         c = KvCacheC(k_layout=self.k_layout)
         if per_group:
             self._k_arr = _ptr_array(ks, "k_bufs")
@@ -821,19 +826,24 @@ def gk_rope_table(params, pos, cos, sin, stream=None) -> None:
 def _heads(t, name, dev, heads=None, dim=None):
     """Checks of a bf16 [tokens, heads, channels] tensor with contiguous heads, as slices of a fused
     projection are; returns (tokens, heads, channels, token stride)."""
+    size, stride = t.shape, t.stride()
+    if len(size) == 3 and t.dtype is _torch().bfloat16 and t.get_device() == dev:
+        T, H, D = size
+        if stride[2] == 1 and stride[1] == D and T > 1 and (heads is None or (H == heads and D == dim)):
+            return T, H, D, stride[0]
     if t.dtype is not _torch().bfloat16:
         raise TypeError(f"{name}: expected {_torch().bfloat16}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (no CPU path)")
     if t.get_device() != dev:
         raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
-    if t.dim() != 3 or (heads is not None and t.shape[1:] != (heads, dim)):
+    if len(size) != 3 or (heads is not None and size[1:] != (heads, dim)):
         raise ValueError(f"{name} must be [tokens, "
                          f"{'heads, channels' if heads is None else f'{heads}, {dim}'}]")
-    T, H, D = t.shape
-    if t.numel() and ((D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D)):
+    T, H, D = size
+    if t.numel() and ((D > 1 and stride[2] != 1) or (H > 1 and stride[1] != D)):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return T, H, D, t.stride(0) if T > 1 else H * D
+    return T, H, D, stride[0] if T > 1 else H * D
 
 
 def gk_rope(x, cos, sin, out, layout="half", stream=None) -> None:
@@ -860,13 +870,18 @@ def gk_rope(x, cos, sin, out, layout="half", stream=None) -> None:
 
 
 def _kv_on(kv, sh, dev):
-    """_kv, of a cache on device `dev` (the current one: the library launches there)."""
-    c = _kv(kv, sh)
-    for t in kv._keep[0] + kv._keep[1]:
-        if not isinstance(t, int) and t.get_device() != dev:
-            raise ValueError(f"a cache buffer is on cuda:{t.get_device()}, the current device is "
-                             f"cuda:{dev}")
-    return c
+    """The gk_kv_cache of a KvCache whose tensors must lie on device `dev` (the current one: the
+    library launches there) and hold the shape."""
+    if not isinstance(kv, KvCache):
+        raise TypeError("kv must be a KvCache (kv_from_group_buffers, kv_stacked)")
+    groups = sh.num_layers // 2
+    half = sh.num_blocks * sh.num_kv_heads * sh.block_size * sh.head_dim
+    if kv._dev is not None and kv._dev != dev:
+        raise ValueError(f"the cache buffers are not all on the current device, cuda:{dev}")
+    if (kv.per_group and len(kv._keep[0]) < groups) or (
+            kv._bytes is not None and kv._bytes < (half if kv.per_group else groups * half)):
+        kv.check(sh)       # names what is wrong
+    return kv.param()
 
 
 def gk_kv_write(shape, k, v, cos, sin, k_scale, v_scale, slot_full, slot_swa, kv: KvCache,
