@@ -65,7 +65,8 @@ __global__ void __launch_bounds__(kPromptPlanThreads)
   __shared__ int first_tile[kPromptMaxSeqs + 1];
   __shared__ int count[kBuckets];
   __shared__ int warps[32];
-  __shared__ int longest, steps_of[kCandidates], recs_of[kCandidates], part, n_splits, n_recs;
+  __shared__ int longest, steps_of[kCandidates], items_of[kCandidates], recs_of[kCandidates];
+  __shared__ int part, n_splits, n_recs;
   const int tid = threadIdx.x, T = p.tile_tokens;
   int tiles = 0;
   bool bad = false;
@@ -91,7 +92,7 @@ __global__ void __launch_bounds__(kPromptPlanThreads)
     return;
   }
   for (int i = tid; i < kBuckets; i += kPromptPlanThreads) count[i] = 0;
-  if (tid < kCandidates) steps_of[tid] = recs_of[tid] = 0;
+  if (tid < kCandidates) steps_of[tid] = items_of[tid] = recs_of[tid] = 0;
   if (tid == 0) {
     first_tile[p.num_seqs] = tiles;
     longest = n_splits = n_recs = part = 0;
@@ -123,9 +124,11 @@ __global__ void __launch_bounds__(kPromptPlanThreads)
     for (int c = 0; c < kCandidates; ++c) {
       const int len = 4 << c, parts = (t.steps + len - 1) / len;
       const int s = __reduce_add_sync(kFull, tid < tiles ? t.steps + max(parts, 1) * kItemSteps : 0);
+      const int n = __reduce_add_sync(kFull, tid < tiles ? max(parts, 1) : 0);
       const int r = __reduce_add_sync(kFull, parts > 1 ? parts : 0);
       if ((tid & 31) == 0) {
         atomicAdd(&steps_of[c], s);
+        atomicAdd(&items_of[c], n);
         atomicAdd(&recs_of[c], r);
       }
     }
@@ -135,8 +138,11 @@ __global__ void __launch_bounds__(kPromptPlanThreads)
       for (int c = 0; c < kCandidates; ++c) {
         const int len = 4 << c;
         const int64_t mean = int64_t(steps_of[c]) * p.Hkv / kPromptSlots;
-        // two steps' time to join parts
-        const int64_t end = max(mean, int64_t(min(len, longest) + kItemSteps)) + (recs_of[c] ? 2 : 0);
+        const int item = min(len, longest) + kItemSteps;
+        // where CTAs have several items, some end half of one later; two steps' time to
+        // join parts
+        const int64_t end = max(mean, int64_t(item)) +
+                            (int64_t(items_of[c]) * p.Hkv > kPromptSlots ? item / 2 : 0) + (recs_of[c] ? 2 : 0);
         if (recs_of[c] <= p.max_recs && end < best) {
           best = end;
           part = recs_of[c] ? len : 0;
