@@ -915,7 +915,8 @@ cudaError_t launch_prompt_attn(PromptAttnParams& p, cudaStream_t st) {
   cudaError_t e = prompt_setup(&d);
   if (e != cudaSuccess) return e;
   bool ok = encode_map(*d, &p.q_map, p.q, p.q_tokens, p.Hq, p.q_stride, p.tile_tokens, p.G);
-  // without keys no item copies any
+  // without keys no item copies any, but the maps are prefetched
+  p.k_map = p.v_map = p.q_map;
   if (p.k_tokens > 0)
     ok = ok && encode_map(*d, &p.k_map, p.k, p.k_tokens, p.Hkv, p.k_stride, kPromptKeys, 1) &&
          encode_map(*d, &p.v_map, p.v, p.k_tokens, p.Hkv, p.v_stride, kPromptKeys, 1);

@@ -93,10 +93,9 @@ def test_groups(G, Hkv):
                                          (13, 7, [1900], 0), (8, 8, [1303, 1200, 40], 513)])
 @pytest.mark.parametrize("window", [0, 1, 128, 700])
 def test_long_sequences(Hkv, G, nq, ctx, window):
-    """Items of two tiles, as long sequences have them: both halves filled, one empty, a last step that
-    only the second half sees, windows that begin behind the second half's first step."""
+    """More items than CTAs: several in turn, of many groups and of one, a last step of a few keys."""
     c = Case(nq, [n + ctx for n in nq], Hkv=Hkv, G=G, window=window, sinks=G == 16, pad=3, seed=G)
-    assert c.plan.numel() < 1 << 20         # no room for parts: two tiles
+    assert c.plan.numel() < 1 << 20         # too many to split
     c.check()
 
 
@@ -131,6 +130,24 @@ def test_context_in_front(window):
     out, f32 = c.run()
     q0 = c.qs[4]
     assert (out[q0:q0 + 13] == 0).all() and (f32[c.qs[5]:c.qs[6]] == 0).all()
+
+
+def test_no_key_at_all():
+    """k_tokens of zero: every query gets zeros."""
+    for nq in ([5], [300, 1]):
+        c = Case(nq, [0] * len(nq), Hkv=2, sinks=True, pad=2)
+        out, f32 = c.run()
+        n = c.qs[-1]
+        assert gk.gk_read_device_error() == 0
+        assert (out[:n] == 0).all() and (f32[:n] == 0).all() and (out[n:] == 7).all()
+
+
+def test_single_tokens():
+    """One query a sequence over its cached keys, as a decode step without a paged cache has it."""
+    rng = np.random.default_rng(5)
+    nk = rng.integers(1, 900, 70)
+    Case([1] * 70, nk, Hkv=2, sinks=True).check()
+    Case([1] * 70, nk, Hkv=1, window=100).check()
 
 
 @pytest.mark.parametrize("nq,nk,Hkv", [(1, 30000, 1), (8, 8184, 8), (5, 65536, 2), (40, 20011, 1)])
@@ -247,4 +264,113 @@ def test_streams_graph_and_reuse():
     c.qs, c.ks = [0, 8, 58], [0, 3000, 5050]
     gk.gk_prompt_plan(c.prompt, i32(c.qs), i32(c.ks), c.plan)
     c.check()
+    assert gk.gk_read_device_error() == 0
+
+
+def test_layers_back_to_back():
+    """Several layers on one plan with nothing between the calls, split and whole ones: each output is
+    the call's alone."""
+    for c in (Case([3, 20], [4000, 9000], Hkv=2, sinks=True, seed=1), Case([900], [900], Hkv=8, seed=2)):
+        layers = []
+        for i in range(6):
+            d = Case.__new__(Case)
+            d.__dict__.update(c.__dict__)
+            g = torch.Generator(device="cuda").manual_seed(i)
+            d.q, d.k, d.v = (torch.randn(t.shape, generator=g, device="cuda").to(torch.bfloat16)
+                             for t in (c.q, c.k, c.v))
+            layers.append(d)
+        alone = []
+        for d in layers:
+            alone.append(d.run()[0])
+            torch.cuda.synchronize()
+        together = [d.run()[0] for d in layers]
+        torch.cuda.synchronize()
+        for a, b in zip(alone, together):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("kv4", [False, True])
+def test_a_prompt_in_chunks_and_a_decode_step(kv4):
+    """The calls together, as an engine makes them: a prompt in two chunks through a window and a full
+    layer (positions, rotation in place, K and V to the cache, attention over what the cache holds of the
+    first chunk and the second chunk's own), then a decode step of the next token over the cache."""
+    torch.manual_seed(1)
+    H, T1, T2, B = 2, 150, 91, 32
+    T, Hq = T1 + T2, 16
+    nb = 2 * (-(-(T + 1) // B)) + 1
+    shape = dict(num_layers=2, batch=1, num_q_heads=Hq, num_kv_heads=H, head_dim=64, block_size=B, num_blocks=nb,
+                 window=128, max_blocks_full=-(-(T + 1) // B), max_blocks_swa=-(-(128 + B - 1) // B))
+    rng = np.random.default_rng(2)
+    perm = rng.permutation(nb)
+    n = -(-(T + 1) // B)
+    tables = perm[n:2 * n], perm[:n]                     # window layer's blocks, full layer's
+    slots = [i32(b[np.arange(T + 1) // B] * B + np.arange(T + 1) % B) for b in tables]
+    ks, vs = torch.tensor([0.011, 0.012], device="cuda"), torch.tensor([0.009, 0.013], device="cuda")
+    if kv4:
+        kv = gk.new_kv4_cache(shape)
+        ks, vs = ks * 30, vs * 30
+        write, read = gk.gk_kv4_write, gk.gk_kv4_read
+    else:
+        kv = gk.KvCache([torch.zeros(nb, H, B // 2, 64, 2, dtype=torch.uint8, device="cuda")],
+                        [torch.zeros(nb, H, B, 64, dtype=torch.uint8, device="cuda")])
+        write, read = gk.gk_kv_write, gk.gk_kv_read
+    rope = dict(rot_dim=64, theta=150000.0, scaling="yarn", factor=32.0)
+    sinks = torch.randn(2, Hq, device="cuda")
+    qkv = torch.randn(2, T + 1, Hq + 2 * H, 64, device="cuda").to(torch.bfloat16)
+    raw = qkv.clone()
+    cos, sin = torch.empty(T + 1, 32, device="cuda"), torch.empty(T + 1, 32, device="cuda")
+    gk.gk_rope_table(rope, i32(np.arange(T + 1)), cos, sin)
+    for first, count in ((0, T1), (T1, T2)):
+        at = slice(first, first + count)
+        for i in range(2):
+            x = qkv[i, at]
+            gk.gk_rope(x[:, :Hq + H], cos[at], sin[at], x[:, :Hq + H])
+            k, v = x[:, Hq:Hq + H], x[:, Hq + H:]
+            write(shape, k[None], v[None], None, None, ks, vs, slots[1][at], slots[0][at], kv, layer0=i)
+            if first:
+                kk, vv = (torch.empty(1, first + count, H, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+                got = torch.empty(2, 1, first, H, 64, dtype=torch.bfloat16, device="cuda")
+                read(shape, kv, ks, vs, slots[1][:first].contiguous(), slots[0][:first].contiguous(), got[0], got[1],
+                     layer0=i)
+                kk[0, :first], vv[0, :first] = got[0, 0], got[1, 0]
+                kk[0, first:], vv[0, first:] = k, v
+                k, v = kk[0], vv[0]
+            window = 0 if i & 1 else 128
+            prompt = dict(num_seqs=1, num_q_heads=Hq, num_kv_heads=H, head_dim=64, window=window, q_tokens=count,
+                          k_tokens=first + count)
+            plan = gk.new_prompt_plan(prompt)
+            gk.gk_prompt_plan(prompt, i32([0, count]), i32([0, first + count]), plan)
+            out = torch.empty(count, Hq, 64, dtype=torch.bfloat16, device="cuda")
+            f32 = torch.empty(count, Hq, 64, device="cuda")
+            gk.gk_prompt_attn(prompt, plan, x[:, :Hq], k, v, out, f32, sinks=sinks[i])
+            want, tol = pp.attention(x[:, :Hq], k, v, [0, count], [0, first + count], window, sinks[i])
+            assert ((f32.double() - want).abs() <= tol).all()
+            # K in the cache is the rotated one's nearest code
+            turned = pp.rope(raw[i, at, Hq:Hq + H].float().cpu().numpy(), cos[at].cpu().numpy(),
+                             sin[at].cpu().numpy(), "half")
+            assert torch.equal(x[:, Hq:Hq + H].cpu(), torch.from_numpy(turned).to(torch.bfloat16))
+    # the next token by a decode step over the cache
+    new = raw[:, T:]
+    control = dict(pos=i32([T]), active=torch.ones(1, dtype=torch.uint8, device="cuda"))
+    first_block = max(0, T - 127) // B
+    bt_full = i32(tables[1][:shape["max_blocks_full"]])
+    trimmed = list(tables[0][first_block:first_block + shape["max_blocks_swa"]])
+    bt_swa = i32(trimmed + [0] * (shape["max_blocks_swa"] - len(trimmed)))
+    q, k, v = (new[:, :, a:b].contiguous() for a, b in ((0, Hq), (Hq, Hq + H), (Hq + H, Hq + 2 * H)))
+    out = torch.empty(2, 1, Hq, 64, dtype=torch.bfloat16, device="cuda")
+    f32 = torch.empty(2, 1, Hq, 64, device="cuda")
+    step = gk.gk_kv4_decode_step if kv4 else gk.gk_decode_step
+    step(shape, q, k, v, cos[T:], sin[T:], ks, vs, slots[1][T:].contiguous(), slots[0][T:].contiguous(), bt_full, bt_swa,
+         control["pos"], i32([T - first_block * B]), control["active"], kv, out, f32, gk.new_workspace(shape), sinks=sinks)
+    got = torch.empty(2, 2, T + 1, H, 64, dtype=torch.bfloat16, device="cuda")
+    read(shape, kv, ks, vs, slots[1], slots[0], got[0], got[1])
+    for i in range(2):
+        turned = torch.from_numpy(pp.rope(q[i].float().cpu().numpy(), cos[T:].cpu().numpy(), sin[T:].cpu().numpy(),
+                                          "half")).cuda()
+        # the cache's values are the codes' times a scale: the read rounds them by half a step of 2^-8,
+        # which moves a score by 2^-8 of its terms' magnitudes at most, and v by as much
+        want, tol = pp.attention(turned, got[0, i], got[1, i], [0, 1], [0, T + 1], 0 if i & 1 else 128, sinks[i])
+        size = (turned.abs().double().repeat(1, 1, 1)[0].view(H, -1, 64) @
+                got[0, i].abs().double().amax(0).unsqueeze(-1)).amax() / 8
+        assert ((f32[i].double() - want).abs() <= tol * (2 + 2 * float(size))).all()
     assert gk.gk_read_device_error() == 0
