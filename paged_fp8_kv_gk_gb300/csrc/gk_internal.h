@@ -221,6 +221,8 @@ struct RopeTableParams {
   float* sinb;
   int64_t n;
   int half;     // R / 2
+  int rows;     // positions a CTA (set by the launcher)
+  FastDiv fd_half;
   float scale;  // of both outputs
   uint64_t freq[kMaxRopePairs];  // turns a position, times 2^64, modulo 2^64
 };
@@ -233,6 +235,8 @@ struct RopeParams {
   int64_t n, x_stride, out_stride;
   int heads, head_dim, rot_dim, interleaved;
   int chunks;  // head_dim / 16
+  int rows;    // tokens a CTA (set by the launcher)
+  FastDiv fd_chunks;
 };
 
 // A prompt's attention.  A tile is up to kPromptRows / G tokens of one sequence
@@ -329,7 +333,7 @@ cudaError_t launch_prompt_plan(const PromptPlanParams& p, cudaStream_t st);
 cudaError_t launch_prompt_attn(PromptAttnParams& p, cudaStream_t st);
 cudaError_t read_prompt_error(uint32_t* bits, bool clear);
 // gk_rope.cu
-cudaError_t launch_rope_table(const RopeTableParams& p, cudaStream_t st);
-cudaError_t launch_rope(const RopeParams& p, cudaStream_t st);
+cudaError_t launch_rope_table(RopeTableParams& p, cudaStream_t st);
+cudaError_t launch_rope(RopeParams& p, cudaStream_t st);
 
 }  // namespace gk

@@ -13,18 +13,23 @@ namespace gk {
 
 constexpr int kRopeThreads = 256;
 
-// One thread a (position, frequency): the product wraps at whole turns, so the
-// upper bits are the angle's place on the circle, exact however far the position.
-// A turn is cut into quarters; the rest, in [-1/8, 1/8] turns, is exact to 2^-64
-// before it becomes a float.
+// One thread a (position, frequency), as many whole positions a CTA as fit: the
+// product wraps at whole turns, so the upper bits are the angle's place on the circle,
+// exact however far the position.  A turn is cut into quarters; the rest, in [-1/8,
+// 1/8] turns, is exact to 2^-64 before it becomes a float.  The frequencies come through
+// shared memory (read from the parameters by a lane's own index, 32 lanes take 32
+// turns: 6.1 us for 8191 positions).
 __global__ void __launch_bounds__(kRopeThreads)
     rope_table_kernel(const __grid_constant__ RopeTableParams p) {
+  __shared__ uint64_t freq[kMaxRopePairs];
+  const int row = fdiv(int(threadIdx.x), p.fd_half), e = int(threadIdx.x) - row * p.half;
+  if (int(threadIdx.x) < p.half) freq[threadIdx.x] = p.freq[threadIdx.x];
+  __syncthreads();
   follow_stream();
-  const int64_t at = int64_t(blockIdx.x) * kRopeThreads + threadIdx.x;
-  const int64_t n = at / p.half;
-  if (n >= p.n) return;
-  const int e = int(at - n * p.half);
-  const uint64_t turns = uint64_t(int64_t(__ldcg(p.pos + n))) * p.freq[e];
+  const int64_t n = int64_t(blockIdx.x) * p.rows + row;
+  if (row >= p.rows || n >= p.n) return;
+  const int64_t at = n * p.half + e;
+  const uint64_t turns = uint64_t(int64_t(__ldcg(p.pos + n))) * freq[e];
   const uint64_t near = turns + (uint64_t(1) << 61);      // to the nearest quarter
   const int quarter = int(near >> 62);
   const int64_t rest = int64_t(turns - (uint64_t(quarter) << 62));
@@ -36,16 +41,17 @@ __global__ void __launch_bounds__(kRopeThreads)
 }
 
 // One thread a (token, 16 channels) of kHeads heads, their loads issued together;
-// cos and sin stay in registers.  16 channels are the eight pairs of a chunk: two
+// cos and sin stay in registers.  Bound by memory: 8191 tokens of 72 heads (151 MB) in
+// about 23 us, 6.5 TB/s.  16 channels are the eight pairs of a chunk: two
 // runs of 8 half of rot_dim apart, or 16 in a row (interleaved, and the
 // channels behind rot_dim, which are copied).
 template <int kHeads>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
+  const int row = fdiv(int(threadIdx.x), p.fd_chunks);
+  const int64_t n = int64_t(blockIdx.x) * p.rows + row;
   follow_stream();
-  const int64_t at = int64_t(blockIdx.x) * kRopeThreads + threadIdx.x;
-  const int64_t n = at / p.chunks;  // p.chunks: of a head
-  if (n >= p.n) return;
-  const int c = int(at - n * p.chunks), h0 = int(blockIdx.y) * kHeads;
+  if (row >= p.rows || n >= p.n) return;
+  const int c = int(threadIdx.x) - row * p.chunks, h0 = int(blockIdx.y) * kHeads;
   const int half = p.rot_dim >> 1;
   const bool turned = 16 * c < p.rot_dim, apart = turned && !p.interleaved;
   const int c0 = apart ? 8 * c : 16 * c, c1 = apart ? half + 8 * c : 16 * c + 8;
@@ -123,12 +129,14 @@ static cudaError_t launch(void (*kernel)(P), const P& p, dim3 grid, cudaStream_t
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-cudaError_t launch_rope_table(const RopeTableParams& p, cudaStream_t st) {
-  const int64_t ctas = (p.n * p.half + kRopeThreads - 1) / kRopeThreads;
+cudaError_t launch_rope_table(RopeTableParams& p, cudaStream_t st) {
+  p.rows = kRopeThreads / p.half;
+  p.fd_half = make_fastdiv(uint32_t(p.half));
+  const int64_t ctas = (p.n + p.rows - 1) / p.rows;
   return launch(rope_table_kernel, p, dim3(unsigned(ctas)), st);
 }
 
-cudaError_t launch_rope(const RopeParams& p, cudaStream_t st) {
+cudaError_t launch_rope(RopeParams& p, cudaStream_t st) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -138,10 +146,14 @@ cudaError_t launch_rope(const RopeParams& p, cudaStream_t st) {
     return cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
   });
   if (e != cudaSuccess) return e;
-  const int64_t ctas = (p.n * p.chunks + kRopeThreads - 1) / kRopeThreads;
-  // four heads a thread where that still leaves every SM its eight CTAs
-  if (ctas * ((p.heads + 3) / 4) >= int64_t(c->sms) * 8)
-    return launch(rope_kernel<4>, p, dim3(unsigned(ctas), unsigned((p.heads + 3) / 4)), st);
+  p.rows = kRopeThreads / p.chunks;
+  p.fd_chunks = make_fastdiv(uint32_t(p.chunks));
+  const int64_t ctas = (p.n + p.rows - 1) / p.rows;
+  // two heads a thread where that still leaves every SM its eight CTAs: with its table,
+  // 8191 tokens of 72 heads take 26.4 us (one head 30.5, four 27.0, eight 30), 64 tokens
+  // the same either way
+  if (ctas * ((p.heads + 1) / 2) >= int64_t(c->sms) * 8)
+    return launch(rope_kernel<2>, p, dim3(unsigned(ctas), unsigned((p.heads + 1) / 2)), st);
   return launch(rope_kernel<1>, p, dim3(unsigned(ctas), unsigned(p.heads)), st);
 }
 
