@@ -178,7 +178,10 @@ gk_status gk_prompt_plan(const gk_prompt *prompt, const int32_t *q_start, const 
  * or infinities; rows of out outside every sequence are left as they were.
  * Scores and the softmax's sums are fp32; the probabilities enter the product with
  * V as bf16 (V's own type: half a step of 2^-8 each, as fine as the output's own
- * rounding).
+ * rounding).  The sums are divided at the end: a row whose sum of p_t |v_t|, p_t =
+ * e^(s_t - max s), passes fp32's range is infinite or NaN.  Rows that meet infinities or
+ * NaN in V, or a score some 80 above those of the 2048 keys before it, are computed by
+ * a second, slow path (a warp a row).
  *   prompt, plan, plan_bytes  as given to gk_prompt_plan (the same prompt)
  *   q        bf16, element (t, h, e) at t * q_stride + h * 64 + e; strides in
  *            elements, multiples of 8; q, k, v and out 16-byte aligned

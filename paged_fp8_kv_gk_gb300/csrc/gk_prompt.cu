@@ -291,9 +291,9 @@ __device__ __forceinline__ float max32(const uint32_t (&s)[32]) {
 // =========================================================================
 // Attention
 // =========================================================================
-// An item is a tile of 128 rows (16 tokens of 8 heads, say) and a run of keys, 128
-// a step, for one kv head.  Warps 0-3 do the softmax, a thread a row.  Warp 4 copies, warp 5 issues the
-// products:
+// An item is a tile of 128 rows, (token, q head of one kv head): 16 tokens of 8 heads,
+// say, and a run of keys, 128 a step.  Warps 0-3 do the softmax, a thread a row, warp 4
+// copies, warp 5 issues the products:
 //   S = Q K^T  128 x 128 x 64  both operands in shared memory, fp32 in tensor memory
 //   O += P V   128 x 64 x 128  P, bf16, in tensor memory; V in shared memory, MN-major
 // A row's scores are loaded into registers as soon as they are there, so that the next
@@ -304,20 +304,31 @@ __device__ __forceinline__ float max32(const uint32_t (&s)[32]) {
 // computed while this one's last exponentials and its output are.
 //
 // The softmax's reference R of a row (log2 units; p = 2^(s - R)) is the largest score
-// of the first step plus kHeadroom (every row sees a key of its first step, or none at
-// all), and no step after it looks for a maximum: p and the sums are floats (bf16 in P,
-// with a float's exponents), as exact at 2^60 as at 1.  Every kCheckSteps steps, a row
-// whose sum has passed kLargest takes a new R, and O and the sum are scaled to it.  A row
-// that overflows all the same (a score 54 or more above all up to the last check, and
-// then values of 2^60) is computed again by attend_row, as are rows with unseen
-// infinities or NaN.
+// of its first step (every row sees a key there, or none at all), and no step after it
+// looks for a maximum: p and the sums are floats (bf16 in P, with a float's exponents),
+// as exact at 2^60 as at 1.  Every kCheckSteps steps, a row whose sum has passed
+// kLargest takes a new R, and O and the sum are scaled to it.  A row that overflows all
+// the same (a score some 80 above all up to the last check, or V near its type's end) is
+// computed again by attend_row, as are rows with unseen infinities or NaN.
+//
+// A tile and step take 512 cycles of the tensor cores and as many of the exponential
+// unit (4 a warp instruction).  Measured: 900 (8192 tokens of 64 heads in 437 us, 1260
+// TFLOP/s; 8192 over 65536 keys in 6.1 ms, 1350): exponentials 58 % busy, issue slots 50 %,
+// the rest latency that two softmax warps a scheduler do not cover: both wait, load and
+// store together.  On the way, 8192 over 65536 keys, in ms: one lane of a diverged warp
+// issuing the products 7.9, an elected one 6.8; P's last use awaited behind the
+// exponentials 6.5; no maxima 5.6 (one item a CTA; 6.0 with items in turns, which
+// shortened windows and ragged batches), polls without a count 5.5.  Not kept: half a
+// row a thread and twice the warps (6.1); two tiles a CTA that share K and V and take
+// turns with their exponentials (7.0: the warps that poll sit beside more softmax
+// warps); waits asleep (6.0); 64 keys a step are 25 % more tensor time (a product of N
+// = 64 from shared memory takes 48 cycles, not 32).
 constexpr int kSoftWarps = 4;
 constexpr int kAttnThreads = 32 * (kSoftWarps + 2);
 constexpr int kKStages = 3, kVStages = 2;               // V is needed a softmax later than K
 constexpr int kTileBytes = kPromptRows * kHeadDim * 2;  // Q, and one step of K or of V: 16 KB
 constexpr int kTmemColumns = 256;                       // S 128, O 64, P 64
 constexpr int kTmemO = 128, kTmemP = 192;
-constexpr float kHeadroom = 24.f;
 constexpr float kLargest = 0x1p30f;  // of a row's sum
 constexpr int kCheckSteps = 16;
 
@@ -384,17 +395,6 @@ __device__ __forceinline__ bool gave_up(PromptSmem& sm) {
   return __any_sync(kFull, *reinterpret_cast<volatile int*>(&sm.failed));
 }
 
-// Whether one of the keys [a, b) has a V that is not finite (a warp).
-__device__ __forceinline__ bool any_not_finite(const PromptAttnParams& p, int a, int b, int h) {
-  bool bad = false;
-  for (int t = a; t < b; ++t) {
-    const uint32_t w = __ldcg(reinterpret_cast<const uint32_t*>(
-        p.v + int64_t(t) * p.v_stride + h * kHeadDim + 2 * (threadIdx.x & 31)));
-    bad = bad || (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
-  }
-  return __any_sync(kFull, bad);
-}
-
 __device__ __forceinline__ void store_part(const PromptAttnParams& p, const Item& it, int h, int r,
                                            int lane, const RowResult& y) {
   float* rec = p.records + (int64_t(it.rec) * p.Hkv + h) * kPromptRecFloats;
@@ -403,6 +403,23 @@ __device__ __forceinline__ void store_part(const PromptAttnParams& p, const Item
     rec[kPromptRows + r] = y.l;
   }
   *reinterpret_cast<float2*>(rec + 2 * kPromptRows + r * kHeadDim + 2 * lane) = y.o;
+}
+
+// The rows row0 + the bits of `rows` of an item (in shared memory, as in the plan), by one
+// warp.
+__device__ __forceinline__ void attend_rows(const PromptAttnParams& p, const volatile int* item, int h,
+                                         uint32_t rows, int row0) {
+  const Item it = {item[0], item[1], item[2], item[3], item[4], item[5]};
+  const int lane = threadIdx.x & 31;
+  for (; rows; rows &= rows - 1) {
+    const int r = row0 + __ffs(rows) - 1, t = fdiv(r, p.fd_g), head = h * p.G + r - t * p.G;
+    const RowResult y = attend_row(p, seen_keys(p, it, t), h,
+                                   p.q + int64_t(it.q0 + t) * p.q_stride + head * kHeadDim);
+    if (it.rec < 0)
+      store_row(p, it.q0 + t, head, lane, y.m, y.l, y.o);
+    else
+      store_part(p, it, h, r, lane, y);
+  }
 }
 
 __global__ void __launch_bounds__(kAttnThreads, 2)
@@ -577,7 +594,6 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
       const int whole_lo = max(at_first.diag + at_first.n - p.W - at_first.k_lo + kPromptKeys - 1, 0) / kPromptKeys;
       const int whole_end = max(min(at_first.diag + 1, at_first.k_end) - at_first.k_lo, 0) / kPromptKeys;
       float R = 0.f;
-      bool over = false;
       float2 sum = make_float2(0.f, 0.f);
       auto step = [&](int j, auto whole) {
         constexpr bool kWhole = decltype(whole)::value;
@@ -614,7 +630,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
           if (j == 0) {
             float top = max32(s[0]);
             if (keys > 32) top = fmaxf(fmaxf(top, max32(s[1])), fmaxf(max32(s[2]), max32(s[3])));
-            if (fabsf(top) < INFINITY) R = fmaf(top, kScoreLog2, kHeadroom);
+            if (fabsf(top) < INFINITY) R = top * kScoreLog2;
           }
         }
         const float2 scale = make_float2(kScoreLog2, kScoreLog2), shift = make_float2(-R, -R);
@@ -678,9 +694,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
         }
         const float total = sum.x + sum.y;
         if (j < steps && __any_sync(kFull, total > kLargest)) {
-          over = over || total > kLargest * kLargest;
           // at most by 2^100, a normal float
-          const float up = fminf(kHeadroom + float(int(__float_as_uint(total) >> 23) - 127), 100.f);
+          const float up = fminf(float(int(__float_as_uint(total) >> 23) - 127), 100.f);
           const float to = total > kLargest ? R + up : R;
           const float f = ex2(R - to);
           R = to;
@@ -718,31 +733,13 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
 #pragma unroll
       for (int c = 0; c < 64; c += 2)
         size = max3_abs_nan(size, __uint_as_float(o[c >> 5][c & 31]), __uint_as_float(o[c >> 5][(c & 31) + 1]));
-      // Zero times an unseen key's infinity or NaN, if it is not a seen key's, or an
-      // overflow: such rows are computed again from the keys that they see.
-      uint32_t todo = __ballot_sync(kFull, valid && !(size < INFINITY)), done = 0;
-      if (__builtin_expect(todo != 0, 0)) {
-        const uint32_t sure = __ballot_sync(kFull, over || l > kLargest * kLargest);
-        while (todo) {
-          const int x = __ffs(todo) - 1, rr = 32 * warp + x, tt = fdiv(rr, p.fd_g), hh = h * p.G + rr - tt * p.G;
-          todo &= todo - 1;
-          const int2 keys = seen_keys(p, it, tt);
-          if (!((sure >> x) & 1) && !any_not_finite(p, it.k_lo, min(keys.x, it.k_end), h) &&
-              !any_not_finite(p, max(keys.y, it.k_lo), it.k_end, h))
-            continue;
-          const RowResult y =
-              attend_row(p, keys, h, p.q + int64_t(it.q0 + tt) * p.q_stride + hh * kHeadDim);
-          if (it.rec < 0)
-            store_row(p, it.q0 + tt, hh, lane, y.m, y.l, y.o);
-          else
-            store_part(p, it, h, rr, lane, y);
-          done |= 1u << x;
-        }
-      }
-      const bool stores = valid && !((done >> lane) & 1u);
+      // A row whose scores are numbers and whose result is not: zero times an unseen key's
+      // infinity or NaN, an overflow, or a seen key's.  It is computed again from the keys
+      // that it sees, by one warp at some ten instructions a key.
+      const uint32_t again = __ballot_sync(kFull, valid && !(size < INFINITY) && l == l);
       const uint32_t q_at = items++ & 1;
       if (it.rec >= 0) {
-        if (stores) {
+        if (valid) {
           float* rec = p.records + (int64_t(it.rec) * p.Hkv + h) * kPromptRecFloats;
           rec[r] = l == 0.f ? -INFINITY : R;
           rec[kPromptRows + r] = l;
@@ -762,7 +759,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
           for (int c = 0; c < 64; ++c)
             if (l == 0.f) o[c >> 5][c & 31] = 0;
         }
-        if (p.out_f32 && stores) {
+        if (p.out_f32 && valid) {
           uint4* to32 = reinterpret_cast<uint4*>(p.out_f32 + (int64_t(it.q0 + token) * p.Hq + head) * kHeadDim);
 #pragma unroll
           for (int c = 0; c < 16; ++c)
@@ -783,7 +780,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
           }
           *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        const uint32_t rows = __ballot_sync(kFull, stores);
+        const uint32_t rows = __ballot_sync(kFull, valid);
         uint16_t* out = p.out + ((int64_t(it.q0) * p.Hq + h * p.G) * kHeadDim + 8 * (lane & 7));
         const int64_t token_step = int64_t(p.Hq - p.G) * kHeadDim;
         __syncwarp();
@@ -798,6 +795,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sm.q_free[q_at]));
+      // over what was stored: here nothing is held in registers across the call
+      if (__builtin_expect(again != 0, 0)) attend_rows(p, sm.item[warp][place], h, again, 32 * warp);
     }
   }
   if (*reinterpret_cast<volatile int*>(&sm.failed)) {  // copies and products in flight

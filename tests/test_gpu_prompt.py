@@ -166,6 +166,29 @@ def test_peaked_scores(spread):
     Case([300, 40], [300, 1500], Hkv=1, sinks=True, seed=3, spread=spread).check()
 
 
+@pytest.mark.parametrize("size", [2.0 ** -110, 2.0 ** 100, 2.0 ** 112])
+def test_tiny_and_huge_values(size):
+    """V near the ends of bf16's range, with scores that differ by some tens.  (A sum of 900 products of
+    up to 4 * 2^112 stays below 2^128: above, fp32 sums before the division overflow.)"""
+    for spread in (1.0, 10.0):
+        c = Case([260], [900], Hkv=1, sinks=True, seed=7, spread=spread)
+        c.v.clamp_(-4, 4).mul_(size)
+        c.check()
+
+
+def test_queries_that_are_not_numbers():
+    """A row whose own scores are NaN is NaN, its neighbours are not."""
+    c = Case([70], [300], Hkv=2, sinks=True, seed=9)
+    c.q[33, 5] = math.nan
+    out, f32 = c.run()
+    assert f32[33, 5].isnan().all() and out[33, 5].isnan().all()
+    c.q[33, 5] = 1
+    want, _ = c.run()
+    keep = torch.ones(70, 16, dtype=torch.bool, device="cuda")
+    keep[33, 5] = False
+    assert torch.equal(out[keep], want[keep])
+
+
 def test_rising_scores():
     """A maximum that rises by more than 2^8 at every step of keys."""
     c = Case([200], [2000], Hkv=1, seed=5)
