@@ -1,6 +1,9 @@
 """Attention of packed prompts on the GPU against the plain form in 64 bits (tests/prompt_plain.py),
 within the tolerance that it derives."""
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -288,6 +291,73 @@ def test_streams_graph_and_reuse():
     gk.gk_prompt_plan(c.prompt, i32(c.qs), i32(c.ks), c.plan)
     c.check()
     assert gk.gk_read_device_error() == 0
+
+
+def test_most_sequences():
+    """8192 sequences of 0 to 3 tokens, the most of a call."""
+    rng = np.random.default_rng(11)
+    nq = rng.integers(0, 4, 8192)
+    Case(nq, nq + rng.integers(0, 3, 8192) * (nq > 0), Hkv=1, G=1, sinks=True, pad=5, seed=11).check()
+
+
+@pytest.mark.parametrize("G", [1, 8])
+def test_many_tokens(G):
+    """A quarter of a million tokens in one call, window layers; pieces of it against the plain form."""
+    n, W = 1 << 18, 128
+    c = Case([1000, n, 77], [1000, n, 77], Hkv=1, G=G, window=W, seed=12)
+    out, f32 = c.run()
+    assert gk.gk_read_device_error() == 0
+    for a in (0, 4096, n // 2 + 5, n - 300):
+        lo = max(0, a - W + 1)
+        q, k, v = c.q[1000 + a:1000 + a + 300], c.k[1000 + lo:1000 + a + 300], c.v[1000 + lo:1000 + a + 300]
+        want, tol = pp.attention(q, k, v, [0, 300], [0, a + 300 - lo], W)
+        assert ((f32[1000 + a:1000 + a + 300].double() - want).abs() <= tol).all()
+
+
+def test_first_calls_captured():
+    """The first calls of a process captured into a graph (their per-device setup included)."""
+    code = """
+import sys
+sys.path[:0] = ['.', 'tests']
+import torch, paged_fp8_kv_gk_gb300 as gk, prompt_plain as pp
+gk.lib()
+T, H, Hq = 90, 1, 8
+qkv = torch.randn(T, Hq + 2 * H, 64, device='cuda').to(torch.bfloat16)
+pos = torch.arange(T, dtype=torch.int32, device='cuda')
+cos, sin = torch.empty(T, 32, device='cuda'), torch.empty(T, 32, device='cuda')
+pr = dict(num_seqs=1, num_q_heads=Hq, num_kv_heads=H, head_dim=64, window=0, q_tokens=T, k_tokens=T)
+plan = gk.new_prompt_plan(pr)
+starts = torch.tensor([0, T], dtype=torch.int32, device='cuda')
+out, f32 = torch.empty(T, Hq, 64, dtype=torch.bfloat16, device='cuda'), torch.empty(T, Hq, 64, device='cuda')
+x = qkv[:, :Hq + H].contiguous()
+sh = dict(num_layers=2, batch=1, num_q_heads=Hq, num_kv_heads=H, head_dim=64, block_size=32, num_blocks=9, window=128,
+          max_blocks_full=4, max_blocks_swa=5)
+kv = gk.KvCache([torch.zeros(9, H, 32, 64, dtype=torch.uint8, device='cuda')],
+                [torch.zeros(9, H, 32, 64, dtype=torch.uint8, device='cuda')])
+sc = torch.ones(2, device='cuda') / 64
+back = torch.empty(2, 1, T, H, 64, dtype=torch.bfloat16, device='cuda')
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    gk.gk_rope_table(dict(rot_dim=64, theta=1e4), pos, cos, sin)
+    gk.gk_rope(qkv[:, :Hq + H], cos, sin, x)
+    gk.gk_kv_write(sh, x[None, :, Hq:], x[None, :, Hq:], None, None, sc, sc,
+                   pos, pos, kv, layer0=1)
+    gk.gk_kv_read(sh, kv, sc, sc, pos, pos, back[0], back[1], layer0=1)
+    gk.gk_prompt_plan(pr, starts, starts, plan)
+    gk.gk_prompt_attn(pr, plan, x[:, :Hq], x[:, Hq:], qkv[:, Hq + H:], out, f32)
+for _ in range(2):
+    g.replay()
+torch.cuda.synchronize()
+want, tol = pp.attention(x[:, :Hq], x[:, Hq:], qkv[:, Hq + H:], [0, T], [0, T])
+assert ((f32.double() - want).abs() <= tol).all()
+code8 = (x[:, Hq:].float() * 64).clamp(-448, 448).to(torch.float8_e4m3fn)
+assert torch.equal(back[0, 0], (code8.float() / 64).to(torch.bfloat16)) and torch.equal(back[0], back[1])
+assert gk.gk_read_device_error() == 0
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    run = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=root, timeout=300)
+    assert run.returncode == 0, run.stderr[-3000:]
 
 
 def test_layers_back_to_back():
