@@ -72,7 +72,7 @@ __device__ __forceinline__ uint4 quantise_e4m3x16(const float2 (&x)[8], const La
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-constexpr int kTokThreads = 128;
+constexpr int kTokThreads = 64;  // write and read of 8191 tokens 200 us; 128: 207, 256: 216
 constexpr int kWriteTok = 8;  // tokens a warp writes at a time: four lanes each
 constexpr int kReadTok = 4;   // tokens a warp reads at a time: eight lanes each
 
@@ -87,10 +87,10 @@ constexpr int kReadTok = 4;   // tokens a warp reads at a time: eight lanes each
 // pair's 16 bytes of the lower channels and the second those of the upper ones;
 // a token alone stores single bytes.
 //
-// Bound by issue slots (59 % busy, 43 % of DRAM's rate): some 400 instructions for 8
-// tokens' K and V, 64 of them the exact divisions.  8191 tokens, 36 layers (460 MB): 120
-// us; 64 to 80 registers instead of 96 and up to twice the warps change nothing.  Layer
-// scales are held a lane a layer: read by every warp from L2, they took 80 us more.
+// 8191 tokens, 36 layers (460 MB): 115 us, 4000 GB/s.  Issue slots are 58 % busy, DRAM
+// 45 %; neither bounds it alone: without rotation and with scales that divide exactly it
+// takes 6 % less, twice the warps, two layers ahead and streaming hints change nothing.
+// Layer scales are held a lane a layer: read by every warp from L2, they took 80 us more.
 __global__ void __launch_bounds__(kTokThreads)
     kv_write_kernel(const __grid_constant__ KvWriteParams p) {
   follow_stream();
@@ -291,7 +291,8 @@ static PerDevice<TokensDevice, 64> g_tokens_dev;
 // layers a CTA as leave kTokWarps warps per SM, so that a thread's slots and places
 // serve several layers of a long prompt while a short call still spreads over the
 // SMs; at most two fifths of them, so that a long call ends with a shorter slice.  Write
-// and read of 8191 tokens, 36 layers: 211 us; 223 with 128 warps or 64, 219 with 32.
+// and read of 8191 tokens, 36 layers: 207 us; 219 with 512 warps, 223 with 128 or 64 (all
+// at CTAs of 128 threads).
 constexpr int kTokWarps = 256;
 
 template <typename P>
