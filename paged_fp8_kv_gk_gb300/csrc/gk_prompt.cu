@@ -407,8 +407,8 @@ __device__ __forceinline__ void store_part(const PromptAttnParams& p, const Item
 
 // The rows row0 + the bits of `rows` of an item (in shared memory, as in the plan), by one
 // warp.
-__device__ __forceinline__ void attend_rows(const PromptAttnParams& p, const volatile int* item, int h,
-                                         uint32_t rows, int row0) {
+__device__ __forceinline__ void attend_rows(const PromptAttnParams& p, const volatile int* item,
+                                            int h, uint32_t rows, int row0) {
   const Item it = {item[0], item[1], item[2], item[3], item[4], item[5]};
   const int lane = threadIdx.x & 31;
   for (; rows; rows &= rows - 1) {
@@ -451,14 +451,17 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
       tma_prefetch_map(&p.k_map);
       tma_prefetch_map(&p.v_map);
     }
-  } else if (warp == kSoftWarps + 1) {
-    tmem_alloc<kTmemColumns>(smem_u32(&sm.tmem));
   }
+  // Tensor memory is taken once the kernel before is complete (its CTAs may still want
+  // theirs) and before a next one may launch (whose CTAs may want this one's and then
+  // wait for it).
+  wait_for_stream();
+  if (warp == kSoftWarps + 1) tmem_alloc<kTmemColumns>(smem_u32(&sm.tmem));
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
   const uint32_t tmem = sm.tmem;
-  follow_stream();
+  open_stream();
   Turn turn(p);
 
   if (warp == kSoftWarps) {

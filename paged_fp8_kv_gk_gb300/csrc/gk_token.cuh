@@ -97,13 +97,19 @@ __device__ __forceinline__ float2 rotate(float a, float b, float c, float s) {
                      __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s)));
 }
 
-// These grids are programmatic dependents of the kernel before
-// them and touch nothing until it is complete; only then may the next grid
-// launch (its CTAs or a planner's work, which waits for this grid before it
-// ends, so that nothing runs two kernels ahead).
-__device__ __forceinline__ void follow_stream() {
+// These grids are programmatic dependents of the kernel before them and touch nothing
+// until it is complete; only then may the next grid launch (its CTAs or a planner's
+// work, which waits for this grid before it ends, so that nothing runs two kernels
+// ahead).
+__device__ __forceinline__ void wait_for_stream() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void open_stream() {
   asm volatile("griddepcontrol.launch_dependents;");
+}
+__device__ __forceinline__ void follow_stream() {
+  wait_for_stream();
+  open_stream();
 }
 
 }  // namespace gk
