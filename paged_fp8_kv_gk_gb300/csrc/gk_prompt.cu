@@ -309,7 +309,9 @@ __device__ __forceinline__ float max32(const uint32_t (&s)[32]) {
 // as exact at 2^60 as at 1.  Every kCheckSteps steps, a row whose sum has passed
 // kLargest takes a new R, and O and the sum are scaled to it.  A row that overflows all
 // the same (a score some 80 above all up to the last check, or V near its type's end) is
-// computed again by attend_row, as are rows with unseen infinities or NaN.
+// computed again by attend_row, as are rows with unseen infinities or NaN: by the warp
+// that has them, behind the CTA's last item (they take seconds where there are many over
+// a hundred thousand keys, and the waits of the other warps are bounded).
 //
 // A tile and step take 512 cycles of the tensor cores and as many of the exponential
 // unit (4 a warp instruction).  Measured: 900 (8192 tokens of 64 heads in 437 us, 1260
@@ -331,6 +333,9 @@ constexpr int kTmemColumns = 256;                       // S 128, O 64, P 64
 constexpr int kTmemO = 128, kTmemP = 192;
 constexpr float kLargest = 0x1p30f;  // of a row's sum
 constexpr int kCheckSteps = 16;
+// What stands in the output (its first two channels) or in the record (its sum) of a row
+// that is to be computed again: NaN of a payload that no conversion and no sum has.
+constexpr uint32_t kAgainOut = 0x7fa57fa5u, kAgainSum = 0x7fa5a5a5u;
 
 struct PromptSmem {
   alignas(1024) uint8_t q[2][kTileBytes];
@@ -341,6 +346,7 @@ struct PromptSmem {
   uint64_t s_full, s_free, p_full, o_full;
   uint32_t tmem;
   int failed;  // a wait gave up
+  int again[kSoftWarps];  // a softmax warp has rows to compute again
   // a softmax warp's item and the one after it, as in the plan: out of its registers
   alignas(16) int item[kSoftWarps][2][8];
 };
@@ -405,20 +411,29 @@ __device__ __forceinline__ void store_part(const PromptAttnParams& p, const Item
   *reinterpret_cast<float2*>(rec + 2 * kPromptRows + r * kHeadDim + 2 * lane) = y.o;
 }
 
-// The rows row0 + the bits of `rows` of an item (in shared memory, as in the plan), by one
-// warp.
-__device__ __forceinline__ void attend_rows(const PromptAttnParams& p, const volatile int* item,
-                                            int h, uint32_t rows, int row0) {
-  const Item it = {item[0], item[1], item[2], item[3], item[4], item[5]};
-  const int lane = threadIdx.x & 31;
-  for (; rows; rows &= rows - 1) {
-    const int r = row0 + __ffs(rows) - 1, t = fdiv(r, p.fd_g), head = h * p.G + r - t * p.G;
-    const RowResult y = attend_row(p, seen_keys(p, it, t), h,
-                                   p.q + int64_t(it.q0 + t) * p.q_stride + head * kHeadDim);
-    if (it.rec < 0)
-      store_row(p, it.q0 + t, head, lane, y.m, y.l, y.o);
-    else
-      store_part(p, it, h, r, lane, y);
+// The rows of the CTA's items that a softmax warp has marked: row 32 warp + lane of each.
+__device__ __noinline__ void attend_marked(const PromptAttnParams& p, int warp) {
+  const int lane = threadIdx.x & 31, r = 32 * warp + lane, token = fdiv(r, p.fd_g);
+  for (Turn turn(p); turn.more(); turn.next()) {
+    const int i = fdiv(turn.at, p.fd_hkv), h = turn.at - i * p.Hkv;
+    const Item it = load_item(p, i);
+    if (it.k_end == it.k_lo) continue;  // no key: zeros
+    bool mine = token < it.n && r < p.tile_tokens * p.G;
+    if (mine && it.rec < 0)
+      mine = __ldcg(reinterpret_cast<const uint32_t*>(
+                 p.out + ((int64_t(it.q0) + token) * p.Hq + h * p.G + r - token * p.G) * kHeadDim)) == kAgainOut;
+    else if (mine)
+      mine = __float_as_uint(__ldcg(p.records + (int64_t(it.rec) * p.Hkv + h) * kPromptRecFloats + kPromptRows + r)) ==
+             kAgainSum;
+    for (uint32_t rows = __ballot_sync(kFull, mine); rows; rows &= rows - 1) {
+      const int x = 32 * warp + __ffs(rows) - 1, t = fdiv(x, p.fd_g), head = h * p.G + x - t * p.G;
+      const RowResult y = attend_row(p, seen_keys(p, it, t), h,
+                                     p.q + int64_t(it.q0 + t) * p.q_stride + head * kHeadDim);
+      if (it.rec < 0)
+        store_row(p, it.q0 + t, head, lane, y.m, y.l, y.o);
+      else
+        store_part(p, it, h, x, lane, y);
+    }
   }
 }
 
@@ -447,6 +462,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
       mbar_init(smem_u32(&sm.o_full), 1);
       mbar_init_fence();
       sm.failed = 0;
+      for (int s = 0; s < kSoftWarps; ++s) sm.again[s] = 0;
       tma_prefetch_map(&p.q_map);
       tma_prefetch_map(&p.k_map);
       tma_prefetch_map(&p.v_map);
@@ -737,15 +753,16 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
       for (int c = 0; c < 64; c += 2)
         size = max3_abs_nan(size, __uint_as_float(o[c >> 5][c & 31]), __uint_as_float(o[c >> 5][(c & 31) + 1]));
       // A row whose scores are numbers and whose result is not: zero times an unseen key's
-      // infinity or NaN, an overflow, or a seen key's.  It is computed again from the keys
-      // that it sees, by one warp at some ten instructions a key.
-      const uint32_t again = __ballot_sync(kFull, valid && !(size < INFINITY) && l == l);
+      // infinity or NaN, an overflow, or a seen key's.  It is marked, and computed again from
+      // the keys that it sees behind the CTA's last item.
+      const bool again = valid && !(size < INFINITY) && l == l;
+      if (__any_sync(kFull, again)) *reinterpret_cast<volatile int*>(&sm.again[warp]) = 1;
       const uint32_t q_at = items++ & 1;
       if (it.rec >= 0) {
         if (valid) {
           float* rec = p.records + (int64_t(it.rec) * p.Hkv + h) * kPromptRecFloats;
           rec[r] = l == 0.f ? -INFINITY : R;
-          rec[kPromptRows + r] = l;
+          rec[kPromptRows + r] = again ? __uint_as_float(kAgainSum) : l;
           uint4* to = reinterpret_cast<uint4*>(rec + 2 * kPromptRows + r * kHeadDim);
 #pragma unroll
           for (int c = 0; c < 16; ++c)
@@ -781,6 +798,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
             const int a = 8 * c + 2 * e;
             w[e] = f32x2_to_bf16x2(__uint_as_float(o[a >> 5][a & 31]), __uint_as_float(o[a >> 5][(a & 31) + 1]));
           }
+          if (c == 0 && again) w[0] = kAgainOut;
           *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
         const uint32_t rows = __ballot_sync(kFull, valid);
@@ -798,9 +816,9 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sm.q_free[q_at]));
-      // over what was stored: here nothing is held in registers across the call
-      if (__builtin_expect(again != 0, 0)) attend_rows(p, sm.item[warp][place], h, again, 32 * warp);
     }
+    // behind the last item, where no other warp waits for this one's next step
+    if (*reinterpret_cast<volatile int*>(&sm.again[warp]) && !gave_up(sm)) attend_marked(p, warp);
   }
   if (*reinterpret_cast<volatile int*>(&sm.failed)) {  // copies and products in flight
     if (threadIdx.x == 0) atomicOr(&g_prompt_error, GK_DEVERR_TIMEOUT);
