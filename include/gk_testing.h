@@ -7,6 +7,7 @@
 
 #include "gk.h"
 #include "gk_kv4.h"
+#include "gk_prompt.h"
 
 #ifdef __cplusplus
 extern "C" {
@@ -54,6 +55,21 @@ gk_status gk_selftest_kv4_decode_attn_split(const gk_shape *shape, const void *q
                                             const float *sinks, void *out, float *out_f32,
                                             void *workspace, size_t ws_bytes,
                                             int32_t split_tokens, void *stream);
+
+/*
+ * gk_selftest_prompt_attn_timeout -- gk_prompt_attn whose copies are left out, so that
+ * its barrier waits run out, each after wait_tries tries (1 .. 2^18; gk_prompt_attn's own
+ * is 2^18, about a second): every warp leaves its work, nothing faults or hangs,
+ * GK_DEVERR_TIMEOUT is set and no row that sees a key is written.  (Of prompts
+ * whose keys are split, rows are written with whatever the plan's room held.)
+ * Synchronises `stream` and returns the error word in *bits (cleared
+ * afterwards), with GK_ERR_DEVICE_BOUNDS when a bit is set.
+ */
+gk_status gk_selftest_prompt_attn_timeout(const gk_prompt *prompt, void *plan, size_t plan_bytes,
+                                          const void *q, int64_t q_stride, const void *k,
+                                          int64_t k_stride, const void *v, int64_t v_stride,
+                                          const float *sinks, void *out, float *out_f32,
+                                          int32_t wait_tries, void *stream, uint32_t *bits);
 
 #ifdef __cplusplus
 }

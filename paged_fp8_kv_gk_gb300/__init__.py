@@ -378,6 +378,9 @@ def lib(build_if_needed: bool = True) -> ctypes.CDLL:
             L.gk_prompt_plan.argtypes = [pp, vp, vp, vp, sz, vp]
             L.gk_prompt_attn.restype = ctypes.c_int
             L.gk_prompt_attn.argtypes = [pp, vp, sz, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp]
+            L.gk_selftest_prompt_attn_timeout.restype = ctypes.c_int
+            L.gk_selftest_prompt_attn_timeout.argtypes = [pp, vp, sz, vp, i64, vp, i64, vp, i64, vp, vp, vp,
+                                                          i32, vp, ctypes.POINTER(ctypes.c_uint32)]
             L.gk_selftest_wait_timeout.restype = ctypes.c_int
             L.gk_selftest_wait_timeout.argtypes = [ctypes.c_uint64, vp,
                                                    ctypes.POINTER(ctypes.c_uint32)]
@@ -961,12 +964,8 @@ def gk_prompt_plan(prompt, q_start, k_start, plan, stream=None) -> None:
     _check(st, "gk_prompt_plan")
 
 
-def gk_prompt_attn(prompt, plan, q, k, v, out, out_f32=None, sinks=None, stream=None) -> None:
-    """Causal attention of packed sequences, one layer, along a plan of gk_prompt_plan.
-
-    q: bf16 [q_tokens, q heads, 64]; k, v: bf16 [k_tokens, kv heads, 64]; the heads of a token are
-    contiguous, tokens may have any stride that is a multiple of 8.  out (bf16) and out_f32 are
-    contiguous; their rows outside every sequence are left as they were.  sinks: fp32 [q heads]."""
+def _prompt_args(prompt, plan, q, k, v, out, out_f32, sinks):
+    """gk_prompt_attn's arguments up to the stream."""
     torch = _torch()
     pr, dev = _as_prompt(prompt), _current_device()
     Hq, H, D = pr.num_q_heads, pr.num_kv_heads, pr.head_dim
@@ -980,13 +979,35 @@ def gk_prompt_attn(prompt, plan, q, k, v, out, out_f32=None, sinks=None, stream=
     if sinks is not None and sinks.numel() != Hq:
         raise ValueError(f"sinks must hold num_q_heads = {Hq} values")
     n = pr.q_tokens * Hq * D
-    st = lib().gk_prompt_attn(
-        ctypes.byref(pr), _ptr4(plan, torch.uint8, "plan", dev, 1), plan.numel(), q.data_ptr(),
-        strides[0], k.data_ptr(), strides[1], v.data_ptr(), strides[2],
-        _ptr4(sinks, torch.float32, "sinks", dev, 1, True),
-        _ptr4(out, torch.bfloat16, "out", dev, n),
-        _ptr4(out_f32, torch.float32, "out_f32", dev, n, True), _stream(stream, q))
+    return (ctypes.byref(pr), _ptr4(plan, torch.uint8, "plan", dev, 1), plan.numel(), q.data_ptr(),
+            strides[0], k.data_ptr(), strides[1], v.data_ptr(), strides[2],
+            _ptr4(sinks, torch.float32, "sinks", dev, 1, True),
+            _ptr4(out, torch.bfloat16, "out", dev, n),
+            _ptr4(out_f32, torch.float32, "out_f32", dev, n, True))
+
+
+def gk_prompt_attn(prompt, plan, q, k, v, out, out_f32=None, sinks=None, stream=None) -> None:
+    """Causal attention of packed sequences, one layer, along a plan of gk_prompt_plan.
+
+    q: bf16 [q_tokens, q heads, 64]; k, v: bf16 [k_tokens, kv heads, 64]; the heads of a token are
+    contiguous, tokens may have any stride that is a multiple of 8.  out (bf16) and out_f32 are
+    contiguous; their rows outside every sequence are left as they were.  sinks: fp32 [q heads]."""
+    st = lib().gk_prompt_attn(*_prompt_args(prompt, plan, q, k, v, out, out_f32, sinks),
+                              _stream(stream, q))
     _check(st, "gk_prompt_attn")
+
+
+def gk_selftest_prompt_attn_timeout(prompt, plan, q, k, v, out, out_f32=None, sinks=None,
+                                    wait_tries: int = 1 << 18, stream=None) -> int:
+    """Test hook (include/gk_testing.h): gk_prompt_attn whose waits run out; returns the device error
+    word (GK_DEVERR_TIMEOUT expected)."""
+    bits = ctypes.c_uint32(0)
+    st = lib().gk_selftest_prompt_attn_timeout(
+        *_prompt_args(prompt, plan, q, k, v, out, out_f32, sinks), int(wait_tries),
+        _stream(stream, q), ctypes.byref(bits))
+    if st not in (GK_OK, GK_ERR_DEVICE_BOUNDS):
+        raise GkError(st, "gk_selftest_prompt_attn_timeout")
+    return int(bits.value)
 
 
 def gk_selftest_wait_timeout(limit_ns: int, stream=None) -> int:

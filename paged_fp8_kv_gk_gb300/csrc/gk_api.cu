@@ -752,10 +752,11 @@ gk_status gk_prompt_plan(const gk_prompt* prompt, const int32_t* q_start, const 
                                                                                 : GK_ERR_CUDA;
 }
 
-gk_status gk_prompt_attn(const gk_prompt* prompt, void* plan, size_t plan_bytes, const void* q,
-                         int64_t q_stride, const void* k, int64_t k_stride, const void* v,
-                         int64_t v_stride, const float* sinks, void* out, float* out_f32,
-                         void* stream) {
+// hold: nothing is copied, and waits end after wait_tries tries (0: the kernel's own).
+static gk_status prompt_attention(const gk_prompt* prompt, void* plan, size_t plan_bytes,
+                                  const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                  const void* v, int64_t v_stride, const float* sinks, void* out,
+                                  float* out_f32, void* stream, bool hold, int32_t wait_tries) {
   const gk_status st = check_prompt(prompt);
   if (st != GK_OK) return st;
   const gk_prompt& s = *prompt;
@@ -802,8 +803,18 @@ gk_status gk_prompt_attn(const gk_prompt* prompt, void* plan, size_t plan_bytes,
   p.tile_tokens = L.tile_tokens;
   p.fd_g = make_fastdiv(uint32_t(p.G));
   p.fd_hkv = make_fastdiv(uint32_t(p.Hkv));
+  p.hold = hold ? 1 : 0;
+  p.wait_tries = wait_tries;
   return launch_prompt_attn(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GK_OK
                                                                                 : GK_ERR_CUDA;
+}
+
+gk_status gk_prompt_attn(const gk_prompt* prompt, void* plan, size_t plan_bytes, const void* q,
+                         int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                         int64_t v_stride, const float* sinks, void* out, float* out_f32,
+                         void* stream) {
+  return prompt_attention(prompt, plan, plan_bytes, q, q_stride, k, k_stride, v, v_stride, sinks, out,
+                          out_f32, stream, false, 0);
 }
 
 gk_status gk_kv_budget(uint64_t total_bytes, uint64_t used_bytes, double gmu, double cap_fraction,
@@ -972,6 +983,17 @@ gk_status gk_selftest_wait_timeout(uint64_t limit_ns, void* stream, uint32_t* bi
   if (launch_wait_timeout(limit_ns, static_cast<cudaStream_t>(stream)) != cudaSuccess)
     return GK_ERR_CUDA;
   return gk_read_device_error(stream, bits, 1);
+}
+
+gk_status gk_selftest_prompt_attn_timeout(const gk_prompt* prompt, void* plan, size_t plan_bytes,
+                                          const void* q, int64_t q_stride, const void* k,
+                                          int64_t k_stride, const void* v, int64_t v_stride,
+                                          const float* sinks, void* out, float* out_f32,
+                                          int32_t wait_tries, void* stream, uint32_t* bits) {
+  if (!bits || wait_tries < 1 || wait_tries > 1 << 18) return GK_ERR_INVALID_ARG;
+  const gk_status st = prompt_attention(prompt, plan, plan_bytes, q, q_stride, k, k_stride, v, v_stride,
+                                        sinks, out, out_f32, stream, true, wait_tries);
+  return st == GK_OK ? gk_read_device_error(stream, bits, 1) : st;
 }
 
 gk_status gk_read_device_error(void* stream, uint32_t* bits, int clear) {

@@ -284,6 +284,8 @@ struct PromptAttnParams {
   int64_t q_stride, k_stride, v_stride;  // elements
   int64_t max_items, max_recs;
   int Hq, Hkv, G, W, q_tokens, k_tokens, tile_tokens;
+  int wait_tries;  // of a barrier wait (0: the launcher's)
+  int hold;        // a test's: nothing is copied, so that the waits run out
   FastDiv fd_g, fd_hkv;
 };
 

@@ -381,24 +381,26 @@ __device__ __forceinline__ int item_steps(const Item& it) {
   return (it.k_end - it.k_lo + kPromptKeys - 1) / kPromptKeys;
 }
 
-// Waits for a barrier's phase.  After 4 kWaitRounds tries (10 ms and more; waits here
-// last a microsecond) the CTA is marked as failed and goes on, so that its warps stay
-// together; from the next item on it does nothing, and it ends once its copies have had
-// time to land.  No clock, no vote, no call here, and no count between the tries: a
-// warp that polls shares its scheduler with the softmax, and each of these cost 4 to 12 %.
-constexpr int kWaitRounds = 1 << 18;
-__device__ __forceinline__ void prompt_wait(PromptSmem& sm, uint64_t& bar, uint32_t parity) {
+// Waits for a barrier's phase; waits here last a microsecond.  False after p.wait_tries
+// tries in vain (a try sleeps some 3.7 us: 2^18 take a second), and soon after another
+// warp's wait has ended so: the warp then leaves its work where it is, so that nothing is
+// copied, issued or arrived at out of turn, and the CTA ends once its copies and products
+// have had time to land.  All lanes of a warp try with one instruction and leave
+// together.  No clock, vote or call between the tries: a warp that polls shares its
+// scheduler with the softmax.  (Against waits whose end nobody looked at, and whose warps went
+// on: 8192 tokens 442 -> 445 us, window of 2 x 8191 108.3 -> 107, 8192 over 65536 keys
+// 6.21 -> 6.29 ms.)
+constexpr int kWaitTries = 1 << 18;
+__device__ __forceinline__ bool prompt_wait(const PromptAttnParams& p, PromptSmem& sm, uint64_t& bar,
+                                            uint32_t parity) {
   const uint32_t at = smem_u32(&bar);
+  int n = 0;
 #pragma unroll 1
-  for (int n = 0; n < kWaitRounds; ++n) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (mbar_try_wait(at, parity)) return;
-  }
+  do {
+    if (mbar_try_wait(at, parity)) return true;
+  } while (++n < p.wait_tries && !*reinterpret_cast<volatile int*>(&sm.failed));
   *reinterpret_cast<volatile int*>(&sm.failed) = 1;
-}
-__device__ __forceinline__ bool gave_up(PromptSmem& sm) {
-  return __any_sync(kFull, *reinterpret_cast<volatile int*>(&sm.failed));
+  return false;
 }
 
 __device__ __forceinline__ void store_part(const PromptAttnParams& p, const Item& it, int h, int r,
@@ -486,32 +488,34 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
     // the first round finds the places free
     auto load = [&](uint64_t& free, uint64_t& full, uint32_t parity, uint8_t* to, const CUtensorMap* map,
                     uint32_t bytes, int head, int token) {
-      prompt_wait(sm, free, parity ^ 1);
+      if (!prompt_wait(p, sm, free, parity ^ 1)) return false;
       if (one) {
         mbar_arrive_expect_tx(smem_u32(&full), bytes);
         tma_load_3d(smem_u32(to), map, 0, head, token, smem_u32(&full));
       }
       __syncwarp();
+      return true;
     };
-    for (; turn.more() && !gave_up(sm); turn.next()) {
+    bool ok = !p.hold;
+    for (; ok && turn.more(); turn.next()) {
       const int i = fdiv(turn.at, p.fd_hkv), h = turn.at - i * p.Hkv;
       const Item it = load_item(p, i);
       const int steps = item_steps(it), k_lo = it.k_lo;
       if (steps == 0) continue;
-      load(sm.q_free[q.at], sm.q_full[q.at], q.parity, sm.q[q.at], &p.q_map,
-           uint32_t(p.tile_tokens * p.G) * kHeadDim * 2, h * p.G, it.q0);
+      ok = load(sm.q_free[q.at], sm.q_full[q.at], q.parity, sm.q[q.at], &p.q_map,
+                uint32_t(p.tile_tokens * p.G) * kHeadDim * 2, h * p.G, it.q0);
       q.next<2>();
       // K a step ahead of V
       auto load_k = [&](int j) {
-        load(sm.k_free[k.at], sm.k_full[k.at], k.parity, sm.k[k.at], &p.k_map, kTileBytes, h,
-             k_lo + j * kPromptKeys);
+        ok = ok && load(sm.k_free[k.at], sm.k_full[k.at], k.parity, sm.k[k.at], &p.k_map, kTileBytes, h,
+                        k_lo + j * kPromptKeys);
         k.next<kKStages>();
       };
       load_k(0);
-      for (int j = 0; j < steps; ++j) {
+      for (int j = 0; ok && j < steps; ++j) {
         if (j + 1 < steps) load_k(j + 1);
-        load(sm.v_free[v.at], sm.v_full[v.at], v.parity, sm.v[v.at], &p.v_map, kTileBytes, h,
-             k_lo + j * kPromptKeys);
+        ok = ok && load(sm.v_free[v.at], sm.v_full[v.at], v.parity, sm.v[v.at], &p.v_map, kTileBytes, h,
+                        k_lo + j * kPromptKeys);
         v.next<kVStages>();
       }
     }
@@ -527,9 +531,9 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
     uint32_t s_parity = 1, p_parity = 0;  // S is free at first
     // S of the next step in turn, `left` steps of its item counting itself
     auto scores = [&](int left, bool first) {
-      if (first) prompt_wait(sm, sm.q_full[q.at], q.parity);
-      prompt_wait(sm, sm.k_full[k.at], k.parity);
-      prompt_wait(sm, sm.s_free, s_parity);
+      if ((first && !prompt_wait(p, sm, sm.q_full[q.at], q.parity)) ||
+          !prompt_wait(p, sm, sm.k_full[k.at], k.parity) || !prompt_wait(p, sm, sm.s_free, s_parity))
+        return false;
       s_parity ^= 1;
       tmem_fence_after();
       const uint64_t qd = qd0 + uint64_t(q.at * (kTileBytes >> 4)), kd = kd0 + uint64_t(k.at * (kTileBytes >> 4));
@@ -543,6 +547,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
       __syncwarp();
       k.next<kKStages>();
       if (left == 1) q.next<2>();
+      return true;
     };
     // keys of the next item that has any; 0: no more
     auto next_item = [&]() -> int {
@@ -555,17 +560,17 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
     };
     auto steps_of = [](int keys) { return (keys + kPromptKeys - 1) / kPromptKeys; };
     int next = next_item();
-    if (next) scores(steps_of(next), true);
-    while (next && !gave_up(sm)) {
+    bool ok = next == 0 || scores(steps_of(next), true);
+    while (ok && next) {
       const int n = next, steps = steps_of(n);
       next = next_item();  // its first S follows this one's last
       for (int j = 0; j < steps; ++j) {
         if (j + 1 < steps)
-          scores(steps - j - 1, false);
+          ok = scores(steps - j - 1, false);
         else if (next)
-          scores(steps_of(next), true);
-        prompt_wait(sm, sm.v_full[v.at], v.parity);
-        prompt_wait(sm, sm.p_full, p_parity);
+          ok = scores(steps_of(next), true);
+        ok = ok && prompt_wait(p, sm, sm.v_full[v.at], v.parity) && prompt_wait(p, sm, sm.p_full, p_parity);
+        if (!ok) break;
         p_parity ^= 1;
         tmem_fence_after();
         const uint64_t vd = vd0 + uint64_t(v.at * (kTileBytes >> 4));
@@ -614,9 +619,9 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
       const int whole_end = max(min(at_first.diag + 1, at_first.k_end) - at_first.k_lo, 0) / kPromptKeys;
       float R = 0.f;
       float2 sum = make_float2(0.f, 0.f);
-      auto step = [&](int j, auto whole) {
+      auto step = [&](int j, auto whole) -> bool {
         constexpr bool kWhole = decltype(whole)::value;
-        prompt_wait(sm, sm.s_full, count & 1);
+        if (!prompt_wait(p, sm, sm.s_full, count & 1)) return false;
         tmem_fence_after();
         uint32_t s[4][32];
 #pragma unroll
@@ -661,17 +666,18 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
         };
         // P of the step before has been used: waited for as late as possible (before the
         // exponentials, it adds the product's time to every step's)
-        auto p_free = [&]() {
+        auto p_free = [&]() -> bool {
           if (kWhole || j > 0) {
-            prompt_wait(sm, sm.o_full, (count - 1) & 1);
+            if (!prompt_wait(p, sm, sm.o_full, (count - 1) & 1)) return false;
             tmem_fence_after();
           }
+          return true;
         };
         if (kWhole || keys > 32) {
           uint32_t pr[2][32];
 #pragma unroll
           for (int e = 0; e < 64; ++e) pr[e >> 5][e & 31] = probabilities(s[e >> 4][2 * e & 31], s[e >> 4][(2 * e & 31) + 1]);
-          p_free();
+          if (!p_free()) return false;
           tmem_st32(lanes + kTmemP, pr[0]);
           tmem_st32(lanes + kTmemP + 32, pr[1]);
         } else {  // the last few keys of a window or a prompt; the product takes no more
@@ -681,13 +687,13 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
             pr[e] = probabilities(s[0][2 * e], s[0][2 * e + 1]);
             pr[16 + e] = 0;
           }
-          p_free();
+          if (!p_free()) return false;
           tmem_st32(lanes + kTmemP, pr);
         }
         if (!kWhole && keys < kPromptKeys) {
           // keys behind the item's, up to the 16 that a product takes: whatever V is there
           // (other sequences, padding), zero times it must be zero
-          prompt_wait(sm, sm.v_full[count % kVStages], count / kVStages & 1);
+          if (!prompt_wait(p, sm, sm.v_full[count % kVStages], count / kVStages & 1)) return false;
           if (r >= keys && r < keys + 15) {
             uint4* row = reinterpret_cast<uint4*>(sm.v[count % kVStages] + r * (kHeadDim * 2));
 #pragma unroll
@@ -700,17 +706,19 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sm.p_full));
         ++count;
+        return true;
       };
-      step(0, std::false_type());
-      for (int j = 1; j < steps;) {
+      bool ok = step(0, std::false_type());
+      for (int j = 1; ok && j < steps;) {
         // runs of whole steps in a loop of their own, without the rare cases' code
         const int end = min(whole_end, j + kCheckSteps);
         if (j >= whole_lo && j < end) {
-          do step(j, std::true_type()); while (++j < end);
+          do ok = step(j, std::true_type()); while (ok && ++j < end);
         } else {
-          step(j, std::false_type());
+          ok = step(j, std::false_type());
           ++j;
         }
+        if (!ok) break;
         const float total = sum.x + sum.y;
         if (j < steps && __any_sync(kFull, total > kLargest)) {
           // at most by 2^100, a normal float
@@ -720,7 +728,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
           R = to;
           sum.x *= f;
           sum.y *= f;
-          prompt_wait(sm, sm.o_full, (count - 1) & 1);
+          ok = prompt_wait(p, sm, sm.o_full, (count - 1) & 1);
+          if (!ok) break;
           tmem_fence_after();
 #pragma unroll 1
           for (int c = 0; c < kHeadDim; c += 32) {
@@ -735,7 +744,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
           tmem_wait_st();
         }
       }
-      prompt_wait(sm, sm.o_full, (count - 1) & 1);
+      if (!ok || !prompt_wait(p, sm, sm.o_full, (count - 1) & 1)) break;
       tmem_fence_after();
       uint32_t o[2][32];
       tmem_ld32(lanes + kTmemO, o[0]);
@@ -744,7 +753,6 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
       tmem_landed(o[0]);
       tmem_landed(o[1]);
       tmem_fence_before();  // the next item's P lets its first product write here
-      if (gave_up(sm)) break;
       const Item it = item();
       const bool valid = token < it.n && r < p.tile_tokens * p.G;
       const float l = sum.x + sum.y;
@@ -818,15 +826,17 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
       if (lane == 0) mbar_arrive(smem_u32(&sm.q_free[q_at]));
     }
     // behind the last item, where no other warp waits for this one's next step
-    if (*reinterpret_cast<volatile int*>(&sm.again[warp]) && !gave_up(sm)) attend_marked(p, warp);
+    if (*reinterpret_cast<volatile int*>(&sm.again[warp]) &&
+        !__any_sync(kFull, *reinterpret_cast<volatile int*>(&sm.failed)))
+      attend_marked(p, warp);
   }
   if (*reinterpret_cast<volatile int*>(&sm.failed)) {  // copies and products in flight
-    if (threadIdx.x == 0) atomicOr(&g_prompt_error, GK_DEVERR_TIMEOUT);
     const uint64_t since = globaltimer_ns();
     while (globaltimer_ns() - since < 10000000) __nanosleep(1000);
   }
   tmem_fence_before();
   __syncthreads();
+  if (sm.failed && threadIdx.x == 0) atomicOr(&g_prompt_error, GK_DEVERR_TIMEOUT);
   __syncwarp();
   if (warp == kSoftWarps + 1) tmem_dealloc<kTmemColumns>(tmem);
 }
@@ -941,6 +951,7 @@ cudaError_t launch_prompt_attn(PromptAttnParams& p, cudaStream_t st) {
     ok = ok && encode_map(*d, &p.k_map, p.k, p.k_tokens, p.Hkv, p.k_stride, kPromptKeys, 1) &&
          encode_map(*d, &p.v_map, p.v, p.k_tokens, p.Hkv, p.v_stride, kPromptKeys, 1);
   if (!ok) return cudaErrorInvalidValue;
+  if (p.wait_tries == 0) p.wait_tries = kWaitTries;
   const int64_t grid = std::min(p.max_items * p.Hkv, int64_t(2) * d->sms);
   e = launch(prompt_attn_kernel, p, unsigned(grid), kAttnThreads, sizeof(PromptSmem), st);
   if (e != cudaSuccess || p.max_recs == 0) return e;
