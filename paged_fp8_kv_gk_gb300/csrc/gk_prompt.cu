@@ -265,11 +265,39 @@ __device__ __noinline__ RowResult attend_row(const PromptAttnParams& p, int2 key
   return r;
 }
 
+// A sum's exponent, and a power of two: normal floats, and so are their inverses.
+__device__ __forceinline__ int exponent_of(float l) {
+  return min(max(int(__float_as_uint(l) >> 23 & 255u) - 127, -126), 126);
+}
+__device__ __forceinline__ float two_to(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }
+
+// A head's sink against sums taken with the reference m (log2 units); -inf without sinks.
+__device__ __forceinline__ float sink_of(const PromptAttnParams& p, int head, float m) {
+  return p.sinks ? __ldg(p.sinks + head) * 1.4426950408889634f - m : -INFINITY;
+}
+
+// What sums are multiplied by, first by `off` and then by the result: 1 / (l + 2^d).  The
+// reference need not be the row's maximum, so l may be anything up to a float's end: where
+// it or the sink is large its exponent comes off first (in `off`, else 1), so that a sink
+// 2^126 times the reference has its part, and no more.  Zero where the sink is 2^126 times l.
+__device__ __forceinline__ float sum_scale(float l, float d, float& off) {
+  const int k = l > 0x1p60f || d > 60.f ? exponent_of(l) : 0;
+  off = two_to(-k);
+  l *= off;
+  d -= float(k);
+  const float e = ex2(-fabsf(d));
+  return d > 0.f ? e * __frcp_rn(fmaf(l, e, 1.f)) : __frcp_rn(l + e);
+}
+
 // A finished row's two channels of a lane; l is 0 where the row sees no key.
 __device__ __forceinline__ void store_row(const PromptAttnParams& p, int64_t token, int head, int lane,
-                                          float m, float l, float2 o) {
-  const float f = l == 0.f ? 0.f : out_scale(l, m, p.sinks ? p.sinks + head : nullptr, 1.f);
-  const float2 y = l == 0.f ? make_float2(0.f, 0.f) : make_float2(o.x * f, o.y * f);
+                                          float sink, float l, float2 o) {
+  float2 y = make_float2(0.f, 0.f);
+  if (l != 0.f) {
+    float off;
+    const float f = sum_scale(l, sink, off);
+    y = make_float2(o.x * off * f, o.y * off * f);
+  }
   const int64_t at = (token * p.Hq + head) * kHeadDim + 2 * lane;
   *reinterpret_cast<uint32_t*>(p.out + at) = f32x2_to_bf16x2(y.x, y.y);
   if (p.out_f32) *reinterpret_cast<float2*>(p.out_f32 + at) = y;
@@ -432,7 +460,7 @@ __device__ __noinline__ void attend_marked(const PromptAttnParams& p, int warp) 
       const RowResult y = attend_row(p, seen_keys(p, it, t), h,
                                      p.q + int64_t(it.q0 + t) * p.q_stride + head * kHeadDim);
       if (it.rec < 0)
-        store_row(p, it.q0 + t, head, lane, y.m, y.l, y.o);
+        store_row(p, it.q0 + t, head, lane, sink_of(p, head, y.m), y.l, y.o);
       else
         store_part(p, it, h, x, lane, y);
     }
@@ -610,7 +638,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
       if (steps == 0) {  // no key: zeros (such a tile is not split)
         for (int x = warp; x < at_first.n * p.G; x += kSoftWarps) {
           const int t = fdiv(x, p.fd_g);
-          store_row(p, at_first.q0 + t, h * p.G + x - t * p.G, lane, 0.f, 0.f, make_float2(0.f, 0.f));
+          store_row(p, at_first.q0 + t, h * p.G + x - t * p.G, lane, -INFINITY, 0.f,
+                    make_float2(0.f, 0.f));
         }
         continue;
       }
@@ -760,10 +789,14 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
 #pragma unroll
       for (int c = 0; c < 64; c += 2)
         size = max3_abs_nan(size, __uint_as_float(o[c >> 5][c & 31]), __uint_as_float(o[c >> 5][(c & 31) + 1]));
+      const int head = h * p.G + r - token * p.G;
+      float off = 1.f, f = 0.f;
+      if (l != 0.f && valid) f = sum_scale(l, sink_of(p, head, R), off) * off;
       // A row whose scores are numbers and whose result is not: zero times an unseen key's
-      // infinity or NaN, an overflow, or a seen key's.  It is marked, and computed again from
-      // the keys that it sees behind the CTA's last item.
-      const bool again = valid && !(size < INFINITY) && l == l;
+      // infinity or NaN, an overflow, or a seen key's; and one whose sum and sink are so
+      // large that a float is not enough for the factor.  It is marked, and computed again
+      // from the keys that it sees behind the CTA's last item.
+      const bool again = valid && ((!(size < INFINITY) && l == l) || (l > 0x1p60f && f < 0x1p-110f));
       if (__any_sync(kFull, again)) *reinterpret_cast<volatile int*>(&sm.again[warp]) = 1;
       const uint32_t q_at = items++ & 1;
       if (it.rec >= 0) {
@@ -778,8 +811,6 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
                                o[c >> 3][4 * (c & 7) + 3]);
         }
       } else {
-        const int head = h * p.G + r - token * p.G;
-        const float f = l == 0.f || !valid ? 0.f : out_scale(l, R, p.sinks ? p.sinks + head : nullptr, 1.f);
 #pragma unroll
         for (int c = 0; c < 64; ++c) o[c >> 5][c & 31] = __float_as_uint(__uint_as_float(o[c >> 5][c & 31]) * f);
         if (__any_sync(kFull, l == 0.f)) {  // no key seen: zeros, whatever the product made of them
@@ -857,22 +888,34 @@ __global__ void __launch_bounds__(kRowThreads)
     const int4 sp = __ldcg(p.splits + y / p.Hkv);
     if (r >= sp.y * p.G) continue;
     auto rec = [&](int i) { return p.records + (int64_t(sp.z + i) * p.Hkv + h) * kPromptRecFloats; };
+    // The parts' references are not their maxima: a sum's exponent counts with it, and comes
+    // off the sums before they are joined (as an integer: references may be so large
+    // that it would be lost in them).
     float m = -INFINITY;
-    for (int i = 0; i < sp.w; ++i) m = fmaxf(m, __ldcg(rec(i) + r));
-    const float ref = m == -INFINITY ? 0.f : m;
+    int e = 0;
+    for (int i = 0; i < sp.w; ++i) {
+      const float lc = __ldcg(rec(i) + kPromptRows + r), mc = __ldcg(rec(i) + r);
+      const int ec = exponent_of(lc);
+      if (lc != 0.f && !(mc + float(ec) <= m + float(e))) {
+        m = mc;
+        e = ec;
+      }
+    }
     float l = 0.f;
     float2 o = make_float2(0.f, 0.f);
     for (int i = 0; i < sp.w; ++i) {
       const float* c = rec(i);
       const float lc = __ldcg(c + kPromptRows + r);
       if (lc == 0.f) continue;  // none of its keys is seen
-      const float f = ex2(__ldcg(c + r) - ref);
+      const int ec = exponent_of(lc);
+      const float f = ex2((__ldcg(c + r) - m) + float(ec - e)), off = two_to(-ec);
       const float2 oc = ldg_cg_f2(c + 2 * kPromptRows + r * kHeadDim + 2 * lane);
-      l = fmaf(lc, f, l);
-      o.x = fmaf(oc.x, f, o.x);
-      o.y = fmaf(oc.y, f, o.y);
+      l = fmaf(lc * off, f, l);
+      o.x = fmaf(oc.x * off, f, o.x);
+      o.y = fmaf(oc.y * off, f, o.y);
     }
-    store_row(p, sp.x + r / p.G, h * p.G + r % p.G, lane, m, l, o);
+    const int head = h * p.G + r % p.G;
+    store_row(p, sp.x + r / p.G, head, lane, sink_of(p, head, m) - float(e), l, o);
   }
 }
 
