@@ -213,7 +213,7 @@ __device__ __forceinline__ int2 seen_keys(const PromptAttnParams& p, const Item&
 
 // Result of one row in one warp: lane l has o of channels 2l, 2l + 1.
 struct RowResult {
-  float m, l;  // reference maximum (log2 units) and sum
+  float m, l;  // reference maximum (log2 units; -inf: every score is -inf or NaN) and sum
   float2 o;
 };
 
@@ -289,11 +289,12 @@ __device__ __forceinline__ float sum_scale(float l, float d, float& off) {
   return d > 0.f ? e * __frcp_rn(fmaf(l, e, 1.f)) : __frcp_rn(l + e);
 }
 
-// A finished row's two channels of a lane; l is 0 where the row sees no key.
+// A finished row's two channels of a lane; zeros where the row sees no key.  (A row that sees
+// keys of no weight has l = 0: NaN, or the sink's all.)
 __device__ __forceinline__ void store_row(const PromptAttnParams& p, int64_t token, int head, int lane,
-                                          float sink, float l, float2 o) {
+                                          bool sees, float sink, float l, float2 o) {
   float2 y = make_float2(0.f, 0.f);
-  if (l != 0.f) {
+  if (sees) {
     float off;
     const float f = sum_scale(l, sink, off);
     y = make_float2(o.x * off * f, o.y * off * f);
@@ -361,6 +362,8 @@ constexpr int kTmemColumns = 256;                       // S 128, O 64, P 64
 constexpr int kTmemO = 128, kTmemP = 192;
 constexpr float kLargest = 0x1p30f;  // of a row's sum
 constexpr int kCheckSteps = 16;
+// The reference of a part whose row sees keys, all of no weight; -inf: it sees none of them.
+constexpr float kNoWeight = -3e38f;
 // What stands in the output (its first two channels) or in the record (its sum) of a row
 // that is to be computed again: NaN of a payload that no conversion and no sum has.
 constexpr uint32_t kAgainOut = 0x7fa57fa5u, kAgainSum = 0x7fa5a5a5u;
@@ -435,7 +438,7 @@ __device__ __forceinline__ void store_part(const PromptAttnParams& p, const Item
                                            int lane, const RowResult& y) {
   float* rec = p.records + (int64_t(it.rec) * p.Hkv + h) * kPromptRecFloats;
   if (lane == 0) {
-    rec[r] = y.m;
+    rec[r] = y.l == 0.f ? kNoWeight : y.m;
     rec[kPromptRows + r] = y.l;
   }
   *reinterpret_cast<float2*>(rec + 2 * kPromptRows + r * kHeadDim + 2 * lane) = y.o;
@@ -460,7 +463,7 @@ __device__ __noinline__ void attend_marked(const PromptAttnParams& p, int warp) 
       const RowResult y = attend_row(p, seen_keys(p, it, t), h,
                                      p.q + int64_t(it.q0 + t) * p.q_stride + head * kHeadDim);
       if (it.rec < 0)
-        store_row(p, it.q0 + t, head, lane, sink_of(p, head, y.m), y.l, y.o);
+        store_row(p, it.q0 + t, head, lane, true, sink_of(p, head, y.m), y.l, y.o);
       else
         store_part(p, it, h, x, lane, y);
     }
@@ -638,7 +641,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
       if (steps == 0) {  // no key: zeros (such a tile is not split)
         for (int x = warp; x < at_first.n * p.G; x += kSoftWarps) {
           const int t = fdiv(x, p.fd_g);
-          store_row(p, at_first.q0 + t, h * p.G + x - t * p.G, lane, -INFINITY, 0.f,
+          store_row(p, at_first.q0 + t, h * p.G + x - t * p.G, lane, false, 0.f, 0.f,
                     make_float2(0.f, 0.f));
         }
         continue;
@@ -793,10 +796,15 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
       float off = 1.f, f = 0.f;
       if (l != 0.f && valid) f = sum_scale(l, sink_of(p, head, R), off) * off;
       // A row whose scores are numbers and whose result is not: zero times an unseen key's
-      // infinity or NaN, an overflow, or a seen key's; and one whose sum and sink are so
-      // large that a float is not enough for the factor.  It is marked, and computed again
-      // from the keys that it sees behind the CTA's last item.
-      const bool again = valid && ((!(size < INFINITY) && l == l) || (l > 0x1p60f && f < 0x1p-110f));
+      // infinity or NaN, an overflow, or a seen key's; one whose sum and sink are so large
+      // that a float is not enough for the factor; and one without a reference (scores of
+      // -inf in its first step; the others' sum is anything then).  It is marked, and
+      // computed again from the keys that it sees behind the CTA's last item.
+      bool again = valid && ((!(size < INFINITY) && l == l) || (l > 0x1p60f && f < 0x1p-110f));
+      if (valid && l < 0.5f) {
+        const int2 seen = seen_keys(p, it, token);
+        again = again || seen.x < seen.y;
+      }
       if (__any_sync(kFull, again)) *reinterpret_cast<volatile int*>(&sm.again[warp]) = 1;
       const uint32_t q_at = items++ & 1;
       if (it.rec >= 0) {
@@ -893,9 +901,11 @@ __global__ void __launch_bounds__(kRowThreads)
     // that it would be lost in them).
     float m = -INFINITY;
     int e = 0;
+    bool sees = false;
     for (int i = 0; i < sp.w; ++i) {
       const float lc = __ldcg(rec(i) + kPromptRows + r), mc = __ldcg(rec(i) + r);
       const int ec = exponent_of(lc);
+      sees = sees || lc != 0.f || mc != -INFINITY;
       if (lc != 0.f && !(mc + float(ec) <= m + float(e))) {
         m = mc;
         e = ec;
@@ -906,7 +916,7 @@ __global__ void __launch_bounds__(kRowThreads)
     for (int i = 0; i < sp.w; ++i) {
       const float* c = rec(i);
       const float lc = __ldcg(c + kPromptRows + r);
-      if (lc == 0.f) continue;  // none of its keys is seen
+      if (lc == 0.f) continue;  // it sees none of the part's keys, or none of weight
       const int ec = exponent_of(lc);
       const float f = ex2((__ldcg(c + r) - m) + float(ec - e)), off = two_to(-ec);
       const float2 oc = ldg_cg_f2(c + 2 * kPromptRows + r * kHeadDim + 2 * lane);
@@ -915,7 +925,7 @@ __global__ void __launch_bounds__(kRowThreads)
       o.y = fmaf(oc.y * off, f, o.y);
     }
     const int head = h * p.G + r % p.G;
-    store_row(p, sp.x + r / p.G, head, lane, sink_of(p, head, m) - float(e), l, o);
+    store_row(p, sp.x + r / p.G, head, lane, sees, sink_of(p, head, m) - float(e), l, o);
   }
 }
 
