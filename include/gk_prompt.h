@@ -188,7 +188,9 @@ gk_status gk_prompt_plan(const gk_prompt *prompt, const int32_t *q_start, const 
  *   k, v     bf16, the same with k_stride and v_stride (slices of a fused
  *            projection, gk_kv_read's outputs)
  *   sinks    fp32 [Hq] or NULL
- *   out      bf16 [q_tokens, Hq, 64];  out_f32  fp32, the same, or NULL
+ *   out      bf16 [q_tokens, Hq, 64];  out_f32  fp32, the same, or NULL; they may
+ *            overlap neither each other nor q, k, v, sinks or the plan
+ *            (GK_ERR_INVALID_ARG): some rows are computed after others are written
  * The plan is read, and its room for parts written: calls that may overlap on the
  * device (other streams, two captured graphs) need a plan each.
  * q_tokens == 0 enqueues nothing.

@@ -991,7 +991,8 @@ def gk_prompt_attn(prompt, plan, q, k, v, out, out_f32=None, sinks=None, stream=
 
     q: bf16 [q_tokens, q heads, 64]; k, v: bf16 [k_tokens, kv heads, 64]; the heads of a token are
     contiguous, tokens may have any stride that is a multiple of 8.  out (bf16) and out_f32 are
-    contiguous; their rows outside every sequence are left as they were.  sinks: fp32 [q heads]."""
+    contiguous; their rows outside every sequence are left as they were; they may not overlap the other
+    tensors.  sinks: fp32 [q heads]."""
     st = lib().gk_prompt_attn(*_prompt_args(prompt, plan, q, k, v, out, out_f32, sinks),
                               _stream(stream, q))
     _check(st, "gk_prompt_attn")

@@ -752,6 +752,18 @@ gk_status gk_prompt_plan(const gk_prompt* prompt, const int32_t* q_start, const 
                                                                                 : GK_ERR_CUDA;
 }
 
+// Whether [a, a + bytes) meets one of n rows of row_bytes, `stride` bytes apart.
+static bool meets_rows(const void* a, int64_t bytes, const void* rows, int64_t n, int64_t stride,
+                       int64_t row_bytes) {
+  if (!a || !rows || n < 1) return false;
+  const int64_t d = int64_t(reinterpret_cast<uintptr_t>(a)) - int64_t(reinterpret_cast<uintptr_t>(rows));
+  // row t meets it where t stride is above d - row_bytes and below d + bytes
+  if (d + bytes <= 0) return false;
+  if (n == 1 || stride <= 0) return d < row_bytes;
+  const int64_t first = d < row_bytes ? 0 : (d - row_bytes) / stride + 1;
+  return first < n && first * stride < d + bytes;
+}
+
 // hold: nothing is copied, and waits end after wait_tries tries (0: the kernel's own).
 static gk_status prompt_attention(const gk_prompt* prompt, void* plan, size_t plan_bytes,
                                   const void* q, int64_t q_stride, const void* k, int64_t k_stride,
@@ -776,6 +788,19 @@ static gk_status prompt_attention(const gk_prompt* prompt, void* plan, size_t pl
   const PromptLayout L = prompt_layout(s);
   if (!plan || (reinterpret_cast<uintptr_t>(plan) & 255u) || plan_bytes < L.total)
     return GK_ERR_WORKSPACE;
+  // some rows are computed after others are written
+  const int64_t bytes = s.q_tokens * q_row * 2;
+  for (int i = 0; i < 2; ++i) {
+    const void* o = i ? static_cast<const void*>(out_f32) : out;
+    const int64_t n = i ? 2 * bytes : bytes;
+    if (meets_rows(o, n, q, s.q_tokens, q_stride * 2, q_row * 2) ||
+        meets_rows(o, n, k, s.k_tokens, k_stride * 2, k_row * 2) ||
+        meets_rows(o, n, v, s.k_tokens, v_stride * 2, k_row * 2) ||
+        meets_rows(o, n, sinks, 1, 0, int64_t(s.num_q_heads) * 4) ||
+        meets_rows(o, n, plan, 1, 0, int64_t(L.total)))
+      return GK_ERR_INVALID_ARG;
+  }
+  if (meets_rows(out, bytes, out_f32, 1, 0, 2 * bytes)) return GK_ERR_INVALID_ARG;
   uint8_t* ws = static_cast<uint8_t*>(plan);
   PromptAttnParams p;
   memset(&p, 0, sizeof(p));

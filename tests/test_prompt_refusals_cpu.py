@@ -17,3 +17,43 @@ def test_timeout_hook_arguments():
         a = list(args)
         a[i] = v
         assert L.gk_selftest_prompt_attn_timeout(*a) == want, i
+
+
+@no_device
+def test_outputs_that_overlap_inputs():
+    """Refused however little they share; neighbours, and outputs between the rows of an input, are not
+    (they get as far as the missing device)."""
+    L, G = gk.lib(), gk.GK_ERR_CUDA
+    T, Hq, H = 5, 16, 2
+    pr = prompt(num_seqs=1, num_q_heads=Hq, num_kv_heads=H, q_tokens=T, k_tokens=T)
+    plan, at = 1 << 30, 1 << 24
+    n = gk.gk_prompt_plan_bytes(pr)
+    row, stride = Hq * 128, 2 * 65536            # q's bytes; rows far apart
+
+    def call(q=at, k=at + (1 << 22), v=at + (2 << 22), out=at + (3 << 22), f32=at + (4 << 22), sinks=None, plan=plan,
+             pr=pr, q_stride=stride // 2, kv_stride=4096):
+        return L.gk_prompt_attn(ctypes.byref(pr), plan, n, q, q_stride, k, kv_stride, v, kv_stride, sinks, out, f32, None)
+    assert call() == G and call(f32=None) == G
+    size = T * row                               # out's bytes; f32 has twice as many
+    for t in range(T):
+        q_row = at + t * stride
+        for out, want in ((q_row, 1), (q_row + row, G), (q_row + row - 16, 1), (q_row - size, G), (q_row - size + 16, 1),
+                          (q_row + 2 * row, G)):
+            assert call(out=out, f32=None) == want, (t, out - q_row)
+            assert call(f32=out, out=at + (5 << 22)) == (1 if q_row - 2 * size < out < q_row + row else G), (t, out - q_row)
+    assert call(out=at + (T - 1) * stride + row) == G and call(out=at + T * stride) == G
+    for name, first in (("k", at + (1 << 22)), ("v", at + (2 << 22))):
+        for t in (0, T - 1):
+            r = first + t * 8192
+            assert call(out=r, f32=None) == 1 and call(out=r + H * 128, f32=None) == (1 if t < T - 1 else G), name
+            assert call(out=r + H * 128 - 16, f32=None) == 1
+        assert call(out=first - size, f32=None) == G
+    assert call(sinks=at + (3 << 22) + size - 4) == 1 and call(sinks=at + (3 << 22) + size) == G
+    assert call(out=plan) == 1 and call(out=plan + n - 256) == 1 and call(out=plan + n) == G
+    assert call(f32=at + (3 << 22) + size - 16) == 1 and call(f32=at + (3 << 22) + size) == G
+    # one token: its stride says nothing
+    one = prompt(num_seqs=1, num_q_heads=Hq, num_kv_heads=H, q_tokens=1, k_tokens=1)
+    n1 = gk.gk_prompt_plan_bytes(one)
+    assert n1 <= n
+    assert call(pr=one, q_stride=0, out=at, f32=None) == 1
+    assert call(pr=one, q_stride=0, kv_stride=0, out=at + row, f32=None) == G
