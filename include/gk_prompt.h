@@ -32,6 +32,8 @@ extern "C" {
 /* Device error-word bit (gk_read_device_error): q_start or k_start is out of
  * order or reaches outside the buffers; the plan is empty then. */
 #define GK_DEVERR_SEQ 0x40u
+/* GK_DEVERR_PLAN, of gk_prompt_attn: the plan is not one that gk_prompt_plan has
+ * filled for this prompt; nothing is written. */
 
 /* ------------------------------------------------------------ rotary positions */
 #define GK_ROPE_PLAIN 0  /* no scaling: factor is not read */
@@ -182,7 +184,8 @@ gk_status gk_prompt_plan(const gk_prompt *prompt, const int32_t *q_start, const 
  * e^(s_t - max s), passes fp32's range is infinite or NaN.  Rows that meet infinities or
  * NaN in V, or a score some 80 above those of the 2048 keys before it, are computed by
  * a second, slow path (a warp a row).
- *   prompt, plan, plan_bytes  as given to gk_prompt_plan (the same prompt)
+ *   prompt, plan, plan_bytes  as given to gk_prompt_plan (the same prompt, field by
+ *            field: another one's plan writes nothing and sets GK_DEVERR_PLAN)
  *   q        bf16, element (t, h, e) at t * q_stride + h * 64 + e; strides in
  *            elements, multiples of 8; q, k, v and out 16-byte aligned
  *   k, v     bf16, the same with k_stride and v_stride (slices of a fused

@@ -179,6 +179,13 @@ PromptLayout prompt_layout(const gk_prompt& s) {
   return L;
 }
 
+uint64_t prompt_stamp(const gk_prompt& s) {
+  uint64_t x = 0xcbf29ce484222325ull;
+  for (int32_t f : {s.num_seqs, s.num_q_heads, s.num_kv_heads, s.head_dim, s.window, s.q_tokens, s.k_tokens})
+    for (int b = 0; b < 32; b += 8) x = (x ^ (uint32_t(f) >> b & 255u)) * 0x100000001b3ull;
+  return x;
+}
+
 }  // namespace gk
 
 using namespace gk;
@@ -742,6 +749,7 @@ gk_status gk_prompt_plan(const gk_prompt* prompt, const int32_t* q_start, const 
   p.splits = reinterpret_cast<int4*>(ws + L.splits);
   p.max_items = L.max_items;
   p.max_recs = L.max_recs;
+  p.stamp = prompt_stamp(*prompt);
   p.num_seqs = prompt->num_seqs;
   p.Hkv = prompt->num_kv_heads;
   p.W = prompt_window(*prompt);
@@ -819,6 +827,7 @@ static gk_status prompt_attention(const gk_prompt* prompt, void* plan, size_t pl
   p.v_stride = v_stride;
   p.max_items = L.max_items;
   p.max_recs = L.max_recs;
+  p.stamp = prompt_stamp(s);
   p.Hq = s.num_q_heads;
   p.Hkv = s.num_kv_heads;
   p.G = s.num_q_heads / s.num_kv_heads;

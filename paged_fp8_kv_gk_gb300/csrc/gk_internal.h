@@ -258,14 +258,18 @@ struct PromptLayout {
   int tile_tokens;
 };
 PromptLayout prompt_layout(const gk_prompt& s);
+// A number of the prompt that its plan holds, so that no other prompt's (or none at all) is
+// taken for it: FNV-1a over its fields.
+uint64_t prompt_stamp(const gk_prompt& s);
 
 struct PromptPlanParams {
   const int32_t* q_start;
   const int32_t* k_start;
-  int32_t* hdr;   // 0: items, 1: split tiles
+  int32_t* hdr;   // 0: items, 1: split tiles, 2 and 3: stamp
   int4* items;    // two an item: (q0, tokens, own key of q0, first key), (end key, record or -1)
   int4* splits;   // a split tile: (q0, tokens, first record, records)
   int64_t max_items, max_recs;
+  uint64_t stamp;
   int num_seqs, Hkv, W, q_tokens, k_tokens, tile_tokens;
 };
 
@@ -283,6 +287,7 @@ struct PromptAttnParams {
   float* records;
   int64_t q_stride, k_stride, v_stride;  // elements
   int64_t max_items, max_recs;
+  uint64_t stamp;
   int Hq, Hkv, G, W, q_tokens, k_tokens, tile_tokens;
   int wait_tries;  // of a barrier wait (0: the launcher's)
   int hold;        // a test's: nothing is copied, so that the waits run out

@@ -83,11 +83,14 @@ __global__ void __launch_bounds__(kPromptPlanThreads)
     if (s < p.num_seqs) first_tile[s] = tiles + at;
     tiles += total;
   }
+  auto finish = [&](int items, int split_tiles) {
+    *reinterpret_cast<int4*>(p.hdr) = make_int4(items, split_tiles, int(uint32_t(p.stamp)), int(p.stamp >> 32));
+  };
   // one range out of order and the others may overlap: no item then
   if (__syncthreads_or(bad)) {
     if (tid == 0) {
       atomicOr(&g_prompt_error, GK_DEVERR_SEQ);
-      p.hdr[0] = p.hdr[1] = 0;
+      finish(0, 0);
     }
     return;
   }
@@ -183,16 +186,21 @@ __global__ void __launch_bounds__(kPromptPlanThreads)
     });
   }
   __syncthreads();
-  if (tid == 0) {
-    p.hdr[0] = items;
-    p.hdr[1] = n_splits;
-  }
+  if (tid == 0) finish(items, n_splits);
 }
 static_assert(kBuckets == kPromptPlanThreads, "a bucket a thread");
 
 // =========================================================================
 // Rows
 // =========================================================================
+// (items, split tiles) of the plan, which may have been written by the grid before this one;
+// none of a plan that is not this prompt's.
+__device__ __forceinline__ int2 plan_counts(const PromptAttnParams& p, bool& ours) {
+  const int4 h = __ldcg(reinterpret_cast<const int4*>(p.hdr));
+  ours = h.z == int(uint32_t(p.stamp)) && h.w == int(p.stamp >> 32);
+  return ours ? make_int2(h.x, h.y) : make_int2(0, 0);
+}
+
 struct Item {
   int q0, n;        // tokens [q0, q0 + n)
   int diag;         // own key of q0
@@ -399,8 +407,9 @@ struct Phase {  // place in a ring of barriers, and the parity of its next phase
 // The places in the plan that a CTA takes, (item, kv head): every grid's width, there
 // and back.
 struct Turn {
+  bool ours;  // the plan is this prompt's
   int n, at, round = 0;
-  __device__ __forceinline__ Turn(const PromptAttnParams& p) : n(__ldcg(p.hdr) * p.Hkv) { next(); }
+  __device__ __forceinline__ Turn(const PromptAttnParams& p) : n(plan_counts(p, ours).x * p.Hkv) { next(); }
   __device__ __forceinline__ bool more() const { return at < n; }
   __device__ __forceinline__ void next() {
     const int g = int(gridDim.x);
@@ -512,6 +521,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
   const uint32_t tmem = sm.tmem;
   open_stream();
   Turn turn(p);
+  if (!turn.ours && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&g_prompt_error, GK_DEVERR_PLAN);
 
   if (warp == kSoftWarps) {
     const bool one = elect_one();
@@ -887,7 +897,8 @@ __global__ void __launch_bounds__(kRowThreads)
     prompt_join_kernel(const __grid_constant__ PromptAttnParams p) {
   follow_stream();
   const int lane = threadIdx.x & 31;
-  const int64_t rows = int64_t(__ldcg(p.hdr + 1)) * p.Hkv * kPromptRows;
+  bool ours;
+  const int64_t rows = int64_t(plan_counts(p, ours).y) * p.Hkv * kPromptRows;
   const int64_t step = int64_t(gridDim.x) * (kRowThreads / 32);
   for (int64_t x = int64_t(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5); x < rows; x += step) {
     const int r = int(x % kPromptRows);
