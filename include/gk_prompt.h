@@ -148,7 +148,7 @@ typedef struct {
     int32_t window;       /* W: a query sees its own key and the W - 1 before it; 0: all */
     int32_t q_tokens;     /* rows of q and out, at most 2^28; those outside every sequence are padding */
     int32_t k_tokens;     /* rows of k and v, at most 2^28 */
-} gk_prompt;
+} gk_prompt; /* up to 2^31 - 2^17 tiles times kv heads (a tile is 128 / (Hq / Hkv) tokens) */
 
 /*
  * Bytes of the plan of a prompt's attention (device memory, 256-byte aligned);

@@ -717,8 +717,10 @@ static gk_status check_prompt(const gk_prompt* s) {
   if (s->head_dim != kHeadDim || s->num_q_heads / s->num_kv_heads > kPromptRows ||
       s->num_seqs > kPromptMaxSeqs || s->q_tokens > (1 << 28) || s->k_tokens > (1 << 28))
     return GK_ERR_UNSUPPORTED;
-  // a CTA for each item and kv head
-  return prompt_layout(*s).max_items * s->num_kv_heads > INT32_MAX ? GK_ERR_UNSUPPORTED : GK_OK;
+  // a CTA's place among the (item, kv head) is an int that runs up to two grids past the
+  // last; 2^16 are more than two of any
+  return prompt_layout(*s).max_items * s->num_kv_heads > INT32_MAX - (1 << 16) ? GK_ERR_UNSUPPORTED
+                                                                                : GK_OK;
 }
 
 // Window in keys: none reaches further than any key.

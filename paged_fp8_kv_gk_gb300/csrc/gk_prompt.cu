@@ -168,6 +168,13 @@ __global__ void __launch_bounds__(kPromptPlanThreads)
   __syncthreads();
   int items;
   const int at = block_scan(count[tid], warps, items);
+  if (items > p.max_items) {  // not if the room was reckoned rightly
+    if (tid == 0) {
+      atomicOr(&g_prompt_error, GK_DEVERR_PLAN);
+      finish(0, 0);
+    }
+    return;
+  }
   count[tid] = at;
   __syncthreads();
   for (int t = tid; t < tiles; t += kPromptPlanThreads) {

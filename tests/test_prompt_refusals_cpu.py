@@ -1,6 +1,8 @@
 """What a prompt's operators refuse before any launch, beyond tests/test_prompt_cpu.py."""
 import ctypes
 
+import pytest
+
 import paged_fp8_kv_gk_gb300 as gk
 from test_prompt_cpu import FAKE, no_device, prompt
 
@@ -57,3 +59,14 @@ def test_outputs_that_overlap_inputs():
     assert n1 <= n
     assert call(pr=one, q_stride=0, out=at, f32=None) == 1
     assert call(pr=one, q_stride=0, kv_stride=0, out=at + row, f32=None) == G
+
+
+def test_most_items():
+    """The kernel's place in a plan, (item, kv head), runs up to two grids past the last in 32 bits: what comes
+    nearer to them than 2^16 is refused."""
+    def size(q):
+        return gk.gk_prompt_plan_bytes(prompt(num_seqs=1, num_q_heads=128 * 8, q_tokens=q))
+    most = (2 ** 31 - 1 - 2 ** 16) // 8           # a token a tile
+    assert size(most) > 32 * most and size(most + 1) == 0 and size(2 ** 28 - 1) == 0
+    with pytest.raises(gk.GkError):
+        gk.new_prompt_plan(prompt(num_seqs=1, num_q_heads=128 * 8, q_tokens=most + 1))
