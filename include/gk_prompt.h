@@ -44,7 +44,7 @@ typedef struct {
     int32_t rot_dim;         /* rotated channels R of a head: a multiple of 16 up to 256 */
     int32_t scaling;         /* GK_ROPE_PLAIN, GK_ROPE_LINEAR or GK_ROPE_YARN */
     double theta;            /* base of the frequencies, > 1 */
-    double factor;           /* > 0; YARN: >= 1 */
+    double factor;           /* > 0, and so that 1 / factor is finite; YARN: >= 1 */
     double original_context; /* YARN: positions the model was trained on, > 0 */
     double beta_fast;        /* YARN: turns within original_context from which a pair is fast */
     double beta_slow;        /* YARN: turns up to which a pair is slow, 0 < beta_slow < beta_fast */
@@ -62,8 +62,9 @@ typedef struct {
  *   cos[t, e] = cos(pos[t] f_e),  sin[t, e] = sin(pos[t] f_e)
  * Any int32 position, negative ones too.  The frequencies are worked out in 64
  * bits on the host, as turns a position in 64-bit fixed point, so that a product
- * with the position wraps at whole turns and far positions lose nothing: the angle
- * is off by at most |pos| 2^-50 radians, and the outputs by 2^-22 of their value more.
+ * with the position wraps at whole turns and far positions lose nothing more: the angle
+ * is off by at most |pos| (f_e 2^-50 + 2^-60) radians, beside what YARN's r_e (in 64
+ * bits as well) is off by, and the outputs by 2^-22 of their value more.
  *   pos  int32 [n]; cos, sin  fp32 [n, R/2], 16-byte aligned.
  * n == 0 enqueues nothing.
  */

@@ -635,7 +635,8 @@ gk_status gk_rope_table(const gk_rope_params* params, int64_t n, const int32_t* 
   switch (r.scaling) {
     case GK_ROPE_PLAIN: break;
     case GK_ROPE_LINEAR:
-      if (!(r.factor > 0.0) || !isfinite(r.factor)) return GK_ERR_INVALID_ARG;
+      // the fastest pair turns 1 / factor a position
+      if (!(r.factor > 0.0) || !isfinite(r.factor) || !isfinite(1.0 / r.factor)) return GK_ERR_INVALID_ARG;
       break;
     case GK_ROPE_YARN: {
       if (!(r.factor >= 1.0) || !isfinite(r.factor) || !(r.original_context > 0.0) ||

@@ -70,3 +70,11 @@ def test_most_items():
     assert size(most) > 32 * most and size(most + 1) == 0 and size(2 ** 28 - 1) == 0
     with pytest.raises(gk.GkError):
         gk.new_prompt_plan(prompt(num_seqs=1, num_q_heads=128 * 8, q_tokens=most + 1))
+
+
+@no_device
+def test_linear_factors_without_an_inverse():
+    L, p = gk.lib(), ctypes.c_void_p(FAKE)
+    for factor, want in ((5e-324, 1), (5e-309, 1), (6e-309, gk.GK_ERR_CUDA), (1e-300, gk.GK_ERR_CUDA), (1e300, gk.GK_ERR_CUDA)):
+        params = gk.RopeParams.make(64, 1e4, scaling="linear", factor=factor)
+        assert L.gk_rope_table(ctypes.byref(params), 3, p, p, p, None) == want, factor
