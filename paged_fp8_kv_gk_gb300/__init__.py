@@ -145,11 +145,7 @@ class KvCache:
         self.per_group = per_group
         self.k_layout = int(k_layout)
         self._keep = (ks, vs)
-        held = [t for t in ks + vs if not isinstance(t, int)]
-        # of the tensors: the smallest one's bytes, and their device (-1: several)
-        self._bytes = min((t.numel() * t.element_size() for t in held), default=None)
-        devs = {t.get_device() for t in held}
-        self._dev = None if not devs else devs.pop() if len(devs) == 1 else -1
+        self._held = None
         c = KvCacheC(k_layout=self.k_layout)
         if per_group:
             self._k_arr = _ptr_array(ks, "k_bufs")
@@ -174,6 +170,16 @@ class KvCache:
             if not isinstance(t, int) and t.numel() * t.element_size() < want:
                 raise ValueError(f"a cache buffer holds {t.numel() * t.element_size()} bytes, "
                                  f"the shape needs {want}")
+
+    def held(self):
+        """Of the buffers that are tensors: the smallest one's bytes, and their device (-1: several);
+        (None, None) when there are none.  Looked up by the first call that asks."""
+        if self._held is None:
+            ts = [t for t in self._keep[0] + self._keep[1] if not isinstance(t, int)]
+            devs = {t.get_device() for t in ts}
+            self._held = (min((t.numel() * t.element_size() for t in ts), default=None),
+                          None if not devs else devs.pop() if len(devs) == 1 else -1)
+        return self._held
 
     def param(self):
         return ctypes.byref(self.c)
@@ -879,10 +885,11 @@ def _kv_on(kv, sh, dev):
         raise TypeError("kv must be a KvCache (kv_from_group_buffers, kv_stacked)")
     groups = sh.num_layers // 2
     half = sh.num_blocks * sh.num_kv_heads * sh.block_size * sh.head_dim
-    if kv._dev is not None and kv._dev != dev:
+    held, on = kv.held()
+    if on is not None and on != dev:
         raise ValueError(f"the cache buffers are not all on the current device, cuda:{dev}")
     if (kv.per_group and len(kv._keep[0]) < groups) or (
-            kv._bytes is not None and kv._bytes < (half if kv.per_group else groups * half)):
+            held is not None and held < (half if kv.per_group else groups * half)):
         kv.check(sh)       # names what is wrong
     return kv.param()
 

@@ -78,3 +78,31 @@ def test_linear_factors_without_an_inverse():
     for factor, want in ((5e-324, 1), (5e-309, 1), (6e-309, gk.GK_ERR_CUDA), (1e-300, gk.GK_ERR_CUDA), (1e300, gk.GK_ERR_CUDA)):
         params = gk.RopeParams.make(64, 1e4, scaling="linear", factor=factor)
         assert L.gk_rope_table(ctypes.byref(params), 3, p, p, p, None) == want, factor
+
+
+class Buffer:
+    """What a KvCache asks of a buffer when it is made, and no more."""
+    is_cuda = True
+
+    def __init__(self, *shape):
+        self.shape = shape
+
+    def dim(self):
+        return len(self.shape)
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return FAKE
+
+
+def test_a_cache_is_made_of_what_it_needs():
+    """Buffers are asked for their sizes and device by the calls that check them, not when the cache is
+    made (which took a quarter longer so, and refused buffers that the decode calls take)."""
+    k, v = Buffer(9, 2, 16, 64, 2), Buffer(9, 2, 32, 64)
+    kv = gk.KvCache([k, k], [v, v])
+    assert kv.k_layout == gk.GK_K_PACKED and kv.c.k_bufs
+    kv = gk.kv_stacked(Buffer(2, 9, 2, 32, 64), Buffer(2, 9, 2, 32, 64))
+    assert kv.k_layout == gk.GK_K_PLAIN
+    assert gk.KvCache([FAKE], [FAKE], k_layout=gk.GK_K_PLAIN).held() == (None, None)
