@@ -14,6 +14,7 @@ namespace gk {
 static size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // Shape checks shared by all entry points.  Returns GK_OK, GK_ERR_INVALID_ARG
 // (inconsistent) or GK_ERR_UNSUPPORTED (valid but outside version 1).
@@ -559,7 +560,8 @@ gk_status gk_kv_write(const gk_shape* shape, int32_t layer0, int32_t n_layers, i
   if (n_layers == 0 || n_tokens == 0) return GK_OK;
   if (!k || !v || !k_scale || !v_scale || !slot_full || !slot_swa || !aligned16(k) ||
       !aligned16(v) || (layer_stride & 7) || (token_stride & 7) ||
-      (cos != nullptr) != (sin != nullptr) || !aligned16(cos) || !aligned16(sin))
+      (cos != nullptr) != (sin != nullptr) || !aligned16(cos) || !aligned16(sin) ||
+      !aligned4(k_scale) || !aligned4(v_scale) || !aligned4(slot_full) || !aligned4(slot_swa))
     return GK_ERR_INVALID_ARG;
   KvWriteParams p;
   memset(&p, 0, sizeof(p));
@@ -594,7 +596,8 @@ gk_status gk_kv_read(const gk_shape* shape, int32_t layer0, int32_t n_layers, in
   if (st != GK_OK) return st;
   if (n_layers == 0 || n_tokens == 0) return GK_OK;
   if (!k_out || !v_out || !k_scale || !v_scale || !slot_full || !slot_swa || !aligned16(k_out) ||
-      !aligned16(v_out))
+      !aligned16(v_out) || !aligned4(k_scale) || !aligned4(v_scale) || !aligned4(slot_full) ||
+      !aligned4(slot_swa))
     return GK_ERR_INVALID_ARG;
   KvReadParams p;
   memset(&p, 0, sizeof(p));

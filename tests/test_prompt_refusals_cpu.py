@@ -4,7 +4,7 @@ import ctypes
 import pytest
 
 import paged_fp8_kv_gk_gb300 as gk
-from test_prompt_cpu import FAKE, no_device, prompt
+from test_prompt_cpu import FAKE, no_device, prompt, shape
 
 
 @no_device
@@ -78,6 +78,24 @@ def test_linear_factors_without_an_inverse():
     for factor, want in ((5e-324, 1), (5e-309, 1), (6e-309, gk.GK_ERR_CUDA), (1e-300, gk.GK_ERR_CUDA), (1e300, gk.GK_ERR_CUDA)):
         params = gk.RopeParams.make(64, 1e4, scaling="linear", factor=factor)
         assert L.gk_rope_table(ctypes.byref(params), 3, p, p, p, None) == want, factor
+
+
+@no_device
+def test_misaligned_slots_and_scales():
+    """A pointer to int32 or fp32 that is no multiple of four: refused, not left to the GPU."""
+    L, p = gk.lib(), ctypes.c_void_p(FAKE)
+    arr = (ctypes.c_void_p * 2)(FAKE, FAKE)
+    kv = gk.KvCacheC(k_bufs=ctypes.cast(arr, ctypes.c_void_p), v_bufs=ctypes.cast(arr, ctypes.c_void_p))
+    # layer0, n_layers, n_tokens, k, v, strides, cos, sin, k_scale, v_scale, slots, active, kv, stream
+    write = [0, 4, 10, p, p, 1280, 128, p, p, p, p, p, p, p, ctypes.byref(kv), None]
+    read = [0, 4, 10, ctypes.byref(kv), p, p, p, p, p, p, p, None]
+    for call, args, where in ((L.gk_kv_write, write, (9, 10, 11, 12)), (L.gk_kv_read, read, (4, 5, 6, 7))):
+        assert call(ctypes.byref(shape()), *args) == gk.GK_ERR_CUDA
+        for i in where:
+            for off in (1, 2, 3):
+                a = list(args)
+                a[i] = ctypes.c_void_p(FAKE + off)
+                assert call(ctypes.byref(shape()), *a) == 1, (i, off)
 
 
 class Buffer:
