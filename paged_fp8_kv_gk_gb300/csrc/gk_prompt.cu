@@ -237,19 +237,23 @@ struct RowResult {
 __device__ __noinline__ RowResult attend_row(const PromptAttnParams& p, int2 keys, int h, const uint16_t* q) {
   const int lane = threadIdx.x & 31;
   RowResult r = {-INFINITY, 0.f, make_float2(0.f, 0.f)};
+  // from L2, as K and V: the grid before may have written it while this one was launched
+  uint4 x[kHeadDim / 8];
+#pragma unroll
+  for (int c = 0; c < kHeadDim / 8; ++c) x[c] = __ldcg(reinterpret_cast<const uint4*>(q) + c);
   for (int t0 = keys.x; t0 < keys.y; t0 += 32) {
     const int t = t0 + lane;
     float s = -INFINITY;
     if (t < keys.y) {
       const uint16_t* kr = p.k + int64_t(t) * p.k_stride + h * kHeadDim;
       float2 a = make_float2(0.f, 0.f);
-      for (int c = 0; c < kHeadDim; c += 8) {
-        const uint4 w = __ldcg(reinterpret_cast<const uint4*>(kr + c));
-        const uint4 x = *reinterpret_cast<const uint4*>(q + c);
-        a = fma2(bf16x2_to_f32x2(w.x), bf16x2_to_f32x2(x.x), a);
-        a = fma2(bf16x2_to_f32x2(w.y), bf16x2_to_f32x2(x.y), a);
-        a = fma2(bf16x2_to_f32x2(w.z), bf16x2_to_f32x2(x.z), a);
-        a = fma2(bf16x2_to_f32x2(w.w), bf16x2_to_f32x2(x.w), a);
+#pragma unroll
+      for (int c = 0; c < kHeadDim / 8; ++c) {
+        const uint4 w = __ldcg(reinterpret_cast<const uint4*>(kr) + c);
+        a = fma2(bf16x2_to_f32x2(w.x), bf16x2_to_f32x2(x[c].x), a);
+        a = fma2(bf16x2_to_f32x2(w.y), bf16x2_to_f32x2(x[c].y), a);
+        a = fma2(bf16x2_to_f32x2(w.z), bf16x2_to_f32x2(x[c].z), a);
+        a = fma2(bf16x2_to_f32x2(w.w), bf16x2_to_f32x2(x[c].w), a);
       }
       s = (a.x + a.y) * kScoreLog2;
     }
