@@ -362,17 +362,18 @@ __device__ __forceinline__ float max32(const uint32_t (&s)[32]) {
 // a hundred thousand keys, and the waits of the other warps are bounded).
 //
 // A tile and step take 512 cycles of the tensor cores and as many of the exponential
-// unit (4 a warp instruction).  Measured: 900 (8192 tokens of 64 heads in 437 us, 1260
-// TFLOP/s; 8192 over 65536 keys in 6.1 ms, 1350): exponentials 58 % busy, issue slots 50 %,
-// the rest latency that two softmax warps a scheduler do not cover: both wait, load and
-// store together.  On the way, 8192 over 65536 keys, in ms: one lane of a diverged warp
-// issuing the products 7.9, an elected one 6.8; P's last use awaited behind the
-// exponentials 6.5; no maxima 5.6 (one item a CTA; 6.0 with items in turns, which
-// shortened windows and ragged batches), polls without a count 5.5.  Not kept: half a
-// row a thread and twice the warps (6.1); two tiles a CTA that share K and V and take
-// turns with their exponentials (7.0: the warps that poll sit beside more softmax
-// warps); waits asleep (6.0); 64 keys a step are 25 % more tensor time (a product of N
-// = 64 from shared memory takes 48 cycles, not 32).
+// unit (4 a warp instruction).  Measured: 920 (8192 tokens of 64 heads in 441 to 446 us, 1240
+// TFLOP/s; 8192 over 65536 keys in 6.2 to 6.3 ms, 1330): exponentials 57 % busy, issue slots
+// 50 %, the rest latency that two softmax warps a scheduler do not cover: both wait, load and
+// store together.  What the steps brought, 8192 over 65536 keys: the products issued by an
+// elected lane of a converged warp instead of one lane of a diverged one 7.9 -> 6.8 ms; P's last
+// use awaited behind the exponentials 6.8 -> 6.5; no maxima behind a row's first step, a
+// seventh less; items in turns instead of one a CTA 5.6 -> 6.0 (5.5, once measured with them, was
+// not met again), for windows and ragged batches that, with short last steps, went from 225
+// to 170 us and from 823 to 728.  Not kept, all slower: half a row a thread and twice the
+// warps; two tiles a CTA that share K and V and take turns with their exponentials (the warps
+// that poll sit beside more softmax warps); waits asleep; 64 keys a step are 25 % more tensor
+// time (a product of N = 64 from shared memory takes 48 cycles, not 32).
 constexpr int kSoftWarps = 4;
 constexpr int kAttnThreads = 32 * (kSoftWarps + 2);
 constexpr int kKStages = 3, kVStages = 2;               // V is needed a softmax later than K
