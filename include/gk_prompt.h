@@ -30,7 +30,8 @@ extern "C" {
 #define GK_KV_SKIP (-1) /* a slot that gk_kv_write and gk_kv_read leave alone */
 
 /* Device error-word bit (gk_read_device_error): q_start or k_start is out of
- * order or reaches outside the buffers; the plan is empty then. */
+ * order or reaches outside the buffers, or a query sees more keys than
+ * gk_prompt_plan can serve; the plan is empty then. */
 #define GK_DEVERR_SEQ 0x40u
 /* GK_DEVERR_PLAN, of gk_prompt_attn: the plan is not one that gk_prompt_plan has
  * filled for this prompt; nothing is written. */
@@ -164,7 +165,10 @@ size_t gk_prompt_plan_bytes(const gk_prompt *prompt);
  * q_start and k_start (DEVICE int32 [num_seqs + 1], ascending).  Run once for all
  * layers (and calls) with these sequences and this window.
  * Where one of them descends or leaves [0, q_tokens] or [0, k_tokens], the plan is
- * empty (calls with it write nothing) and GK_DEVERR_SEQ is set.
+ * empty (calls with it write nothing) and GK_DEVERR_SEQ is set.  So it is where a tile
+ * of queries sees more than 2^20 keys and they cannot be split into parts that do not:
+ * there is room for 640 / Hkv parts, and only where tiles times Hkv are below 608.  (A
+ * chunk over more keys than that is given in smaller chunks.)
  */
 gk_status gk_prompt_plan(const gk_prompt *prompt, const int32_t *q_start, const int32_t *k_start,
                          void *plan, size_t plan_bytes, void *stream);

@@ -28,6 +28,10 @@ constexpr int kPromptPlanThreads = 1024;
 constexpr int kBuckets = 1024;
 constexpr int kCandidates = 16;  // keys of a part: 4 steps << candidate
 constexpr int kItemSteps = 3;    // an item's fixed time, in steps (start, first loads, output)
+// An item's most steps, 2^20 keys.  Every product adds 16 keys to the running sum of p v and
+// cuts it at 2^-23 of its value: 2^-7 of the sum of p |v| after 2^16 of them at worst.  (At 2^22
+// keys of one weight 0.7 % were missing, and from 2^26 on the row's own sum stood still.)
+constexpr int kMostSteps = 1 << 13;
 
 struct Tile {
   int q0, n, diag, k_lo, k_end, steps;
@@ -146,7 +150,7 @@ __global__ void __launch_bounds__(kPromptPlanThreads)
         // join parts
         const int64_t end = max(mean, int64_t(item)) +
                             (int64_t(items_of[c]) * p.Hkv > kPromptSlots ? item / 2 : 0) + (recs_of[c] ? 2 : 0);
-        if (recs_of[c] <= p.max_recs && end < best) {
+        if (recs_of[c] <= p.max_recs && min(len, longest) <= kMostSteps && end < best) {
           best = end;
           part = recs_of[c] ? len : 0;
         }
@@ -155,6 +159,13 @@ __global__ void __launch_bounds__(kPromptPlanThreads)
     __syncthreads();
   }
   const int len = part > 0 ? part : max(longest, 1);
+  if (min(len, longest) > kMostSteps) {
+    if (tid == 0) {
+      atomicOr(&g_prompt_error, GK_DEVERR_SEQ);
+      finish(0, 0);
+    }
+    return;
+  }
   auto bucket = [&](int steps) -> int {
     return kBuckets - 1 - int(int64_t(steps) * (kBuckets - 1) / len);  // the longest first
   };
