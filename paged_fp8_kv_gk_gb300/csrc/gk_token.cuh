@@ -65,12 +65,11 @@ __device__ __forceinline__ float2 bf16x2_to_f32x2(uint32_t w) {
 // What divides by a layer scale.
 struct LayerScale {
   float scale;
-  float rcp;   // 1 / scale, correctly rounded; 0 outside 2^-40 .. 2^40
+  float rcp;   // 1 / scale, correctly rounded; 0 outside 2^-40 .. 2^40 (negative scales: neg_div)
   bool exact;  // rcp is 1 / scale
 };
 __device__ __forceinline__ LayerScale layer_scale(float s) {
-  const float a = fabsf(s);
-  return {s, a >= 0x1p-40f && a <= 0x1p40f ? __frcp_rn(s) : 0.f, exact_reciprocal(s) != 0.f};
+  return {s, s >= 0x1p-40f && s <= 0x1p40f ? __frcp_rn(s) : 0.f, exact_reciprocal(s) != 0.f};
 }
 
 // -(x / s), correctly rounded, for |x| < 2^60: a quotient by 1 / s in two terms
@@ -83,7 +82,8 @@ __device__ __forceinline__ LayerScale layer_scale(float s) {
 // every x whose quotient is that near to a middle.  For |x| < 2^-100 the remainder
 // may underflow; such a quotient is far below half of the smallest block scale and
 // only its sign counts.  The terms have one sign and the quotient is negated, so
-// that a zero comes out of x + q0 s and q0 - rem / s with its own.
+// that a zero comes out of x + q0 s and q0 - rem / s with its own (for s > 0: a -0 of x by
+// a negative s came out as -0).
 __device__ __forceinline__ float2 neg_div(float2 x, float2 s, float2 nr, float2 nh, float2 nl) {
   const float2 q0 = fma2(x, nh, mul2(x, nl));
   return fma2(fma2(q0, s, x), nr, q0);
