@@ -332,10 +332,10 @@ __device__ __forceinline__ void write_tokens(const Kv4WriteParams& p, int tg, in
       for (int q = 0; q < 4; ++q) {
         const float4 c4 = kKeep ? lds_f4(cs0 + 512 * q) : ldg_nc_f4(p.cosb + rope_at + 4 * q);
         const float4 s4 = kKeep ? lds_f4(cs0 + 512 * q + 256) : ldg_nc_f4(p.sinb + rope_at + 4 * q);
-        x[2 * q] = add2(mul2(x[2 * q], make_float2(c4.x, c4.y)),
-                        mul2(bf16x2_to_f32x2(yw[2 * q] ^ flip), make_float2(s4.x, s4.y)));
-        x[2 * q + 1] = add2(mul2(x[2 * q + 1], make_float2(c4.z, c4.w)),
-                            mul2(bf16x2_to_f32x2(yw[2 * q + 1] ^ flip), make_float2(s4.z, s4.w)));
+        x[2 * q] = sum_apart(mul2(x[2 * q], make_float2(c4.x, c4.y)),
+                             mul2(bf16x2_to_f32x2(yw[2 * q] ^ flip), make_float2(s4.x, s4.y)));
+        x[2 * q + 1] = sum_apart(mul2(x[2 * q + 1], make_float2(c4.z, c4.w)),
+                                 mul2(bf16x2_to_f32x2(yw[2 * q + 1] ^ flip), make_float2(s4.z, s4.w)));
       }
     }
     if (ok) {

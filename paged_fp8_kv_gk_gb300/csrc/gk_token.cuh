@@ -51,6 +51,12 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return r;
 }
 
+// a + b of two products that are rounded on their own: of mul2 and add2 the compiler makes
+// one fused operation, of scalar intrinsics it may not.
+__device__ __forceinline__ float2 sum_apart(float2 a, float2 b) {
+  return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y));
+}
+
 // max(|a|, |b|, |c|), NaN when one of them is.
 __device__ __forceinline__ float max3_abs_nan(float a, float b, float c) {
   float r;

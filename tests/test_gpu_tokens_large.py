@@ -149,3 +149,24 @@ def test_negative_scales_of_the_4_bit_write():
     assert gk.gk_read_device_error() == 0
     for got, w in zip(cache, want):
         assert np.array_equal(got.reshape(-1).cpu().numpy(), w)
+
+
+def test_every_operation_of_the_4_bit_rotation_is_rounded():
+    """Products and sums on their own, as in the append: 40000 tokens of two layers, where a fused sum gives
+    two other bytes (the second seed)."""
+    T, H, NL, B = 20000, 2, 2, 32
+    nb = 2 * (T // B + 1)
+    sh = shape_of(NL=NL, Hkv=H, B=B, nb=nb)
+    at, other = np.arange(T).astype(np.int32), (nb // 2 * B + np.arange(T)).astype(np.int32)
+    for seed in (0, 4):
+        torch.manual_seed(seed)
+        k = torch.randn(NL, T, H, 64).to(torch.bfloat16)
+        cos, sin = angles(T, np.random.default_rng(seed))
+        scales = np.array([0.0137, 0.25], np.float32)
+        cache = torch.zeros(1, nb, H, B // 16, gk.GK_KV4_TILE_BYTES, dtype=torch.uint8, device="cuda")
+        want = [cache[0].reshape(-1).cpu().numpy().copy()]
+        gk.gk_kv4_write(sh, k.cuda(), k.cuda(), f32(cos), f32(sin), f32(scales), f32(scales), i32(at), i32(other), cache)
+        x = k.float().numpy()
+        k4.write(want, sh, x, x, cos, sin, scales, scales, at, other)
+        assert np.array_equal(cache[0].reshape(-1).cpu().numpy(), want[0])
+    assert gk.gk_read_device_error() == 0
